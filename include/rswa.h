@@ -15,8 +15,8 @@
  *     "KV cache management" and "Model architecture".
  * Readings where the pages are silent: prefix rows attend causally among
  * themselves; the window of n includes the current token; the softmax scale
- * is 1/sqrt(head_dim); positions are applied by the caller (RoPE etc. before
- * Q/K reach this library); one KV head per query head (standard MHA, the
+ * is 1/sqrt(head_dim); positions are applied before Q/K reach the attention
+ * calls (by the caller, or by rswa_qk_norm_rope and rswa_append_kv_rope); one KV head per query head (standard MHA, the
  * pages' baseline) unless the cache is created by rswa_cache_create_gqa,
  * which lets several query heads share one KV head.
  *
@@ -67,8 +67,9 @@ enum rswa_status {
   RSWA_EDTYPE = 3,    /* unsupported dtype / head_dim combination */
   RSWA_EHANDLE = 4,   /* NULL, destroyed or foreign handle */
   RSWA_ECUDA = 5,     /* a CUDA runtime call or launch failed */
-  RSWA_EDEVICE = 6    /* a kernel flagged an error (bounded wait ran out, or a
-                        launch shape that does not cover its work) */
+  RSWA_EDEVICE = 6    /* a kernel flagged an error (bounded wait ran out, a
+                        launch shape that does not cover its work, or a draft
+                        tree or accepted path that is not one) */
 };
 
 enum rswa_dtype { RSWA_F32 = 0, RSWA_BF16 = 1 };
@@ -263,6 +264,141 @@ RSWA_API int rswa_decode_block(rswa_cache* cache, const void* q, const void* k,
 RSWA_API int rswa_decode_step_fused_static(rswa_cache* cache, const void* q,
                                            const void* k, const void* v,
                                            void* o, float* lse, void* stream);
+
+/*
+ * Norm and rotation of the query and key heads of a layer (host struct; the
+ * arrays it points to are on the device and are read by the calls that take
+ * it).  Of a head x with d = head_dim elements:
+ *   y = x * weight / sqrt(mean(x^2) + eps)   (y = x where the weight is NULL)
+ *   y's first rotary_dim elements are turned pair by pair by the angle
+ *   position * inv_freq[i], i = 0 .. rotary_dim/2 - 1:
+ *     (a, b) -> (a cos - b sin, b cos + a sin),
+ *   with (a, b) = (y[i], y[i + rotary_dim/2]), or (y[2i], y[2i+1]) when
+ *   `interleaved` is not 0; the other elements stay.
+ * The result is rounded once, to the tensors' dtype.  The angle is held as a
+ * 64-bit fraction of a turn, so that it is as exact at position 10^6 as at 1
+ * (its error is below position * 2^-52 turns).  Scaled and extended rotations
+ * are a matter of inv_freq.
+ */
+typedef struct rswa_rope {
+  const void* q_weight;   /* [d], dtype of the heads; NULL: queries not normed */
+  const void* k_weight;   /* [d], dtype of the heads; NULL: keys not normed */
+  const double* inv_freq; /* [rotary_dim/2] radians per position, finite; may
+                             be NULL when rotary_dim is 0 */
+  float eps;              /* >= 0, finite */
+  int rotary_dim;         /* a multiple of 16 in 0 .. head_dim */
+  int interleaved;        /* 0: pairs half the rotated elements apart */
+} rswa_rope;
+
+/*
+ * Norm and rotate the query and key heads of `rows` rows in one pass: what
+ * rswa_prefill, rswa_decode_step_fused and the block and tree calls take.
+ *   q, k         rows of [heads][d] and [kv_heads][d] elements, q_stride and
+ *                k_stride elements apart (a multiple of 16 bytes each, at
+ *                least the row's own length unless rows < 2): the output of
+ *                one projection of queries, keys and values needs no copy.
+ *   positions    device array of `rows` positions (any int64 value).
+ *   q_out, k_out [rows][heads][d] and [rows][kv_heads][d], contiguous.  q_out
+ *                may be q and k_out may be k where the stride is the row's own
+ *                length; they must not overlap the inputs in another way.
+ * Needs no cache; runs on the current device, to which the stream and all
+ * pointers belong.  All pointers 16-byte aligned (positions and inv_freq
+ * 8-byte).  rows = 0 does nothing.
+ * Errors: RSWA_EINVAL, RSWA_EDTYPE (dtype, head_dim), RSWA_ECUDA.
+ */
+RSWA_API int rswa_qk_norm_rope(const rswa_rope* rope, const void* q,
+                               int64_t q_stride, const void* k,
+                               int64_t k_stride, const int64_t* positions,
+                               int64_t rows, int heads, int kv_heads,
+                               int head_dim, int dtype, void* q_out,
+                               void* k_out, void* stream);
+
+/*
+ * rswa_qk_norm_rope for `tokens` new tokens of every sequence of a cache, at
+ * the positions that follow it: row b * tokens + i stands at
+ * m_b + t_b + offsets[b][i] (offsets: device int32 [B][tokens]; NULL: i).  For
+ * rswa_decode_step_fused (tokens = 1), rswa_decode_block, and rswa_decode_tree
+ * (offsets = the nodes' depths).  Heads, head_dim and dtype are the cache's.
+ * m_b and t_b are read on the device; the cache is not changed.
+ * Errors: RSWA_EHANDLE, RSWA_EINVAL, RSWA_ECUDA.
+ */
+RSWA_API int rswa_qk_norm_rope_cached(rswa_cache* cache, const rswa_rope* rope,
+                                      const void* q, int64_t q_stride,
+                                      const void* k, int64_t k_stride,
+                                      const int32_t* offsets, int64_t tokens,
+                                      void* q_out, void* k_out, void* stream);
+
+/*
+ * rswa_append_kv with the norm and the rotation on the way: for every
+ * sequence, q_out = norm and rotation of q at position m_b + t_b, ring slot
+ * t_b mod n takes the normed and rotated k and the v as it is, and t_b
+ * advances by one.  rswa_decode_step(q_out) follows.  q, k, v: B rows with the
+ * strides of rswa_qk_norm_rope; q_out: [B][H][d], may be q where q_stride is
+ * H * d.  Errors: RSWA_EHANDLE, RSWA_EINVAL, RSWA_ECUDA.
+ */
+RSWA_API int rswa_append_kv_rope(rswa_cache* cache, const rswa_rope* rope,
+                                 const void* q, int64_t q_stride,
+                                 const void* k, int64_t k_stride,
+                                 const void* v, int64_t v_stride, void* q_out,
+                                 void* stream);
+
+/*
+ * Device bytes of workspace that rswa_decode_tree needs for trees of up to
+ * `nodes` nodes on this cache (at least 256).  The workspace need not be
+ * initialised and keeps nothing between calls; calls that may overlap on the
+ * GPU need one each.  Host-only.  Errors: RSWA_EHANDLE, RSWA_EINVAL.
+ */
+RSWA_API int rswa_decode_tree_workspace(rswa_cache* cache, int64_t nodes,
+                                        size_t* out_bytes);
+
+/*
+ * Attention of a tree of drafted tokens per sequence over the cache, to
+ * verify several drafts in one call; the cache is not changed.
+ *   q, o       [B][nodes][H][d]; k, v [B][nodes][H_kv][d]; 1 <= nodes <= 1024.
+ *   parents    device int32 [B][nodes]: the node before, -1 <= parents[b][i]
+ *              < i; -1 for a node that follows the last output directly.
+ *   counts     device int32 [B], the live nodes of each sequence, 0 <=
+ *              counts[b] <= nodes; or NULL: all of them.  Rows of o and lse
+ *              past the count are left as they are, and rows of q, k and v
+ *              past it may hold anything.
+ *   lse        [B][nodes][H] float32 natural-log log-sum-exp, or NULL.
+ *   workspace  device buffer of rswa_decode_tree_workspace bytes, 256-byte
+ *              aligned.
+ * Node i has depth(i) = 0 when its parent is -1, else depth(parent) + 1, and
+ * stands for output t_b + depth(i): it attends to the prefix, to the cached
+ * outputs j > t_b + depth(i) - n, and to itself and its ancestors a with
+ * depth(i) - depth(a) < n - what rswa_decode_block would give for the chain
+ * that ends in it.  Keys and values of live nodes and of the cache must be
+ * finite.  Accepted nodes are stored with rswa_commit_tree.
+ * A parent or a count outside its range sets the device flag (RSWA_EDEVICE of
+ * rswa_sync_status); the parent is then taken as -1 and the count as the
+ * nearest in range.  The ordering rule of rswa_decode_step for the prefix
+ * rows holds here too.
+ * Errors: RSWA_EHANDLE, RSWA_EINVAL, RSWA_ECAPACITY (workspace too small),
+ * RSWA_ECUDA.
+ */
+RSWA_API int rswa_decode_tree(rswa_cache* cache, const void* q, const void* k,
+                              const void* v, const int32_t* parents,
+                              const int32_t* counts, int64_t nodes, void* o,
+                              float* lse, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * Append the accepted path of a tree: for i < accepted[b], output t_b + i
+ * takes the key and value of node path[b][i] (its last n only, where more are
+ * accepted), then t_b advances by accepted[b].
+ *   k, v       [B][nodes][H_kv][d], as given to rswa_decode_tree.
+ *   path       device int32 [B][max_path], nodes in order; accepted device
+ *              int32 [B], 0 <= accepted[b] <= max_path.
+ * 1 <= nodes <= 1024, 1 <= max_path <= 1024.  A count or a node outside its
+ * range (nodes past accepted[b] are not looked at) sets the device flag
+ * (RSWA_EDEVICE of rswa_sync_status) and leaves that sequence as it was.
+ * Errors: RSWA_EHANDLE, RSWA_EINVAL, RSWA_ECUDA.
+ */
+RSWA_API int rswa_commit_tree(rswa_cache* cache, const void* k, const void* v,
+                              int64_t nodes, const int32_t* path,
+                              const int32_t* accepted, int64_t max_path,
+                              void* stream);
 
 /*
  * Live cache size of sequence b in bytes: C(t_b) * H_kv * d * 2 (K and V) *

@@ -47,6 +47,9 @@ bool injected_failure() {
   return false;
 }
 
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
 int status_of(cudaError_t e) { return e == cudaSuccess ? RSWA_OK : RSWA_ECUDA; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -79,6 +82,21 @@ int run_decode(rswa_cache* cache, F launch) {
   const cudaError_t e = launch(prefetch);
   if (e == cudaSuccess) cache->prefix_stable.store(true);
   return status_of(e);
+}
+
+// A norm and rotation that the kernels can run on heads of head_dim elements.
+bool valid_rope(const rswa_rope* r, int head_dim) {
+  if (!r || !(r->eps >= 0.f) || r->eps > 1e30f) return false;
+  if (r->rotary_dim < 0 || r->rotary_dim > head_dim || r->rotary_dim % 16 != 0) return false;
+  if (r->rotary_dim > 0 && (!r->inv_freq || !aligned8(r->inv_freq))) return false;
+  return aligned16(r->q_weight) && aligned16(r->k_weight);
+}
+
+// `rows` rows of `len` elements, `stride` apart, of 16-byte vectors.
+bool valid_rows(const void* p, int64_t stride, int64_t len, int64_t rows, int dtype) {
+  const int64_t elt = dtype == RSWA_F32 ? 4 : 2;
+  if (!p || !aligned16(p) || stride < 0 || stride > (int64_t(1) << 40)) return false;
+  return rows < 2 || (stride >= len && stride * elt % 16 == 0);
 }
 
 struct Layout {
@@ -454,6 +472,141 @@ int rswa_decode_step_fused_static(rswa_cache* cache, const void* q,
     return launch_decode_fused_static(cache->cv, cache->device, q, k, v, o, lse,
                                       pf, static_cast<cudaStream_t>(stream));
   });
+}
+
+int rswa_qk_norm_rope(const rswa_rope* rope, const void* q, int64_t q_stride,
+                      const void* k, int64_t k_stride, const int64_t* positions,
+                      int64_t rows, int heads, int kv_heads, int head_dim, int dtype,
+                      void* q_out, void* k_out, void* stream) {
+  if (dtype != RSWA_F32 && dtype != RSWA_BF16) return RSWA_EDTYPE;
+  if (head_dim != 64 && head_dim != 128) return RSWA_EDTYPE;
+  if (!valid_rope(rope, head_dim)) return RSWA_EINVAL;
+  if (rows < 0 || rows > (int64_t(1) << 40) || heads < 1 || kv_heads < 1 ||
+      heads > 4096 || kv_heads > 4096)
+    return RSWA_EINVAL;
+  if (rows == 0) return RSWA_OK;
+  if (!positions || !aligned8(positions) || !q_out || !k_out || !aligned16(q_out) ||
+      !aligned16(k_out) ||
+      !valid_rows(q, q_stride, (int64_t)heads * head_dim, rows, dtype) ||
+      !valid_rows(k, k_stride, (int64_t)kv_heads * head_dim, rows, dtype))
+    return RSWA_EINVAL;
+  if (injected_failure()) return RSWA_ECUDA;
+  RopeRows rr{};
+  rr.q = q;
+  rr.k = k;
+  rr.q_stride = q_stride;
+  rr.k_stride = k_stride;
+  rr.q_out = q_out;
+  rr.k_out = k_out;
+  rr.pos = positions;
+  rr.rows = rows;
+  rr.tokens = 1;
+  rr.H = heads;
+  rr.Hkv = kv_heads;
+  return status_of(launch_norm_rope(*rope, rr, nullptr, head_dim, dtype,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+int rswa_qk_norm_rope_cached(rswa_cache* cache, const rswa_rope* rope, const void* q,
+                             int64_t q_stride, const void* k, int64_t k_stride,
+                             const int32_t* offsets, int64_t tokens, void* q_out,
+                             void* k_out, void* stream) {
+  if (!live(cache)) return RSWA_EHANDLE;
+  const CacheView& cv = cache->cv;
+  if (!valid_rope(rope, cv.d) || tokens < 1 || tokens > (int64_t(1) << 24))
+    return RSWA_EINVAL;
+  const int64_t rows = tokens * cv.B;
+  if (!aligned4(offsets) || !q_out || !k_out || !aligned16(q_out) || !aligned16(k_out) ||
+      !valid_rows(q, q_stride, (int64_t)cv.H * cv.d, rows, cv.dtype) ||
+      !valid_rows(k, k_stride, (int64_t)cv.Hkv * cv.d, rows, cv.dtype))
+    return RSWA_EINVAL;
+  if (injected_failure()) return RSWA_ECUDA;
+  DeviceGuard g(cache->device);
+  if (!g.ok) return RSWA_ECUDA;
+  RopeRows rr{};
+  rr.q = q;
+  rr.k = k;
+  rr.q_stride = q_stride;
+  rr.k_stride = k_stride;
+  rr.q_out = q_out;
+  rr.k_out = k_out;
+  rr.offsets = offsets;
+  rr.rows = rows;
+  rr.tokens = tokens;
+  rr.H = cv.H;
+  rr.Hkv = cv.Hkv;
+  return status_of(launch_norm_rope(*rope, rr, &cv, cv.d, cv.dtype,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+int rswa_append_kv_rope(rswa_cache* cache, const rswa_rope* rope, const void* q,
+                        int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, void* q_out, void* stream) {
+  if (!live(cache)) return RSWA_EHANDLE;
+  const CacheView& cv = cache->cv;
+  if (!valid_rope(rope, cv.d) || !q_out || !aligned16(q_out) ||
+      !valid_rows(q, q_stride, (int64_t)cv.H * cv.d, cv.B, cv.dtype) ||
+      !valid_rows(k, k_stride, (int64_t)cv.Hkv * cv.d, cv.B, cv.dtype) ||
+      !valid_rows(v, v_stride, (int64_t)cv.Hkv * cv.d, cv.B, cv.dtype))
+    return RSWA_EINVAL;
+  if (injected_failure()) return RSWA_ECUDA;
+  DeviceGuard g(cache->device);
+  if (!g.ok) return RSWA_ECUDA;
+  return status_of(launch_append_rope(cv, *rope, q, q_stride, k, k_stride, v, v_stride,
+                                      q_out, static_cast<cudaStream_t>(stream)));
+}
+
+int rswa_decode_tree_workspace(rswa_cache* cache, int64_t nodes, size_t* out_bytes) {
+  if (!live(cache)) return RSWA_EHANDLE;
+  if (!out_bytes || nodes < 1 || nodes > kMaxTreeNodes) return RSWA_EINVAL;
+  *out_bytes = decode_tree_workspace(cache->cv, (int)nodes);
+  return RSWA_OK;
+}
+
+int rswa_decode_tree(rswa_cache* cache, const void* q, const void* k, const void* v,
+                     const int32_t* parents, const int32_t* counts, int64_t nodes, void* o,
+                     float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!live(cache)) return RSWA_EHANDLE;
+  // grid limits of the CUDA-core kernel: B on grid.y, nodes * H on grid.x
+  if (nodes < 1 || nodes > kMaxTreeNodes || cache->cv.B > 65535) return RSWA_EINVAL;
+  if (!q || !k || !v || !o || !parents || !workspace || !aligned16(q) || !aligned16(k) ||
+      !aligned16(v) || !aligned16(o) || !aligned4(parents) || !aligned4(counts) ||
+      !aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0)
+    return RSWA_EINVAL;
+  if (workspace_bytes < decode_tree_workspace(cache->cv, (int)nodes)) return RSWA_ECAPACITY;
+  if (injected_failure()) return RSWA_ECUDA;
+  DeviceGuard g(cache->device);
+  if (!g.ok) return RSWA_ECUDA;
+  TreeArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.parents = parents;
+  a.counts = counts;
+  a.nodes = (int)nodes;
+  a.o = o;
+  a.lse = lse;
+  a.ws = workspace;
+  return run_decode(cache, [&](bool pf) {
+    return launch_decode_tree(cache->cv, a, pf, static_cast<cudaStream_t>(stream));
+  });
+}
+
+int rswa_commit_tree(rswa_cache* cache, const void* k, const void* v, int64_t nodes,
+                     const int32_t* path, const int32_t* accepted, int64_t max_path,
+                     void* stream) {
+  if (!live(cache)) return RSWA_EHANDLE;
+  if (nodes < 1 || nodes > kMaxTreeNodes || max_path < 1 || max_path > kMaxTreeNodes ||
+      cache->cv.B > 65535)
+    return RSWA_EINVAL;
+  if (!k || !v || !path || !accepted || !aligned16(k) || !aligned16(v) || !aligned4(path) ||
+      !aligned4(accepted))
+    return RSWA_EINVAL;
+  if (injected_failure()) return RSWA_ECUDA;
+  DeviceGuard g(cache->device);
+  if (!g.ok) return RSWA_ECUDA;
+  return status_of(launch_commit_tree(cache->cv, k, v, (int)nodes, path, accepted,
+                                      (int)max_path, static_cast<cudaStream_t>(stream)));
 }
 
 static int read_state(rswa_cache* cache, int b, int64_t* m_b, int64_t* t_b) {

@@ -18,6 +18,7 @@ enum DeviceErr : int32_t {
   kErrNone = 0,
   kErrWaitTimeout = 1,
   kErrLaunchShape = 2,   // a launch whose grid does not cover its work
+  kErrBadTree = 3,       // a parent, count or path node outside its range
 };
 
 __device__ __forceinline__ void flag_error(int32_t* err, int32_t code) {

@@ -144,6 +144,62 @@ cudaError_t launch_prefill_tc(const CacheView& cv, const SeqTable& st,
                               void* O, int64_t total_rows, cudaStream_t s);
 bool prefill_tc_supported(const CacheView& cv);
 
+// Norm and rotation of query and key heads (norm_rope.cu).  pos: positions
+// [rows], or NULL: row r stands at m_b + t_b + (offsets ? offsets[r] : i) of
+// the cache `cv`, r = b * tokens + i.
+struct RopeRows {
+  const void *q, *k;
+  int64_t q_stride, k_stride;
+  void *q_out, *k_out;
+  const int64_t* pos;
+  const int32_t* offsets;
+  int64_t rows, tokens;
+  int H, Hkv;
+};
+cudaError_t launch_norm_rope(const rswa_rope& rope, const RopeRows& rr,
+                             const CacheView* cv, int d, int dtype, cudaStream_t s);
+cudaError_t launch_append_rope(const CacheView& cv, const rswa_rope& rope, const void* q,
+                               int64_t q_stride, const void* k, int64_t k_stride,
+                               const void* v, int64_t v_stride, void* q_out,
+                               cudaStream_t s);
+
+// Attention of a tree of drafted tokens (decode_tree.cu), and the append of
+// its accepted path.
+struct TreeArgs {
+  const void *q, *k, *v;
+  const int32_t *parents, *counts;
+  int nodes;
+  void* o;
+  float* lse;
+  void* ws;
+};
+constexpr int kMaxTreeNodes = 1024;
+size_t decode_tree_workspace(const CacheView& cv, int nodes);
+cudaError_t launch_decode_tree(const CacheView& cv, const TreeArgs& a, bool prefetch,
+                               cudaStream_t s);
+cudaError_t launch_commit_tree(const CacheView& cv, const void* k, const void* v, int nodes,
+                               const int32_t* path, const int32_t* accepted, int max_path,
+                               cudaStream_t s);
+
+// Programmatic stream serialization: a kernel may begin launching while the
+// previous kernel of the stream drains; each one waits (griddepcontrol) before
+// it touches memory that the previous one writes.
+template <typename K, typename... Args>
+inline cudaError_t launch_dependent(K kernel, dim3 grid, dim3 block, size_t smem,
+                                    cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Fused decode step with split-K scratch in the library's static device array
 // (decode_static.cu).  Fails with cudaErrorInvalidValue when the cache needs
 // more than static_scratch_capacity() bytes of scratch.

@@ -1,0 +1,800 @@
+"""GPU parity of the draft-and-verify operators (norm and rotation of query and
+key heads, rotated append, tree attention, commit of the accepted path) against
+their float64 oracle.
+
+Tolerances come from the arithmetic of each operator; a rounding to a type is
+off by at most half a step, eps / 2 (bf16 2^-8, float32 2^-24) relative to the
+value.
+
+norm_rope.  In float32, relative to the length |a| + |b| of a rotated pair: the
+sum of squares (at most 16 products in sequence and 4 shuffle sums, halved by the
+square root: 10 half steps), the reciprocal root (4), the products with it and the
+weight (2), sine and cosine (4) of an angle off by half a step of at most pi (4),
+the rotation's products and sum (3): 27, taken as 32.  Then one rounding to the
+type.
+
+tree.  A logit is a dot product of d terms, off by at most (d + 8) half steps of
+sum |q k| / sqrt(d) (twice that on the tensor cores, which truncate); weights and
+sums over S keys by S half steps more, and 2^-21 for the exponential.  That bounds
+the log-sum-exp directly, and o relative to sum p |v|, twice (numerator and
+denominator).  In bf16 the weights are rounded to bf16 (2^-8 of sum p |v|) and o is
+(2^-8 of |o|).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import workloads
+from oracle import drafts
+
+pytestmark = pytest.mark.gpu
+
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+RSWA_EDEVICE = 6
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def inv_freq(rot):
+    if rot == 0:
+        return None
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    return (10000.0 ** (-2.0 * i / rot)).cuda()
+
+
+def normal(shape, seed, dtype=torch.bfloat16, std=1.0):
+    return workloads.normal(shape, seed, std, dtype, "cuda")
+
+
+def weight(d, seed, dtype):
+    return (1 + 0.2 * normal((d,), seed, torch.float32)).to(dtype)
+
+
+def same(got, want):
+    np.testing.assert_array_equal(f64(got), want)
+
+
+# ---------------------------------------------------------------------------
+# norm and rotation
+# ---------------------------------------------------------------------------
+
+def check_rope(got, x, w, pos, rope, what):
+    rot = rope.rotary_dim
+    f = [] if rot == 0 else f64(rope.inv_freq)
+    il = bool(rope._struct.interleaved)
+    eps = rope._struct.eps
+    ref = drafts.norm_rope(f64(x), None if w is None else f64(w), pos, f, eps, il)
+    size = np.abs(ref)
+    if rot:                                    # |a| + |b| of each pair, before the turn
+        y = np.abs(drafts.norm_rope(f64(x), None if w is None else f64(w),
+                                    [0] * len(pos), f, eps, il))
+        a, b = (slice(0, rot, 2), slice(1, rot, 2)) if il else (slice(0, rot // 2),
+                                                                slice(rot // 2, rot))
+        size[..., a] = size[..., b] = y[..., a] + y[..., b]
+    tol = 32 * 2.0 ** -24 * size
+    if got.dtype == torch.bfloat16:
+        tol = tol + HALF[torch.bfloat16] * (np.abs(ref) + tol)
+    err = np.abs(f64(got) - ref)
+    assert np.isfinite(err).all() and (err <= tol).all(), \
+        f"{what}: worst {np.max(err / np.maximum(tol, 1e-300)):.3g} of the bound"
+
+
+ROPE_CASES = [
+    # rows, H, Hkv, d, rot, interleaved, norm, dtype
+    (1, 1, 1, 64, 64, False, True, torch.float32),
+    (1, 10, 10, 128, 128, False, True, torch.bfloat16),
+    (3, 5, 1, 128, 128, True, True, torch.bfloat16),
+    (7, 32, 8, 128, 64, False, True, torch.bfloat16),
+    (5, 9, 3, 128, 16, False, True, torch.bfloat16),
+    (6, 4, 2, 128, 112, True, True, torch.bfloat16),
+    (6, 7, 7, 64, 48, False, True, torch.bfloat16),
+    (9, 6, 2, 64, 32, True, True, torch.float32),
+    (4, 3, 3, 128, 80, False, True, torch.float32),
+    (4, 3, 1, 128, 128, True, False, torch.float32),
+    (11, 10, 10, 128, 0, False, True, torch.bfloat16),
+    (2, 2, 2, 64, 0, True, False, torch.bfloat16),
+    (700, 10, 10, 128, 128, False, True, torch.bfloat16),
+    (333, 33, 11, 64, 64, False, True, torch.bfloat16),
+]
+
+
+@pytest.mark.parametrize("rows,H,Hkv,d,rot,il,norm,dtype", ROPE_CASES)
+@pytest.mark.parametrize("packed", [False, True])
+def test_norm_rope(cuda_lib, rows, H, Hkv, d, rot, il, norm, dtype, packed):
+    rswa = cuda_lib
+    if packed:
+        qkv = normal((rows, H + 2 * Hkv, d), 1, dtype)
+        q, k = qkv[:, :H], qkv[:, H:H + Hkv]
+    else:
+        q, k = normal((rows, H, d), 1, dtype), normal((rows, Hkv, d), 2, dtype)
+    qw, kw = (weight(d, 3, dtype), weight(d, 4, dtype)) if norm else (None, None)
+    rope = rswa.RswaRope(inv_freq(rot), qw, kw, eps=1e-5, interleaved=il)
+    pos = (torch.arange(rows, dtype=torch.int64) * 37 + 5) % 1500
+    qo, ko = (torch.full((rows, h, d), float("nan"), dtype=dtype, device="cuda")
+              for h in (H, Hkv))
+    rswa.rswa_qk_norm_rope(rope, q, k, pos.cuda(), qo, ko)
+    check_rope(qo, q, qw, pos.tolist(), rope, "q")
+    check_rope(ko, k, kw, pos.tolist(), rope, "k")
+
+
+def test_norm_rope_far_and_negative_positions(cuda_lib):
+    """Far positions keep the accuracy of near ones; a negative one turns back."""
+    rswa = cuda_lib
+    pos = [0, 1, -1, -77777, 999_983, 2 ** 24 + 1, 2 ** 31 - 1, 2 ** 31 + 5]
+    q, k = normal((len(pos), 2, 128), 5, torch.float32), normal((len(pos), 1, 128), 6, torch.float32)
+    qw = weight(128, 7, torch.float32)
+    rope = rswa.RswaRope(inv_freq(128), qw, None)
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    rswa.rswa_qk_norm_rope(rope, q, k, torch.tensor(pos).cuda(), qo, ko)
+    check_rope(qo, q, qw, pos, rope, "q")
+    check_rope(ko, k, None, pos, rope, "k")
+    same(qo[:0], f64(q[:0]))
+
+
+def test_norm_rope_in_place_and_only_one_norm(cuda_lib):
+    rswa = cuda_lib
+    q, k = normal((50, 4, 64), 8), normal((50, 2, 64), 9)
+    kw = weight(64, 10, torch.bfloat16)
+    rope = rswa.RswaRope(inv_freq(64), None, kw)
+    q0, k0 = q.clone(), k.clone()
+    pos = torch.arange(50)
+    rswa.rswa_qk_norm_rope(rope, q, k, pos.cuda(), q, k)
+    check_rope(q, q0, None, pos.tolist(), rope, "q")
+    check_rope(k, k0, kw, pos.tolist(), rope, "k")
+
+
+def test_norm_rope_extreme_rows(cuda_lib):
+    """A zero row stays zero (eps), a NaN or an infinity stays in its own head,
+    elements that are not rotated are not mixed."""
+    rswa = cuda_lib
+    q = normal((4, 3, 64), 11, torch.float32)
+    k = torch.zeros(4, 1, 64, device="cuda")
+    q[1, 1, 40] = float("inf")
+    q[2, 2, 3] = float("nan")
+    rope = rswa.RswaRope(inv_freq(32), None, weight(64, 12, torch.float32))
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    rswa.rswa_qk_norm_rope(rope, q, k, torch.arange(4).cuda(), qo, ko)
+    assert (ko == 0).all()
+    bad = ~torch.isfinite(qo)
+    where = bad.nonzero().tolist()
+    assert where == [[1, 1, 40], [2, 2, 3], [2, 2, 19]]
+
+
+def test_norm_rope_refusals(cuda_lib):
+    rswa = cuda_lib
+    q, k = normal((4, 2, 64), 13), normal((4, 1, 64), 14)
+    pos = torch.arange(4).cuda()
+    rope = rswa.RswaRope(inv_freq(64), weight(64, 15, torch.bfloat16))
+    out = torch.empty_like(q), torch.empty_like(k)
+    rswa.rswa_qk_norm_rope(rope, q, k, pos, *out)
+    rswa.rswa_qk_norm_rope(rope, q[:0], k[:0], pos[:0], out[0][:0], out[1][:0])
+    for bad in [
+        (rope, q, k, pos.int(), *out), (rope, q, k, pos[:3], *out),
+        (rope, q, k[:3], pos, *out), (rope, q, k.float(), pos, *out),
+        (rope, q, k, pos, out[0].float(), out[1]), (rope, q, k, pos, out[0][:3], out[1]),
+        (rope, q.half(), k.half(), pos, *out), (rope, q.float(), k.float(), pos, *out),
+        (rope, q.transpose(0, 1), k, pos, *out), (rope, q, k, pos, *(x.cpu() for x in out)),
+        (rswa.RswaRope(inv_freq(128)[:20].contiguous()), q, k, pos, *out),    # 40: no multiple of 16
+        (rswa.RswaRope(inv_freq(128)), q, k, pos, *out),                      # more than the head
+    ]:
+        with pytest.raises((ValueError, rswa.RswaError)):
+            rswa.rswa_qk_norm_rope(*bad)
+
+
+# ---------------------------------------------------------------------------
+# caches
+# ---------------------------------------------------------------------------
+
+def make_cache(rswa, m, t, n, H, Hkv, d, dtype, seed, cap=None):
+    """A cache of sequences with prefixes m[b] and t[b] outputs, and their
+    oracle states."""
+    code = rswa.RSWA_F32 if dtype == torch.float32 else rswa.RSWA_BF16
+    rows = sum(m) + sum(t)
+    K, V = normal((rows, Hkv, d), seed, dtype), normal((rows, Hkv, d), seed + 1, dtype)
+    cache = rswa.RswaCache(max(m) if cap is None else cap, n, H, d, len(m), code, kv_heads=Hkv)
+    cache.prefill_varlen(None, K if rows else None, V if rows else None, None, m, t)
+    states, at = [], 0
+    for mb, tb in zip(m, t):
+        sl = slice(at, at + mb + tb)
+        states.append(oracle.prefill_cache(f64(K[sl]), f64(V[sl]), mb, n, tb))
+        at += mb + tb
+    return cache, states
+
+
+def check_ring(cache, states, n):
+    Ks, Vs = cache.slabs()
+    for b, st in enumerate(states):
+        assert cache.get_t(b) == st["t"]
+        filled = sorted(oracle.ring_outputs(st["t"], n))
+        for slab, name in ((Ks, "Kr"), (Vs, "Vr")):
+            got = f64(slab[b, :, cache.m:]).transpose(1, 0, 2)
+            np.testing.assert_array_equal(got[filled], st[name][filled])
+
+
+@pytest.mark.parametrize("dtype,H,Hkv,d,rot,il", [
+    (torch.bfloat16, 10, 10, 128, 128, False), (torch.bfloat16, 32, 8, 128, 64, True),
+    (torch.bfloat16, 7, 1, 64, 64, False), (torch.float32, 6, 2, 64, 32, False),
+    (torch.float32, 40, 1, 128, 128, True)])
+@pytest.mark.parametrize("strided", [False, True])
+def test_append_kv_rope(cuda_lib, dtype, H, Hkv, d, rot, il, strided):
+    """Several steps over a wrapping ring: the queries, the stored keys and
+    values and t_b of every step, and the decode step that follows."""
+    rswa = cuda_lib
+    m, t, n = [3, 0, 290], [0, 5, 9], 4
+    cache, states = make_cache(rswa, m, t, n, H, Hkv, d, dtype, 20)
+    qw, kw = weight(d, 21, dtype), weight(d, 22, dtype)
+    rope = rswa.RswaRope(inv_freq(rot), qw, kw, interleaved=il)
+    Ks, Vs = cache.slabs()
+    for step in range(6):
+        qkv = normal((3, H + 2 * Hkv, d), 30 + step, dtype)
+        q, k, v = qkv[:, :H], qkv[:, H:H + Hkv], qkv[:, H + Hkv:]
+        if not strided:
+            q, k, v = (x.contiguous() for x in (q, k, v))
+        qo = torch.full((3, H, d), float("nan"), dtype=dtype, device="cuda")
+        before = Ks.clone(), Vs.clone()
+        cache.append_kv_rope(rope, q, k, v, qo)
+        pos = [a + b for a, b in zip(m, t)]
+        check_rope(qo, q, qw, pos, rope, "q")
+        stored = torch.stack([Ks[b, :, cache.m + t[b] % n] for b in range(3)])
+        check_rope(stored, k, kw, pos, rope, "k")
+        for b in range(3):
+            slot = cache.m + t[b] % n
+            same(Vs[b, :, slot], f64(v[b]))
+            for old, new in zip(before, (Ks, Vs)):         # nothing else was written
+                old[b, :, slot] = new[b, :, slot]
+            states[b] = oracle.append_kv(states[b], f64(stored[b]), f64(v[b]), n)
+        assert torch.equal(before[0], Ks) and torch.equal(before[1], Vs)
+        t = [x + 1 for x in t]
+        o = torch.empty(3, H, d, dtype=dtype, device="cuda")
+        cache.decode_step(qo, o)
+        for b in range(3):
+            ref, _ = oracle.decode_step(states[b], f64(qo[b]), n)
+            err = np.abs(f64(o[b]) - ref)
+            assert err.max() <= (1e-4 if dtype == torch.float32 else 2e-2)
+    check_ring(cache, states, n)
+    assert cache.sync_status() == 0
+
+
+def test_qk_norm_rope_of_a_cache(cuda_lib):
+    """Positions m_b + t_b + offsets; without offsets m_b + t_b + i; the same
+    rows as with those positions given."""
+    rswa = cuda_lib
+    m, t, n, H, Hkv, d, N = [17, 0, 5], [3, 200, 0], 6, 4, 2, 128, 5
+    cache, states = make_cache(rswa, m, t, n, H, Hkv, d, torch.bfloat16, 40)
+    rope = rswa.RswaRope(inv_freq(d), weight(d, 41, torch.bfloat16), weight(d, 42, torch.bfloat16))
+    qkv = normal((3 * N, H + 2 * Hkv, d), 43)
+    q, k = qkv[:, :H], qkv[:, H:H + Hkv]
+    off = torch.tensor([[0, 1, 1, 2, 7], [0, 0, 1, 2, 3], [4, 0, 0, 0, -2]], dtype=torch.int32).cuda()
+    for offsets in (None, off):
+        rel = torch.arange(N).expand(3, N) if offsets is None else off.cpu().long()
+        pos = (torch.tensor(m)[:, None] + torch.tensor(t)[:, None] + rel).reshape(-1)
+        a = torch.empty(3 * N, H, d, dtype=torch.bfloat16, device="cuda"), \
+            torch.empty(3 * N, Hkv, d, dtype=torch.bfloat16, device="cuda")
+        b = torch.empty_like(a[0]), torch.empty_like(a[1])
+        cache.qk_norm_rope(rope, q, k, *a, offsets=offsets)
+        rswa.rswa_qk_norm_rope(rope, q, k, pos.cuda(), *b)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        check_rope(a[0], q, rope.q_weight, pos.tolist(), rope, "q")
+    check_ring(cache, states, n)
+
+
+# ---------------------------------------------------------------------------
+# tree attention
+# ---------------------------------------------------------------------------
+
+def random_tree(N, seed):
+    g = np.random.default_rng(seed)
+    return [-1 if i == 0 or g.random() < 0.1 else
+            (i - 1 if g.random() < 0.4 else int(g.integers(max(0, i - 20), i)))
+            for i in range(N)]
+
+
+def check_tree(o, lse, q, k, v, state, parents, n, what, rows=None):
+    """o, lse, q, k, v: one sequence's live rows."""
+    dtype, d = q.dtype, q.shape[-1]
+    H, Hkv = q.shape[1], k.shape[1]
+    G = H // Hkv
+    half = 2.0 ** -24 * (1 if dtype == torch.float32 else 2)
+    qd = f64(q)
+    ro, rl, seen = drafts.tree_attention(state, qd, f64(k), f64(v), parents, n)
+    go, gl = f64(o), f64(lse)
+    for i in range(len(parents)):
+        K, V = seen[i]
+        S = len(K)
+        Kh, Vh = np.repeat(K, G, 1), np.repeat(V, G, 1)           # [S][H][d]
+        logit = np.einsum("shd,hd->sh", Kh, qd[i]) / np.sqrt(d)
+        p = np.exp(logit - rl[i])
+        big = np.einsum("shd,hd->sh", np.abs(Kh), np.abs(qd[i])).max(0) / np.sqrt(d)
+        rel = (d + 8) * half * big + 2 * S * half + 2.0 ** -21    # [H]
+        assert np.isfinite(gl[i]).all() and np.isfinite(go[i]).all(), f"{what} node {i}"
+        assert (np.abs(gl[i] - rl[i]) <= rel + 2 * half * (1 + np.abs(rl[i]))).all(), \
+            f"{what} node {i}: lse {np.abs(gl[i] - rl[i]).max():.3g}, bound {rel.min():.3g}"
+        mass = np.einsum("sh,shd->hd", p, np.abs(Vh))
+        tol = (2 * rel[:, None] + half) * mass
+        if dtype == torch.bfloat16:
+            tol = tol + HALF[dtype] * (mass + np.abs(ro[i]))
+        err = np.abs(go[i] - ro[i])
+        assert (err <= tol).all(), f"{what} node {i}: {np.max(err / tol):.3g} of the bound"
+
+
+def run_tree(rswa, m, t, n, H, Hkv, d, N, dtype, seed, counts=None, cap=None, std=1.0,
+             parents=None):
+    B = len(m)
+    cache, states = make_cache(rswa, m, t, n, H, Hkv, d, dtype, seed, cap)
+    q = normal((B, N, H, d), seed + 2, dtype, std)
+    k, v = (normal((B, N, Hkv, d), seed + 3 + i, dtype) for i in range(2))
+    par = parents or [random_tree(N, seed + b) for b in range(B)]
+    o = torch.full((B, N, H, d), 7.0, dtype=dtype, device="cuda")
+    lse = torch.full((B, N, H), 7.0, device="cuda")
+    cnt = None if counts is None else torch.tensor(counts, dtype=torch.int32).cuda()
+    live = [N] * B if counts is None else counts
+    if counts is not None:                       # padding may hold anything
+        for b in range(B):
+            for x in (q, k, v):
+                x[b, live[b]:] = float("nan")
+    Ks, Vs = cache.slabs()
+    before = Ks.clone(), Vs.clone()
+    cache.decode_tree(q, k, v, torch.tensor(par, dtype=torch.int32).cuda(), o, lse, counts=cnt)
+    assert cache.sync_status() == 0
+    for b in range(B):
+        c = live[b]
+        check_tree(o[b, :c], lse[b, :c], q[b, :c], k[b, :c], v[b, :c], states[b], par[b][:c], n,
+                   f"sequence {b}")
+        assert (o[b, c:] == 7).all() and (lse[b, c:] == 7).all()
+    assert torch.equal(before[0], Ks) and torch.equal(before[1], Vs)
+    check_ring(cache, states, n)
+    return cache, states, (q, k, v, par, o, lse)
+
+
+BF, F32 = torch.bfloat16, torch.float32
+TREE_CASES = [
+    # m, t, n, H, Hkv, d, nodes, dtype
+    ([0], [0], 8, 1, 1, 128, 1, BF),                      # only itself
+    ([0], [0], 1, 2, 2, 128, 7, BF),                      # a window of one
+    ([1], [0], 4, 2, 1, 128, 9, BF),
+    ([288], [200], 128, 10, 10, 128, 16, BF),             # a page
+    ([288], [1], 128, 10, 10, 128, 33, BF),
+    ([127], [127], 127, 3, 3, 128, 31, BF),
+    ([128], [128], 128, 3, 3, 128, 32, BF),
+    ([129], [129], 129, 3, 3, 128, 64, BF),
+    ([1000], [700], 300, 2, 2, 128, 65, BF),
+    ([130], [40], 20, 2, 2, 128, 127, BF),
+    ([130], [40], 20, 2, 2, 128, 128, BF),
+    ([130], [40], 20, 2, 2, 128, 129, BF),
+    ([260], [333], 77, 2, 1, 128, 200, BF),
+    ([260], [333], 5, 1, 1, 128, 400, BF),
+    ([100], [10], 128, 32, 8, 128, 16, BF),               # 64 rows a key head
+    ([100], [300], 128, 32, 8, 128, 33, BF),              # 132 rows
+    ([700], [300], 128, 32, 8, 128, 64, BF),              # 256 rows
+    ([64], [300], 128, 12, 4, 128, 50, BF),               # groups of 3: 42 nodes a tile
+    ([64], [300], 16, 20, 2, 128, 30, BF),                # groups of 10
+    ([200], [20], 16, 130, 1, 128, 3, BF),                # more heads than a tile has rows
+    ([200], [20], 16, 128, 1, 128, 3, BF),
+    ([300], [20], 16, 100, 1, 128, 3, BF),
+    ([288], [200], 128, 10, 10, 64, 16, BF),              # head_dim 64
+    ([500], [60], 40, 8, 2, 64, 70, BF),
+    ([260], [333], 77, 2, 1, 64, 200, BF),
+    ([3000], [100], 64, 2, 2, 128, 20, BF),               # split over many CTAs
+    ([5, 0, 300, 129], [0, 3, 500, 128], 128, 5, 5, 128, 12, BF),
+    ([9] * 70, [12] * 70, 8, 2, 2, 128, 5, BF),
+    ([300 + 11 * i for i in range(20)], [30 * i for i in range(20)], 128, 8, 2, 128, 24, BF),
+    ([16], [20], 8, 1, 1, 64, 64, F32),
+    ([288], [200], 128, 4, 2, 128, 16, F32),
+    ([310, 0, 77], [30, 90, 0], 77, 4, 2, 64, 33, F32),
+    ([260], [333], 77, 2, 1, 64, 150, F32),
+]
+
+
+@pytest.mark.parametrize("m,t,n,H,Hkv,d,N,dtype", TREE_CASES)
+def test_decode_tree(cuda_lib, m, t, n, H, Hkv, d, N, dtype):
+    run_tree(cuda_lib, m, t, n, H, Hkv, d, N, dtype, 50)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H,Hkv,d,N", [(4, 4, 128, 40), (8, 2, 128, 70), (8, 2, 64, 70)])
+def test_decode_tree_ragged_counts(cuda_lib, H, Hkv, d, N, dtype):
+    """Padded trees: rows past the count are left, whatever the padding holds;
+    an empty sequence and a whole one among them, and all of them empty."""
+    counts = [N, 0, 1, 17, N - 1, 33]
+    m, t = [200, 10, 0, 129, 300, 5], [0, 4, 50, 140, 9, 64]
+    run_tree(cuda_lib, m, t, 64, H, Hkv, d, N, dtype, 60, counts)
+    run_tree(cuda_lib, m[:2], t[:2], 64, H, Hkv, d, N, dtype, 61, [0, 0])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_tree_deep_chain_and_star(cuda_lib, d):
+    """Depth beyond the window (ancestors and the ring fall out of it), and all
+    nodes at depth 0."""
+    N = 150
+    run_tree(cuda_lib, [40], [60], 48, 2, 2, d, N, BF, 70, parents=[list(range(-1, N - 1))])
+    run_tree(cuda_lib, [40], [60], 48, 2, 2, d, N, BF, 71, parents=[[-1] * N])
+    run_tree(cuda_lib, [40], [60], 48, 2, 2, d, N, BF, 72, parents=[[-1] + [0] * (N - 1)])
+
+
+def test_decode_tree_1024_nodes(cuda_lib):
+    run_tree(cuda_lib, [150], [100], 64, 1, 1, 128, 1024, BF, 73)
+
+
+def test_decode_tree_a_prefix_capacity_with_room(cuda_lib):
+    """Prefixes far below the capacity: tiles behind them hold zeros."""
+    run_tree(cuda_lib, [10, 700, 0], [5, 0, 300], 100, 4, 2, 128, 20, BF, 74, cap=2000)
+
+
+def test_decode_tree_large_logits(cuda_lib):
+    """Logits of several hundred: the running maximum moves, nothing overflows."""
+    run_tree(cuda_lib, [700], [200], 128, 4, 2, 128, 40, BF, 75, std=40.0)
+    run_tree(cuda_lib, [300], [20], 16, 2, 2, 64, 20, F32, 76, std=40.0)
+
+
+@pytest.mark.parametrize("d,dtype", [(128, BF), (64, BF), (64, F32)])
+def test_decode_tree_counts_its_keys(cuda_lib, d, dtype):
+    """q = 0 weighs every visible key alike, and with it exactly: lse is the
+    logarithm of their number, and with values 1 for the tree's nodes and 0 in
+    the cache o is the share of ancestors."""
+    rswa = cuda_lib
+    m, t, n, H, N = 200, 90, 50, 2, 140
+    cache, states = make_cache(rswa, [m], [t], n, H, H, d, dtype, 80)
+    Ks, Vs = cache.slabs()
+    Vs.zero_()
+    cache.set_t([t])
+    par = random_tree(N, 81)
+    q = torch.zeros(1, N, H, d, dtype=dtype, device="cuda")
+    k = normal((1, N, H, d), 82, dtype)
+    v = torch.ones(1, N, H, d, dtype=dtype, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(1, N, H, device="cuda")
+    cache.decode_tree(q, k, v, torch.tensor([par], dtype=torch.int32).cuda(), o, lse)
+    for i in range(N):
+        up = drafts.chain(par, i)
+        here = t + len(up) - 1
+        keys = m + (t - max(0, here - n + 1) if here - n + 1 < t else 0) + len(up[:n])
+        assert abs(lse[0, i, 0].item() - np.log(keys)) <= 2.0 ** -20
+        share = len(up[:n]) / keys
+        assert (o[0, i].double() - share).abs().max().item() <= share * (HALF[dtype] + 2.0 ** -20)
+
+
+def test_decode_tree_bad_parents_and_counts(cuda_lib):
+    """Parents that do not come before their child and counts out of range set
+    the flag; the parent counts as -1, the count as the nearest in range."""
+    rswa = cuda_lib
+    m, t, n, H, d, N = [50, 60], [5, 6], 16, 2, 128, 12
+    for dtype in (BF, F32):
+        cache, states = make_cache(rswa, m, t, n, H, H, d, dtype, 85)
+        q, k, v = (normal((2, N, H, d), 86 + i, dtype) for i in range(3))
+        good = [random_tree(N, 88), random_tree(N, 89)]
+        good[0][3], good[0][4], good[1][5], good[1][11] = -1, -1, -1, -1
+        bad = [list(x) for x in good]
+        bad[0][3], bad[0][4], bad[1][5], bad[1][11] = 3, 2 ** 31 - 1, -2, 7000
+        for par, counts, status in ((bad, None, RSWA_EDEVICE), (good, [N + 1, -3], RSWA_EDEVICE),
+                                    (good, None, 0)):
+            o = torch.full_like(q, 7)
+            lse = torch.full((2, N, H), 7.0, device="cuda")
+            cnt = None if counts is None else torch.tensor(counts, dtype=torch.int32).cuda()
+            cache.decode_tree(q, k, v, torch.tensor(par, dtype=torch.int32).cuda(), o, lse, counts=cnt)
+            assert cache.sync_status() == status
+            assert cache.sync_status() == 0
+            for b in range(2):
+                if counts is not None and counts[b] < 0:
+                    assert (o[b] == 7).all() and (lse[b] == 7).all()
+                    continue
+                check_tree(o[b], lse[b], q[b], k[b], v[b], states[b], good[b], n, f"{dtype} {b}")
+
+
+def test_decode_tree_equals_block_on_a_chain(cuda_lib):
+    """A chain of drafts is a block of outputs."""
+    rswa = cuda_lib
+    m, t, n, H, Hkv, d, N = [290], [40], 128, 8, 2, 128, 20
+    cache, states = make_cache(rswa, m, t, n, H, Hkv, d, BF, 90)
+    q, k, v = normal((1, N, H, d), 91), normal((1, N, Hkv, d), 92), normal((1, N, Hkv, d), 93)
+    par = torch.arange(-1, N - 1, dtype=torch.int32)[None].cuda()
+    o, ob = torch.empty_like(q), torch.empty_like(q)
+    lse, lb = torch.empty(1, N, H, device="cuda"), torch.empty(1, N, H, device="cuda")
+    cache.decode_tree(q, k, v, par, o, lse)
+    cache.decode_block(q, k, v, ob, lb)
+    assert (lse - lb).abs().max().item() <= 1e-4
+    assert (o - ob).abs().max().item() <= 2e-2
+    assert cache.get_t(0) == t[0] + N
+
+
+def test_decode_tree_refusals(cuda_lib):
+    rswa = cuda_lib
+    H, Hkv, d, N = 4, 2, 128, 6
+    cache, _ = make_cache(rswa, [9], [0], 8, H, Hkv, d, BF, 95)
+    q, k, v = normal((1, N, H, d), 96), normal((1, N, Hkv, d), 97), normal((1, N, Hkv, d), 98)
+    par = torch.full((1, N), -1, dtype=torch.int32, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(1, N, H, device="cuda")
+    cnt = torch.ones(1, dtype=torch.int32, device="cuda")
+    ws = cache.tree_workspace(N)
+    ok = dict(q=q, k=k, v=v, parents=par, o=o, lse=lse, counts=cnt, workspace=ws)
+    cache.decode_tree(**ok)
+    cache.decode_tree(**dict(ok, lse=None, counts=None, workspace=None))
+    for bad in [dict(q=q.float()), dict(k=k[:, :5].contiguous()), dict(v=v.transpose(1, 2)),
+                dict(parents=par.long()), dict(parents=par[:, :5].contiguous()),
+                dict(o=o[:, :, :2].contiguous()), dict(lse=lse.double()), dict(counts=cnt.long()),
+                dict(counts=cnt.cpu()), dict(workspace=ws[:0]), dict(workspace=ws[16:])]:
+        with pytest.raises((ValueError, rswa.RswaError)):
+            cache.decode_tree(**dict(ok, **bad))
+    big = torch.zeros(1, 1025, H, d, dtype=BF, device="cuda")
+    bk = torch.zeros(1, 1025, Hkv, d, dtype=BF, device="cuda")
+    with pytest.raises(rswa.RswaError):
+        cache.decode_tree(big, bk, bk, torch.full((1, 1025), -1, dtype=torch.int32).cuda(),
+                          torch.empty_like(big), workspace=ws)
+    lib, h = rswa.load(), cache.handle
+    p = lambda x: x.data_ptr()                                         # noqa: E731
+    good = [p(q), p(k), p(v), p(par), None, N, p(o), None, p(ws), ws.numel(), None]
+    for at, value, status in ((0, None, 1), (0, p(q) + 2, 1), (1, None, 1), (2, p(v) + 8, 1),
+                              (3, None, 1), (3, p(par) + 2, 1), (4, p(cnt) + 1, 1), (5, 0, 1),
+                              (5, 1025, 1), (6, None, 1), (6, p(o) + 4, 1), (7, p(lse) + 2, 1),
+                              (8, None, 1), (8, p(ws) + 16, 1), (9, ws.numel() - 1, 2)):
+        args = list(good)
+        args[at] = value
+        assert lib.rswa_decode_tree(h, *args) == status, at
+    rswa.rswa_debug_fail_next_cuda(1)
+    assert lib.rswa_decode_tree(h, *good) == 5
+    assert lib.rswa_decode_tree(h, *good) == 0
+    assert cache.sync_status() == 0
+
+
+# ---------------------------------------------------------------------------
+# commit
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,H,Hkv,d", [(BF, 10, 10, 128), (BF, 32, 8, 64), (F32, 6, 1, 128)])
+@pytest.mark.parametrize("n", [1, 3, 40])
+def test_commit_tree(cuda_lib, dtype, H, Hkv, d, n):
+    """Accepted counts from none to all, more than the window, the same node
+    twice; nodes past the count may be anything; a bad path changes nothing in
+    its sequence alone."""
+    rswa = cuda_lib
+    N, P = 30, 8
+    m, t = [5, 0, 12, 3, 7, 9], [0, 2, 100, 41, 6, 1]
+    cache, states = make_cache(rswa, m, t, n, H, Hkv, d, dtype, 100)
+    k, v = normal((6, N, Hkv, d), 101, dtype), normal((6, N, Hkv, d), 102, dtype)
+    path = torch.tensor([[0, 2, 5, 9, 29, -7, 99, 1], [3] * 8, [0, 1, 2, 3, 4, 5, 6, 7],
+                         [-1] * 8, [4, 4, 4, 9, 9, 1, 1, 0], [28, 29, -9, 0, 0, 0, 0, 0]],
+                        dtype=torch.int32)
+    acc = [5, 1, 8, 0, 7, 2]
+    Ks, Vs = cache.slabs()
+    for _ in range(2):
+        before = Ks.clone(), Vs.clone()
+        cache.commit_tree(k, v, path.cuda(), torch.tensor(acc, dtype=torch.int32).cuda())
+        assert cache.sync_status() == 0
+        for b in range(6):
+            nodes = path[b, :acc[b]].tolist()
+            for j in range(acc[b]):
+                slot = cache.m + (states[b]["t"] + j) % n
+                before[0][b, :, slot], before[1][b, :, slot] = Ks[b, :, slot], Vs[b, :, slot]
+            states[b] = drafts.commit_tree(states[b], f64(k[b]), f64(v[b]), nodes, n)
+        check_ring(cache, states, n)
+        assert torch.equal(before[0], Ks) and torch.equal(before[1], Vs)
+    for b, value, where in ((0, N, 4), (2, -1, 0), (4, 2 ** 31 - 1, 6)):
+        p2 = path.clone()
+        p2[b, where] = value
+        cache.commit_tree(k, v, p2.cuda(), torch.tensor(acc, dtype=torch.int32).cuda())
+        assert cache.sync_status() == RSWA_EDEVICE
+        for x in range(6):
+            if x != b:
+                states[x] = drafts.commit_tree(states[x], f64(k[x]), f64(v[x]),
+                                               path[x, :acc[x]].tolist(), n)
+        check_ring(cache, states, n)
+    for bad in (-1, P + 1):
+        cache.commit_tree(k, v, path.cuda(), torch.tensor([bad, 0, 0, 0, 0, 0], dtype=torch.int32).cuda())
+        assert cache.sync_status() == RSWA_EDEVICE
+        check_ring(cache, states, n)
+
+
+def test_commit_and_append_refusals(cuda_lib):
+    rswa = cuda_lib
+    H, Hkv, d = 4, 2, 128
+    cache, states = make_cache(rswa, [9, 3], [0, 2], 8, H, Hkv, d, BF, 110)
+    k, v = normal((2, 5, Hkv, d), 111), normal((2, 5, Hkv, d), 112)
+    path = torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    acc = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for bad in ((k.float(), v, path, acc), (k, v[:, :4].contiguous(), path, acc),
+                (k, v, path.long(), acc), (k, v, path, acc.long()), (k, v, path[:1], acc),
+                (k, v, path, acc[:1]), (k[:1], v, path, acc),
+                (k, v, torch.zeros(2, 1025, dtype=torch.int32).cuda(), acc)):
+        with pytest.raises((ValueError, rswa.RswaError)):
+            cache.commit_tree(*bad)
+    rope = rswa.RswaRope(inv_freq(d))
+    q1, k1 = normal((2, H, d), 113), normal((2, Hkv, d), 114)
+    out = torch.empty_like(q1)
+    for bad in ((q1[:1], k1, k1, out), (q1, k1, k1.float(), out), (q1, k1[:, :1], k1, out),
+                (q1, k1, k1, out[:1]), (q1, k1, k1, out.float()), (q1.transpose(1, 2), k1, k1, out)):
+        with pytest.raises(ValueError):
+            cache.append_kv_rope(rope, *bad)
+    lib, h, p = rswa.load(), cache.handle, torch.Tensor.data_ptr
+    good = [rope.ref, p(q1), H * d, p(k1), Hkv * d, p(k1), Hkv * d, p(out), None]
+    for at, value in ((0, None), (1, None), (2, H * d - 8), (2, H * d + 4), (3, p(k1) + 2),
+                      (5, None), (6, 1), (7, None), (7, p(out) + 8)):
+        args = list(good)
+        args[at] = value
+        assert lib.rswa_append_kv_rope(h, *args) == 1, at
+    check_ring(cache, states, 8)
+    assert cache.sync_status() == 0
+
+
+# ---------------------------------------------------------------------------
+# the operators together, streams and graphs
+# ---------------------------------------------------------------------------
+
+def draft_round(rswa, cache, states, rope, m, n, H, Hkv, d, N, seed, ws=None):
+    """One round of draft and verify through the entry points, checked."""
+    B = len(m)
+    qkv = normal((B * N, H + 2 * Hkv, d), seed)
+    q, k = qkv[:, :H], qkv[:, H:H + Hkv]
+    v = qkv[:, H + Hkv:].contiguous().view(B, N, Hkv, d)
+    par = [random_tree(N, seed + b) for b in range(B)]
+    depth = torch.tensor([[len(drafts.chain(p, i)) - 1 for i in range(N)] for p in par],
+                         dtype=torch.int32)
+    qr = torch.empty(B * N, H, d, dtype=BF, device="cuda")
+    kr = torch.empty(B * N, Hkv, d, dtype=BF, device="cuda")
+    cache.qk_norm_rope(rope, q, k, qr, kr, offsets=depth.cuda())
+    pos = (torch.tensor([mb + st["t"] for mb, st in zip(m, states)])[:, None] + depth).reshape(-1)
+    check_rope(qr, q, rope.q_weight, pos.tolist(), rope, "q")
+    check_rope(kr, k, rope.k_weight, pos.tolist(), rope, "k")
+    qt, kt = qr.view(B, N, H, d), kr.view(B, N, Hkv, d)
+    o, lse = torch.empty_like(qt), torch.empty(B, N, H, device="cuda")
+    cache.decode_tree(qt, kt, v, torch.tensor(par, dtype=torch.int32).cuda(), o, lse, workspace=ws)
+    g = np.random.default_rng(seed)
+    paths, acc = [], []
+    for b in range(B):
+        check_tree(o[b], lse[b], qt[b], kt[b], v[b], states[b], par[b], n, f"sequence {b}")
+        best = drafts.chain(par[b], int(g.integers(N)))[::-1]
+        acc.append(int(g.integers(len(best) + 1)))
+        paths.append((best + [0] * N)[:N])
+    cache.commit_tree(kt, v, torch.tensor(paths, dtype=torch.int32).cuda(),
+                      torch.tensor(acc, dtype=torch.int32).cuda())
+    for b in range(B):
+        states[b] = drafts.commit_tree(states[b], f64(kt[b]), f64(v[b]), paths[b][:acc[b]], n)
+    check_ring(cache, states, n)
+
+
+def test_prefill_draft_verify_and_decode_together(cuda_lib):
+    """Prompt normed, rotated and prefilled; rounds of drafts; then single
+    steps through the rotated append and through the fused step."""
+    rswa = cuda_lib
+    m, n, H, Hkv, d, N = [150, 40], 32, 8, 2, 128, 13
+    rope = rswa.RswaRope(inv_freq(d), weight(d, 120, BF), weight(d, 121, BF))
+    rows = sum(m)
+    qkv = normal((rows, H + 2 * Hkv, d), 122)
+    pos = torch.cat([torch.arange(x) for x in m])
+    q, k = torch.empty(rows, H, d, dtype=BF, device="cuda"), torch.empty(rows, Hkv, d, dtype=BF, device="cuda")
+    rswa.rswa_qk_norm_rope(rope, qkv[:, :H], qkv[:, H:H + Hkv], pos.cuda(), q, k)
+    v = qkv[:, H + Hkv:].contiguous()
+    cache = rswa.RswaCache(max(m), n, H, d, 2, rswa.RSWA_BF16, kv_heads=Hkv)
+    O = torch.empty_like(q)
+    cache.prefill(q, k, v, O, m, 0)
+    states, at = [], 0
+    for mb in m:
+        sl = slice(at, at + mb)
+        states.append(oracle.prefill_cache(f64(k[sl]), f64(v[sl]), mb, n, 0))
+        ref, _ = oracle.prefill_attention(f64(q[sl]), f64(k[sl]), f64(v[sl]), mb, n)
+        assert np.abs(f64(O[sl]) - ref).max() <= 2e-2
+        at += mb
+    for r in range(5):
+        draft_round(rswa, cache, states, rope, m, n, H, Hkv, d, N, 130 + r)
+        qkv = normal((2, H + 2 * Hkv, d), 140 + r)
+        q1, k1, v1 = qkv[:, :H], qkv[:, H:H + Hkv], qkv[:, H + Hkv:].contiguous()
+        qo, ko = torch.empty(2, H, d, dtype=BF, device="cuda"), torch.empty(2, Hkv, d, dtype=BF, device="cuda")
+        o = torch.empty_like(qo)
+        if r % 2:
+            cache.append_kv_rope(rope, q1, k1, v1, qo)
+            cache.decode_step(qo, o)
+            Ks, _ = cache.slabs()
+            ko = torch.stack([Ks[b, :, cache.m + states[b]["t"] % n] for b in range(2)])
+        else:
+            cache.qk_norm_rope(rope, q1, k1, qo, ko)
+            cache.decode_step_fused(qo, ko, v1, o)
+        for b in range(2):
+            states[b], ref, _ = oracle.decode_step_fused(states[b], f64(qo[b]), f64(ko[b]), f64(v1[b]), n)
+            assert np.abs(f64(o[b]) - ref).max() <= 2e-2
+    check_ring(cache, states, n)
+    assert cache.sync_status() == 0
+
+
+@pytest.mark.parametrize("H,Hkv,d,dtype", [(10, 10, 128, BF), (8, 2, 64, BF), (4, 2, 64, F32)])
+def test_captured_round_replays_on_new_inputs(cuda_lib, H, Hkv, d, dtype):
+    """Norm and rotation, tree, commit and a rotated append captured in one
+    graph: each replay works on the state that the last one left, and gives
+    what the same calls give one by one."""
+    rswa = cuda_lib
+    m, t, n, N, P = [260, 30], [7, 90], 48, 21, 6
+    caches = [make_cache(rswa, m, t, n, H, Hkv, d, dtype, 150)[0] for _ in range(2)]
+    rope = rswa.RswaRope(inv_freq(d), weight(d, 151, dtype), weight(d, 152, dtype))
+    q, k = normal((2 * N, H, d), 153, dtype), normal((2 * N, Hkv, d), 154, dtype)
+    v = normal((2, N, Hkv, d), 155, dtype)
+    par = torch.tensor([random_tree(N, 1), random_tree(N, 2)], dtype=torch.int32).cuda()
+    off = torch.tensor([[len(drafts.chain(p, i)) - 1 for i in range(N)] for p in par.tolist()],
+                       dtype=torch.int32).cuda()
+    path = torch.tensor([[0, 3, 4, 6, 9, 20], [0, 1, 2, 3, 4, 5]], dtype=torch.int32).cuda()
+    acc = torch.tensor([4, 2], dtype=torch.int32).cuda()
+    q1, k1, v1 = normal((2, H, d), 156, dtype), normal((2, Hkv, d), 157, dtype), normal((2, Hkv, d), 158, dtype)
+
+    def buffers():
+        return dict(qr=torch.zeros_like(q), kr=torch.zeros_like(k),
+                    o=torch.zeros(2, N, H, d, dtype=dtype, device="cuda"),
+                    lse=torch.zeros(2, N, H, device="cuda"), qo=torch.zeros_like(q1), o1=torch.zeros_like(q1))
+
+    def calls(c, x, ws):
+        c.qk_norm_rope(rope, q, k, x["qr"], x["kr"], offsets=off)
+        kt = x["kr"].view(2, N, Hkv, d)
+        c.decode_tree(x["qr"].view(2, N, H, d), kt, v, par, x["o"], x["lse"], workspace=ws)
+        c.commit_tree(kt, v, path, acc)
+        c.append_kv_rope(rope, q1, k1, v1, x["qo"])
+        c.decode_step(x["qo"], x["o1"])
+
+    x, y = buffers(), buffers()
+    ws = caches[0].tree_workspace(N)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls(caches[0], x, ws)                    # once outside the capture, on another stream
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls(caches[0], x, ws)
+    calls(caches[1], y, None)
+    for r in range(3):
+        for a in (q, k, v, q1, k1, v1):
+            a.copy_(normal(a.shape, 160 + r, dtype))
+        acc.copy_(torch.tensor([[0, 6], [5, 1], [6, 0]][r], dtype=torch.int32))
+        graph.replay()
+        calls(caches[1], y, None)
+        torch.cuda.synchronize()
+        for name in x:
+            assert torch.equal(x[name], y[name]), name
+        for b in range(2):
+            assert caches[0].get_t(b) == caches[1].get_t(b)
+        assert all(torch.equal(a, b) for a, b in zip(caches[0].slabs(), caches[1].slabs()))
+    assert caches[0].sync_status() == 0 and caches[1].sync_status() == 0
+
+
+def test_capture_needs_a_workspace(cuda_lib):
+    rswa = cuda_lib
+    cache, _ = make_cache(rswa, [9], [0], 8, 2, 2, 128, BF, 170)
+    q = normal((1, 4, 2, 128), 171)
+    par = torch.full((1, 4), -1, dtype=torch.int32, device="cuda")
+    o = torch.empty_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError):
+            cache.decode_tree(q, q, q, par, o)
+    cache.decode_tree(q, q, q, par, o)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.decode_tree(q, q, q, par, o)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert cache.sync_status() == 0
+
+
+def test_two_caches_on_two_streams(cuda_lib):
+    """Calls on different caches overlap; each has its own workspace."""
+    rswa = cuda_lib
+    made = [make_cache(rswa, [900], [100], 64, 10, 10, 128, BF, 180 + i) for i in range(2)]
+    x = [[normal((1, 24, 10, 128), 190 + 10 * i + j) for j in range(3)] for i in range(2)]
+    par = [random_tree(24, i) for i in range(2)]
+    dev = [torch.tensor([p], dtype=torch.int32).cuda() for p in par]
+    out = [(torch.empty_like(x[i][0]), torch.empty(1, 24, 10, device="cuda")) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            made[i][0].decode_tree(*x[i], dev[i], *out[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        check_tree(out[i][0][0], out[i][1][0], *(a[0] for a in x[i]), made[i][1][0], par[i], 64, f"cache {i}")
+
+
+def test_decode_tree_is_deterministic(cuda_lib):
+    rswa = cuda_lib
+    _, _, (q, k, v, par, o, lse) = run_tree(rswa, [1500], [90], 64, 4, 2, 128, 30, BF, 200)
+    cache, _ = make_cache(rswa, [1500], [90], 64, 4, 2, 128, BF, 200)
+    for _ in range(5):
+        o2, l2 = torch.empty_like(o), torch.empty_like(lse)
+        cache.decode_tree(q, k, v, torch.tensor(par, dtype=torch.int32).cuda(), o2, l2)
+        assert torch.equal(o, o2) and torch.equal(lse, l2)
