@@ -11,20 +11,12 @@
 #include <algorithm>
 
 #include "attend.cuh"
+#include "decode_tree.cuh"
 
 namespace rswa {
 namespace {
 
 constexpr int kTreeWarps = 8;
-
-// Live nodes of sequence b; a count outside 0..nodes is flagged and clamped.
-__device__ __forceinline__ int live_nodes(const int32_t* counts, int b, int nodes,
-                                          int32_t* err) {
-  if (!counts) return nodes;
-  const int c = counts[b];
-  if (c < 0 || c > nodes) flag_error(err, kErrBadTree);
-  return min(max(c, 0), nodes);
-}
 
 // One CTA of 8 warps per (node, query head, sequence): the warps split every
 // key segment between them and merge in shared memory.  A node past the
@@ -167,10 +159,13 @@ cudaError_t launch_tree_t(const CacheView& cv, const TreeArgs& a, cudaStream_t s
 
 }  // namespace
 
-size_t decode_tree_workspace(const CacheView&, int) { return 256; }
+size_t decode_tree_workspace(const CacheView& cv, int nodes) {
+  return decode_tree_tc_supported(cv, nodes) ? decode_tree_tc_workspace(cv, nodes) : 256;
+}
 
 cudaError_t launch_decode_tree(const CacheView& cv, const TreeArgs& a, bool,
                                cudaStream_t s) {
+  if (decode_tree_tc_supported(cv, a.nodes)) return launch_decode_tree_tc(cv, a, s);
   if (cv.dtype == RSWA_F32)
     return cv.d == 64 ? launch_tree_t<float, 64>(cv, a, s)
                       : launch_tree_t<float, 128>(cv, a, s);
