@@ -22,9 +22,12 @@
 // leaves at most two: of the unit that a CTA before it began, and of the one
 // that it begins and does not end.
 //
-// Roles (320 threads): warps 0-3 / 4-7 softmax and epilogue of half 0 / 1
+// Roles (352 threads): warps 0-3 / 4-7 softmax and epilogue of half 0 / 1
 // (thread r owns row r = TMEM lane r), warp 8 TMA producer, warp 9 TMEM
-// allocator and MMA issuer.  Steps (a half's turn on a key tile) alternate
+// allocator and MMA issuer, warp 10 planner: it cuts the list, walks the CTA's
+// range ahead of the others and hands them, through shared memory, each
+// segment (the part of a unit inside the range) and its nodes' depths and
+// ancestors.  Steps (a half's turn on a key tile) alternate
 // between the halves through the whole range; the MMA order is QK(0) QK(1)
 // PV(0) QK(2) PV(1) QK(3) ..., so the tensor core works on one half while the
 // other half's softmax runs.  TMEM: S0 | S1 | O0 | O1, P over S.  O is
@@ -48,8 +51,8 @@ using namespace ptx;
 
 constexpr int BM = 128, BN = 128;
 constexpr int kSoftmaxThreads = 256;
-constexpr int kThreads = kSoftmaxThreads + 64;
-constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = kSoftmaxThreads + 96;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kPlanWarp = 10;
 constexpr int NS = 4;                          // K/V ring slots
 constexpr uint32_t kSub = BM * 64 * 2;         // [128][64] bf16, 128B-swizzled
 constexpr uint32_t kTileB = 2 * kSub;          // [128][128] bf16 = 32 KB
@@ -57,8 +60,15 @@ constexpr uint32_t OFF_Q = 0;                  // two query tiles
 constexpr uint32_t OFF_RING = 2 * kTileB;
 constexpr uint32_t OFF_ML = OFF_RING + NS * kTileB;      // [2][2][2][128] floats
 constexpr uint32_t OFF_BAR = OFF_ML + 2 * 2 * 2 * BM * 4;
-constexpr uint32_t OFF_SCAN = OFF_BAR + 256;             // scan of the work list
-constexpr uint32_t kSmemBytes = OFF_SCAN + 128 + 1024;   // + 1 KB alignment slack
+constexpr int NSEG = 4;                        // segments handed over at a time
+constexpr uint32_t OFF_SEG = OFF_BAR + 256;
+constexpr uint32_t OFF_PAR = OFF_SEG + NSEG * 64;        // a sequence's parents
+constexpr int NODES = 2 * BM;                  // most nodes of a unit
+constexpr int NTT = 2;                         // tree tiles whose masks are handed over
+constexpr uint32_t kNodeWords = NODES * (1 + 4 * NTT);   // depth and masks of a unit's nodes
+constexpr uint32_t OFF_NODE = OFF_PAR + kMaxTreeNodes * 4;
+constexpr uint32_t kSmemBytes = OFF_NODE + 2 * kNodeWords * 4 + 1024;  // + alignment slack
+static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 
 __host__ __device__ constexpr uint32_t tm_s(int half) { return half ? 128u : 0u; }
 __host__ __device__ constexpr uint32_t tm_o(int half) { return half ? 384u : 256u; }
@@ -78,7 +88,10 @@ constexpr int B_O = B_P + 2;                   // 2 halves: the segment's last P
 constexpr int B_F = B_O + 2;                   // the segment's O read out
 constexpr int B_ML = B_F + 1;                  // split: both halves' (m, l) in smem
 constexpr int B_FIN = B_ML + 1;
-constexpr int NBAR = B_FIN + 1;
+constexpr int B_SEG = B_FIN + 1;               // NSEG segments handed over
+constexpr int B_NODE = B_SEG + NSEG;           // 2 segments' nodes handed over
+constexpr int B_NFREE = B_NODE + 2;            // and read by every row
+constexpr int NBAR = B_NFREE + 2;
 static_assert(8 * NBAR + 16 <= 256, "barriers");
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x,
@@ -101,87 +114,48 @@ struct Shape {
 struct Seq {
   int cnt, m_b;
   int64_t t_b;
-  int np, nr, nb, tl, units;
+  int np, nr, tl, units;
   __device__ void load(const CacheView& cv, const TreeArgs& a, const Shape& sh, int b) {
     cnt = live_nodes(a.counts, b, a.nodes, cv.err);
     m_b = cv.m_dev[b];
     t_b = cv.t_dev[(size_t)b * cv.H];
     np = (m_b + BN - 1) / BN;
     nr = (int)((min(cv.n, t_b) + BN - 1) / BN);
-    nb = (cnt + BN - 1) / BN;
-    tl = np + nr + nb;
+    tl = np + nr + (cnt + BN - 1) / BN;
     const int per = sh.npt << sh.pair;
     units = (cnt + per - 1) / per * cv.Hkv;
   }
-  __device__ int64_t work() const { return (int64_t)tl * units; }
 };
 
 enum TileKind { kPrefix = 0, kRing = 1, kTree = 2 };
 
-// A walk through a CTA's range: each segment is the part of a unit that the
-// range covers, key tiles j0..j1-1 of the unit's tl.
-struct Walk {
-  Seq sq;
-  int b, u;               // sequence and unit of the segment
-  int j0, j1;
-  int64_t left;           // tiles of the range from the segment's first on
-  int idx;                // segments before it
-  __device__ void begin(const CacheView& cv, const TreeArgs& a, const Shape& sh, int b_,
-                        int64_t off, int64_t count) {
-    b = b_;
-    left = count;
-    idx = 0;
-    if (left <= 0) return;
-    sq.load(cv, a, sh, b);
-    u = (int)(off / sq.tl);
-    j0 = (int)(off % sq.tl);
-    j1 = (int)min((int64_t)sq.tl, j0 + left);
-  }
-  __device__ bool done() const { return left <= 0; }
-  __device__ void next(const CacheView& cv, const TreeArgs& a, const Shape& sh) {
-    left -= j1 - j0;
-    ++idx;
-    if (left <= 0) return;
-    if (++u == sq.units) {
-      u = 0;
-      sq.units = 0;
-      while (sq.units == 0 && b + 1 < cv.B) sq.load(cv, a, sh, ++b);
-      if (sq.units == 0) {              // the list ends with the last sequence
-        left = 0;
-        return;
-      }
-    }
-    j0 = 0;
-    j1 = (int)min((int64_t)sq.tl, left);
-  }
-  __device__ int kvh(const CacheView& cv) const { return u % cv.Hkv; }
-  __device__ int node0(const CacheView& cv, const Shape& sh) const {
-    return u / cv.Hkv * (sh.npt << sh.pair);
-  }
-  // A unit without rows for a second query tile is split like all others of a
-  // launch without pairs.
-  __device__ bool split(const CacheView& cv, const Shape& sh) const {
-    return !sh.pair || node0(cv, sh) + sh.npt >= sq.cnt;
-  }
-  // Kind of key tile j, its index among its kind, and its keys' number (the
-  // tree's: live nodes; the ring's: slots; the prefix's: rows).
-  __device__ void tile(int j, int64_t n, int& kind, int& i, int& keys) const {
-    if (j < sq.np) {
+// A segment as the planner hands it over.
+struct Segment {
+  int b, kvh, node0, cnt;
+  int j0, j1;             // key tiles of the unit inside the range; j1 = 0: no more segments
+  int np, nr;             // the unit's prefix and ring tiles, then come the tree's
+  int m_b, ring;          // prefix rows, filled ring slots
+  int newest, age;        // ring slot of output t_b - 1, and t_b - 1 (clamped)
+  int split, whole, begins;
+  // Kind of key tile j, its index among its kind, and its keys.
+  __device__ void tile(int j, int& kind, int& i, int& keys) const {
+    if (j < np) {
       kind = kPrefix;
       i = j;
-      keys = sq.m_b;
-    } else if (j < sq.np + sq.nr) {
+      keys = m_b;
+    } else if (j < np + nr) {
       kind = kRing;
-      i = j - sq.np;
-      keys = (int)min(n, sq.t_b);
+      i = j - np;
+      keys = ring;
     } else {
       kind = kTree;
-      i = j - sq.np - sq.nr;
-      keys = sq.cnt;
+      i = j - np - nr;
+      keys = cnt;
     }
     keys = min(BN, keys - i * BN);
   }
 };
+static_assert(sizeof(Segment) <= 64, "segment");
 
 // Bits e of word c (columns 32 c + e) with lo <= column <= hi.
 __device__ __forceinline__ uint32_t range_mask(int lo, int hi, int c) {
@@ -209,10 +183,6 @@ __device__ __forceinline__ float* partial_at(void* ws, int grid, int slot, int D
          (size_t)slot * partial_floats(D, pair);
 }
 
-__device__ __forceinline__ int64_t range_start(int64_t W, int c, int ctas) {
-  return W * c / ctas;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -235,7 +205,8 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
   volatile int* abort_flag =
       reinterpret_cast<volatile int*>(smem + OFF_BAR + 8 * NBAR + 4);
   volatile int* never = reinterpret_cast<volatile int*>(smem + OFF_BAR + 8 * NBAR + 8);
-  int64_t* scan = reinterpret_cast<int64_t*>(smem + OFF_SCAN);   // 10 warp sums, found b, off
+  const Segment* segs = reinterpret_cast<const Segment*>(smem + OFF_SEG);
+  int32_t* nodes_smem = reinterpret_cast<int32_t*>(smem + OFF_NODE);
   constexpr int NSUB = D / 64;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -243,7 +214,9 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
 
   if (threadIdx.x == 0) {
     for (int k = 0; k < NBAR; ++k)
-      mbar_init(bar(k), k == B_P || k == B_P + 1 ? 128u : (k == B_F || k == B_ML ? 256u : 1u));
+      mbar_init(bar(k), k == B_P || k == B_P + 1
+                           ? 128u
+                           : (k == B_F || k == B_ML || k >= B_NFREE ? 256u : 1u));
     *abort_flag = 0;
     *never = 0;
     fence_mbar_init();
@@ -253,56 +226,18 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     tmem_alloc(smem_u32(tmem_slot), TM_COLS);
     tmem_relinquish();
   }
-  griddep_wait();
-  griddep_launch_dependents();
-
-  // This CTA's range of the work list: an exclusive scan of the sequences'
-  // shares, each thread with a run of `per` sequences.
-  const int per = (cv.B + kThreads - 1) / kThreads;
-  int64_t mine = 0, before, total = 0;
-  const int b_lo = min((int)threadIdx.x * per, cv.B), b_hi = min(b_lo + per, cv.B);
-  for (int b = b_lo; b < b_hi; ++b) {
-    Seq s;
-    s.load(cv, a, sh, b);
-    mine += s.work();
-  }
-  int64_t inc = mine;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, inc, off);
-    if (lane >= off) inc += x;
-  }
-  if (lane == 31) scan[warp] = inc;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  before = inc - mine;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
-  }
-  const int ctas = (int)min((int64_t)grid, max((int64_t)1, total / kMinTiles));
-  const int64_t g0 = cta < ctas ? range_start(total, cta, ctas) : 0;
-  const int64_t g1 = cta < ctas ? range_start(total, cta + 1, ctas) : 0;
-  if (g0 < g1 && before <= g0 && g0 < before + mine) {
-    int64_t at = before;
-    for (int b = b_lo; b < b_hi; ++b) {
-      Seq s;
-      s.load(cv, a, sh, b);
-      if (g0 < at + s.work()) {
-        scan[10] = b;
-        scan[11] = g0 - at;
-        break;
-      }
-      at += s.work();
-    }
-  }
-  __syncthreads();
   const uint32_t tmem = *tmem_slot;
-  const int first_b = (int)scan[10];
-  const int64_t first_off = scan[11];
-  Walk wk;
+  griddep_wait();
+  griddep_launch_dependents();
+  // Segment k, from the planner; false: the wait gave up.
+  auto segment = [&](int k, Segment& w) {
+    if (!mbar_wait(bar(B_SEG + k % NSEG), (k / NSEG) & 1, abort_flag, wait_ns)) return false;
+    w = segs[k % NSEG];
+    return true;
+  };
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
@@ -310,13 +245,16 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       prefetch_tmap(&tmQ);
       prefetch_tmap(&tmKc);
       prefetch_tmap(&tmVc);
+      prefetch_tmap(&tmKt16);
+      prefetch_tmap(&tmVt16);
+      prefetch_tmap(&tmKc16);
+      prefetch_tmap(&tmVc16);
       uint32_t gi = 0, qi = 0;                   // K/V loads and query tiles issued
       bool ok = true;
       const uint32_t qbytes = (uint32_t)NSUB * sh.npt * sh.G * 128u;
-      for (wk.begin(cv, a, sh, first_b, first_off, g1 - g0); ok && !wk.done();
-           wk.next(cv, a, sh)) {
-        const int kvh = wk.kvh(cv), node0 = wk.node0(cv, sh);
-        const int nq = wk.split(cv, sh) ? 1 : 2;
+      Segment w;
+      for (int k = 0; ok && segment(k, w) && w.j1 > 0; ++k) {
+        const int nq = w.split ? 1 : 2;
         for (int x = 0; ok && x < nq; ++x, ++qi) {
           const uint32_t s = qi & 1;
           if (qi >= 2 && !mbar_wait(bar(B_QE + s), ((qi >> 1) - 1) & 1, abort_flag, wait_ns)) {
@@ -326,17 +264,17 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
           mbar_arrive_expect_tx(bar(B_QF + s), qbytes);
 #pragma unroll
           for (int c = 0; c < NSUB; ++c)
-            tma_load_3d(sb + OFF_Q + s * kTileB + c * kSub, &tmQ, c * 64, kvh * sh.G,
-                        wk.b * a.nodes + node0 + x * sh.npt, bar(B_QF + s));
+            tma_load_3d(sb + OFF_Q + s * kTileB + c * kSub, &tmQ, c * 64, w.kvh * sh.G,
+                        w.b * a.nodes + w.node0 + x * sh.npt, bar(B_QF + s));
         }
-        const int64_t slab0 = ((int64_t)wk.b * cv.Hkv + kvh) * cv.slab_rows;
-        for (int j = wk.j0; ok && j < wk.j1; ++j) {
+        const int64_t slab0 = ((int64_t)w.b * cv.Hkv + w.kvh) * cv.slab_rows;
+        for (int j = w.j0; ok && j < w.j1; ++j) {
           int kind, i, keys;
-          wk.tile(j, cv.n, kind, i, keys);
+          w.tile(j, kind, i, keys);
           const int boxes = (keys + 15) / 16;
-          const int x0 = kind == kTree ? kvh * D : 0;
+          const int x0 = kind == kTree ? w.kvh * D : 0;
           const int y0 = kind == kTree
-                             ? wk.b * a.nodes + i * BN
+                             ? w.b * a.nodes + i * BN
                              : (int)(slab0 + (kind == kRing ? cv.m_cap : 0) + (int64_t)i * BN);
           for (int isv = 0; isv < 2; ++isv, ++gi) {
             const uint32_t s = gi % NS;
@@ -380,41 +318,39 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       return __all_sync(0xffffffffu, mbar_wait(bar(k), phase & 1, abort_flag, wait_ns)) != 0;
     };
     struct Cursor {
-      Walk w;
+      Segment w;
+      int k;                  // segment
       int j, sub;             // key tile; in a pair unit the first or second half's turn
       uint32_t step, load, q; // steps, key tiles and query tiles before
-      bool split;
+      bool more;
     };
-    auto start = [&](Cursor& c) {
-      c.w.begin(cv, a, sh, first_b, first_off, g1 - g0);
+    auto enter = [&](Cursor& c) {
+      const bool got = segment(c.k, c.w);
+      c.more = __all_sync(0xffffffffu, got) && c.w.j1 > 0;
       c.j = c.w.j0;
       c.sub = 0;
-      c.step = c.load = c.q = 0;
-      c.split = !c.w.done() && c.w.split(cv, sh);
     };
     auto advance = [&](Cursor& c) {
       ++c.step;
-      if (!c.split && c.sub == 0) {
+      if (!c.w.split && c.sub == 0) {
         c.sub = 1;
         return;
       }
       c.sub = 0;
       ++c.load;
       if (++c.j == c.w.j1) {
-        c.q += c.split ? 1 : 2;
-        c.w.next(cv, a, sh);
-        if (c.w.done()) return;
-        c.j = c.w.j0;
-        c.split = c.w.split(cv, sh);
+        c.q += c.w.split ? 1 : 2;
+        ++c.k;
+        enter(c);
       }
     };
-    Cursor qc, pc;
-    start(qc);
-    start(pc);
+    Cursor qc = {}, pc = {};
+    enter(qc);
+    enter(pc);
     // S = Q K^T of qc's step, then on to the next.
     auto qk = [&]() {
       const uint32_t half = qc.step & 1;
-      const uint32_t qt = qc.split ? qc.q : qc.q + half;
+      const uint32_t qt = qc.w.split ? qc.q : qc.q + half;
       const uint32_t ki = 2 * qc.load;
       if (!wait(B_QF + (qt & 1), qt >> 1) || !wait(B_FULL + ki % NS, ki / NS)) return false;
       tc_fence_after();
@@ -428,10 +364,10 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                       desc_sw128(kb + off, 16, 1024), idesc_qk, k > 0);
         }
         mma_commit(bar(B_S + half));
-        if (qc.split || qc.sub == 1) mma_commit(bar(B_EMPTY + ki % NS));
-        if (qc.j + 1 == qc.w.j1 && (qc.split || qc.sub == 1)) {
+        if (qc.w.split || qc.sub == 1) mma_commit(bar(B_EMPTY + ki % NS));
+        if (qc.j + 1 == qc.w.j1 && (qc.w.split || qc.sub == 1)) {
           mma_commit(bar(B_QE + (qc.q & 1)));
-          if (!qc.split) mma_commit(bar(B_QE + ((qc.q + 1) & 1)));
+          if (!qc.w.split) mma_commit(bar(B_QE + ((qc.q + 1) & 1)));
         }
       }
       __syncwarp();
@@ -439,20 +375,20 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       return true;
     };
     bool ok = true;
-    for (int x = 0; x < 2 && ok && !qc.w.done(); ++x) ok = qk();
-    while (ok && !pc.w.done()) {
+    for (int x = 0; x < 2 && ok && qc.more; ++x) ok = qk();
+    while (ok && pc.more) {
       const uint32_t half = pc.step & 1;
       const uint32_t vi = 2 * pc.load + 1;
       int kind, i, keys;
-      pc.w.tile(pc.j, cv.n, kind, i, keys);
+      pc.w.tile(pc.j, kind, i, keys);
       // The half's first and last step of the segment.
-      const int span = pc.split ? 2 : 1;
+      const int span = pc.w.split ? 2 : 1;
       const bool first = pc.j - pc.w.j0 < span, last = pc.j + span >= pc.w.j1;
-      if (first && pc.w.idx > 0 && !wait(B_F, pc.w.idx - 1)) break;
+      if (first && pc.k > 0 && !wait(B_F, pc.k - 1)) break;
       if (!wait(B_P + half, pc.step >> 1) || !wait(B_FULL + vi % NS, vi / NS)) break;
       const uint32_t vb = sb + OFF_RING + (vi % NS) * kTileB;
       const int ks = (keys + 15) / 16;
-      if (kind == kTree && keys % 16 != 0 && (pc.split || pc.sub == 0)) {
+      if (kind == kTree && keys % 16 != 0 && (pc.w.split || pc.sub == 0)) {
         // value rows keys .. 16 ks - 1: nodes past the count
         const int rows = 16 * ks - keys;
         for (int x = lane; x < rows * 8 * NSUB; x += 32) {
@@ -469,12 +405,12 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
           mma_bf16_ts(tmem + tm_o(half), tmem + tm_s(half) + k * 8,
                       desc_sw128(vb + k * 2048, kSub, 1024), idesc_pv,
                       (!first || k > 0) ? 1u : 0u);
-        if (pc.split || pc.sub == 1) mma_commit(bar(B_EMPTY + vi % NS));
+        if (pc.w.split || pc.sub == 1) mma_commit(bar(B_EMPTY + vi % NS));
         if (last) mma_commit(bar(B_O + half));
       }
       __syncwarp();
       advance(pc);
-      if (!qc.w.done()) ok = qk();
+      if (qc.more) ok = qk();
     }
     // Drain: all MMAs of this CTA have finished before TMEM is freed.
     if (lane == 0) {
@@ -482,10 +418,145 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       mbar_wait(bar(B_FIN), 0, never, kWaitLimitNs);
     }
     __syncwarp();
+  } else if (warp == kPlanWarp) {
+    // ------------------------------------------------------------ planner
+    Segment* out = reinterpret_cast<Segment*>(smem + OFF_SEG);
+    int32_t* par = reinterpret_cast<int32_t*>(smem + OFF_PAR);
+    // The list's length, and the sequences of each lane in it.
+    const int per = (cv.B + 31) / 32;
+    const int b_lo = min(lane * per, cv.B), b_hi = min(b_lo + per, cv.B);
+    Seq sq;
+    int mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+      sq.load(cv, a, sh, b);
+      mine += sq.tl * sq.units;
+    }
+    int inc = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += x;
+    }
+    const int total = __shfl_sync(0xffffffffu, inc, 31);
+    // Range c: `each` tiles, one more for the first `rem` CTAs.
+    const int ctas = min(grid, max(1, total / kMinTiles));
+    const int each = total / ctas, rem = total - each * ctas;
+    const int g0 = cta * each + min(cta, rem);
+    int left = cta < ctas ? each + (cta < rem ? 1 : 0) : 0;
+    JoinDesc jd = {0, 0, 0, -1, 0, {0, 0, 0}};
+    int k = 0;
+    if (left > 0) {
+      // The sequence and unit that tile g0 is in.
+      int b = 0, off = 0;
+      const bool here = inc - mine <= g0 && g0 < inc;
+      if (here) {
+        int at = inc - mine;
+        for (b = b_lo; b < b_hi; ++b) {
+          sq.load(cv, a, sh, b);
+          if (g0 < at + sq.tl * sq.units) break;
+          at += sq.tl * sq.units;
+        }
+        off = g0 - at;
+      }
+      const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+      b = __shfl_sync(0xffffffffu, b, src);
+      off = __shfl_sync(0xffffffffu, off, src);
+      sq.load(cv, a, sh, b);
+      int u = off / sq.tl, j0 = off - u * sq.tl, g = g0, par_b = -1;
+      const int unit_nodes = sh.npt << sh.pair;
+      const int n = (int)min(cv.n, (int64_t)1 << 30);
+      for (;;) {
+        Segment w;
+        w.b = b;
+        w.kvh = u % cv.Hkv;
+        w.node0 = u / cv.Hkv * unit_nodes;
+        w.cnt = sq.cnt;
+        w.j0 = j0;
+        w.j1 = min(sq.tl, j0 + left);
+        w.np = sq.np;
+        w.nr = sq.nr;
+        w.m_b = sq.m_b;
+        w.ring = (int)min(cv.n, sq.t_b);
+        w.age = (int)min(sq.t_b - 1, (int64_t)1 << 30);
+        w.newest = sq.t_b > cv.n ? (int)((sq.t_b - 1) % cv.n) : (int)sq.t_b - 1;
+        // A unit without rows for a second query tile is split like all
+        // others of a launch without pairs.
+        w.split = !sh.pair || w.node0 + sh.npt >= sq.cnt;
+        w.whole = j0 == 0 && w.j1 == sq.tl;
+        w.begins = j0 == 0;
+        // Slot k % NSEG was segment k - 4's: all roles had left it when the
+        // nodes of segment k - 1 were handed over (which waited until those
+        // of segment k - 3 had been read).
+        if (lane == 0) {
+          out[k % NSEG] = w;
+          mbar_arrive(bar(B_SEG + k % NSEG));
+        }
+        if (j0 == 0 && !w.whole) {       // begun here, ended by a later CTA
+          const int x = g + sq.tl - 1;   // the unit's last tile
+          const int cut = rem * (each + 1);
+          jd = {b, w.node0, w.kvh, x < cut ? x / (each + 1) : rem + (x - cut) / each,
+                sq.cnt, {0, 0, 0}};
+        }
+        // Depths and ancestors of the unit's nodes.
+        if (par_b != b) {
+          __syncwarp();
+          for (int i = lane; i < sq.cnt; i += 32) par[i] = a.parents[(size_t)b * a.nodes + i];
+          par_b = b;
+          __syncwarp();
+        }
+        if (k >= 2 &&
+            !__all_sync(0xffffffffu, mbar_wait(bar(B_NFREE + (k & 1)), ((k >> 1) - 1) & 1,
+                                               abort_flag, wait_ns)))
+          break;
+        int32_t* nd = nodes_smem + (k & 1) * kNodeWords;
+        const int nn = min(unit_nodes, sq.cnt - w.node0);
+        for (int i = lane; i < nn; i += 32) {
+          uint32_t m[4 * NTT];
+#pragma unroll
+          for (int e = 0; e < 4 * NTT; ++e) m[e] = 0u;
+          int up = 0;
+          for (int x = w.node0 + i;;) {
+            if (up < n) {
+#pragma unroll
+              for (int e = 0; e < 4 * NTT; ++e)
+                if (x >> 5 == e) m[e] |= 1u << (x & 31);
+            }
+            const int p = par[x];
+            if (p < -1 || p >= x) flag_error(cv.err, kErrBadTree);
+            if (p < 0 || p >= x) break;
+            x = p;
+            ++up;
+          }
+          nd[i] = up;
+#pragma unroll
+          for (int e = 0; e < 4 * NTT; ++e) nd[(1 + e) * NODES + i] = (int32_t)m[e];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_NODE + (k & 1)));
+        ++k;
+        g += w.j1 - w.j0;
+        left -= w.j1 - w.j0;
+        if (left <= 0) break;
+        j0 = 0;
+        if (++u == sq.units) {
+          u = 0;
+          sq.units = 0;
+          while (sq.units == 0 && b + 1 < cv.B) sq.load(cv, a, sh, ++b);
+          if (sq.units == 0) break;      // (the list ends with the last sequence)
+        }
+      }
+    }
+    if (lane == 0) {
+      out[k % NSEG].j1 = 0;              // no more segments
+      mbar_arrive(bar(B_SEG + k % NSEG));
+      static_cast<JoinDesc*>(a.ws)[cta] = jd;
+    }
+    __syncwarp();
   } else {
     // -------------------------------------------------- softmax and epilogue
     const int half = warp >> 2;
     const int r = threadIdx.x & 127;                    // row of the query tile
+    const int rg = r / sh.G, hg = r - rg * sh.G;        // its node in the tile, its head
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const float sl2 = rsqrtf((float)D) * kLog2e;
     const uint32_t s_addr = tmem + lane_off + tm_s(half);
@@ -493,49 +564,33 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     const int n = (int)min(cv.n, (int64_t)1 << 30);
     float* ml = reinterpret_cast<float*>(smem + OFF_ML);
     uint32_t step = 0, turns = 0;                       // steps before; this half's among them
-    uint32_t done_o[2] = {0, 0};                        // segments with steps of each half
-    int64_t g = g0;                                     // list index of the segment's first tile
-    JoinDesc jd = {0, 0, 0, -1, 0, {0, 0, 0}};
+    uint32_t o_phase0 = 0, o_phase1 = 0, ml_phase = 0;  // segments with steps of each half; split
     bool ok = true;
-    for (wk.begin(cv, a, sh, first_b, first_off, g1 - g0); !wk.done(); wk.next(cv, a, sh)) {
-      const bool split = wk.split(cv, sh);
-      const int kvh = wk.kvh(cv), node0 = wk.node0(cv, sh), cnt = wk.sq.cnt;
-      const int nseg = wk.j1 - wk.j0;
-      const int node = node0 + (split ? 0 : half * sh.npt) + r / sh.G;
-      const bool live = r < sh.npt * sh.G && node < cnt;
+    Segment w;
+    for (int k = 0;; ++k) {
+      if (!__all_sync(0xffffffffu, segment(k, w)) || w.j1 == 0) break;
+      const bool split = w.split != 0;
+      const int nseg = w.j1 - w.j0;
+      const int ni = (split ? 0 : half * sh.npt) + rg;  // node of the unit
+      const int node = w.node0 + ni;
+      const bool live = rg < sh.npt && node < w.cnt;
       const bool any = __any_sync(0xffffffffu, live);
-      // The chain to the root: depth, and this row's keys among the tree's
-      // first 128 nodes.
-      const int32_t* par = a.parents + (size_t)wk.b * a.nodes;
-      int depth = 0;
-      uint32_t tree0[4] = {0, 0, 0, 0};
-      auto chain = [&](int k0, uint32_t* w) {
-        int up = 0;
-        for (int x = node;;) {
-          const int c = x - k0;
-          if (up < n && c >= 0 && c < BN) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (c >> 5 == e) w[e] |= 1u << (c & 31);
-          }
-          const int p = par[x];
-          if (p < -1 || p >= x) flag_error(cv.err, kErrBadTree);
-          if (p < 0 || p >= x) break;
-          x = p;
-          ++up;
-        }
-        return up;
-      };
-      if (live) depth = chain(0, tree0);
+      const int32_t* nd = nodes_smem + (k & 1) * kNodeWords;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(B_NODE + (k & 1)), (k >> 1) & 1, abort_flag,
+                                             wait_ns))) {
+        ok = false;
+        break;
+      }
+      const int depth = live ? nd[ni] : 0;
       // Ring: slot s is a key iff its age (r0 - s) mod n is at most lim.
-      const int lim = (int)min(wk.sq.t_b - 1, (int64_t)n - 2 - depth);
-      const int r0 = wk.sq.t_b > 0 ? (int)((wk.sq.t_b - 1) % n) : 0;
+      const int lim = min(w.age, n - 2 - depth);
+      const int r0 = w.newest;
       float m_run = -INFINITY, l_run = 0.f;
       bool started = false;
-      for (int j = wk.j0; j < wk.j1; ++j) {
-        if (split && ((step + (uint32_t)(j - wk.j0)) & 1) != (uint32_t)half) continue;
+      for (int j = w.j0; j < w.j1; ++j) {
+        if (split && ((step + (uint32_t)(j - w.j0)) & 1) != (uint32_t)half) continue;
         int kind, i, keys;
-        wk.tile(j, cv.n, kind, i, keys);
+        w.tile(j, kind, i, keys);
         const int k0 = i * BN;
         const bool full = kind == kPrefix && keys == BN;
         if (!__all_sync(0xffffffffu,
@@ -547,12 +602,27 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         tc_fence_after();
         if (any) {
           // This row's keys among the tile's columns.
-          uint32_t w[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+          uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
           if (!full) {
             if (kind == kTree) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c) w[c] = i == 0 ? tree0[c] : 0u;
-              if (i > 0 && live) chain(k0, w);
+              for (int c = 0; c < 4; ++c)
+                see[c] = live && i < NTT ? (uint32_t)nd[(1 + 4 * i + c) * NODES + ni] : 0u;
+              if (i >= NTT && live) {
+                // a further tile of a large tree: walk up from the node
+                const int32_t* par = a.parents + (size_t)w.b * a.nodes;
+                int up = 0;
+                for (int x = node; x >= k0 && up < n; ++up) {
+                  if (x < k0 + BN) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                      if ((x - k0) >> 5 == e) see[e] |= 1u << (x & 31);
+                  }
+                  const int p = par[x];
+                  if (p >= x) break;
+                  x = p;
+                }
+              }
             } else {
               int a1 = 0, b1 = keys - 1, a2 = 1, b2 = 0;
               if (kind == kRing) {
@@ -569,7 +639,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
               }
 #pragma unroll
               for (int c = 0; c < 4; ++c)
-                w[c] = range_mask(a1, b1, c) | range_mask(a2, b2, c);
+                see[c] = range_mask(a1, b1, c) | range_mask(a2, b2, c);
             }
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -578,7 +648,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
             if (!full) {
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (!(w[c] >> e & 1u)) v[e] = 0xff800000u;         // -inf
+                if (!(see[c] >> e & 1u)) v[e] = 0xff800000u;         // -inf
               tmem_st32(s_addr + 32 * c, v);
             }
 #pragma unroll
@@ -668,31 +738,23 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         started = true;
         mbar_arrive(bar(B_P + half));
       }
+      mbar_arrive(bar(B_NFREE + (k & 1)));
       // ------------------------------------------------------- epilogue
-      // Steps of each half in this segment.
-      int nh[2] = {nseg, nseg};
-      if (split) {
-        nh[step & 1] = (nseg + 1) / 2;
-        nh[(step + 1) & 1] = nseg / 2;
-      }
-      const bool whole = wk.j0 == 0 && wk.j1 == wk.sq.tl;
-      const int seg = wk.idx & 1;
-      auto wait_all = [&](int k, uint32_t phase) {
-        return __all_sync(0xffffffffu, mbar_wait(bar(k), phase & 1, abort_flag, wait_ns)) != 0;
+      // Steps of this half and of the other in this segment.
+      const int own = !split ? nseg : ((step & 1) == (uint32_t)half ? (nseg + 1) / 2 : nseg / 2);
+      const int other = split ? nseg - own : nseg;
+      auto wait_all = [&](int b, uint32_t phase) {
+        return __all_sync(0xffffffffu, mbar_wait(bar(b), phase & 1, abort_flag, wait_ns)) != 0;
       };
       // Weights of the two halves' O, the row's reference and sum.
       float a0 = 1.f, a1 = 0.f, M = m_run, L = l_run;
-      int h0 = half;                                     // O_h0 a0 + O_(1 - h0) a1
       if (split) {
-        float* mine_ml = ml + (seg * 2 + half) * 2 * BM;
-        mine_ml[r] = m_run;
-        mine_ml[BM + r] = l_run;
+        float* own_ml = ml + ((k & 1) * 2 + half) * 2 * BM;
+        own_ml[r] = m_run;
+        own_ml[BM + r] = l_run;
         mbar_arrive(bar(B_ML));
-      }
-      if (ok && split) {
-        // B_ML completes once for each split segment
-        if (wait_all(B_ML, done_o[0] >> 16)) {
-          const float* o_ml = ml + (seg * 2 + (1 - half)) * 2 * BM;
+        if (ok && wait_all(B_ML, ml_phase)) {
+          const float* o_ml = ml + ((k & 1) * 2 + 1 - half) * 2 * BM;
           const float m1 = o_ml[r], l1 = o_ml[BM + r];
           M = fmaxf(m_run, m1);
           const float ref = (M == -INFINITY) ? 0.f : M;
@@ -702,31 +764,30 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         } else {
           ok = false;
         }
+        ++ml_phase;
       }
-      if (ok) {
-        for (int h = 0; h < 2; ++h)
-          if (nh[h] > 0 && (split || h == half))
-            ok = ok && wait_all(B_O + h, done_o[h] & 0xffffu);
-      }
+      if (ok && own > 0) ok = wait_all(B_O + half, half ? o_phase1 : o_phase0);
+      if (ok && split && other > 0) ok = wait_all(B_O + 1 - half, half ? o_phase0 : o_phase1);
       if (!ok) break;
       tc_fence_after();
       if (any) {
-        const int slot = 2 * cta + (wk.j0 == 0 ? 1 : 0);
+        const int slot = 2 * cta + w.begins;
         float* part = partial_at(a.ws, grid, slot, D, sh.pair);
         const int prow = (split ? 0 : half * BM) + r;
         const int prows = BM << sh.pair;
         const float inv = 1.f / L;
-        const size_t orow = ((size_t)wk.b * a.nodes + node) * cv.H + (size_t)kvh * sh.G + r % sh.G;
+        const bool whole = w.whole != 0;
+        const size_t orow = ((size_t)w.b * a.nodes + node) * cv.H + (size_t)w.kvh * sh.G + hg;
         __nv_bfloat16* orow_p = static_cast<__nv_bfloat16*>(a.o) + orow * D;
         // Split: each half writes half of the columns of the joined row.
         const int c_lo = split ? half * (D / 64) : 0, c_hi = split ? c_lo + D / 64 : D / 32;
-        const bool use0 = nh[h0] > 0, use1 = split && nh[1 - h0] > 0;
+        const bool use0 = own > 0, use1 = split && other > 0;
 #pragma unroll 1
         for (int c = c_lo; c < c_hi; ++c) {
           uint32_t ov[32];
           float x[32];
           if (use0) {
-            tmem_ld32_sync(tmem + lane_off + tm_o(h0) + c * 32, ov);
+            tmem_ld32_sync(tmem + lane_off + tm_o(half) + c * 32, ov);
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(ov[e]) * a0;
           } else {
@@ -734,7 +795,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
             for (int e = 0; e < 32; ++e) x[e] = 0.f;
           }
           if (use1) {
-            tmem_ld32_sync(tmem + lane_off + tm_o(1 - h0) + c * 32, ov);
+            tmem_ld32_sync(tmem + lane_off + tm_o(1 - half) + c * 32, ov);
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(ov[e]), a1, x[e]);
           }
@@ -765,21 +826,10 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       }
       tc_fence_before();
       mbar_arrive(bar(B_F));
-      if (!whole && wk.j0 == 0) {
-        // This CTA begins the unit and a later one ends it.
-        const int64_t x = g + wk.sq.tl - 1;             // the unit's last tile
-        int last = (int)min((int64_t)ctas - 1, x * ctas / total);
-        while (last + 1 < ctas && range_start(total, last + 1, ctas) <= x) ++last;
-        while (range_start(total, last, ctas) > x) --last;
-        jd = {wk.b, node0, kvh, last, cnt, {0, 0, 0}};
-      }
-      if (split) done_o[0] += 0x10000u;                  // split segments, for B_ML
-      for (int h = 0; h < 2; ++h)
-        if (nh[h] > 0) done_o[h] = (done_o[h] & 0xffff0000u) | ((done_o[h] + 1) & 0xffffu);
+      if ((half ? other : own) > 0) ++o_phase0;
+      if ((half ? own : other) > 0) ++o_phase1;
       step += split ? nseg : 2 * nseg;
-      g += nseg;
     }
-    if (threadIdx.x == 0) static_cast<JoinDesc*>(a.ws)[cta] = jd;
   }
 
   tc_fence_before();
@@ -793,9 +843,11 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
 
 // Joins the partials of the units that the CTAs' ranges cut.  Block (c, y):
 // rows 32 y .. 32 y + 31 of the unit that CTA c begins and does not end; lane =
-// row, warp = a quarter of the columns.
+// row, each of 16 warps D / 16 columns; 8 partials are read at a time.
+constexpr int kJoinWarps = 16;
+
 template <int D>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kJoinWarps * 32)
 join_tree_kernel(CacheView cv, TreeArgs a, Shape sh) {
   griddep_wait();
   griddep_launch_dependents();
@@ -804,44 +856,66 @@ join_tree_kernel(CacheView cv, TreeArgs a, Shape sh) {
   if (jd.last < 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int prow = blockIdx.y * 32 + lane, prows = BM << sh.pair;
-  const int r = prow & (BM - 1);
-  const int node = jd.node0 + (prow >= BM ? sh.npt : 0) + r / sh.G;
-  if (r >= sh.npt * sh.G || node >= jd.cnt) return;
-  constexpr int NV = D / 16;                       // float4 of a thread
+  const int r = prow & (BM - 1), rg = r / sh.G;
+  const int node = jd.node0 + (prow >= BM ? sh.npt : 0) + rg;
+  if (rg >= sh.npt || node >= jd.cnt) return;
+  constexpr int NV = D / 4 / kJoinWarps;           // float4 of a thread
+  constexpr int PB = 8;                            // partials read at a time
   float M = -INFINITY, L = 0.f;
-  float4 acc[NV];
+  float x[4 * NV];
 #pragma unroll
-  for (int v = 0; v < NV; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p = c; p <= jd.last; ++p) {
-    const float* part = partial_at(a.ws, grid, 2 * p + (p == c ? 1 : 0), D, sh.pair);
-    const float m = __ldcg(part + (size_t)prows * D + prow);
-    const float l = __ldcg(part + (size_t)prows * (D + 1) + prow);
-    float4 x[NV];
+  for (int e = 0; e < 4 * NV; ++e) x[e] = 0.f;
+  for (int p0 = c; p0 <= jd.last; p0 += PB) {
+    float m[PB], l[PB];
+    float4 v[PB][NV];
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-      x[v] = __ldcg(reinterpret_cast<const float4*>(part) + (size_t)(warp * NV + v) * prows + prow);
-    const float mn = fmaxf(M, m), ref = (mn == -INFINITY) ? 0.f : mn;
-    const float s0 = fast_exp2(M - ref), s1 = fast_exp2(m - ref);
+    for (int i = 0; i < PB; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+      const int p = p0 + i;
+      if (p <= jd.last) {
+        const float* part = partial_at(a.ws, grid, 2 * p + (p == c ? 1 : 0), D, sh.pair);
+        m[i] = __ldcg(part + (size_t)prows * D + prow);
+        l[i] = __ldcg(part + (size_t)prows * (D + 1) + prow);
+#pragma unroll
+        for (int e = 0; e < NV; ++e)
+          v[i][e] = __ldcg(reinterpret_cast<const float4*>(part) +
+                           (size_t)(warp * NV + e) * prows + prow);
+      } else {
+#pragma unroll
+        for (int e = 0; e < NV; ++e) v[i][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+    float mn = M;
+#pragma unroll
+    for (int i = 0; i < PB; ++i) mn = fmaxf(mn, m[i]);
+    const float ref = (mn == -INFINITY) ? 0.f : mn;
+    const float s0 = fast_exp2(M - ref);
     M = mn;
-    L = L * s0 + l * s1;
+    L *= s0;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      acc[v].x = acc[v].x * s0 + x[v].x * s1;
-      acc[v].y = acc[v].y * s0 + x[v].y * s1;
-      acc[v].z = acc[v].z * s0 + x[v].z * s1;
-      acc[v].w = acc[v].w * s0 + x[v].w * s1;
+    for (int e = 0; e < 4 * NV; ++e) x[e] *= s0;
+#pragma unroll
+    for (int i = 0; i < PB; ++i) {
+      const float s = fast_exp2(m[i] - ref);
+      L += l[i] * s;
+#pragma unroll
+      for (int e = 0; e < NV; ++e) {
+        x[4 * e] += v[i][e].x * s;
+        x[4 * e + 1] += v[i][e].y * s;
+        x[4 * e + 2] += v[i][e].z * s;
+        x[4 * e + 3] += v[i][e].w * s;
+      }
     }
   }
   const float inv = 1.f / L;                       // self is visible: L > 0
-  const size_t orow = ((size_t)jd.b * a.nodes + node) * cv.H + (size_t)jd.kvh * sh.G + r % sh.G;
-  uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + orow * D +
-                                        warp * (D / 4));
+  const size_t orow =
+      ((size_t)jd.b * a.nodes + node) * cv.H + (size_t)jd.kvh * sh.G + (r - rg * sh.G);
+  uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + orow * D) + warp * NV;
 #pragma unroll
-  for (int v = 0; v < NV; v += 2)
-    dst[v / 2] = make_uint4(pack_bf16(acc[v].x * inv, acc[v].y * inv),
-                            pack_bf16(acc[v].z * inv, acc[v].w * inv),
-                            pack_bf16(acc[v + 1].x * inv, acc[v + 1].y * inv),
-                            pack_bf16(acc[v + 1].z * inv, acc[v + 1].w * inv));
+  for (int e = 0; e < NV; ++e)
+    dst[e] = make_uint2(pack_bf16(x[4 * e] * inv, x[4 * e + 1] * inv),
+                        pack_bf16(x[4 * e + 2] * inv, x[4 * e + 3] * inv));
   if (warp == 0 && a.lse) a.lse[orow] = (M + log2f(L)) * kLn2;
 }
 
@@ -853,12 +927,18 @@ Shape shape_of(const CacheView& cv, int nodes) {
   return sh;
 }
 
-// CTAs of the launch: one per SM, no more than the largest list could feed.
-int grid_of(const CacheView& cv, int nodes, const Shape& sh) {
+// Key tiles of the largest work list.
+int64_t list_bound(const CacheView& cv, int nodes, const Shape& sh) {
+  if (sh.npt < 1) return INT64_MAX;
   const int per = sh.npt << sh.pair;
   const int64_t units = (int64_t)cv.B * cv.Hkv * ((nodes + per - 1) / per);
   const int64_t tiles = (cv.m_cap + BN - 1) / BN + (cv.n + BN - 1) / BN + (nodes + BN - 1) / BN;
-  const int64_t most = units * tiles / kMinTiles;
+  return units * tiles;
+}
+
+// CTAs of the launch: one per SM, no more than the largest list could feed.
+int grid_of(const CacheView& cv, int nodes, const Shape& sh) {
+  const int64_t most = list_bound(cv, nodes, sh) / kMinTiles;
   return (int)std::max<int64_t>(1, std::min<int64_t>(cv.sms, most));
 }
 
@@ -887,14 +967,16 @@ cudaError_t launch_d(const CacheView& cv, const TreeArgs& a, cudaStream_t s) {
                        mkc, mvc, mkt, mvt, mkc16, mvc16, mkt16, mvt16, cv, a, sh,
                        phase_wait_limit_ns());
   if (e != cudaSuccess) return e;
-  return launch_dependent(join_tree_kernel<D>, dim3(grid, (BM << sh.pair) / 32), dim3(128), 0, s,
+  return launch_dependent(join_tree_kernel<D>, dim3(grid, (BM << sh.pair) / 32),
+                          dim3(kJoinWarps * 32), 0, s,
                           cv, a, sh);
 }
 
 }  // namespace
 
 bool decode_tree_tc_supported(const CacheView& cv, int nodes) {
-  return cv.dtype == RSWA_BF16 && cv.H / cv.Hkv <= BM &&
+  const Shape sh = shape_of(cv, nodes);
+  return list_bound(cv, nodes, sh) < (int64_t(1) << 31) && cv.dtype == RSWA_BF16 && cv.H / cv.Hkv <= BM &&
          (int64_t)cv.B * nodes < (int64_t(1) << 30) &&
          (int64_t)cv.B * cv.Hkv * cv.slab_rows + cv.n < (int64_t(1) << 31);
 }
