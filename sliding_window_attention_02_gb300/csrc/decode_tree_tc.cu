@@ -25,9 +25,9 @@
 // Roles (352 threads): warps 0-3 / 4-7 softmax and epilogue of half 0 / 1
 // (thread r owns row r = TMEM lane r), warp 8 TMA producer, warp 9 TMEM
 // allocator and MMA issuer, warp 10 planner: it cuts the list, walks the CTA's
-// range ahead of the others and hands them, through shared memory, each
-// segment (the part of a unit inside the range) and its nodes' depths and
-// ancestors.  Steps (a half's turn on a key tile) alternate
+// range ahead of the others, hands them, through shared memory, each segment
+// (the part of a unit inside the range) and its nodes' depths and ancestors,
+// and requests the query tiles.  Steps (a half's turn on a key tile) alternate
 // between the halves through the whole range; the MMA order is QK(0) QK(1)
 // PV(0) QK(2) PV(1) QK(3) ..., so the tensor core works on one half while the
 // other half's softmax runs.  TMEM: S0 | S1 | O0 | O1, P over S.  O is
@@ -53,46 +53,61 @@ constexpr int BM = 128, BN = 128;
 constexpr int kSoftmaxThreads = 256;
 constexpr int kThreads = kSoftmaxThreads + 96;
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kPlanWarp = 10;
-constexpr int NS = 4;                          // K/V ring slots
 constexpr uint32_t kSub = BM * 64 * 2;         // [128][64] bf16, 128B-swizzled
-constexpr uint32_t kTileB = 2 * kSub;          // [128][128] bf16 = 32 KB
-constexpr uint32_t OFF_Q = 0;                  // two query tiles
-constexpr uint32_t OFF_RING = 2 * kTileB;
-constexpr uint32_t OFF_ML = OFF_RING + NS * kTileB;      // [2][2][2][128] floats
-constexpr uint32_t OFF_BAR = OFF_ML + 2 * 2 * 2 * BM * 4;
 constexpr int NSEG = 4;                        // segments handed over at a time
-constexpr uint32_t OFF_SEG = OFF_BAR + 256;
-constexpr uint32_t OFF_PAR = OFF_SEG + NSEG * 64;        // a sequence's parents
-constexpr int NODES = 2 * BM;                  // most nodes of a unit
 constexpr int NTT = 2;                         // tree tiles whose masks are handed over
-constexpr uint32_t kNodeWords = NODES * (1 + 4 * NTT);   // depth and masks of a unit's nodes
-constexpr uint32_t OFF_NODE = OFF_PAR + kMaxTreeNodes * 4;
-constexpr uint32_t kSmemBytes = OFF_NODE + 2 * kNodeWords * 4 + 1024;  // + alignment slack
-static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
+
+// Shared memory.  A launch without pairs needs one query tile and so has room
+// for a fifth pair of 64-column K/V slots.
+template <int D, bool PAIR>
+struct Smem {
+  static constexpr int NSUB = D / 64;
+  static constexpr uint32_t kTile = NSUB * kSub;             // a query, key or value tile
+  static constexpr int NQ = PAIR ? 2 : 1;                    // query tiles
+  static constexpr int NS = (PAIR ? 8 : 10) / NSUB;          // K/V ring slots
+  static constexpr int NODES = PAIR ? 2 * BM : BM;           // most nodes of a unit
+  static constexpr uint32_t kNodeWords = NODES * (1 + 4 * NTT);  // depths and masks
+  static constexpr uint32_t OFF_Q = 0;
+  static constexpr uint32_t OFF_RING = NQ * kTile;
+  static constexpr uint32_t OFF_ML = OFF_RING + NS * kTile;  // [2][2][2][128] floats
+  static constexpr uint32_t OFF_BAR = OFF_ML + 2 * 2 * 2 * BM * 4;
+  static constexpr uint32_t OFF_SEG = OFF_BAR + 512;
+  static constexpr uint32_t OFF_PAR = OFF_SEG + NSEG * 64;   // a sequence's parents
+  static constexpr uint32_t OFF_NODE = OFF_PAR + kMaxTreeNodes * 4;
+  static constexpr uint32_t kBytes = OFF_NODE + 2 * kNodeWords * 4 + 1024;  // + alignment
+  static_assert(kBytes <= 232448, "shared memory of a CTA");
+  // barriers
+  static constexpr int B_FULL = 0;                 // NS slots landed
+  static constexpr int B_EMPTY = B_FULL + NS;      // and free
+  static constexpr int B_QF = B_EMPTY + NS;        // NQ query tiles landed
+  static constexpr int B_QE = B_QF + NQ;           // and free
+  static constexpr int B_S = B_QE + NQ;            // 2 halves: S ready
+  static constexpr int B_P = B_S + 2;              // 2 halves: P written
+  static constexpr int B_O = B_P + 2;              // 2 halves: the segment's last PV done
+  static constexpr int B_F = B_O + 2;              // the segment's O read out
+  static constexpr int B_ML = B_F + 1;             // split: both halves' (m, l) in smem
+  static constexpr int B_FIN = B_ML + 1;
+  static constexpr int B_SEG = B_FIN + 1;          // NSEG segments handed over
+  static constexpr int B_NODE = B_SEG + NSEG;      // 2 segments' nodes handed over
+  static constexpr int B_NFREE = B_NODE + 2;       // and read by every row
+  static constexpr int NBAR = B_NFREE + 2;
+  static_assert(8 * NBAR + 16 <= 512, "barriers");
+};
 
 __host__ __device__ constexpr uint32_t tm_s(int half) { return half ? 128u : 0u; }
 __host__ __device__ constexpr uint32_t tm_o(int half) { return half ? 384u : 256u; }
 constexpr uint32_t TM_COLS = 512;
 constexpr float kRescaleThreshold = 8.0f;      // log2 units
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
-// A CTA's least share of the list: one key tile for each half.
-constexpr int kMinTiles = 2;
 
-constexpr int B_QF = 0;                        // 2 query tiles loaded
-constexpr int B_QE = 2;                        // 2 query tiles free
-constexpr int B_FULL = 4;                      // NS slots
-constexpr int B_EMPTY = B_FULL + NS;           // NS slots
-constexpr int B_S = B_EMPTY + NS;              // 2 halves: S ready
-constexpr int B_P = B_S + 2;                   // 2 halves: P written
-constexpr int B_O = B_P + 2;                   // 2 halves: the segment's last PV done
-constexpr int B_F = B_O + 2;                   // the segment's O read out
-constexpr int B_ML = B_F + 1;                  // split: both halves' (m, l) in smem
-constexpr int B_FIN = B_ML + 1;
-constexpr int B_SEG = B_FIN + 1;               // NSEG segments handed over
-constexpr int B_NODE = B_SEG + NSEG;           // 2 segments' nodes handed over
-constexpr int B_NFREE = B_NODE + 2;            // and read by every row
-constexpr int NBAR = B_NFREE + 2;
-static_assert(8 * NBAR + 16 <= 256, "barriers");
+// Cost of a key tile in the cut of the work list, in loads of 16 keys: what it
+// reads, but at least what its matrix products and softmax take meanwhile; a
+// unit's first tile carries the unit's start and end too.  A CTA's share is
+// never below kMinCost, so that it holds a tile at least (and no join is made
+// for less work than it costs).
+// A pair of query tiles takes as long for few keys as for many.
+constexpr int kTileCost = 8, kTileLeast = 4, kPairLeast = 8, kUnitCost = 8, kMinCost = 40;
+static_assert(kMinCost >= kTileCost + kUnitCost, "a share holds a tile");
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x,
                                             int32_t y, int32_t z, uint32_t bar) {
@@ -103,27 +118,110 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// 2-D load with an L2 policy: cache tiles of a large cache are read once a
+// launch, evict-first so that they do not displace the partials; the tree's
+// and a small cache's (read again by the next launch) are normal.
+__device__ __forceinline__ void tma_load_2d_pol(uint32_t dst, const CUtensorMap* map, int32_t x,
+                                                int32_t y, uint32_t bar, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(pol)
+      : "memory");
+}
+__device__ __forceinline__ uint64_t evict_first_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t evict_normal_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
+// Wait for this thread's outstanding TMEM loads; r (the registers of the last
+// one) are in-out operands, so no use of them moves above the wait.
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld8_sync(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
+// 2^k of a whole number k <= 0 held as a float; 0 below 2^-126.
+__device__ __forceinline__ float power_of_two(float k) {
+  return k < -126.f ? 0.f : __int_as_float((127 + (int)k) << 23);
+}
+
 // The shape of a launch.
 struct Shape {
   int npt;      // nodes of a query tile
   int pair;     // 1: units of two query tiles
   int G;        // query heads of a KV head
+  int evict;    // 1: cache tiles are loaded evict-first
+  int joins;    // units of the launch, or its CTAs where those are fewer
 };
 
-// What a sequence adds to the work list: units of `tl` key tiles each.
+// Cost of `keys` keys in tiles.
+__device__ __forceinline__ int keys_cost(int keys, int least) {
+  const int rest = keys % BN;
+  return keys / BN * kTileCost + (rest ? max(least, (rest + 15) / 16) : 0);
+}
+
+// What a sequence adds to the work list: `units` units of `tl` key tiles, that
+// cost `cost` each.
 struct Seq {
-  int cnt, m_b;
+  int cnt, m_b, ring;
   int64_t t_b;
-  int np, nr, tl, units;
-  __device__ void load(const CacheView& cv, const TreeArgs& a, const Shape& sh, int b) {
-    cnt = live_nodes(a.counts, b, a.nodes, cv.err);
+  int np, nr, tl, cost, units, least;
+  __device__ __noinline__ void load(const CacheView& cv, const TreeArgs& a, const Shape& sh,
+                                   int b) {
+    const int c = a.counts ? a.counts[b] : a.nodes;
     m_b = cv.m_dev[b];
     t_b = cv.t_dev[(size_t)b * cv.H];
+    if (a.counts && blockIdx.x == 0 && (c < 0 || c > a.nodes)) flag_error(cv.err, kErrBadTree);
+    cnt = min(max(c, 0), a.nodes);
+    ring = (int)min(min(cv.n, t_b), (int64_t)1 << 30);
     np = (m_b + BN - 1) / BN;
-    nr = (int)((min(cv.n, t_b) + BN - 1) / BN);
+    nr = (ring + BN - 1) / BN;
     tl = np + nr + (cnt + BN - 1) / BN;
+    least = sh.pair ? kPairLeast : kTileLeast;
+    cost = before(tl);
     const int per = sh.npt << sh.pair;
     units = (cnt + per - 1) / per * cv.Hkv;
+  }
+  // Cost of a unit's tiles before tile j.
+  __device__ __noinline__ int before(int j) const {
+    const int jp = min(j, np), jr = min(max(j - np, 0), nr), jt = max(j - np - nr, 0);
+    return keys_cost(min(m_b, jp * BN), least) + keys_cost(min(ring, jr * BN), least) +
+           keys_cost(min(cnt, jt * BN), least) + (j > 0 ? kUnitCost : 0);
+  }
+  // The first tile that begins at or after cost x of a unit (tl: none).
+  __device__ __noinline__ int at(int x) const {
+    if (x <= 0) return 0;
+    int j = min(max((x - kUnitCost + kTileCost - 1) / kTileCost, 1), tl);
+    while (j > 1 && before(j - 1) >= x) --j;
+    while (j < tl && before(j) < x) ++j;
+    return j;
   }
 };
 
@@ -137,6 +235,7 @@ struct Segment {
   int m_b, ring;          // prefix rows, filled ring slots
   int newest, age;        // ring slot of output t_b - 1, and t_b - 1 (clamped)
   int split, whole, begins;
+  int tiles;              // the CTA's key tiles before the segment
   // Kind of key tile j, its index among its kind, and its keys.
   __device__ void tile(int j, int& kind, int& i, int& keys) const {
     if (j < np) {
@@ -183,7 +282,7 @@ __device__ __forceinline__ float* partial_at(void* ws, int grid, int slot, int D
          (size_t)slot * partial_floats(D, pair);
 }
 
-template <int D>
+template <int D, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmKc,
@@ -195,28 +294,31 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmKt16,
                       const __grid_constant__ CUtensorMap tmVt16, CacheView cv, TreeArgs a,
                       Shape sh, uint64_t wait_ns) {
+  using SM = Smem<D, PAIR>;
+  constexpr int NSUB = SM::NSUB, NS = SM::NS, NQ = SM::NQ, NODES = SM::NODES;
+  constexpr uint32_t kTile = SM::kTile;
+  constexpr int NBAR = SM::NBAR;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
-  const uint32_t bar0 = sb + OFF_BAR;
+  const uint32_t bar0 = sb + SM::OFF_BAR;
   auto bar = [&](int k) { return bar0 + 8u * (uint32_t)k; };
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_BAR + 8 * NBAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::OFF_BAR + 8 * NBAR);
   volatile int* abort_flag =
-      reinterpret_cast<volatile int*>(smem + OFF_BAR + 8 * NBAR + 4);
-  volatile int* never = reinterpret_cast<volatile int*>(smem + OFF_BAR + 8 * NBAR + 8);
-  const Segment* segs = reinterpret_cast<const Segment*>(smem + OFF_SEG);
-  int32_t* nodes_smem = reinterpret_cast<int32_t*>(smem + OFF_NODE);
-  constexpr int NSUB = D / 64;
+      reinterpret_cast<volatile int*>(smem + SM::OFF_BAR + 8 * NBAR + 4);
+  volatile int* never = reinterpret_cast<volatile int*>(smem + SM::OFF_BAR + 8 * NBAR + 8);
+  const Segment* segs = reinterpret_cast<const Segment*>(smem + SM::OFF_SEG);
+  int32_t* nodes_smem = reinterpret_cast<int32_t*>(smem + SM::OFF_NODE);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x, grid = gridDim.x;
 
   if (threadIdx.x == 0) {
     for (int k = 0; k < NBAR; ++k)
-      mbar_init(bar(k), k == B_P || k == B_P + 1
+      mbar_init(bar(k), k == SM::B_P || k == SM::B_P + 1
                            ? 128u
-                           : (k == B_F || k == B_ML || k >= B_NFREE ? 256u : 1u));
+                           : (k == SM::B_F || k == SM::B_ML || k >= SM::B_NFREE ? 256u : 1u));
     *abort_flag = 0;
     *never = 0;
     fence_mbar_init();
@@ -234,7 +336,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
   griddep_launch_dependents();
   // Segment k, from the planner; false: the wait gave up.
   auto segment = [&](int k, Segment& w) {
-    if (!mbar_wait(bar(B_SEG + k % NSEG), (k / NSEG) & 1, abort_flag, wait_ns)) return false;
+    if (!mbar_wait(bar(SM::B_SEG + k % NSEG), (k / NSEG) & 1, abort_flag, wait_ns)) return false;
     w = segs[k % NSEG];
     return true;
   };
@@ -242,186 +344,196 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      prefetch_tmap(&tmQ);
       prefetch_tmap(&tmKc);
       prefetch_tmap(&tmVc);
       prefetch_tmap(&tmKt16);
       prefetch_tmap(&tmVt16);
       prefetch_tmap(&tmKc16);
       prefetch_tmap(&tmVc16);
-      uint32_t gi = 0, qi = 0;                   // K/V loads and query tiles issued
+      const uint64_t normal = evict_normal_policy();
+      const uint64_t stream = sh.evict ? evict_first_policy() : normal;
+      uint32_t gi = 0;                           // loads issued
       bool ok = true;
-      const uint32_t qbytes = (uint32_t)NSUB * sh.npt * sh.G * 128u;
       Segment w;
       for (int k = 0; ok && segment(k, w) && w.j1 > 0; ++k) {
-        const int nq = w.split ? 1 : 2;
-        for (int x = 0; ok && x < nq; ++x, ++qi) {
-          const uint32_t s = qi & 1;
-          if (qi >= 2 && !mbar_wait(bar(B_QE + s), ((qi >> 1) - 1) & 1, abort_flag, wait_ns)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(bar(B_QF + s), qbytes);
-#pragma unroll
-          for (int c = 0; c < NSUB; ++c)
-            tma_load_3d(sb + OFF_Q + s * kTileB + c * kSub, &tmQ, c * 64, w.kvh * sh.G,
-                        w.b * a.nodes + w.node0 + x * sh.npt, bar(B_QF + s));
-        }
         const int64_t slab0 = ((int64_t)w.b * cv.Hkv + w.kvh) * cv.slab_rows;
         for (int j = w.j0; ok && j < w.j1; ++j) {
           int kind, i, keys;
           w.tile(j, kind, i, keys);
           const int boxes = (keys + 15) / 16;
+          const uint64_t pol = kind == kTree ? normal : stream;
           const int x0 = kind == kTree ? w.kvh * D : 0;
           const int y0 = kind == kTree
                              ? w.b * a.nodes + i * BN
                              : (int)(slab0 + (kind == kRing ? cv.m_cap : 0) + (int64_t)i * BN);
+#pragma unroll 1
           for (int isv = 0; isv < 2; ++isv, ++gi) {
             const uint32_t s = gi % NS;
             if (gi >= (uint32_t)NS &&
-                !mbar_wait(bar(B_EMPTY + s), ((gi / NS) - 1) & 1, abort_flag, wait_ns)) {
+                !mbar_wait(bar(SM::B_EMPTY + s), ((gi / NS) - 1) & 1, abort_flag, wait_ns)) {
               ok = false;
               break;
             }
-            const uint32_t dst = sb + OFF_RING + s * kTileB;
-            mbar_arrive_expect_tx(bar(B_FULL + s), (uint32_t)NSUB * boxes * 2048u);
-            if (boxes == BN / 16) {
-              const CUtensorMap* map = kind == kTree ? (isv ? &tmVt : &tmKt)
-                                                     : (isv ? &tmVc : &tmKc);
+            const uint32_t dst = sb + SM::OFF_RING + s * kTile;
+            mbar_arrive_expect_tx(bar(SM::B_FULL + s), (uint32_t)NSUB * boxes * 2048u);
+            // one box of 128 keys, or one for every 16
+            const bool whole = boxes == BN / 16;
+            const CUtensorMap* map =
+                whole ? (kind == kTree ? (isv ? &tmVt : &tmKt) : (isv ? &tmVc : &tmKc))
+                      : (kind == kTree ? (isv ? &tmVt16 : &tmKt16) : (isv ? &tmVc16 : &tmKc16));
+            const int parts = whole ? 1 : boxes;
+#pragma unroll 1
+            for (int r = 0; r < parts; ++r)
 #pragma unroll
               for (int c = 0; c < NSUB; ++c)
-                tma_load_2d(dst + c * kSub, map, x0 + c * 64, y0, bar(B_FULL + s));
-            } else {
-              const CUtensorMap* map = kind == kTree ? (isv ? &tmVt16 : &tmKt16)
-                                                     : (isv ? &tmVc16 : &tmKc16);
-              for (int r = 0; r < boxes; ++r)
-#pragma unroll
-                for (int c = 0; c < NSUB; ++c)
-                  tma_load_2d(dst + c * kSub + r * 2048, map, x0 + c * 64, y0 + 16 * r,
-                              bar(B_FULL + s));
-            }
+                tma_load_2d_pol(dst + c * kSub + r * 2048, map, x0 + c * 64, y0 + 16 * r,
+                                bar(SM::B_FULL + s), pol);
           }
         }
       }
       // Drain: every copy issued has landed before the CTA may exit.
-      for (uint32_t k = qi > 2 ? qi - 2 : 0; k < qi; ++k)
-        mbar_wait(bar(B_QF + (k & 1)), (k >> 1) & 1, never, kWaitLimitNs);
       for (uint32_t k = gi > (uint32_t)NS ? gi - NS : 0; k < gi; ++k)
-        mbar_wait(bar(B_FULL + k % NS), (k / NS) & 1, never, kWaitLimitNs);
+        mbar_wait(bar(SM::B_FULL + k % NS), (k / NS) & 1, never, kWaitLimitNs);
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
-    // The whole warp walks; one lane issues.  qc runs two steps ahead of pc.
-    constexpr uint32_t idesc_qk = idesc_bf16(BM, BN, false);
-    constexpr uint32_t idesc_pv = idesc_bf16(BM, D, true);
-    auto wait = [&](int k, uint32_t phase) {
-      return __all_sync(0xffffffffu, mbar_wait(bar(k), phase & 1, abort_flag, wait_ns)) != 0;
-    };
-    struct Cursor {
-      Segment w;
-      int k;                  // segment
-      int j, sub;             // key tile; in a pair unit the first or second half's turn
-      uint32_t step, load, q; // steps, key tiles and query tiles before
-      bool more;
-    };
-    auto enter = [&](Cursor& c) {
-      const bool got = segment(c.k, c.w);
-      c.more = __all_sync(0xffffffffu, got) && c.w.j1 > 0;
-      c.j = c.w.j0;
-      c.sub = 0;
-    };
-    auto advance = [&](Cursor& c) {
-      ++c.step;
-      if (!c.w.split && c.sub == 0) {
-        c.sub = 1;
-        return;
-      }
-      c.sub = 0;
-      ++c.load;
-      if (++c.j == c.w.j1) {
-        c.q += c.w.split ? 1 : 2;
+    // One lane issues; QK runs two steps ahead of PV.
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = idesc_bf16(BM, BN, false);
+      constexpr uint32_t idesc_pv = idesc_bf16(BM, D, true);
+      auto wait = [&](int k, uint32_t phase) {
+        return mbar_wait(bar(k), phase & 1, abort_flag, wait_ns);
+      };
+      // Load 2 t is the key tile of the CTA's tile t, load 2 t + 1 its value
+      // tile: `slot` and `phase` of the one a cursor is at.
+      struct Cursor {
+        int k = 0, left = 0;             // segment, its tiles left
+        int split = 1, sub = 0;          // in a pair unit the first or second half's turn
+        uint32_t step = 0, slot, phase = 0, q = 0;   // q: query tiles before
+      };
+      auto enter = [&](Cursor& c) {
+        if (!wait(SM::B_SEG + c.k % NSEG, c.k / NSEG)) return false;
+        const Segment& w = segs[c.k % NSEG];
+        c.left = w.j1 - w.j0;
+        c.split = w.split;
+        return w.j1 > 0;
+      };
+      auto advance = [&](Cursor& c) {    // false: no more steps
+        ++c.step;
+        if (!c.split && c.sub == 0) {
+          c.sub = 1;
+          return true;
+        }
+        c.sub = 0;
+        c.slot += 2;
+        if (c.slot >= (uint32_t)NS) {
+          c.slot -= NS;
+          c.phase ^= 1;
+        }
+        if (--c.left > 0) return true;
+        c.q += c.split ? 1 : 2;
         ++c.k;
-        enter(c);
-      }
-    };
-    Cursor qc = {}, pc = {};
-    enter(qc);
-    enter(pc);
-    // S = Q K^T of qc's step, then on to the next.
-    auto qk = [&]() {
-      const uint32_t half = qc.step & 1;
-      const uint32_t qt = qc.w.split ? qc.q : qc.q + half;
-      const uint32_t ki = 2 * qc.load;
-      if (!wait(B_QF + (qt & 1), qt >> 1) || !wait(B_FULL + ki % NS, ki / NS)) return false;
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t kb = sb + OFF_RING + (ki % NS) * kTileB;
-        const uint32_t qb = sb + OFF_Q + (qt & 1) * kTileB;
+        return enter(c);
+      };
+      Cursor qc, pc;
+      qc.slot = 0;
+      pc.slot = 1;
+      bool qmore = enter(qc), pmore = enter(pc);
+      // S = Q K^T of qc's step, then on to the next.
+      auto qk = [&]() {
+        const uint32_t half = qc.step & 1;
+        const uint32_t qt = qc.split ? qc.q : qc.q + half;
+        if (!wait(SM::B_QF + qt % NQ, qt / NQ) || !wait(SM::B_FULL + qc.slot, qc.phase))
+          return false;
+        tc_fence_after();
+        const uint32_t kb = sb + SM::OFF_RING + qc.slot * kTile;
+        const uint32_t qb = sb + SM::OFF_Q + (qt % NQ) * kTile;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k >> 2) * kSub + (k & 3) * 32;
           mma_bf16_ss(tmem + tm_s(half), desc_sw128(qb + off, 16, 1024),
                       desc_sw128(kb + off, 16, 1024), idesc_qk, k > 0);
         }
-        mma_commit(bar(B_S + half));
-        if (qc.w.split || qc.sub == 1) mma_commit(bar(B_EMPTY + ki % NS));
-        if (qc.j + 1 == qc.w.j1 && (qc.w.split || qc.sub == 1)) {
-          mma_commit(bar(B_QE + (qc.q & 1)));
-          if (!qc.w.split) mma_commit(bar(B_QE + ((qc.q + 1) & 1)));
+        mma_commit(bar(SM::B_S + half));
+        if (qc.split || qc.sub == 1) {
+          mma_commit(bar(SM::B_EMPTY + qc.slot));
+          if (qc.left == 1) {
+            mma_commit(bar(SM::B_QE + qc.q % NQ));
+            if (!qc.split) mma_commit(bar(SM::B_QE + (qc.q + 1) % NQ));
+          }
         }
-      }
-      __syncwarp();
-      advance(qc);
-      return true;
-    };
-    bool ok = true;
-    for (int x = 0; x < 2 && ok && qc.more; ++x) ok = qk();
-    while (ok && pc.more) {
-      const uint32_t half = pc.step & 1;
-      const uint32_t vi = 2 * pc.load + 1;
-      int kind, i, keys;
-      pc.w.tile(pc.j, kind, i, keys);
-      // The half's first and last step of the segment.
-      const int span = pc.w.split ? 2 : 1;
-      const bool first = pc.j - pc.w.j0 < span, last = pc.j + span >= pc.w.j1;
-      if (first && pc.k > 0 && !wait(B_F, pc.k - 1)) break;
-      if (!wait(B_P + half, pc.step >> 1) || !wait(B_FULL + vi % NS, vi / NS)) break;
-      const uint32_t vb = sb + OFF_RING + (vi % NS) * kTileB;
-      const int ks = (keys + 15) / 16;
-      if (kind == kTree && keys % 16 != 0 && (pc.w.split || pc.sub == 0)) {
-        // value rows keys .. 16 ks - 1: nodes past the count
-        const int rows = 16 * ks - keys;
-        for (int x = lane; x < rows * 8 * NSUB; x += 32) {
-          const int c = x / (rows * 8), y = x % (rows * 8);
-          *reinterpret_cast<uint4*>(smem + (vb - sb) + c * kSub + keys * 128 + y * 16) =
-              make_uint4(0, 0, 0, 0);
+        qmore = advance(qc);
+        return true;
+      };
+      bool ok = true;
+      int tiles = pc.left;                       // of pc's segment
+#pragma unroll 1
+      for (int lead = 2; ok && pmore;) {
+        if (lead > 0) {                          // the first two steps
+          --lead;
+          if (qmore) ok = qk();
+          continue;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      tc_fence_after();
-      if (lane == 0) {
-        for (int k = 0; k < ks; ++k)
+        const uint32_t half = pc.step & 1;
+        const Segment& w = segs[pc.k % NSEG];
+        const int j = w.j1 - pc.left;
+        // The half's first and last step of the segment.
+        const int span = pc.split ? 2 : 1;
+        const bool first = tiles - pc.left < span, last = pc.left <= span;
+        if (first && pc.k > 0 && !wait(SM::B_F, pc.k - 1)) break;
+        if (!wait(SM::B_P + half, pc.step >> 1) || !wait(SM::B_FULL + pc.slot, pc.phase)) break;
+        const uint32_t vb = sb + SM::OFF_RING + pc.slot * kTile;
+        int ks = BN / 16;
+        if (j + 1 >= w.np) {
+          int kind, i, keys;
+          w.tile(j, kind, i, keys);
+          ks = (keys + 15) / 16;
+        }
+        tc_fence_after();
+        auto pv = [&](int k) {
           mma_bf16_ts(tmem + tm_o(half), tmem + tm_s(half) + k * 8,
                       desc_sw128(vb + k * 2048, kSub, 1024), idesc_pv,
                       (!first || k > 0) ? 1u : 0u);
-        if (pc.w.split || pc.sub == 1) mma_commit(bar(B_EMPTY + vi % NS));
-        if (last) mma_commit(bar(B_O + half));
+        };
+#pragma unroll
+        for (int k = 0; k < BN / 16; ++k)
+          if (k < ks) pv(k);
+        if (pc.split || pc.sub == 1) mma_commit(bar(SM::B_EMPTY + pc.slot));
+        if (last) mma_commit(bar(SM::B_O + half));
+        const int at = pc.k;
+        pmore = advance(pc);
+        if (pc.k != at) tiles = pc.left;
+        lead = 1;
       }
-      __syncwarp();
-      advance(pc);
-      if (qc.more) ok = qk();
-    }
-    // Drain: all MMAs of this CTA have finished before TMEM is freed.
-    if (lane == 0) {
-      mma_commit(bar(B_FIN));
-      mbar_wait(bar(B_FIN), 0, never, kWaitLimitNs);
+      // Drain: all MMAs of this CTA have finished before TMEM is freed.
+      mma_commit(bar(SM::B_FIN));
+      mbar_wait(bar(SM::B_FIN), 0, never, kWaitLimitNs);
     }
     __syncwarp();
   } else if (warp == kPlanWarp) {
     // ------------------------------------------------------------ planner
-    Segment* out = reinterpret_cast<Segment*>(smem + OFF_SEG);
-    int32_t* par = reinterpret_cast<int32_t*>(smem + OFF_PAR);
+    Segment* out = reinterpret_cast<Segment*>(smem + SM::OFF_SEG);
+    int32_t* par = reinterpret_cast<int32_t*>(smem + SM::OFF_PAR);
+    if (lane == 0) prefetch_tmap(&tmQ);
+    int qi = 0, tiles = 0;                       // query tiles requested, key tiles planned
+    // Requests a segment's query tiles once their buffers are free.
+    auto queries = [&](const Segment& w) {
+      for (int x = 0; x < (w.split ? 1 : 2); ++x, ++qi) {
+        const int s = qi % NQ;
+        if (qi >= NQ && !__all_sync(0xffffffffu, mbar_wait(bar(SM::B_QE + s), (qi / NQ - 1) & 1,
+                                                           abort_flag, wait_ns)))
+          return false;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(SM::B_QF + s), (uint32_t)NSUB * sh.npt * sh.G * 128u);
+#pragma unroll
+          for (int c = 0; c < NSUB; ++c)
+            tma_load_3d(sb + SM::OFF_Q + s * kTile + c * kSub, &tmQ, c * 64, w.kvh * sh.G,
+                        w.b * a.nodes + w.node0 + x * sh.npt, bar(SM::B_QF + s));
+        }
+        __syncwarp();
+      }
+      return true;
+    };
     // The list's length, and the sequences of each lane in it.
     const int per = (cv.B + 31) / 32;
     const int b_lo = min(lane * per, cv.B), b_hi = min(b_lo + per, cv.B);
@@ -429,7 +541,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     int mine = 0;
     for (int b = b_lo; b < b_hi; ++b) {
       sq.load(cv, a, sh, b);
-      mine += sq.tl * sq.units;
+      mine += sq.cost * sq.units;
     }
     int inc = mine;
 #pragma unroll
@@ -438,89 +550,112 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       if (lane >= off) inc += x;
     }
     const int total = __shfl_sync(0xffffffffu, inc, 31);
-    // Range c: `each` tiles, one more for the first `rem` CTAs.
-    const int ctas = min(grid, max(1, total / kMinTiles));
+    // CTA c takes the tiles that begin in [from(c), from(c + 1)).
+    const int ctas = min(grid, max(1, total / kMinCost));
     const int each = total / ctas, rem = total - each * ctas;
-    const int g0 = cta * each + min(cta, rem);
-    int left = cta < ctas ? each + (cta < rem ? 1 : 0) : 0;
+    auto from = [&](int c) { return c * each + min(c, rem); };
     JoinDesc jd = {0, 0, 0, -1, 0, {0, 0, 0}};
     int k = 0;
-    if (left > 0) {
-      // The sequence and unit that tile g0 is in.
-      int b = 0, off = 0;
-      const bool here = inc - mine <= g0 && g0 < inc;
+    if (cta < ctas && total > 0) {
+      const int x0 = from(cta), x1 = from(cta + 1);
+      // The sequence that x0 is in, and where it begins.
+      int b = 0, base = 0;
+      const bool here = inc - mine <= x0 && x0 < inc;
       if (here) {
-        int at = inc - mine;
-        for (b = b_lo; b < b_hi; ++b) {
-          sq.load(cv, a, sh, b);
-          if (g0 < at + sq.tl * sq.units) break;
-          at += sq.tl * sq.units;
+        base = inc - mine;
+        b = b_lo;
+        if (per > 1) {
+          for (;; ++b) {
+            sq.load(cv, a, sh, b);
+            if (x0 < base + sq.cost * sq.units) break;
+            base += sq.cost * sq.units;
+          }
         }
-        off = g0 - at;
       }
       const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
       b = __shfl_sync(0xffffffffu, b, src);
-      off = __shfl_sync(0xffffffffu, off, src);
+      base = __shfl_sync(0xffffffffu, base, src);
       sq.load(cv, a, sh, b);
-      int u = off / sq.tl, j0 = off - u * sq.tl, g = g0, par_b = -1;
+      int u = (x0 - base) / sq.cost;
+      int ubase = base + u * sq.cost;            // where unit u begins
+      int j0 = sq.at(x0 - ubase), par_b = -1;
       const int unit_nodes = sh.npt << sh.pair;
       const int n = (int)min(cv.n, (int64_t)1 << 30);
-      for (;;) {
+      for (bool next_unit = j0 == sq.tl;; next_unit = true) {
+        if (next_unit) {
+          ubase += sq.cost;
+          j0 = 0;
+          if (++u == sq.units) {
+            u = 0;
+            sq.units = 0;
+            while (sq.units == 0 && b + 1 < cv.B) sq.load(cv, a, sh, ++b);
+            if (sq.units == 0) break;            // the list's end
+          }
+        }
+        if (ubase + sq.before(j0) >= x1) break;  // a later CTA's
         Segment w;
         w.b = b;
         w.kvh = u % cv.Hkv;
         w.node0 = u / cv.Hkv * unit_nodes;
         w.cnt = sq.cnt;
         w.j0 = j0;
-        w.j1 = min(sq.tl, j0 + left);
+        w.j1 = sq.at(x1 - ubase);
         w.np = sq.np;
         w.nr = sq.nr;
         w.m_b = sq.m_b;
-        w.ring = (int)min(cv.n, sq.t_b);
+        w.ring = sq.ring;
         w.age = (int)min(sq.t_b - 1, (int64_t)1 << 30);
-        w.newest = sq.t_b > cv.n ? (int)((sq.t_b - 1) % cv.n) : (int)sq.t_b - 1;
+        w.newest = sq.t_b <= cv.n ? (int)sq.t_b - 1
+                   : sq.t_b < (int64_t)1 << 31
+                       ? (int)((uint32_t)(sq.t_b - 1) % (uint32_t)cv.n)
+                       : (int)((sq.t_b - 1) % cv.n);
         // A unit without rows for a second query tile is split like all
         // others of a launch without pairs.
-        w.split = !sh.pair || w.node0 + sh.npt >= sq.cnt;
+        w.split = !PAIR || w.node0 + sh.npt >= sq.cnt;
         w.whole = j0 == 0 && w.j1 == sq.tl;
         w.begins = j0 == 0;
+        w.tiles = tiles;
+        tiles += w.j1 - j0;
         // Slot k % NSEG was segment k - 4's: all roles had left it when the
         // nodes of segment k - 1 were handed over (which waited until those
         // of segment k - 3 had been read).
         if (lane == 0) {
           out[k % NSEG] = w;
-          mbar_arrive(bar(B_SEG + k % NSEG));
+          mbar_arrive(bar(SM::B_SEG + k % NSEG));
         }
-        if (j0 == 0 && !w.whole) {       // begun here, ended by a later CTA
-          const int x = g + sq.tl - 1;   // the unit's last tile
-          const int cut = rem * (each + 1);
-          jd = {b, w.node0, w.kvh, x < cut ? x / (each + 1) : rem + (x - cut) / each,
-                sq.cnt, {0, 0, 0}};
+        // The first segment's queries come at once, a later one's after its
+        // nodes: their buffers are free later than those.
+        if (k == 0) queries(w);
+        if (j0 == 0 && !w.whole) {       // begun here, ended by the CTA of its last tile
+          const int x = ubase + sq.before(sq.tl - 1), cut = rem * (each + 1);
+          jd = {b, w.node0, w.kvh,
+                min(ctas - 1, x < cut ? x / (each + 1) : rem + (x - cut) / each), sq.cnt,
+                {0, 0, 0}};
         }
-        // Depths and ancestors of the unit's nodes.
-        if (par_b != b) {
+        // Depths and ancestors of the unit's nodes, where the segment's ring
+        // and tree tiles ask for them.
+        const bool ask = w.j1 > sq.np;
+        if (ask && par_b != b) {
           __syncwarp();
           for (int i = lane; i < sq.cnt; i += 32) par[i] = a.parents[(size_t)b * a.nodes + i];
           par_b = b;
           __syncwarp();
         }
         if (k >= 2 &&
-            !__all_sync(0xffffffffu, mbar_wait(bar(B_NFREE + (k & 1)), ((k >> 1) - 1) & 1,
+            !__all_sync(0xffffffffu, mbar_wait(bar(SM::B_NFREE + (k & 1)), ((k >> 1) - 1) & 1,
                                                abort_flag, wait_ns)))
           break;
-        int32_t* nd = nodes_smem + (k & 1) * kNodeWords;
-        const int nn = min(unit_nodes, sq.cnt - w.node0);
+        int32_t* nd = nodes_smem + (k & 1) * SM::kNodeWords;
+        const int nn = ask ? min(unit_nodes, sq.cnt - w.node0) : 0;
         for (int i = lane; i < nn; i += 32) {
-          uint32_t m[4 * NTT];
+          uint64_t m[2 * NTT];
 #pragma unroll
-          for (int e = 0; e < 4 * NTT; ++e) m[e] = 0u;
+          for (int e = 0; e < 2 * NTT; ++e) m[e] = 0u;
           int up = 0;
           for (int x = w.node0 + i;;) {
-            if (up < n) {
+            const uint64_t bit = up < n ? (uint64_t)1 << (x & 63) : 0;
 #pragma unroll
-              for (int e = 0; e < 4 * NTT; ++e)
-                if (x >> 5 == e) m[e] |= 1u << (x & 31);
-            }
+            for (int e = 0; e < 2 * NTT; ++e) m[e] |= x >> 6 == e ? bit : 0;
             const int p = par[x];
             if (p < -1 || p >= x) flag_error(cv.err, kErrBadTree);
             if (p < 0 || p >= x) break;
@@ -529,27 +664,22 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
           }
           nd[i] = up;
 #pragma unroll
-          for (int e = 0; e < 4 * NTT; ++e) nd[(1 + e) * NODES + i] = (int32_t)m[e];
+          for (int e = 0; e < 4 * NTT; ++e)
+            nd[(1 + e) * NODES + i] = (int32_t)(uint32_t)(m[e >> 1] >> (e & 1 ? 32 : 0));
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_NODE + (k & 1)));
+        if (lane == 0) mbar_arrive(bar(SM::B_NODE + (k & 1)));
+        if (k > 0 && !queries(w)) break;
         ++k;
-        g += w.j1 - w.j0;
-        left -= w.j1 - w.j0;
-        if (left <= 0) break;
-        j0 = 0;
-        if (++u == sq.units) {
-          u = 0;
-          sq.units = 0;
-          while (sq.units == 0 && b + 1 < cv.B) sq.load(cv, a, sh, ++b);
-          if (sq.units == 0) break;      // (the list ends with the last sequence)
-        }
       }
     }
     if (lane == 0) {
       out[k % NSEG].j1 = 0;              // no more segments
-      mbar_arrive(bar(B_SEG + k % NSEG));
+      mbar_arrive(bar(SM::B_SEG + k % NSEG));
       static_cast<JoinDesc*>(a.ws)[cta] = jd;
+      // Drain: every copy issued has landed before the CTA may exit.
+      for (int x = max(qi - NQ, 0); x < qi; ++x)
+        mbar_wait(bar(SM::B_QF + x % NQ), (x / NQ) & 1, never, kWaitLimitNs);
     }
     __syncwarp();
   } else {
@@ -562,7 +692,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     const uint32_t s_addr = tmem + lane_off + tm_s(half);
     const uint32_t o_addr = tmem + lane_off + tm_o(half);
     const int n = (int)min(cv.n, (int64_t)1 << 30);
-    float* ml = reinterpret_cast<float*>(smem + OFF_ML);
+    float* ml = reinterpret_cast<float*>(smem + SM::OFF_ML);
     uint32_t step = 0, turns = 0;                       // steps before; this half's among them
     uint32_t o_phase0 = 0, o_phase1 = 0, ml_phase = 0;  // segments with steps of each half; split
     bool ok = true;
@@ -575,15 +705,15 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       const int node = w.node0 + ni;
       const bool live = rg < sh.npt && node < w.cnt;
       const bool any = __any_sync(0xffffffffu, live);
-      const int32_t* nd = nodes_smem + (k & 1) * kNodeWords;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(B_NODE + (k & 1)), (k >> 1) & 1, abort_flag,
-                                             wait_ns))) {
-        ok = false;
-        break;
-      }
-      const int depth = live ? nd[ni] : 0;
-      // Ring: slot s is a key iff its age (r0 - s) mod n is at most lim.
-      const int lim = min(w.age, n - 2 - depth);
+      const int32_t* nd = nodes_smem + (k & 1) * SM::kNodeWords;
+      // The planner's depths and masks, first asked for by a ring or tree tile.
+      bool have = false;
+      auto nodes = [&]() {
+        if (!have)
+          have = __all_sync(0xffffffffu, mbar_wait(bar(SM::B_NODE + (k & 1)), (k >> 1) & 1,
+                                                   abort_flag, wait_ns));
+        return have;
+      };
       const int r0 = w.newest;
       float m_run = -INFINITY, l_run = 0.f;
       bool started = false;
@@ -594,151 +724,166 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         const int k0 = i * BN;
         const bool full = kind == kPrefix && keys == BN;
         if (!__all_sync(0xffffffffu,
-                        mbar_wait(bar(B_S + half), turns & 1, abort_flag, wait_ns))) {
+                        mbar_wait(bar(SM::B_S + half), turns & 1, abort_flag, wait_ns))) {
           ok = false;
           break;
         }
         ++turns;
+        if (kind != kPrefix && !nodes()) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
         if (any) {
-          // This row's keys among the tile's columns.
-          uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
           if (!full) {
-            if (kind == kTree) {
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                see[c] = live && i < NTT ? (uint32_t)nd[(1 + 4 * i + c) * NODES + ni] : 0u;
-              if (i >= NTT && live) {
-                // a further tile of a large tree: walk up from the node
-                const int32_t* par = a.parents + (size_t)w.b * a.nodes;
-                int up = 0;
-                for (int x = node; x >= k0 && up < n; ++up) {
-                  if (x < k0 + BN) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                      if ((x - k0) >> 5 == e) see[e] |= 1u << (x & 31);
-                  }
-                  const int p = par[x];
-                  if (p >= x) break;
-                  x = p;
-                }
+            // Scores of columns that are no keys of this row become -inf.  Ring:
+            // slot s is a key iff its age (r0 - s) mod n is at most lim.
+            int a1 = 0, b1 = keys - 1, a2 = 1, b2 = 0;
+            if (kind == kRing) {
+              const int lim = min(w.age, n - 2 - (live ? nd[ni] : 0));
+              if (lim < 0) {
+                b1 = -1;
+              } else if (r0 >= lim) {
+                a1 = r0 - lim - k0;
+                b1 = r0 - k0;
+              } else {
+                b1 = r0 - k0;
+                a2 = r0 - lim + n - k0;
+                b2 = n - 1 - k0;
               }
-            } else {
-              int a1 = 0, b1 = keys - 1, a2 = 1, b2 = 0;
-              if (kind == kRing) {
-                if (lim < 0) {
-                  b1 = -1;
-                } else if (r0 >= lim) {
-                  a1 = r0 - lim - k0;
-                  b1 = r0 - k0;
-                } else {
-                  b1 = r0 - k0;
-                  a2 = r0 - lim + n - k0;
-                  b2 = n - 1 - k0;
-                }
-              }
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                see[c] = range_mask(a1, b1, c) | range_mask(a2, b2, c);
             }
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          uint32_t va[32], vb[32];
-          auto max_chunk = [&](uint32_t* v, int c) {
-            if (!full) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t see = range_mask(a1, b1, c) | range_mask(a2, b2, c);
+              if (kind == kTree) {
+                see = 0u;
+                if (live && i < NTT) {
+                  see = (uint32_t)nd[(1 + 4 * i + c) * NODES + ni];
+                } else if (live) {
+                  // a further tile of a large tree: walk up from the node
+                  const int32_t* par = a.parents + (size_t)w.b * a.nodes;
+                  const int c0 = k0 + 32 * c;
+                  int up = 0;
+                  for (int x = node; x >= c0 && up < n; ++up) {
+                    if (x < c0 + 32) see |= 1u << (x - c0);
+                    const int p = par[x];
+                    if (p >= x) break;
+                    x = p;
+                  }
+                }
+              }
+              uint32_t v[32];
+              tmem_ld32_sync(s_addr + 32 * c, v);
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (!(see[c] >> e & 1u)) v[e] = 0xff800000u;         // -inf
+                if (!(see >> e & 1u)) v[e] = 0xff800000u;
               tmem_st32(s_addr + 32 * c, v);
             }
+            tmem_wait_st();
+          }
+          // One pass over S in chunks of 16 columns, each exponentiated relative
+          // to the running reference and stored as P over columns already read.
+          // Any reference gives the same o and lse, so it stays until a score
+          // exceeds it by more than 2^8 (a row's first key always does); then it
+          // becomes the score rounded up to a whole number of log2 units, so that
+          // what was stored relative to the old one (O, l, this tile's P so far)
+          // is scaled by a power of two, exactly.  A rolled loop: with few warps
+          // at work, straight-line code waits for its instructions (a turn of
+          // one warp 4000-8000 cycles unrolled).
+          const uint64_t sl2x2 = f2_pack(sl2, sl2);
+          uint64_t ps2 = 0;
+          uint32_t va[16], vb[16];
+          auto chunk = [&](const uint32_t* v, int c) {
+            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
+            for (int e = 0; e < 16; e += 4) {
               mx[0] = fmax3(mx[0], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
               mx[1] = fmax3(mx[1], __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
-              mx[2] = fmax3(mx[2], __uint_as_float(v[e + 4]), __uint_as_float(v[e + 5]));
-              mx[3] = fmax3(mx[3], __uint_as_float(v[e + 6]), __uint_as_float(v[e + 7]));
             }
-          };
-          tmem_ld32(s_addr, va);
-          tmem_wait_ld32(va);
-          tmem_ld32(s_addr + 32, vb);
-          max_chunk(va, 0);
-          tmem_wait_ld32(vb);
-          tmem_ld32(s_addr + 64, va);
-          max_chunk(vb, 1);
-          tmem_wait_ld32(va);
-          tmem_ld32(s_addr + 96, vb);
-          max_chunk(va, 2);
-          tmem_wait_ld32(vb);
-          max_chunk(vb, 3);
-          if (!full) tmem_wait_st();
-          const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-          // Lazy rescale.  O_h is stable here: S_h of this step completing
-          // implies that the half's PV before it has.
-          float alpha = 1.f;
-          bool resc = false;
-          const float m_new = fmaxf(m_run, tmax);
-          if (m_run == -INFINITY) {
-            m_run = m_new;
-          } else if (m_new > m_run + kRescaleThreshold) {
-            alpha = ex2(m_run - m_new);
-            m_run = m_new;
-            l_run *= alpha;
-            resc = true;
-          }
-          const float nref = (m_run == -INFINITY) ? 0.f : -m_run;
-          if (started && __any_sync(0xffffffffu, resc)) {
+            const float tmax = fmaxf(mx[0], mx[1]) * sl2;
+            const bool over = tmax > m_run + kRescaleThreshold;    // also where m_run is -inf
+            if (__any_sync(0xffffffffu, over)) {
+              const float m_new = over ? ceilf(tmax) : m_run;
+              const float alpha = power_of_two(over ? m_run - m_new : 0.f);
+              m_run = m_new;
+              l_run *= alpha;
+              ps2 = f2_mul(ps2, f2_pack(alpha, alpha));
+              const __nv_bfloat162 a2 = __float2bfloat162_rn(alpha);
+              tmem_wait_st();
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t ov[32];
-              tmem_ld32_sync(o_addr + c * 32, ov);
+              for (int x = 0; x < c; ++x) {
+                uint32_t p[8];
+                tmem_ld8_sync(s_addr + 8 * x, p);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-              tmem_st32(o_addr + c * 32, ov);
+                for (int e = 0; e < 8; ++e) {
+                  const __nv_bfloat162 y = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&p[e]), a2);
+                  p[e] = *reinterpret_cast<const uint32_t*>(&y);
+                }
+                tmem_st8(s_addr + 8 * x, p);
+              }
+              // O_h is stable here: S_h of this step completing implies that
+              // the half's PV before it has.
+#pragma unroll 1
+              for (int x = 0; started && x < D / 8; ++x) {
+                uint32_t o[8];
+                tmem_ld8_sync(o_addr + 8 * x, o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st8(o_addr + 8 * x, o);
+              }
             }
-          }
-          uint32_t pk[2][32];
-          const uint64_t sl2x2 = f2_pack(sl2, sl2), nref2 = f2_pack(nref, nref);
-          uint64_t ps2[2] = {0, 0};
-          auto exp_chunk = [&](const uint32_t* v, uint32_t* out) {
+            const float nref = (m_run == -INFINITY) ? 0.f : -m_run;
+            const uint64_t nref2 = f2_pack(nref, nref);
+            uint32_t p[8];
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const int e = 2 * c;
+            for (int e = 0; e < 8; ++e) {
               float x0, x1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
                                sl2x2, nref2),
                         x0, x1);
               const float p0 = ex2(x0), p1 = ex2(x1);
-              ps2[c & 1] = f2_add(ps2[c & 1], f2_pack(p0, p1));
-              out[c] = pack_bf16(p0, p1);
+              ps2 = f2_add(ps2, f2_pack(p0, p1));
+              p[e] = pack_bf16(p0, p1);
             }
+            tmem_st8(s_addr + 8 * c, p);
           };
-          tmem_ld32(s_addr, va);
-          tmem_wait_ld32(va);
-          tmem_ld32(s_addr + 32, vb);
-          exp_chunk(va, pk[0]);
-          tmem_wait_ld32(vb);
-          tmem_ld32(s_addr + 64, va);
-          exp_chunk(vb, pk[0] + 16);
-          tmem_wait_ld32(va);
-          tmem_ld32(s_addr + 96, vb);
-          exp_chunk(va, pk[1]);
-          tmem_wait_ld32(vb);
-          exp_chunk(vb, pk[1] + 16);
-          float s0, s1, s2, s3;
-          f2_unpack(ps2[0], s0, s1);
-          f2_unpack(ps2[1], s2, s3);
-          tmem_st32(s_addr, pk[0]);
-          tmem_st32(s_addr + 32, pk[1]);
-          l_run += (s0 + s1) + (s2 + s3);
+          tmem_ld16(s_addr, va);
+          tmem_wait_ld16(va);
+#pragma unroll 1
+          for (int c = 0; c < 8; c += 2) {
+            tmem_ld16(s_addr + 16 * (c + 1), vb);
+            chunk(va, c);
+            tmem_wait_ld16(vb);
+            if (c + 2 < 8) tmem_ld16(s_addr + 16 * (c + 2), va);
+            chunk(vb, c + 1);
+            tmem_wait_ld16(va);
+          }
+          float s0, s1;
+          f2_unpack(ps2, s0, s1);
+          l_run += s0 + s1;
           tmem_wait_st();
           tc_fence_before();
         }
         started = true;
-        mbar_arrive(bar(B_P + half));
+        if (kind == kTree && keys % 16 != 0 && (warp & 3) == 0) {
+          // Value rows keys .. up to the next 16 belong to nodes past the
+          // count, or to the next sequence, and may hold anything: zero.
+          const uint32_t vi = 2u * (uint32_t)(w.tiles + j - w.j0) + 1u;
+          if (__all_sync(0xffffffffu, mbar_wait(bar(SM::B_FULL + vi % NS), (vi / NS) & 1,
+                                                abort_flag, wait_ns))) {
+            const int rows = 16 - keys % 16;
+            uint8_t* v = smem + SM::OFF_RING + (vi % NS) * kTile + keys * 128;
+            for (int x = lane; x < rows * 8 * NSUB; x += 32)
+              *reinterpret_cast<uint4*>(v + x / (rows * 8) * kSub + x % (rows * 8) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+          }
+        }
+        mbar_arrive(bar(SM::B_P + half));
       }
-      mbar_arrive(bar(B_NFREE + (k & 1)));
+      ok = ok && nodes();                                // keeps step with the planner
+      mbar_arrive(bar(SM::B_NFREE + (k & 1)));
       // ------------------------------------------------------- epilogue
       // Steps of this half and of the other in this segment.
       const int own = !split ? nseg : ((step & 1) == (uint32_t)half ? (nseg + 1) / 2 : nseg / 2);
@@ -752,8 +897,8 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         float* own_ml = ml + ((k & 1) * 2 + half) * 2 * BM;
         own_ml[r] = m_run;
         own_ml[BM + r] = l_run;
-        mbar_arrive(bar(B_ML));
-        if (ok && wait_all(B_ML, ml_phase)) {
+        mbar_arrive(bar(SM::B_ML));
+        if (ok && wait_all(SM::B_ML, ml_phase)) {
           const float* o_ml = ml + ((k & 1) * 2 + 1 - half) * 2 * BM;
           const float m1 = o_ml[r], l1 = o_ml[BM + r];
           M = fmaxf(m_run, m1);
@@ -766,8 +911,8 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         }
         ++ml_phase;
       }
-      if (ok && own > 0) ok = wait_all(B_O + half, half ? o_phase1 : o_phase0);
-      if (ok && split && other > 0) ok = wait_all(B_O + 1 - half, half ? o_phase0 : o_phase1);
+      if (ok && own > 0) ok = wait_all(SM::B_O + half, half ? o_phase1 : o_phase0);
+      if (ok && split && other > 0) ok = wait_all(SM::B_O + 1 - half, half ? o_phase0 : o_phase1);
       if (!ok) break;
       tc_fence_after();
       if (any) {
@@ -784,15 +929,14 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         const bool use0 = own > 0, use1 = split && other > 0;
 #pragma unroll 1
         for (int c = c_lo; c < c_hi; ++c) {
-          uint32_t ov[32];
           float x[32];
+          uint32_t ov[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = 0.f;
           if (use0) {
             tmem_ld32_sync(tmem + lane_off + tm_o(half) + c * 32, ov);
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(ov[e]) * a0;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = 0.f;
           }
           if (use1) {
             tmem_ld32_sync(tmem + lane_off + tm_o(1 - half) + c * 32, ov);
@@ -800,13 +944,13 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
             for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(ov[e]), a1, x[e]);
           }
           if (live && whole) {
-            uint32_t wv[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) wv[e] = pack_bf16(x[2 * e] * inv, x[2 * e + 1] * inv);
             uint4* dst = reinterpret_cast<uint4*>(orow_p + c * 32);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              dst[e] = make_uint4(wv[4 * e], wv[4 * e + 1], wv[4 * e + 2], wv[4 * e + 3]);
+              dst[e] = make_uint4(pack_bf16(x[8 * e] * inv, x[8 * e + 1] * inv),
+                                  pack_bf16(x[8 * e + 2] * inv, x[8 * e + 3] * inv),
+                                  pack_bf16(x[8 * e + 4] * inv, x[8 * e + 5] * inv),
+                                  pack_bf16(x[8 * e + 6] * inv, x[8 * e + 7] * inv));
           } else if (live) {
             float4* dst = reinterpret_cast<float4*>(part) + prow;
 #pragma unroll
@@ -815,17 +959,20 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                   make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
           }
         }
+        tc_fence_before();
+        mbar_arrive(bar(SM::B_F));
         if (live && (!split || half == 0)) {
-          if (whole) {
-            if (a.lse) a.lse[orow] = (M + log2f(L)) * kLn2;
-          } else {
+          if (!whole) {
             part[(size_t)prows * D + prow] = M;
             part[(size_t)prows * (D + 1) + prow] = L;
+          } else if (a.lse) {
+            a.lse[orow] = (M + log2f(L)) * kLn2;
           }
         }
+      } else {
+        tc_fence_before();
+        mbar_arrive(bar(SM::B_F));
       }
-      tc_fence_before();
-      mbar_arrive(bar(B_F));
       if ((half ? other : own) > 0) ++o_phase0;
       if ((half ? own : other) > 0) ++o_phase1;
       step += split ? nseg : 2 * nseg;
@@ -841,49 +988,60 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
   if (threadIdx.x == 0 && *abort_flag) flag_error(cv.err, kErrWaitTimeout);
 }
 
-// Joins the partials of the units that the CTAs' ranges cut.  Block (c, y):
-// rows 32 y .. 32 y + 31 of the unit that CTA c begins and does not end; lane =
-// row, each of 16 warps D / 16 columns; 8 partials are read at a time.
-constexpr int kJoinWarps = 16;
+// Joins the partials of the units that the CTAs' ranges cut.  Block (x, y, z):
+// the x-th CTA that begins a unit and does not end it, rows 32 y .. 32 y + 31
+// of that unit (lane = row), 16 columns (4 a warp).  Few threads and registers,
+// so that blocks are resident beside the first kernel's CTAs before those end.
+constexpr int kJoinWarps = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32)
-join_tree_kernel(CacheView cv, TreeArgs a, Shape sh) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 10)
+join_tree_kernel(CacheView cv, TreeArgs a, Shape sh, int ctas) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_wait();
   griddep_launch_dependents();
-  const int c = blockIdx.x, grid = gridDim.x;
-  const JoinDesc jd = static_cast<const JoinDesc*>(a.ws)[c];
-  if (jd.last < 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const JoinDesc* desc = static_cast<const JoinDesc*>(a.ws);
+  int c = -1;
+  for (int c0 = 0, skip = blockIdx.x; c0 < ctas; c0 += 256) {
+    int last[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int x = c0 + 32 * i + lane;
+      last[i] = x < ctas ? desc[x].last : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t on = __ballot_sync(0xffffffffu, last[i] >= 0);
+      const int cnt = __popc(on);
+      if (c < 0 && skip < cnt) c = c0 + 32 * i + (int)__fns(on, 0, skip + 1);
+      skip -= cnt;
+    }
+    if (c >= 0) break;
+  }
+  if (c < 0) return;
+  const JoinDesc jd = desc[c];
   const int prow = blockIdx.y * 32 + lane, prows = BM << sh.pair;
   const int r = prow & (BM - 1), rg = r / sh.G;
   const int node = jd.node0 + (prow >= BM ? sh.npt : 0) + rg;
   if (rg >= sh.npt || node >= jd.cnt) return;
-  constexpr int NV = D / 4 / kJoinWarps;           // float4 of a thread
-  constexpr int PB = 8;                            // partials read at a time
+  const int col4 = blockIdx.z * kJoinWarps + warp;       // float4 of the row
+  constexpr int PB = 4;                                  // partials read at a time
   float M = -INFINITY, L = 0.f;
-  float x[4 * NV];
-#pragma unroll
-  for (int e = 0; e < 4 * NV; ++e) x[e] = 0.f;
+  float x[4] = {0.f, 0.f, 0.f, 0.f};
   for (int p0 = c; p0 <= jd.last; p0 += PB) {
     float m[PB], l[PB];
-    float4 v[PB][NV];
+    float4 v[PB];
 #pragma unroll
     for (int i = 0; i < PB; ++i) {
       m[i] = -INFINITY;
       l[i] = 0.f;
+      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       const int p = p0 + i;
       if (p <= jd.last) {
-        const float* part = partial_at(a.ws, grid, 2 * p + (p == c ? 1 : 0), D, sh.pair);
+        const float* part = partial_at(a.ws, ctas, 2 * p + (p == c ? 1 : 0), D, sh.pair);
         m[i] = __ldcg(part + (size_t)prows * D + prow);
         l[i] = __ldcg(part + (size_t)prows * (D + 1) + prow);
-#pragma unroll
-        for (int e = 0; e < NV; ++e)
-          v[i][e] = __ldcg(reinterpret_cast<const float4*>(part) +
-                           (size_t)(warp * NV + e) * prows + prow);
-      } else {
-#pragma unroll
-        for (int e = 0; e < NV; ++e) v[i][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        v[i] = __ldcg(reinterpret_cast<const float4*>(part) + (size_t)col4 * prows + prow);
       }
     }
     float mn = M;
@@ -894,57 +1052,55 @@ join_tree_kernel(CacheView cv, TreeArgs a, Shape sh) {
     M = mn;
     L *= s0;
 #pragma unroll
-    for (int e = 0; e < 4 * NV; ++e) x[e] *= s0;
+    for (int e = 0; e < 4; ++e) x[e] *= s0;
 #pragma unroll
     for (int i = 0; i < PB; ++i) {
       const float s = fast_exp2(m[i] - ref);
       L += l[i] * s;
-#pragma unroll
-      for (int e = 0; e < NV; ++e) {
-        x[4 * e] += v[i][e].x * s;
-        x[4 * e + 1] += v[i][e].y * s;
-        x[4 * e + 2] += v[i][e].z * s;
-        x[4 * e + 3] += v[i][e].w * s;
-      }
+      x[0] += v[i].x * s;
+      x[1] += v[i].y * s;
+      x[2] += v[i].z * s;
+      x[3] += v[i].w * s;
     }
   }
   const float inv = 1.f / L;                       // self is visible: L > 0
   const size_t orow =
       ((size_t)jd.b * a.nodes + node) * cv.H + (size_t)jd.kvh * sh.G + (r - rg * sh.G);
-  uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + orow * D) + warp * NV;
-#pragma unroll
-  for (int e = 0; e < NV; ++e)
-    dst[e] = make_uint2(pack_bf16(x[4 * e] * inv, x[4 * e + 1] * inv),
-                        pack_bf16(x[4 * e + 2] * inv, x[4 * e + 3] * inv));
-  if (warp == 0 && a.lse) a.lse[orow] = (M + log2f(L)) * kLn2;
+  reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + orow * D)[col4] =
+      make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+  if (col4 == 0 && a.lse) a.lse[orow] = (M + log2f(L)) * kLn2;
 }
+
+// A cache of more than this is streamed: half of L2.
+constexpr uint64_t kEvictBytes = 64u << 20;
 
 Shape shape_of(const CacheView& cv, int nodes) {
   Shape sh;
   sh.G = cv.H / cv.Hkv;
   sh.npt = BM / sh.G;
   sh.pair = nodes > sh.npt ? 1 : 0;
+  sh.evict = sh.joins = 0;
   return sh;
 }
 
-// Key tiles of the largest work list.
-int64_t list_bound(const CacheView& cv, int nodes, const Shape& sh) {
-  if (sh.npt < 1) return INT64_MAX;
+// Units of the largest work list, and the cost of all of them.
+int64_t most_units(const CacheView& cv, int nodes, const Shape& sh) {
   const int per = sh.npt << sh.pair;
-  const int64_t units = (int64_t)cv.B * cv.Hkv * ((nodes + per - 1) / per);
+  return (int64_t)cv.B * cv.Hkv * ((nodes + per - 1) / per);
+}
+int64_t most_cost(const CacheView& cv, int nodes, const Shape& sh) {
   const int64_t tiles = (cv.m_cap + BN - 1) / BN + (cv.n + BN - 1) / BN + (nodes + BN - 1) / BN;
-  return units * tiles;
+  return most_units(cv, nodes, sh) * (tiles * kTileCost + kUnitCost);
 }
 
 // CTAs of the launch: one per SM, no more than the largest list could feed.
 int grid_of(const CacheView& cv, int nodes, const Shape& sh) {
-  const int64_t most = list_bound(cv, nodes, sh) / kMinTiles;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(cv.sms, most));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(cv.sms, most_cost(cv, nodes, sh) / kMinCost));
 }
 
-template <int D>
+template <int D, bool PAIR>
 cudaError_t launch_d(const CacheView& cv, const TreeArgs& a, cudaStream_t s) {
-  const Shape sh = shape_of(cv, a.nodes);
+  Shape sh = shape_of(cv, a.nodes);
   const int grid = grid_of(cv, a.nodes, sh);
   const uint64_t trows = (uint64_t)cv.B * a.nodes;
   const uint64_t crows = (uint64_t)cv.B * cv.Hkv * cv.slab_rows;
@@ -959,24 +1115,27 @@ cudaError_t launch_d(const CacheView& cv, const TreeArgs& a, cudaStream_t s) {
       !make_tmap_rows_bf16(&mkt16, a.k, (uint64_t)cv.Hkv * D, trows, 16) ||
       !make_tmap_rows_bf16(&mvt16, a.v, (uint64_t)cv.Hkv * D, trows, 16))
     return cudaErrorInvalidValue;
+  sh.evict = crows * D * 4 > kEvictBytes;
+  sh.joins = (int)std::min<int64_t>(most_units(cv, a.nodes, sh), grid);
   // Per device (the attribute belongs to the current device's context).
-  cudaError_t e = cudaFuncSetAttribute(decode_tree_tc_kernel<D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(decode_tree_tc_kernel<D, PAIR>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, PAIR>::kBytes);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(decode_tree_tc_kernel<D>, dim3(grid), dim3(kThreads), kSmemBytes, s, mq,
+  e = launch_dependent(decode_tree_tc_kernel<D, PAIR>, dim3(grid), dim3(kThreads), Smem<D, PAIR>::kBytes, s, mq,
                        mkc, mvc, mkt, mvt, mkc16, mvc16, mkt16, mvt16, cv, a, sh,
                        phase_wait_limit_ns());
   if (e != cudaSuccess) return e;
-  return launch_dependent(join_tree_kernel<D>, dim3(grid, (BM << sh.pair) / 32),
-                          dim3(kJoinWarps * 32), 0, s,
-                          cv, a, sh);
+  const int rows = PAIR ? 2 * BM : std::min(a.nodes, sh.npt) * sh.G;
+  return launch_dependent(join_tree_kernel<D>,
+                          dim3(sh.joins, (rows + 31) / 32, D / (4 * kJoinWarps)),
+                          dim3(kJoinWarps * 32), 0, s, cv, a, sh, grid);
 }
 
 }  // namespace
 
 bool decode_tree_tc_supported(const CacheView& cv, int nodes) {
-  const Shape sh = shape_of(cv, nodes);
-  return list_bound(cv, nodes, sh) < (int64_t(1) << 31) && cv.dtype == RSWA_BF16 && cv.H / cv.Hkv <= BM &&
+  if (cv.dtype != RSWA_BF16 || cv.H / cv.Hkv > BM) return false;
+  return most_cost(cv, nodes, shape_of(cv, nodes)) < (int64_t(1) << 31) &&
          (int64_t)cv.B * nodes < (int64_t(1) << 30) &&
          (int64_t)cv.B * cv.Hkv * cv.slab_rows + cv.n < (int64_t(1) << 31);
 }
@@ -989,7 +1148,9 @@ size_t decode_tree_tc_workspace(const CacheView& cv, int nodes) {
 }
 
 cudaError_t launch_decode_tree_tc(const CacheView& cv, const TreeArgs& a, cudaStream_t s) {
-  return cv.d == 64 ? launch_d<64>(cv, a, s) : launch_d<128>(cv, a, s);
+  if (shape_of(cv, a.nodes).pair)
+    return cv.d == 64 ? launch_d<64, true>(cv, a, s) : launch_d<128, true>(cv, a, s);
+  return cv.d == 64 ? launch_d<64, false>(cv, a, s) : launch_d<128, false>(cv, a, s);
 }
 
 }  // namespace rswa
