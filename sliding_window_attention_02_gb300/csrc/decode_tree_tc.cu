@@ -97,17 +97,19 @@ struct Smem {
 __host__ __device__ constexpr uint32_t tm_s(int half) { return half ? 128u : 0u; }
 __host__ __device__ constexpr uint32_t tm_o(int half) { return half ? 384u : 256u; }
 constexpr uint32_t TM_COLS = 512;
+constexpr int kTurnUnroll = 1;                 // rolled softmax loop
+constexpr int kMmaUnroll = 8;
 constexpr float kRescaleThreshold = 8.0f;      // log2 units
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
-// Cost of a key tile in the cut of the work list, in loads of 16 keys: what it
-// reads, but at least what its matrix products and softmax take meanwhile; a
-// unit's first tile carries the unit's start and end too.  A CTA's share is
-// never below kMinCost, so that it holds a tile at least (and no join is made
-// for less work than it costs).
-// A pair of query tiles takes as long for few keys as for many.
-constexpr int kTileCost = 8, kTileLeast = 4, kPairLeast = 8, kUnitCost = 8, kMinCost = 40;
-static_assert(kMinCost >= kTileCost + kUnitCost, "a share holds a tile");
+// The work list is cut by cost.  Every key tile costs 1, a partial one too: a
+// step takes as long as its chain of matrix products and softmax (2600 cycles,
+// about the time in which an SM's share of HBM brings a whole tile).  A unit's
+// first tile carries the unit's start and end as well.  A CTA's share is never
+// below kMinCost, so that it holds a tile at least and no join is made for less
+// work than it costs.
+constexpr int kUnitCost = 2, kMinCost = 7;
+static_assert(kMinCost >= 1 + kUnitCost, "a share holds a tile");
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x,
                                             int32_t y, int32_t z, uint32_t bar) {
@@ -140,36 +142,15 @@ __device__ __forceinline__ uint64_t evict_normal_policy() {
   return p;
 }
 
-// Wait for this thread's outstanding TMEM loads; r (the registers of the last
-// one) are in-out operands, so no use of them moves above the wait.
-__device__ __forceinline__ void tmem_wait_ld16(uint32_t* r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
+// mbar_wait with its polling loop out of line: the waits are many, and
+// instructions that are not there need not be fetched.
+__device__ __noinline__ bool wait_on(uint32_t b, uint32_t phase, volatile int* abort_flag,
+                                     uint64_t ns) {
+  return mbar_wait(b, phase, abort_flag, ns);
 }
-
-__device__ __forceinline__ void tmem_ld8_sync(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-      : "memory");
-}
-
-// 2^k of a whole number k <= 0 held as a float; 0 below 2^-126.
-__device__ __forceinline__ float power_of_two(float k) {
-  return k < -126.f ? 0.f : __int_as_float((127 + (int)k) << 23);
+__device__ __forceinline__ bool wait_for(uint32_t b, uint32_t phase, volatile int* abort_flag,
+                                         uint64_t ns) {
+  return mbar_try_wait(b, phase) || wait_on(b, phase, abort_flag, ns);
 }
 
 // The shape of a launch.
@@ -181,48 +162,30 @@ struct Shape {
   int joins;    // units of the launch, or its CTAs where those are fewer
 };
 
-// Cost of `keys` keys in tiles.
-__device__ __forceinline__ int keys_cost(int keys, int least) {
-  const int rest = keys % BN;
-  return keys / BN * kTileCost + (rest ? max(least, (rest + 15) / 16) : 0);
-}
-
-// What a sequence adds to the work list: `units` units of `tl` key tiles, that
-// cost `cost` each.
+// What a sequence adds to the work list: `units` units of `tl` key tiles each.
 struct Seq {
   int cnt, m_b, ring;
   int64_t t_b;
-  int np, nr, tl, cost, units, least;
-  __device__ __noinline__ void load(const CacheView& cv, const TreeArgs& a, const Shape& sh,
-                                   int b) {
+  int np, nr, tl, units;
+  __device__ __forceinline__ void load(const CacheView& cv, const TreeArgs& a, const Shape& sh,
+                                       int b) {
     const int c = a.counts ? a.counts[b] : a.nodes;
     m_b = cv.m_dev[b];
     t_b = cv.t_dev[(size_t)b * cv.H];
-    if (a.counts && blockIdx.x == 0 && (c < 0 || c > a.nodes)) flag_error(cv.err, kErrBadTree);
     cnt = min(max(c, 0), a.nodes);
+    if (c != cnt) flag_error(cv.err, kErrBadTree);
     ring = (int)min(min(cv.n, t_b), (int64_t)1 << 30);
     np = (m_b + BN - 1) / BN;
     nr = (ring + BN - 1) / BN;
     tl = np + nr + (cnt + BN - 1) / BN;
-    least = sh.pair ? kPairLeast : kTileLeast;
-    cost = before(tl);
     const int per = sh.npt << sh.pair;
     units = (cnt + per - 1) / per * cv.Hkv;
   }
-  // Cost of a unit's tiles before tile j.
-  __device__ __noinline__ int before(int j) const {
-    const int jp = min(j, np), jr = min(max(j - np, 0), nr), jt = max(j - np - nr, 0);
-    return keys_cost(min(m_b, jp * BN), least) + keys_cost(min(ring, jr * BN), least) +
-           keys_cost(min(cnt, jt * BN), least) + (j > 0 ? kUnitCost : 0);
-  }
-  // The first tile that begins at or after cost x of a unit (tl: none).
-  __device__ __noinline__ int at(int x) const {
-    if (x <= 0) return 0;
-    int j = min(max((x - kUnitCost + kTileCost - 1) / kTileCost, 1), tl);
-    while (j > 1 && before(j - 1) >= x) --j;
-    while (j < tl && before(j) < x) ++j;
-    return j;
-  }
+  __device__ int cost() const { return tl + kUnitCost; }          // of a unit
+  // Cost of a unit's tiles before tile j, and the first tile that begins at or
+  // after cost x (tl: none).
+  __device__ int before(int j) const { return j > 0 ? j + kUnitCost : 0; }
+  __device__ int at(int x) const { return x <= 0 ? 0 : min(max(x - kUnitCost, 1), tl); }
 };
 
 enum TileKind { kPrefix = 0, kRing = 1, kTree = 2 };
@@ -336,7 +299,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
   griddep_launch_dependents();
   // Segment k, from the planner; false: the wait gave up.
   auto segment = [&](int k, Segment& w) {
-    if (!mbar_wait(bar(SM::B_SEG + k % NSEG), (k / NSEG) & 1, abort_flag, wait_ns)) return false;
+    if (!wait_for(bar(SM::B_SEG + k % NSEG), (k / NSEG) & 1, abort_flag, wait_ns)) return false;
     w = segs[k % NSEG];
     return true;
   };
@@ -370,7 +333,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
           for (int isv = 0; isv < 2; ++isv, ++gi) {
             const uint32_t s = gi % NS;
             if (gi >= (uint32_t)NS &&
-                !mbar_wait(bar(SM::B_EMPTY + s), ((gi / NS) - 1) & 1, abort_flag, wait_ns)) {
+                !wait_for(bar(SM::B_EMPTY + s), ((gi / NS) - 1) & 1, abort_flag, wait_ns)) {
               ok = false;
               break;
             }
@@ -393,7 +356,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       }
       // Drain: every copy issued has landed before the CTA may exit.
       for (uint32_t k = gi > (uint32_t)NS ? gi - NS : 0; k < gi; ++k)
-        mbar_wait(bar(SM::B_FULL + k % NS), (k / NS) & 1, never, kWaitLimitNs);
+        wait_for(bar(SM::B_FULL + k % NS), (k / NS) & 1, never, kWaitLimitNs);
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
@@ -402,7 +365,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       constexpr uint32_t idesc_qk = idesc_bf16(BM, BN, false);
       constexpr uint32_t idesc_pv = idesc_bf16(BM, D, true);
       auto wait = [&](int k, uint32_t phase) {
-        return mbar_wait(bar(k), phase & 1, abort_flag, wait_ns);
+        return wait_for(bar(k), phase & 1, abort_flag, wait_ns);
       };
       // Load 2 t is the key tile of the CTA's tile t, load 2 t + 1 its value
       // tile: `slot` and `phase` of the one a cursor is at.
@@ -448,7 +411,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         tc_fence_after();
         const uint32_t kb = sb + SM::OFF_RING + qc.slot * kTile;
         const uint32_t qb = sb + SM::OFF_Q + (qt % NQ) * kTile;
-#pragma unroll
+#pragma unroll kMmaUnroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k >> 2) * kSub + (k & 3) * 32;
           mma_bf16_ss(tmem + tm_s(half), desc_sw128(qb + off, 16, 1024),
@@ -495,7 +458,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                       desc_sw128(vb + k * 2048, kSub, 1024), idesc_pv,
                       (!first || k > 0) ? 1u : 0u);
         };
-#pragma unroll
+#pragma unroll kMmaUnroll
         for (int k = 0; k < BN / 16; ++k)
           if (k < ks) pv(k);
         if (pc.split || pc.sub == 1) mma_commit(bar(SM::B_EMPTY + pc.slot));
@@ -507,7 +470,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       }
       // Drain: all MMAs of this CTA have finished before TMEM is freed.
       mma_commit(bar(SM::B_FIN));
-      mbar_wait(bar(SM::B_FIN), 0, never, kWaitLimitNs);
+      wait_for(bar(SM::B_FIN), 0, never, kWaitLimitNs);
     }
     __syncwarp();
   } else if (warp == kPlanWarp) {
@@ -520,7 +483,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     auto queries = [&](const Segment& w) {
       for (int x = 0; x < (w.split ? 1 : 2); ++x, ++qi) {
         const int s = qi % NQ;
-        if (qi >= NQ && !__all_sync(0xffffffffu, mbar_wait(bar(SM::B_QE + s), (qi / NQ - 1) & 1,
+        if (qi >= NQ && !__all_sync(0xffffffffu, wait_for(bar(SM::B_QE + s), (qi / NQ - 1) & 1,
                                                            abort_flag, wait_ns)))
           return false;
         if (lane == 0) {
@@ -539,9 +502,10 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     const int b_lo = min(lane * per, cv.B), b_hi = min(b_lo + per, cv.B);
     Seq sq;
     int mine = 0;
+#pragma unroll 2
     for (int b = b_lo; b < b_hi; ++b) {
       sq.load(cv, a, sh, b);
-      mine += sq.cost * sq.units;
+      mine += sq.cost() * sq.units;
     }
     int inc = mine;
 #pragma unroll
@@ -567,8 +531,8 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         if (per > 1) {
           for (;; ++b) {
             sq.load(cv, a, sh, b);
-            if (x0 < base + sq.cost * sq.units) break;
-            base += sq.cost * sq.units;
+            if (x0 < base + sq.cost() * sq.units) break;
+            base += sq.cost() * sq.units;
           }
         }
       }
@@ -576,14 +540,14 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       b = __shfl_sync(0xffffffffu, b, src);
       base = __shfl_sync(0xffffffffu, base, src);
       sq.load(cv, a, sh, b);
-      int u = (x0 - base) / sq.cost;
-      int ubase = base + u * sq.cost;            // where unit u begins
+      int u = (x0 - base) / sq.cost();
+      int ubase = base + u * sq.cost();            // where unit u begins
       int j0 = sq.at(x0 - ubase), par_b = -1;
       const int unit_nodes = sh.npt << sh.pair;
       const int n = (int)min(cv.n, (int64_t)1 << 30);
       for (bool next_unit = j0 == sq.tl;; next_unit = true) {
         if (next_unit) {
-          ubase += sq.cost;
+          ubase += sq.cost();
           j0 = 0;
           if (++u == sq.units) {
             u = 0;
@@ -642,7 +606,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
           __syncwarp();
         }
         if (k >= 2 &&
-            !__all_sync(0xffffffffu, mbar_wait(bar(SM::B_NFREE + (k & 1)), ((k >> 1) - 1) & 1,
+            !__all_sync(0xffffffffu, wait_for(bar(SM::B_NFREE + (k & 1)), ((k >> 1) - 1) & 1,
                                                abort_flag, wait_ns)))
           break;
         int32_t* nd = nodes_smem + (k & 1) * SM::kNodeWords;
@@ -679,7 +643,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       static_cast<JoinDesc*>(a.ws)[cta] = jd;
       // Drain: every copy issued has landed before the CTA may exit.
       for (int x = max(qi - NQ, 0); x < qi; ++x)
-        mbar_wait(bar(SM::B_QF + x % NQ), (x / NQ) & 1, never, kWaitLimitNs);
+        wait_for(bar(SM::B_QF + x % NQ), (x / NQ) & 1, never, kWaitLimitNs);
     }
     __syncwarp();
   } else {
@@ -710,7 +674,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       bool have = false;
       auto nodes = [&]() {
         if (!have)
-          have = __all_sync(0xffffffffu, mbar_wait(bar(SM::B_NODE + (k & 1)), (k >> 1) & 1,
+          have = __all_sync(0xffffffffu, wait_for(bar(SM::B_NODE + (k & 1)), (k >> 1) & 1,
                                                    abort_flag, wait_ns));
         return have;
       };
@@ -724,7 +688,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         const int k0 = i * BN;
         const bool full = kind == kPrefix && keys == BN;
         if (!__all_sync(0xffffffffu,
-                        mbar_wait(bar(SM::B_S + half), turns & 1, abort_flag, wait_ns))) {
+                        wait_for(bar(SM::B_S + half), turns & 1, abort_flag, wait_ns))) {
           ok = false;
           break;
         }
@@ -735,9 +699,33 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         }
         tc_fence_after();
         if (any) {
-          if (!full) {
-            // Scores of columns that are no keys of this row become -inf.  Ring:
-            // slot s is a key iff its age (r0 - s) mod n is at most lim.
+          // Pass 1: the row's maximum; scores of columns that are no keys of it
+          // become -inf.  Both passes are short rolled loops: this many warps do
+          // not hide the fetch of straight-line code (a turn took 4000-8000
+          // cycles unrolled, 2000 rolled).
+          float mx[2] = {-INFINITY, -INFINITY};
+          uint32_t va[32], vb[32];
+          auto maxima = [&](const uint32_t* v) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              mx[0] = fmax3(mx[0], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+              mx[1] = fmax3(mx[1], __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+            }
+          };
+          if (full) {
+            tmem_ld32(s_addr, va);
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 64) {
+              tmem_wait_ld32(va);
+              tmem_ld32(s_addr + c + 32, vb);
+              maxima(va);
+              tmem_wait_ld32(vb);
+              tmem_ld32(s_addr + ((c + 64) & 127), va);
+              maxima(vb);
+            }
+            tmem_wait_ld32(va);                          // columns 0-31, for pass 2
+          } else {
+            // Ring: slot s is a key iff its age (r0 - s) mod n is at most lim.
             int a1 = 0, b1 = keys - 1, a2 = 1, b2 = 0;
             if (kind == kRing) {
               const int lim = min(w.age, n - 2 - (live ? nd[ni] : 0));
@@ -772,72 +760,43 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                   }
                 }
               }
-              uint32_t v[32];
-              tmem_ld32_sync(s_addr + 32 * c, v);
+              tmem_ld32_sync(s_addr + 32 * c, va);
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (!(see >> e & 1u)) v[e] = 0xff800000u;
-              tmem_st32(s_addr + 32 * c, v);
+                if (!(see >> e & 1u)) va[e] = 0xff800000u;
+              tmem_st32(s_addr + 32 * c, va);
+              maxima(va);
             }
             tmem_wait_st();
+            tmem_ld32_sync(s_addr, va);
           }
-          // One pass over S in chunks of 16 columns, each exponentiated relative
-          // to the running reference and stored as P over columns already read.
-          // Any reference gives the same o and lse, so it stays until a score
-          // exceeds it by more than 2^8 (a row's first key always does); then it
-          // becomes the score rounded up to a whole number of log2 units, so that
-          // what was stored relative to the old one (O, l, this tile's P so far)
-          // is scaled by a power of two, exactly.  A rolled loop: with few warps
-          // at work, straight-line code waits for its instructions (a turn of
-          // one warp 4000-8000 cycles unrolled).
-          const uint64_t sl2x2 = f2_pack(sl2, sl2);
+          // The reference of a row's exponentials stays until a score exceeds
+          // it by more than 2^8 (any reference gives the same o and lse); then O
+          // and l are rescaled.  O_h is stable here: S_h of this step completing
+          // implies that the half's PV before it has.
+          const float tmax = fmaxf(mx[0], mx[1]) * sl2;
+          const bool over = tmax > m_run + kRescaleThreshold;      // also where m_run is -inf
+          if (__any_sync(0xffffffffu, over)) {
+            const float alpha = over ? ex2(m_run - tmax) : 1.f;
+            if (over) m_run = tmax;
+            l_run *= alpha;
+#pragma unroll 1
+            for (int c = 0; started && c < D; c += 32) {
+              tmem_ld32_sync(o_addr + c, vb);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                vb[e] = __float_as_uint(__uint_as_float(vb[e]) * alpha);
+              tmem_st32(o_addr + c, vb);
+            }
+          }
+          // Pass 2: P, over columns of S already read, and its sum.
+          const float nref = (m_run == -INFINITY) ? 0.f : -m_run;
+          const uint64_t sl2x2 = f2_pack(sl2, sl2), nref2 = f2_pack(nref, nref);
           uint64_t ps2 = 0;
-          uint32_t va[16], vb[16];
-          auto chunk = [&](const uint32_t* v, int c) {
-            float mx[2] = {-INFINITY, -INFINITY};
+          auto exponentials = [&](const uint32_t* v, uint32_t to) {
+            uint32_t p[16];
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              mx[0] = fmax3(mx[0], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-              mx[1] = fmax3(mx[1], __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
-            }
-            const float tmax = fmaxf(mx[0], mx[1]) * sl2;
-            const bool over = tmax > m_run + kRescaleThreshold;    // also where m_run is -inf
-            if (__any_sync(0xffffffffu, over)) {
-              const float m_new = over ? ceilf(tmax) : m_run;
-              const float alpha = power_of_two(over ? m_run - m_new : 0.f);
-              m_run = m_new;
-              l_run *= alpha;
-              ps2 = f2_mul(ps2, f2_pack(alpha, alpha));
-              const __nv_bfloat162 a2 = __float2bfloat162_rn(alpha);
-              tmem_wait_st();
-#pragma unroll 1
-              for (int x = 0; x < c; ++x) {
-                uint32_t p[8];
-                tmem_ld8_sync(s_addr + 8 * x, p);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const __nv_bfloat162 y = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&p[e]), a2);
-                  p[e] = *reinterpret_cast<const uint32_t*>(&y);
-                }
-                tmem_st8(s_addr + 8 * x, p);
-              }
-              // O_h is stable here: S_h of this step completing implies that
-              // the half's PV before it has.
-#pragma unroll 1
-              for (int x = 0; started && x < D / 8; ++x) {
-                uint32_t o[8];
-                tmem_ld8_sync(o_addr + 8 * x, o);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                tmem_st8(o_addr + 8 * x, o);
-              }
-            }
-            const float nref = (m_run == -INFINITY) ? 0.f : -m_run;
-            const uint64_t nref2 = f2_pack(nref, nref);
-            uint32_t p[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 16; ++e) {
               float x0, x1;
               f2_unpack(f2_fma(f2_pack(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
                                sl2x2, nref2),
@@ -846,18 +805,16 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
               ps2 = f2_add(ps2, f2_pack(p0, p1));
               p[e] = pack_bf16(p0, p1);
             }
-            tmem_st8(s_addr + 8 * c, p);
+            tmem_st16(to, p);
           };
-          tmem_ld16(s_addr, va);
-          tmem_wait_ld16(va);
-#pragma unroll 1
-          for (int c = 0; c < 8; c += 2) {
-            tmem_ld16(s_addr + 16 * (c + 1), vb);
-            chunk(va, c);
-            tmem_wait_ld16(vb);
-            if (c + 2 < 8) tmem_ld16(s_addr + 16 * (c + 2), va);
-            chunk(vb, c + 1);
-            tmem_wait_ld16(va);
+#pragma unroll kTurnUnroll
+          for (int c = 0; c < 2; ++c) {
+            tmem_ld32(s_addr + 64 * c + 32, vb);
+            exponentials(va, s_addr + 32 * c);
+            tmem_wait_ld32(vb);
+            if (c == 0) tmem_ld32(s_addr + 64, va);
+            exponentials(vb, s_addr + 32 * c + 16);
+            tmem_wait_ld32(va);
           }
           float s0, s1;
           f2_unpack(ps2, s0, s1);
@@ -870,7 +827,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
           // Value rows keys .. up to the next 16 belong to nodes past the
           // count, or to the next sequence, and may hold anything: zero.
           const uint32_t vi = 2u * (uint32_t)(w.tiles + j - w.j0) + 1u;
-          if (__all_sync(0xffffffffu, mbar_wait(bar(SM::B_FULL + vi % NS), (vi / NS) & 1,
+          if (__all_sync(0xffffffffu, wait_for(bar(SM::B_FULL + vi % NS), (vi / NS) & 1,
                                                 abort_flag, wait_ns))) {
             const int rows = 16 - keys % 16;
             uint8_t* v = smem + SM::OFF_RING + (vi % NS) * kTile + keys * 128;
@@ -889,7 +846,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       const int own = !split ? nseg : ((step & 1) == (uint32_t)half ? (nseg + 1) / 2 : nseg / 2);
       const int other = split ? nseg - own : nseg;
       auto wait_all = [&](int b, uint32_t phase) {
-        return __all_sync(0xffffffffu, mbar_wait(bar(b), phase & 1, abort_flag, wait_ns)) != 0;
+        return __all_sync(0xffffffffu, wait_for(bar(b), phase & 1, abort_flag, wait_ns)) != 0;
       };
       // Weights of the two halves' O, the row's reference and sum.
       float a0 = 1.f, a1 = 0.f, M = m_run, L = l_run;
@@ -1090,7 +1047,7 @@ int64_t most_units(const CacheView& cv, int nodes, const Shape& sh) {
 }
 int64_t most_cost(const CacheView& cv, int nodes, const Shape& sh) {
   const int64_t tiles = (cv.m_cap + BN - 1) / BN + (cv.n + BN - 1) / BN + (nodes + BN - 1) / BN;
-  return most_units(cv, nodes, sh) * (tiles * kTileCost + kUnitCost);
+  return most_units(cv, nodes, sh) * (tiles + kUnitCost);
 }
 
 // CTAs of the launch: one per SM, no more than the largest list could feed.
