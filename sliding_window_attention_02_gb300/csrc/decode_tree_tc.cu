@@ -219,6 +219,14 @@ struct Segment {
 };
 static_assert(sizeof(Segment) <= 64, "segment");
 
+// Waits for a segment: its key tiles, and whether it is split in bit 24; 0: no
+// more segments, or the wait gave up.
+__device__ __noinline__ int enter_segment(uint32_t b, uint32_t phase, const Segment* w,
+                                          volatile int* abort_flag, uint64_t ns) {
+  if (!mbar_wait(b, phase, abort_flag, ns) || w->j1 == 0) return 0;
+  return (w->j1 - w->j0) | w->split << 24;
+}
+
 // Bits e of word c (columns 32 c + e) with lo <= column <= hi.
 __device__ __forceinline__ uint32_t range_mask(int lo, int hi, int c) {
   const int a = max(lo - 32 * c, 0), b = min(hi - 32 * c, 31);
@@ -360,7 +368,11 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
-    // One lane issues; QK runs two steps ahead of PV.
+    // One lane issues.  Step s: PV of step s - 2, then QK of step s, both of half
+    // s & 1.  What the lane does between the products holds the tensor core up
+    // (2700 cycles a step with 1350 of them in products), so waits are made
+    // where their answer can be new only, descriptors advance by constants, and
+    // the rare paths are out of line.
     if (lane == 0) {
       constexpr uint32_t idesc_qk = idesc_bf16(BM, BN, false);
       constexpr uint32_t idesc_pv = idesc_bf16(BM, D, true);
@@ -370,24 +382,23 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       // Load 2 t is the key tile of the CTA's tile t, load 2 t + 1 its value
       // tile: `slot` and `phase` of the one a cursor is at.
       struct Cursor {
-        int k = 0, left = 0;             // segment, its tiles left
-        int split = 1, sub = 0;          // in a pair unit the first or second half's turn
-        uint32_t step = 0, slot, phase = 0, q = 0;   // q: query tiles before
+        int k = 0, left;                 // segment, its tiles left
+        bool split, second = false;      // in a pair unit: the second half's turn
+        uint32_t slot, phase = 0, q = 0; // q: query tiles before
       };
       auto enter = [&](Cursor& c) {
-        if (!wait(SM::B_SEG + c.k % NSEG, c.k / NSEG)) return false;
-        const Segment& w = segs[c.k % NSEG];
-        c.left = w.j1 - w.j0;
-        c.split = w.split;
-        return w.j1 > 0;
+        const int x = enter_segment(bar(SM::B_SEG + c.k % NSEG), (c.k / NSEG) & 1,
+                                    &segs[c.k % NSEG], abort_flag, wait_ns);
+        c.left = x & 0xffffff;
+        c.split = x >> 24;
+        return x != 0;
       };
       auto advance = [&](Cursor& c) {    // false: no more steps
-        ++c.step;
-        if (!c.split && c.sub == 0) {
-          c.sub = 1;
+        if (!c.split && !c.second) {
+          c.second = true;
           return true;
         }
-        c.sub = 0;
+        c.second = false;
         c.slot += 2;
         if (c.slot >= (uint32_t)NS) {
           c.slot -= NS;
@@ -402,71 +413,80 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       qc.slot = 0;
       pc.slot = 1;
       bool qmore = enter(qc), pmore = enter(pc);
-      // S = Q K^T of qc's step, then on to the next.
-      auto qk = [&]() {
-        const uint32_t half = qc.step & 1;
-        const uint32_t qt = qc.split ? qc.q : qc.q + half;
-        if (!wait(SM::B_QF + qt % NQ, qt / NQ) || !wait(SM::B_FULL + qc.slot, qc.phase))
-          return false;
-        tc_fence_after();
-        const uint32_t kb = sb + SM::OFF_RING + qc.slot * kTile;
-        const uint32_t qb = sb + SM::OFF_Q + (qt % NQ) * kTile;
-#pragma unroll kMmaUnroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * kSub + (k & 3) * 32;
-          mma_bf16_ss(tmem + tm_s(half), desc_sw128(qb + off, 16, 1024),
-                      desc_sw128(kb + off, 16, 1024), idesc_qk, k > 0);
-        }
-        mma_commit(bar(SM::B_S + half));
-        if (qc.split || qc.sub == 1) {
-          mma_commit(bar(SM::B_EMPTY + qc.slot));
-          if (qc.left == 1) {
-            mma_commit(bar(SM::B_QE + qc.q % NQ));
-            if (!qc.split) mma_commit(bar(SM::B_QE + (qc.q + 1) % NQ));
+      int pfresh = 2, qfresh = 2;        // steps until both halves have had one
+      if (pmore && pc.split && pc.left == 1) pfresh = 1;
+      if (qmore && qc.split && qc.left == 1) qfresh = 1;
+      const uint64_t qdesc = desc_sw128(sb + SM::OFF_Q, 16, 1024);
+      const uint64_t kdesc = desc_sw128(sb + SM::OFF_RING, 16, 1024);
+      const uint64_t vdesc = desc_sw128(sb + SM::OFF_RING, kSub, 1024);
+      int np = pmore ? segs[0].np - segs[0].j0 : 0, tl = pc.left;   // see `whole` below
+#pragma unroll 1
+      for (uint32_t s = 0; pmore; ++s) {
+        const uint32_t half = s & 1;
+        if (s >= 2) {
+          const bool first = pfresh > 0, last = pc.left <= (pc.split ? 2 : 1);
+          if (first) {
+            --pfresh;
+            if (pc.k > 0 && !wait(SM::B_F, pc.k - 1)) break;
+          }
+          if (!wait(SM::B_P + half, (s >> 1) - 1)) break;
+          if (!pc.second && !wait(SM::B_FULL + pc.slot, pc.phase)) break;
+          tc_fence_after();
+          const uint64_t vd = vdesc + (uint64_t)(pc.slot * (kTile >> 4));
+          // Tile tl - left of the segment holds 128 keys if a prefix tile comes
+          // after it.
+          if (tl - pc.left + 1 < np) {
+#pragma unroll
+            for (int k = 0; k < BN / 16; ++k)
+              mma_bf16_ts(tmem + tm_o(half), tmem + tm_s(half) + k * 8, vd + k * 128, idesc_pv,
+                          k > 0 ? 1u : (first ? 0u : 1u));
+          } else {
+            const Segment& w = segs[pc.k % NSEG];
+            int kind, i, keys;
+            w.tile(w.j1 - pc.left, kind, i, keys);
+#pragma unroll 1
+            for (int k = 0; 16 * k < keys; ++k)
+              mma_bf16_ts(tmem + tm_o(half), tmem + tm_s(half) + k * 8, vd + k * 128, idesc_pv,
+                          (!first || k > 0) ? 1u : 0u);
+          }
+          if (pc.split || pc.second) mma_commit(bar(SM::B_EMPTY + pc.slot));
+          if (last) mma_commit(bar(SM::B_O + half));
+          const int at = pc.k;
+          pmore = advance(pc);
+          if (pc.k != at) {
+            pfresh = pc.split && pc.left == 1 ? 1 : 2;
+            np = segs[pc.k % NSEG].np - segs[pc.k % NSEG].j0;
+            tl = pc.left;
           }
         }
-        qmore = advance(qc);
-        return true;
-      };
-      bool ok = true;
-      int tiles = pc.left;                       // of pc's segment
-#pragma unroll 1
-      for (int lead = 2; ok && pmore;) {
-        if (lead > 0) {                          // the first two steps
-          --lead;
-          if (qmore) ok = qk();
-          continue;
+        if (qmore) {
+          // S = Q K^T
+          const uint32_t qt = qc.split ? qc.q : qc.q + half;
+          if (qfresh > 0) {
+            --qfresh;
+            if (!wait(SM::B_QF + qt % NQ, qt / NQ)) break;
+          }
+          if (!qc.second && !wait(SM::B_FULL + qc.slot, qc.phase)) break;
+          tc_fence_after();
+          const uint64_t kd = kdesc + (uint64_t)(qc.slot * (kTile >> 4));
+          const uint64_t qd = qdesc + (uint64_t)((qt % NQ) * (kTile >> 4));
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * kSub + (k & 3) * 32) >> 4;
+            mma_bf16_ss(tmem + tm_s(half), qd + off, kd + off, idesc_qk, k > 0);
+          }
+          mma_commit(bar(SM::B_S + half));
+          if (qc.split || qc.second) {
+            mma_commit(bar(SM::B_EMPTY + qc.slot));
+            if (qc.left == 1) {
+              mma_commit(bar(SM::B_QE + qc.q % NQ));
+              if (!qc.split) mma_commit(bar(SM::B_QE + (qc.q + 1) % NQ));
+            }
+          }
+          const int at = qc.k;
+          qmore = advance(qc);
+          if (qc.k != at) qfresh = qc.split && qc.left == 1 ? 1 : 2;
         }
-        const uint32_t half = pc.step & 1;
-        const Segment& w = segs[pc.k % NSEG];
-        const int j = w.j1 - pc.left;
-        // The half's first and last step of the segment.
-        const int span = pc.split ? 2 : 1;
-        const bool first = tiles - pc.left < span, last = pc.left <= span;
-        if (first && pc.k > 0 && !wait(SM::B_F, pc.k - 1)) break;
-        if (!wait(SM::B_P + half, pc.step >> 1) || !wait(SM::B_FULL + pc.slot, pc.phase)) break;
-        const uint32_t vb = sb + SM::OFF_RING + pc.slot * kTile;
-        int ks = BN / 16;
-        if (j + 1 >= w.np) {
-          int kind, i, keys;
-          w.tile(j, kind, i, keys);
-          ks = (keys + 15) / 16;
-        }
-        tc_fence_after();
-        auto pv = [&](int k) {
-          mma_bf16_ts(tmem + tm_o(half), tmem + tm_s(half) + k * 8,
-                      desc_sw128(vb + k * 2048, kSub, 1024), idesc_pv,
-                      (!first || k > 0) ? 1u : 0u);
-        };
-#pragma unroll kMmaUnroll
-        for (int k = 0; k < BN / 16; ++k)
-          if (k < ks) pv(k);
-        if (pc.split || pc.sub == 1) mma_commit(bar(SM::B_EMPTY + pc.slot));
-        if (last) mma_commit(bar(SM::B_O + half));
-        const int at = pc.k;
-        pmore = advance(pc);
-        if (pc.k != at) tiles = pc.left;
-        lead = 1;
       }
       // Drain: all MMAs of this CTA have finished before TMEM is freed.
       mma_commit(bar(SM::B_FIN));
