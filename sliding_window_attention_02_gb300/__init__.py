@@ -174,33 +174,44 @@ def _device_index(t) -> int:
 def _stream_of(stream, index: int):
     """The given stream, or the current one of device `index`."""
     if stream is None:
-        import torch
-        return torch.cuda.current_stream(index).cuda_stream
+        return _current_stream(index)
     return getattr(stream, "cuda_stream", stream)
 
 
-def _rows(t, heads, d, dtype, index, name):
+def _current_stream(index: int):
+    """torch.cuda.current_stream(index).cuda_stream, without the Stream object
+    (1.1 us of a call) where torch gives the pointer itself."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _raw_stream(index)
+
+
+_raw_stream = None
+
+
+def _rows(t, shape, dtype, index, name):
     """(pointer, elements between rows) of rows of [heads][d] elements: a
     tensor [rows][heads][d] whose rows may be part of longer ones."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.dtype != dtype:
-        raise ValueError(f"{name}: expected [rows][{heads}][{d}] of {dtype}, "
-                         f"got {tuple(t.shape)} of {t.dtype}")
-    s = t.stride()
-    if (s[2] != 1 and d > 1) or (s[1] != d and heads > 1):
-        raise ValueError(f"{name}: the heads of a row must be contiguous")
-    if t.get_device() != index:
-        raise ValueError(f"{name}: expected a CUDA tensor of device {index}")
-    return t.data_ptr(), s[0]
+    if t.shape == shape and t.dtype is dtype and t.get_device() == index:
+        stride, inner, last = t.stride()
+        if last == 1 and (inner == shape[2] or shape[1] == 1):
+            return t.data_ptr(), stride
+    raise ValueError(f"{name}: expected {tuple(shape)} of {dtype} on CUDA device {index} with "
+                     f"the heads of a row contiguous, got {tuple(t.shape)} of {t.dtype} on "
+                     f"{t.device}, strides {t.stride()}")
 
 
 def _dense(t, shape, dtype, index, name):
     """Pointer of a contiguous CUDA tensor of this shape and type."""
-    if t.shape != shape or t.dtype != dtype:
-        raise ValueError(f"{name}: expected {tuple(shape)} of {dtype}, got "
-                         f"{tuple(t.shape)} of {t.dtype}")
-    if t.get_device() != index or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous CUDA tensor of device {index}")
-    return t.data_ptr()
+    if (t.shape == shape and t.dtype is dtype and t.get_device() == index
+            and t.is_contiguous()):
+        return t.data_ptr()
+    raise ValueError(f"{name}: expected {tuple(shape)} of {dtype}, contiguous on CUDA device "
+                     f"{index}, got {tuple(t.shape)} of {t.dtype} on {t.device}, strides "
+                     f"{t.stride()}")
 
 
 def rswa_strerror(status: int) -> str:
@@ -313,28 +324,21 @@ def rswa_qk_norm_rope(rope, q, k, positions, q_out, k_out, stream=None) -> None:
     """rope: RswaRope; q, k: [rows][heads][d], the rows possibly part of longer
     ones (a fused projection's output); positions: int64 [rows]; q_out, k_out:
     contiguous, or q and k themselves."""
-    import torch
     index = _device_index(q)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k: expected [rows][heads][d]")
     rows, heads, d = q.shape
-    kv_heads = k.shape[1] if k.dim() == 3 else 0
-    dt = q.dtype
-    if k.shape[0] != rows:
-        raise ValueError("q and k: different numbers of rows")
+    kv_heads, dt = k.shape[1], q.dtype
     rope.check(d, dt, index)
-    qp, qs = _rows(q, heads, d, dt, index, "q")
-    kp, ks = _rows(k, kv_heads, d, dt, index, "k")
-    args = (rope.ref, qp, qs, kp, ks,
-            _dense(positions, (rows,), torch.int64, index, "positions"), rows, heads,
-            kv_heads, d, _rswa_dtype(dt),
+    qp, qs = _rows(q, (rows, heads, d), dt, index, "q")
+    kp, ks = _rows(k, (rows, kv_heads, d), dt, index, "k")
+    args = (rope.ref, qp, qs, kp, ks, _dense(positions, (rows,), _int64(), index, "positions"),
+            rows, heads, kv_heads, d, _rswa_dtype(dt),
             _dense(q_out, (rows, heads, d), dt, index, "q_out"),
-            _dense(k_out, (rows, kv_heads, d), dt, index, "k_out"))
-    if index == torch.cuda.current_device():
-        _check(load().rswa_qk_norm_rope(*args, _stream_of(stream, index)),
-               "rswa_qk_norm_rope")
-    else:
-        with torch.cuda.device(index):
-            _check(load().rswa_qk_norm_rope(*args, _stream_of(stream, index)),
-                   "rswa_qk_norm_rope")
+            _dense(k_out, (rows, kv_heads, d), dt, index, "k_out"), _stream_of(stream, index))
+    status = _on_device(index, load().rswa_qk_norm_rope, args)
+    if status:
+        raise RswaError(status, "rswa_qk_norm_rope")
 
 
 def rswa_qk_norm_rope_cached(handle, rope, q, q_stride, k, k_stride, offsets, tokens,
@@ -422,11 +426,25 @@ def rswa_sync_status(handle) -> int:
 
 def _rswa_dtype(dt) -> int:
     import torch
-    if dt == torch.bfloat16:
+    if dt is torch.bfloat16:
         return RSWA_BF16
-    if dt == torch.float32:
+    if dt is torch.float32:
         return RSWA_F32
     raise ValueError(f"expected bfloat16 or float32, got {dt}")
+
+
+def _int64():
+    import torch
+    return torch.int64
+
+
+def _on_device(index, call, args):
+    """call(*args) with device `index` current."""
+    import torch
+    if index == torch.cuda.current_device():
+        return call(*args)
+    with torch.cuda.device(index):
+        return call(*args)
 
 
 class RswaRope:
@@ -485,9 +503,14 @@ class RswaCache:
         self.buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.handle = rswa_cache_create_gqa(m, n, heads, self.kv_heads,
                                             head_dim, batch, dtype, self.buf)
-        self._torch_dtype = torch.float32 if dtype == RSWA_F32 else torch.bfloat16
-        self._index = self.buf.get_device()
-        self._tree_ws = []          # smaller ones stay: captured graphs hold them
+        # what the checks of the draft-and-verify calls compare with
+        self._shape = (batch, heads, self.kv_heads, head_dim,
+                       torch.float32 if dtype == RSWA_F32 else torch.bfloat16,
+                       self.buf.get_device())
+        self._int32, self._float32 = torch.int32, torch.float32
+        # decode_tree's own workspaces, by node count; all stay, as captured
+        # graphs hold them
+        self._tree_ws = {}
 
     def close(self):
         if self.handle is not None:
@@ -524,37 +547,36 @@ class RswaCache:
         """Norm and rotate the heads of the next tokens of every sequence: q, k
         of [B * tokens][heads][d] rows (possibly part of longer ones), at
         positions m_b + t_b + offsets (int32 [B][tokens]; None: 0, 1, ...)."""
-        import torch
-        H, Hkv, d, dt, ix = (self.heads, self.kv_heads, self.head_dim,
-                             self._torch_dtype, self._index)
-        rope.check(d, dt, ix)
-        _, qs = _rows(q, H, d, dt, ix, "q")
-        _, ks = _rows(k, Hkv, d, dt, ix, "k")
+        B, H, Hkv, d, dt, ix = self._shape
         rows = q.shape[0]
-        if rows % self.batch or k.shape[0] != rows:
-            raise ValueError("q, k: expected batch * tokens rows each")
-        _dense(q_out, (rows, H, d), dt, ix, "q_out")
-        _dense(k_out, (rows, Hkv, d), dt, ix, "k_out")
-        if offsets is not None:
-            _dense(offsets, (self.batch, rows // self.batch), torch.int32, ix, "offsets")
-        rswa_qk_norm_rope_cached(self.handle, rope, q, qs, k, ks, offsets,
-                                 rows // self.batch, q_out, k_out, stream)
+        if rows % B:
+            raise ValueError("q: expected batch * tokens rows")
+        rope.check(d, dt, ix)
+        qp, qs = _rows(q, (rows, H, d), dt, ix, "q")
+        kp, ks = _rows(k, (rows, Hkv, d), dt, ix, "k")
+        op = None if offsets is None else _dense(offsets, (B, rows // B), self._int32, ix,
+                                                 "offsets")
+        status = load().rswa_qk_norm_rope_cached(
+            self.handle, rope.ref, qp, qs, kp, ks, op, rows // B,
+            _dense(q_out, (rows, H, d), dt, ix, "q_out"),
+            _dense(k_out, (rows, Hkv, d), dt, ix, "k_out"), _stream_of(stream, ix))
+        if status:
+            raise RswaError(status, "rswa_qk_norm_rope_cached")
 
     def append_kv_rope(self, rope, q, k, v, q_out, stream=None):
         """append_kv with the norm and rotation on the way: q, k, v of
         [B][heads][d] rows (possibly part of longer ones); q_out takes the
         normed and rotated queries for decode_step."""
-        H, Hkv, d, dt, ix = (self.heads, self.kv_heads, self.head_dim,
-                             self._torch_dtype, self._index)
+        B, H, Hkv, d, dt, ix = self._shape
         rope.check(d, dt, ix)
-        B = self.batch
-        _, qs = _rows(q, H, d, dt, ix, "q")
-        _, ks = _rows(k, Hkv, d, dt, ix, "k")
-        _, vs = _rows(v, Hkv, d, dt, ix, "v")
-        if q.shape[0] != B or k.shape[0] != B or v.shape[0] != B:
-            raise ValueError(f"q, k, v: expected {B} rows each")
-        _dense(q_out, (B, H, d), dt, ix, "q_out")
-        rswa_append_kv_rope(self.handle, rope, q, qs, k, ks, v, vs, q_out, stream)
+        qp, qs = _rows(q, (B, H, d), dt, ix, "q")
+        kp, ks = _rows(k, (B, Hkv, d), dt, ix, "k")
+        vp, vs = _rows(v, (B, Hkv, d), dt, ix, "v")
+        status = load().rswa_append_kv_rope(
+            self.handle, rope.ref, qp, qs, kp, ks, vp, vs,
+            _dense(q_out, (B, H, d), dt, ix, "q_out"), _stream_of(stream, ix))
+        if status:
+            raise RswaError(status, "rswa_append_kv_rope")
 
     def tree_workspace(self, nodes):
         """A workspace for decode_tree calls of up to `nodes` nodes."""
@@ -568,39 +590,51 @@ class RswaCache:
         (see rswa_decode_tree).  workspace: from tree_workspace; None: one the
         cache keeps, which has to exist before a stream capture (by a call
         outside it) and serves calls that do not overlap."""
-        import torch
-        B, H, Hkv, d, dt, ix = (self.batch, self.heads, self.kv_heads, self.head_dim,
-                                self._torch_dtype, self._index)
+        B, H, Hkv, d, dt, ix = self._shape
         nodes = q.shape[1]
-        _dense(q, (B, nodes, H, d), dt, ix, "q")
-        _dense(k, (B, nodes, Hkv, d), dt, ix, "k")
-        _dense(v, (B, nodes, Hkv, d), dt, ix, "v")
-        _dense(parents, (B, nodes), torch.int32, ix, "parents")
-        _dense(o, (B, nodes, H, d), dt, ix, "o")
-        if lse is not None:
-            _dense(lse, (B, nodes, H), torch.float32, ix, "lse")
-        if counts is not None:
-            _dense(counts, (B,), torch.int32, ix, "counts")
+        i32 = self._int32
+        qp = _dense(q, (B, nodes, H, d), dt, ix, "q")
+        kp = _dense(k, (B, nodes, Hkv, d), dt, ix, "k")
+        vp = _dense(v, (B, nodes, Hkv, d), dt, ix, "v")
+        pp = _dense(parents, (B, nodes), i32, ix, "parents")
+        op = _dense(o, (B, nodes, H, d), dt, ix, "o")
+        lp = None if lse is None else _dense(lse, (B, nodes, H), self._float32, ix, "lse")
+        cp = None if counts is None else _dense(counts, (B,), i32, ix, "counts")
         if workspace is None:
+            workspace = self._own_workspace(nodes)
+        status = load().rswa_decode_tree(
+            self.handle, qp, kp, vp, pp, cp, nodes, op, lp, _ptr(workspace),
+            workspace.numel(), _stream_of(stream, ix))
+        if status:
+            raise RswaError(status, "rswa_decode_tree")
+
+    def _own_workspace(self, nodes):
+        """The cache's workspace for trees of `nodes` nodes, made by the first
+        call that needs it (or a larger one)."""
+        have = self._tree_ws.get(nodes)
+        if have is None:
+            import torch
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError("decode_tree: no workspace of the cache's own yet: call it "
+                                 "once before the capture, or pass one")
             need = rswa_decode_tree_workspace(self.handle, nodes)
-            if not self._tree_ws or self._tree_ws[-1].numel() < need:
-                if torch.cuda.is_current_stream_capturing():
-                    raise ValueError("decode_tree: no workspace of the cache's own yet: "
-                                     "call it once before the capture, or pass one")
-                self._tree_ws.append(self.tree_workspace(nodes))
-            workspace = self._tree_ws[-1]
-        rswa_decode_tree(self.handle, q, k, v, parents, o, lse, workspace, counts, stream)
+            have = next((w for w in self._tree_ws.values() if w.numel() >= need), None)
+            if have is None:
+                have = self.tree_workspace(nodes)
+            self._tree_ws[nodes] = have
+        return have
 
     def commit_tree(self, k, v, path, accepted, stream=None):
         """Append the accepted nodes path[b][:accepted[b]] of a tree."""
-        import torch
-        B, ix = self.batch, self._index
-        shape = (B, k.shape[1], self.kv_heads, self.head_dim)
-        _dense(k, shape, self._torch_dtype, ix, "k")
-        _dense(v, shape, self._torch_dtype, ix, "v")
-        _dense(path, (B, path.shape[1]), torch.int32, ix, "path")
-        _dense(accepted, (B,), torch.int32, ix, "accepted")
-        rswa_commit_tree(self.handle, k, v, path, accepted, stream)
+        B, _, Hkv, d, dt, ix = self._shape
+        nodes, most = k.shape[1], path.shape[-1]
+        status = load().rswa_commit_tree(
+            self.handle, _dense(k, (B, nodes, Hkv, d), dt, ix, "k"),
+            _dense(v, (B, nodes, Hkv, d), dt, ix, "v"), nodes,
+            _dense(path, (B, most), self._int32, ix, "path"),
+            _dense(accepted, (B,), self._int32, ix, "accepted"), most, _stream_of(stream, ix))
+        if status:
+            raise RswaError(status, "rswa_commit_tree")
 
     def cache_bytes(self, b):
         return rswa_cache_bytes(self.handle, b)

@@ -21,6 +21,9 @@ struct rswa_cache {
   // decode launch: the launch right after one of those must not read prefix
   // rows or m_b before its dependency wait, later decode launches may.
   std::atomic<bool> prefix_stable{false};
+  // Tensor maps of the slabs for the tensor-core tree attention.
+  bool maps_ok = false;
+  SlabMaps maps;
 };
 
 namespace {
@@ -307,6 +310,7 @@ int rswa_cache_create_gqa(int64_t m, int64_t n, int heads, int kv_heads,
     delete c;
     return RSWA_ECUDA;
   }
+  if (dtype == RSWA_BF16) c->maps_ok = make_slab_maps(cv, &c->maps);
   {
     std::lock_guard<std::mutex> lk(g_mu);
     g_live.insert(c);
@@ -587,8 +591,10 @@ int rswa_decode_tree(rswa_cache* cache, const void* q, const void* k, const void
   a.o = o;
   a.lse = lse;
   a.ws = workspace;
+  if (decode_tree_tc_supported(cache->cv, a.nodes) && !cache->maps_ok) return RSWA_ECUDA;
   return run_decode(cache, [&](bool pf) {
-    return launch_decode_tree(cache->cv, a, pf, static_cast<cudaStream_t>(stream));
+    return launch_decode_tree(cache->cv, a, &cache->maps, pf,
+                              static_cast<cudaStream_t>(stream));
   });
 }
 

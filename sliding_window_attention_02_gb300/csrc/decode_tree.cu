@@ -163,9 +163,9 @@ size_t decode_tree_workspace(const CacheView& cv, int nodes) {
   return decode_tree_tc_supported(cv, nodes) ? decode_tree_tc_workspace(cv, nodes) : 256;
 }
 
-cudaError_t launch_decode_tree(const CacheView& cv, const TreeArgs& a, bool,
-                               cudaStream_t s) {
-  if (decode_tree_tc_supported(cv, a.nodes)) return launch_decode_tree_tc(cv, a, s);
+cudaError_t launch_decode_tree(const CacheView& cv, const TreeArgs& a, const SlabMaps* maps,
+                               bool, cudaStream_t s) {
+  if (decode_tree_tc_supported(cv, a.nodes)) return launch_decode_tree_tc(cv, a, *maps, s);
   if (cv.dtype == RSWA_F32)
     return cv.d == 64 ? launch_tree_t<float, 64>(cv, a, s)
                       : launch_tree_t<float, 128>(cv, a, s);

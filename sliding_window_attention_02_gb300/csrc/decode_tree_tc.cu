@@ -159,6 +159,7 @@ struct Shape {
   int pair;     // 1: units of two query tiles
   int G;        // query heads of a KV head
   int evict;    // 1: cache tiles are loaded evict-first
+  int flat;     // 1: a CTA for every unit, no unit is cut
   int joins;    // units of the launch, or its CTAs where those are fewer
 };
 
@@ -181,11 +182,15 @@ struct Seq {
     const int per = sh.npt << sh.pair;
     units = (cnt + per - 1) / per * cv.Hkv;
   }
-  __device__ int cost() const { return tl + kUnitCost; }          // of a unit
+  __device__ int cost(bool flat) const { return flat ? 1 : tl + kUnitCost; }   // of a unit
   // Cost of a unit's tiles before tile j, and the first tile that begins at or
-  // after cost x (tl: none).
-  __device__ int before(int j) const { return j > 0 ? j + kUnitCost : 0; }
-  __device__ int at(int x) const { return x <= 0 ? 0 : min(max(x - kUnitCost, 1), tl); }
+  // after cost x (tl: none).  Where no unit is cut, a unit costs 1 as a whole.
+  __device__ int before(int j, bool flat) const {
+    return j > 0 ? (flat ? 1 : j + kUnitCost) : 0;
+  }
+  __device__ int at(int x, bool flat) const {
+    return x <= 0 ? 0 : (flat ? tl : min(max(x - kUnitCost, 1), tl));
+  }
 };
 
 enum TileKind { kPrefix = 0, kRing = 1, kTree = 2 };
@@ -517,6 +522,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       }
       return true;
     };
+    const bool flat = sh.flat != 0;
     // The list's length, and the sequences of each lane in it.
     const int per = (cv.B + 31) / 32;
     const int b_lo = min(lane * per, cv.B), b_hi = min(b_lo + per, cv.B);
@@ -525,7 +531,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
 #pragma unroll 2
     for (int b = b_lo; b < b_hi; ++b) {
       sq.load(cv, a, sh, b);
-      mine += sq.cost() * sq.units;
+      mine += sq.cost(flat) * sq.units;
     }
     int inc = mine;
 #pragma unroll
@@ -535,7 +541,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     }
     const int total = __shfl_sync(0xffffffffu, inc, 31);
     // CTA c takes the tiles that begin in [from(c), from(c + 1)).
-    const int ctas = min(grid, max(1, total / kMinCost));
+    const int ctas = min(grid, max(1, flat ? total : total / kMinCost));
     const int each = total / ctas, rem = total - each * ctas;
     auto from = [&](int c) { return c * each + min(c, rem); };
     JoinDesc jd = {0, 0, 0, -1, 0, {0, 0, 0}};
@@ -551,8 +557,8 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         if (per > 1) {
           for (;; ++b) {
             sq.load(cv, a, sh, b);
-            if (x0 < base + sq.cost() * sq.units) break;
-            base += sq.cost() * sq.units;
+            if (x0 < base + sq.cost(flat) * sq.units) break;
+            base += sq.cost(flat) * sq.units;
           }
         }
       }
@@ -560,14 +566,14 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       b = __shfl_sync(0xffffffffu, b, src);
       base = __shfl_sync(0xffffffffu, base, src);
       sq.load(cv, a, sh, b);
-      int u = (x0 - base) / sq.cost();
-      int ubase = base + u * sq.cost();            // where unit u begins
-      int j0 = sq.at(x0 - ubase), par_b = -1;
+      int u = (x0 - base) / sq.cost(flat);
+      int ubase = base + u * sq.cost(flat);            // where unit u begins
+      int j0 = sq.at(x0 - ubase, flat), par_b = -1;
       const int unit_nodes = sh.npt << sh.pair;
       const int n = (int)min(cv.n, (int64_t)1 << 30);
       for (bool next_unit = j0 == sq.tl;; next_unit = true) {
         if (next_unit) {
-          ubase += sq.cost();
+          ubase += sq.cost(flat);
           j0 = 0;
           if (++u == sq.units) {
             u = 0;
@@ -576,14 +582,14 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
             if (sq.units == 0) break;            // the list's end
           }
         }
-        if (ubase + sq.before(j0) >= x1) break;  // a later CTA's
+        if (ubase + sq.before(j0, flat) >= x1) break;  // a later CTA's
         Segment w;
         w.b = b;
         w.kvh = u % cv.Hkv;
         w.node0 = u / cv.Hkv * unit_nodes;
         w.cnt = sq.cnt;
         w.j0 = j0;
-        w.j1 = sq.at(x1 - ubase);
+        w.j1 = sq.at(x1 - ubase, flat);
         w.np = sq.np;
         w.nr = sq.nr;
         w.m_b = sq.m_b;
@@ -611,7 +617,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         // nodes: their buffers are free later than those.
         if (k == 0) queries(w);
         if (j0 == 0 && !w.whole) {       // begun here, ended by the CTA of its last tile
-          const int x = ubase + sq.before(sq.tl - 1), cut = rem * (each + 1);
+          const int x = ubase + sq.before(sq.tl - 1, flat), cut = rem * (each + 1);
           jd = {b, w.node0, w.kvh,
                 min(ctas - 1, x < cut ? x / (each + 1) : rem + (x - cut) / each), sq.cnt,
                 {0, 0, 0}};
@@ -660,7 +666,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     if (lane == 0) {
       out[k % NSEG].j1 = 0;              // no more segments
       mbar_arrive(bar(SM::B_SEG + k % NSEG));
-      static_cast<JoinDesc*>(a.ws)[cta] = jd;
+      if (!flat) static_cast<JoinDesc*>(a.ws)[cta] = jd;
       // Drain: every copy issued has landed before the CTA may exit.
       for (int x = max(qi - NQ, 0); x < qi; ++x)
         wait_for(bar(SM::B_QF + x % NQ), (x / NQ) & 1, never, kWaitLimitNs);
@@ -1056,7 +1062,7 @@ Shape shape_of(const CacheView& cv, int nodes) {
   sh.G = cv.H / cv.Hkv;
   sh.npt = BM / sh.G;
   sh.pair = nodes > sh.npt ? 1 : 0;
-  sh.evict = sh.joins = 0;
+  sh.evict = sh.joins = sh.flat = 0;
   return sh;
 }
 
@@ -1065,30 +1071,35 @@ int64_t most_units(const CacheView& cv, int nodes, const Shape& sh) {
   const int per = sh.npt << sh.pair;
   return (int64_t)cv.B * cv.Hkv * ((nodes + per - 1) / per);
 }
-int64_t most_cost(const CacheView& cv, int nodes, const Shape& sh) {
-  const int64_t tiles = (cv.m_cap + BN - 1) / BN + (cv.n + BN - 1) / BN + (nodes + BN - 1) / BN;
-  return most_units(cv, nodes, sh) * (tiles + kUnitCost);
+int64_t most_tiles(const CacheView& cv, int nodes) {
+  return (cv.m_cap + BN - 1) / BN + (cv.n + BN - 1) / BN + (nodes + BN - 1) / BN;
 }
+int64_t most_cost(const CacheView& cv, int nodes, const Shape& sh) {
+  return most_units(cv, nodes, sh) * (most_tiles(cv, nodes) + kUnitCost);
+}
+
+// Units of up to this many tiles, no more of them than SMs, have a CTA each:
+// the second kernel would take longer than what cutting them saves.
+constexpr int kFlatTiles = 8;
 
 // CTAs of the launch: one per SM, no more than the largest list could feed.
 int grid_of(const CacheView& cv, int nodes, const Shape& sh) {
+  if (sh.flat) return (int)most_units(cv, nodes, sh);
   return (int)std::max<int64_t>(1, std::min<int64_t>(cv.sms, most_cost(cv, nodes, sh) / kMinCost));
 }
 
 template <int D, bool PAIR>
-cudaError_t launch_d(const CacheView& cv, const TreeArgs& a, cudaStream_t s) {
+cudaError_t launch_d(const CacheView& cv, const TreeArgs& a, const SlabMaps& maps,
+                     cudaStream_t s) {
   Shape sh = shape_of(cv, a.nodes);
+  sh.flat = most_units(cv, a.nodes, sh) <= cv.sms && most_tiles(cv, a.nodes) <= kFlatTiles;
   const int grid = grid_of(cv, a.nodes, sh);
   const uint64_t trows = (uint64_t)cv.B * a.nodes;
   const uint64_t crows = (uint64_t)cv.B * cv.Hkv * cv.slab_rows;
-  CUtensorMap mq, mkc, mvc, mkt, mvt, mkc16, mvc16, mkt16, mvt16;
+  CUtensorMap mq, mkt, mvt, mkt16, mvt16;
   if (!make_tmap_heads_bf16(&mq, a.q, D, cv.H, trows, sh.G, sh.npt) ||
-      !make_tmap_rows_bf16(&mkc, cv.K, D, crows) ||
-      !make_tmap_rows_bf16(&mvc, cv.V, D, crows) ||
       !make_tmap_rows_bf16(&mkt, a.k, (uint64_t)cv.Hkv * D, trows) ||
       !make_tmap_rows_bf16(&mvt, a.v, (uint64_t)cv.Hkv * D, trows) ||
-      !make_tmap_rows_bf16(&mkc16, cv.K, D, crows, 16) ||
-      !make_tmap_rows_bf16(&mvc16, cv.V, D, crows, 16) ||
       !make_tmap_rows_bf16(&mkt16, a.k, (uint64_t)cv.Hkv * D, trows, 16) ||
       !make_tmap_rows_bf16(&mvt16, a.v, (uint64_t)cv.Hkv * D, trows, 16))
     return cudaErrorInvalidValue;
@@ -1099,9 +1110,10 @@ cudaError_t launch_d(const CacheView& cv, const TreeArgs& a, cudaStream_t s) {
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, PAIR>::kBytes);
   if (e != cudaSuccess) return e;
   e = launch_dependent(decode_tree_tc_kernel<D, PAIR>, dim3(grid), dim3(kThreads), Smem<D, PAIR>::kBytes, s, mq,
-                       mkc, mvc, mkt, mvt, mkc16, mvc16, mkt16, mvt16, cv, a, sh,
+                       maps.k, maps.v, mkt, mvt, maps.k16, maps.v16, mkt16, mvt16, cv, a, sh,
                        phase_wait_limit_ns());
   if (e != cudaSuccess) return e;
+  if (sh.flat) return cudaSuccess;
   const int rows = PAIR ? 2 * BM : std::min(a.nodes, sh.npt) * sh.G;
   return launch_dependent(join_tree_kernel<D>,
                           dim3(sh.joins, (rows + 31) / 32, D / (4 * kJoinWarps)),
@@ -1124,10 +1136,19 @@ size_t decode_tree_tc_workspace(const CacheView& cv, int nodes) {
          grid * 2 * partial_floats(cv.d, sh.pair) * sizeof(float);
 }
 
-cudaError_t launch_decode_tree_tc(const CacheView& cv, const TreeArgs& a, cudaStream_t s) {
+bool make_slab_maps(const CacheView& cv, SlabMaps* maps) {
+  const uint64_t rows = (uint64_t)cv.B * cv.Hkv * cv.slab_rows;
+  return make_tmap_rows_bf16(&maps->k, cv.K, cv.d, rows) &&
+         make_tmap_rows_bf16(&maps->v, cv.V, cv.d, rows) &&
+         make_tmap_rows_bf16(&maps->k16, cv.K, cv.d, rows, 16) &&
+         make_tmap_rows_bf16(&maps->v16, cv.V, cv.d, rows, 16);
+}
+
+cudaError_t launch_decode_tree_tc(const CacheView& cv, const TreeArgs& a, const SlabMaps& maps,
+                                  cudaStream_t s) {
   if (shape_of(cv, a.nodes).pair)
-    return cv.d == 64 ? launch_d<64, true>(cv, a, s) : launch_d<128, true>(cv, a, s);
-  return cv.d == 64 ? launch_d<64, false>(cv, a, s) : launch_d<128, false>(cv, a, s);
+    return cv.d == 64 ? launch_d<64, true>(cv, a, maps, s) : launch_d<128, true>(cv, a, maps, s);
+  return cv.d == 64 ? launch_d<64, false>(cv, a, maps, s) : launch_d<128, false>(cv, a, maps, s);
 }
 
 }  // namespace rswa

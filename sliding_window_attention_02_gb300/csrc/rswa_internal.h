@@ -179,13 +179,21 @@ size_t decode_tree_workspace(const CacheView& cv, int nodes);
 // (decode_tree_tc.cu); the rest on the CUDA cores.
 bool decode_tree_tc_supported(const CacheView& cv, int nodes);
 size_t decode_tree_tc_workspace(const CacheView& cv, int nodes);
-cudaError_t launch_decode_tree_tc(const CacheView& cv, const TreeArgs& a, cudaStream_t s);
+// Its tensor maps of the cache slabs (boxes of 128 and of 16 rows): the slabs
+// stay where they are, so a handle makes them once.
+struct SlabMaps {
+  CUtensorMap k, v, k16, v16;
+};
+bool make_slab_maps(const CacheView& cv, SlabMaps* maps);
+cudaError_t launch_decode_tree_tc(const CacheView& cv, const TreeArgs& a, const SlabMaps& maps,
+                                  cudaStream_t s);
 // [rows][heads][d] bf16 as a 3-D TMA map: box 64 columns x box_heads heads x
 // box_rows rows, 128-byte swizzle.
 bool make_tmap_heads_bf16(CUtensorMap* map, const void* base, uint64_t d, uint64_t heads,
                           uint64_t rows, uint32_t box_heads, uint32_t box_rows);
-cudaError_t launch_decode_tree(const CacheView& cv, const TreeArgs& a, bool prefetch,
-                               cudaStream_t s);
+// maps: of decode_tree_tc_supported shapes, else unused.
+cudaError_t launch_decode_tree(const CacheView& cv, const TreeArgs& a, const SlabMaps* maps,
+                               bool prefetch, cudaStream_t s);
 cudaError_t launch_commit_tree(const CacheView& cv, const void* k, const void* v, int nodes,
                                const int32_t* path, const int32_t* accepted, int max_path,
                                cudaStream_t s);
