@@ -332,11 +332,19 @@ def rswa_qk_norm_rope(rope, q, k, positions, q_out, k_out, stream=None) -> None:
     rope.check(d, dt, index)
     qp, qs = _rows(q, (rows, heads, d), dt, index, "q")
     kp, ks = _rows(k, (rows, kv_heads, d), dt, index, "k")
-    args = (rope.ref, qp, qs, kp, ks, _dense(positions, (rows,), _int64(), index, "positions"),
-            rows, heads, kv_heads, d, _rswa_dtype(dt),
-            _dense(q_out, (rows, heads, d), dt, index, "q_out"),
+    torch = rope.torch
+    code = RSWA_BF16 if dt is torch.bfloat16 else RSWA_F32 if dt is torch.float32 else -1
+    if code < 0:
+        raise ValueError(f"q, k: expected bfloat16 or float32, got {dt}")
+    args = (rope.ref, qp, qs, kp, ks,
+            _dense(positions, (rows,), torch.int64, index, "positions"), rows, heads, kv_heads,
+            d, code, _dense(q_out, (rows, heads, d), dt, index, "q_out"),
             _dense(k_out, (rows, kv_heads, d), dt, index, "k_out"), _stream_of(stream, index))
-    status = _on_device(index, load().rswa_qk_norm_rope, args)
+    if index == torch.cuda.current_device():
+        status = load().rswa_qk_norm_rope(*args)
+    else:
+        with torch.cuda.device(index):
+            status = load().rswa_qk_norm_rope(*args)
     if status:
         raise RswaError(status, "rswa_qk_norm_rope")
 
@@ -424,29 +432,6 @@ def rswa_sync_status(handle) -> int:
     return load().rswa_sync_status(handle)
 
 
-def _rswa_dtype(dt) -> int:
-    import torch
-    if dt is torch.bfloat16:
-        return RSWA_BF16
-    if dt is torch.float32:
-        return RSWA_F32
-    raise ValueError(f"expected bfloat16 or float32, got {dt}")
-
-
-def _int64():
-    import torch
-    return torch.int64
-
-
-def _on_device(index, call, args):
-    """call(*args) with device `index` current."""
-    import torch
-    if index == torch.cuda.current_device():
-        return call(*args)
-    with torch.cuda.device(index):
-        return call(*args)
-
-
 class RswaRope:
     """The norm and rotation of a layer's query and key heads (struct
     rswa_rope), with the tensors it points to.
@@ -460,6 +445,7 @@ class RswaRope:
     def __init__(self, inv_freq, q_weight=None, k_weight=None, eps=1e-6,
                  interleaved=False):
         import torch
+        self.torch = torch
         self.inv_freq, self.q_weight, self.k_weight = inv_freq, q_weight, k_weight
         if inv_freq is not None and (inv_freq.dtype != torch.float64
                                      or inv_freq.dim() != 1):
