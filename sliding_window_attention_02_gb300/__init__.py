@@ -324,22 +324,24 @@ def rswa_qk_norm_rope(rope, q, k, positions, q_out, k_out, stream=None) -> None:
     """rope: RswaRope; q, k: [rows][heads][d], the rows possibly part of longer
     ones (a fused projection's output); positions: int64 [rows]; q_out, k_out:
     contiguous, or q and k themselves."""
-    index = _device_index(q)
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k: expected [rows][heads][d]")
-    rows, heads, d = q.shape
-    kv_heads, dt = k.shape[1], q.dtype
-    rope.check(d, dt, index)
-    qp, qs = _rows(q, (rows, heads, d), dt, index, "q")
-    kp, ks = _rows(k, (rows, kv_heads, d), dt, index, "k")
-    torch = rope.torch
+    index, dt, torch = q.get_device(), q.dtype, rope.torch
+    rows, heads, d = shape = q.shape
+    kv_heads = k.shape[1]
+    k_shape = (rows, kv_heads, d)
+    if index < 0:
+        raise ValueError("q: expected a CUDA tensor")
     code = RSWA_BF16 if dt is torch.bfloat16 else RSWA_F32 if dt is torch.float32 else -1
     if code < 0:
         raise ValueError(f"q, k: expected bfloat16 or float32, got {dt}")
+    rope.check(d, dt, index)
+    qp, qs = _rows(q, shape, dt, index, "q")
+    kp, ks = _rows(k, k_shape, dt, index, "k")
     args = (rope.ref, qp, qs, kp, ks,
             _dense(positions, (rows,), torch.int64, index, "positions"), rows, heads, kv_heads,
-            d, code, _dense(q_out, (rows, heads, d), dt, index, "q_out"),
-            _dense(k_out, (rows, kv_heads, d), dt, index, "k_out"), _stream_of(stream, index))
+            d, code, _dense(q_out, shape, dt, index, "q_out"),
+            _dense(k_out, k_shape, dt, index, "k_out"), _stream_of(stream, index))
     if index == torch.cuda.current_device():
         status = load().rswa_qk_norm_rope(*args)
     else:
@@ -464,15 +466,19 @@ class RswaRope:
         # what its calls' heads have to be
         self._need = [(w.numel(), w.dtype) for w in weights]
         self._index = _device_index(tensors[0]) if tensors else None
+        self._fits = None               # the last heads that passed
 
     def check(self, d, dtype, index):
         """Raise unless it fits heads of d elements of dtype on device index."""
+        if (d, dtype, index) == self._fits:
+            return
         for need in self._need:
             if need != (d, dtype):
                 raise ValueError(f"rope: weights of {need[0]} {need[1]}, heads of "
                                  f"{d} {dtype}")
         if self._index is not None and self._index != index:
             raise ValueError("rope: on another device than the heads")
+        self._fits = (d, dtype, index)
 
 
 class RswaCache:

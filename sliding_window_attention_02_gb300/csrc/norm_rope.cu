@@ -26,7 +26,7 @@
 // of every pair into shared memory, while its warps' first heads are on their
 // way, and a head costs a' = r (a A - b B), b' = r (b C + a D), two elements an
 // instruction (f32x2): 3.5 instructions an element with the conversions.
-#include <algorithm>
+#include <atomic>
 
 #include "rswa_device.cuh"
 
@@ -140,7 +140,6 @@ struct RopeLane {
   using C = RopeCfg<T, D>;
   int c0, c1;
   bool r0, r1;
-  uint64_t k0[C::E], k1[C::E];                 // its entries' halves
   __device__ __forceinline__ RopeLane(int rotary_dim, int lane) {
     const int j = lane % C::L, rc = rotary_dim / C::E;
     if (IL) {
@@ -154,17 +153,12 @@ struct RopeLane {
       c1 = r0 ? j + rc / 2 : 2 * j + 1;
     }
   }
-  __device__ __forceinline__ void entries(const float4* tab, int lane) {
-#pragma unroll
-    for (int e = 0; e < C::E; ++e) {
-      const float4 x = tab[e * C::L + lane % C::L];
-      k0[e] = f2_pack(x.x, x.y);
-      k1[e] = f2_pack(x.z, x.w);
-    }
-  }
   // The head's vectors, normed (`norm`) and rotated, in place.  Every lane of
-  // the warp calls it.
-  __device__ __forceinline__ void apply(uint4& v0, uint4& v1, bool norm, float eps) const {
+  // the warp calls it.  tab: this lane's first table entry; each is used once,
+  // straight from shared memory (held in registers for all heads of the row,
+  // the entries cost 32 registers and with them a third of the CTAs).
+  __device__ __forceinline__ void apply(uint4& v0, uint4& v1, const float4* tab, bool norm,
+                                        float eps) const {
     float x0[C::E], x1[C::E];
     Elt<T>::widen(v0, x0);
     Elt<T>::widen(v1, x1);
@@ -184,11 +178,12 @@ struct RopeLane {
     const uint64_t r2 = f2_pack(r, r);
     if (IL) {
       auto turn = [&](uint64_t x, int e, bool rot) {
-        uint64_t y = f2_mul(x, k0[e]);
+        const float4 k = tab[e * C::L];
+        uint64_t y = f2_mul(x, f2_pack(k.x, k.y));
         if (rot) {
           float p, q;
           f2_unpack(x, p, q);
-          y = f2_fma(f2_pack(q, p), k1[e], y);
+          y = f2_fma(f2_pack(q, p), f2_pack(k.z, k.w), y);
         }
         return f2_mul(y, r2);
       };
@@ -200,10 +195,11 @@ struct RopeLane {
     } else {
 #pragma unroll
       for (int e = 0; e < C::E / 2; ++e) {
-        uint64_t x = f2_mul(a[e], k0[2 * e]), y = f2_mul(b[e], k0[2 * e + 1]);
+        const float4 k = tab[2 * e * C::L], l = tab[(2 * e + 1) * C::L];
+        uint64_t x = f2_mul(a[e], f2_pack(k.x, k.y)), y = f2_mul(b[e], f2_pack(l.x, l.y));
         if (r0) {
-          x = f2_fma(b[e], k1[2 * e], x);
-          y = f2_fma(a[e], k1[2 * e + 1], y);
+          x = f2_fma(b[e], f2_pack(k.z, k.w), x);
+          y = f2_fma(a[e], f2_pack(l.z, l.w), y);
         }
         a[e] = f2_mul(x, r2);
         b[e] = f2_mul(y, r2);
@@ -219,14 +215,17 @@ struct RopeLane {
   }
 };
 
-constexpr int kRopeThreads = 256, kRopeWarps = kRopeThreads / 32;
-constexpr int kRopeBatch = 5;                  // head groups a warp has in flight
+constexpr int kRopeThreads = 128, kRopeWarps = kRopeThreads / 32;
+constexpr int kRopeBatch = 2;                  // head groups a warp has in flight
 
-// CTAs of 8 warps for R = 1, 2, 4 or 8 rows; the 8 / R warps of a row share its
+// CTAs of 4 warps for R = 1, 2 or 4 rows; the 4 / R warps of a row share its
 // head groups (HPW heads, queries then keys).  Bound by HBM: every head is read
-// and written once.
+// and written once.  Many small CTAs (8 an SM, 64 registers a thread) hide each
+// other's start: 32768 rows of 10 + 10 heads, d 128, bf16 take 57.7 us (5.8
+// TB/s) so, 63.6 with 4 CTAs of an SM and five groups in flight, 72 with CTAs of
+// 8 warps that held the entries in registers.
 template <typename T, int D, bool IL>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, 8)
 norm_rope_kernel(rswa_rope rp, RopeRows rr, CacheView cv, int R) {
   using C = RopeCfg<T, D>;
   __shared__ float4 tab[kRopeWarps][2][C::P];
@@ -277,7 +276,6 @@ norm_rope_kernel(rswa_rope rp, RopeRows rr, CacheView cv, int R) {
   }
   __syncthreads();
   const int groups = (heads + C::HPW - 1) / C::HPW;
-  int type = -1;                               // of the entries held: 0 queries, 1 keys
   for (int i = 0; warp % wpr + wpr * kRopeBatch * i < groups; ++i) {
     if (i > 0) load(i);
 #pragma unroll
@@ -285,11 +283,8 @@ norm_rope_kernel(rswa_rope rp, RopeRows rr, CacheView cv, int R) {
       const int h = head_of(i, x);
       const int t = h >= rr.H;
       if (h - lane / C::L >= heads) break;     // the warp's groups end
-      if (__any_sync(0xffffffffu, t != type)) {
-        type = t;
-        rl.entries(tab[lr][t], lane);
-      }
-      rl.apply(v0[x], v1[x], (t ? rp.k_weight : rp.q_weight) != nullptr, rp.eps);
+      rl.apply(v0[x], v1[x], tab[lr][t] + lane % C::L,
+               (t ? rp.k_weight : rp.q_weight) != nullptr, rp.eps);
       if (on_row && h < heads) {
         T* out = t ? static_cast<T*>(rr.k_out) + (row * rr.Hkv + h - rr.H) * D
                    : static_cast<T*>(rr.q_out) + (row * rr.H + h) * D;
@@ -347,8 +342,7 @@ append_rope_kernel(CacheView cv, rswa_rope rp, const T* q, int64_t q_stride, con
     const int h = h0 + lane / C::L;
     const int t = h >= per_kv;
     if (h0 > warp * C::HPW) load(h);
-    rl.entries(tab[t], lane);
-    rl.apply(v0, v1, (t ? rp.k_weight : rp.q_weight) != nullptr, rp.eps);
+    rl.apply(v0, v1, tab[t] + lane % C::L, (t ? rp.k_weight : rp.q_weight) != nullptr, rp.eps);
     if (h <= per_kv) {
       T* out = t ? static_cast<T*>(cv.K) + slot * D
                  : q_out + ((int64_t)b * cv.H + (int64_t)kvh * per_kv + h) * D;
@@ -362,8 +356,8 @@ append_rope_kernel(CacheView cv, rswa_rope rp, const T* q, int64_t q_stride, con
 template <typename T, int D, bool IL>
 cudaError_t norm_rope_t(const rswa_rope& rp, const RopeRows& rr, const CacheView& cv, int sms,
                         cudaStream_t s) {
-  // Rows of a CTA: 8 where that still fills the SMs twice, else fewer, with more
-  // warps for each.
+  // Rows of a CTA: one a warp where that still fills the SMs twice, else fewer,
+  // with more warps for each.
   int R = kRopeWarps;
   while (R > 1 && (rr.rows + R - 1) / R < 2 * (int64_t)sms) R >>= 1;
   const int64_t blocks = (rr.rows + R - 1) / R;
@@ -391,10 +385,12 @@ cudaError_t append_rope_d(const CacheView& cv, const rswa_rope& rp, const void* 
 
 // SMs of the current device.
 int current_sms() {
+  static std::atomic<int> known[64];           // a device's count does not change
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+  if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
 
