@@ -301,7 +301,8 @@ typedef struct rswa_rope {
  *   q_out, k_out [rows][heads][d] and [rows][kv_heads][d], contiguous.  q_out
  *                may be q and k_out may be k where the stride is the row's own
  *                length; they must not overlap the inputs in another way.
- * Needs no cache; runs on the current device, to which the stream and all
+ * 0 <= rows < 2^31, heads and kv_heads 1 .. 4096.  Needs no cache; runs on the
+ * current device, to which the stream and all
  * pointers belong.  All pointers 16-byte aligned (positions and inv_freq
  * 8-byte).  rows = 0 does nothing.
  * Errors: RSWA_EINVAL, RSWA_EDTYPE (dtype, head_dim), RSWA_ECUDA.
@@ -320,6 +321,7 @@ RSWA_API int rswa_qk_norm_rope(const rswa_rope* rope, const void* q,
  * rswa_decode_step_fused (tokens = 1), rswa_decode_block, and rswa_decode_tree
  * (offsets = the nodes' depths).  Heads, head_dim and dtype are the cache's.
  * m_b and t_b are read on the device; the cache is not changed.
+ * tokens >= 1, B * tokens < 2^31.
  * Errors: RSWA_EHANDLE, RSWA_EINVAL, RSWA_ECUDA.
  */
 RSWA_API int rswa_qk_norm_rope_cached(rswa_cache* cache, const rswa_rope* rope,

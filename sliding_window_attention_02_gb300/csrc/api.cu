@@ -485,7 +485,7 @@ int rswa_qk_norm_rope(const rswa_rope* rope, const void* q, int64_t q_stride,
   if (dtype != RSWA_F32 && dtype != RSWA_BF16) return RSWA_EDTYPE;
   if (head_dim != 64 && head_dim != 128) return RSWA_EDTYPE;
   if (!valid_rope(rope, head_dim)) return RSWA_EINVAL;
-  if (rows < 0 || rows > (int64_t(1) << 40) || heads < 1 || kv_heads < 1 ||
+  if (rows < 0 || rows >= (int64_t(1) << 31) || heads < 1 || kv_heads < 1 ||
       heads > 4096 || kv_heads > 4096)
     return RSWA_EINVAL;
   if (rows == 0) return RSWA_OK;
@@ -520,6 +520,7 @@ int rswa_qk_norm_rope_cached(rswa_cache* cache, const rswa_rope* rope, const voi
   if (!valid_rope(rope, cv.d) || tokens < 1 || tokens > (int64_t(1) << 24))
     return RSWA_EINVAL;
   const int64_t rows = tokens * cv.B;
+  if (rows >= (int64_t(1) << 31)) return RSWA_EINVAL;
   if (!aligned4(offsets) || !q_out || !k_out || !aligned16(q_out) || !aligned16(k_out) ||
       !valid_rows(q, q_stride, (int64_t)cv.H * cv.d, rows, cv.dtype) ||
       !valid_rows(k, k_stride, (int64_t)cv.Hkv * cv.d, rows, cv.dtype))
@@ -591,7 +592,7 @@ int rswa_decode_tree(rswa_cache* cache, const void* q, const void* k, const void
   a.o = o;
   a.lse = lse;
   a.ws = workspace;
-  if (decode_tree_tc_supported(cache->cv, a.nodes) && !cache->maps_ok) return RSWA_ECUDA;
+  if (decode_tree_use_tc(cache->cv, a.nodes) && !cache->maps_ok) return RSWA_ECUDA;
   return run_decode(cache, [&](bool pf) {
     return launch_decode_tree(cache->cv, a, &cache->maps, pf,
                               static_cast<cudaStream_t>(stream));

@@ -20,8 +20,12 @@ constexpr int kTreeWarps = 8;
 
 // One CTA of 8 warps per (node, query head, sequence): the warps split every
 // key segment between them and merge in shared memory.  A node past the
-// sequence's count is left alone.
-template <typename T, int D>
+// sequence's count is left alone.  Bound by latency for the few nodes it is
+// used for: the walk to the root runs in one lane while the warps are at the
+// prefix, whose first rows are requested before the dependency wait where the
+// preceding kernel of the stream writes no prefix row (PREFETCH, the handle's
+// flag).
+template <typename T, int D, bool PREFETCH>
 __global__ void __launch_bounds__(kTreeWarps * 32)
 decode_tree_kernel(CacheView cv, TreeArgs a) {
   using C = AttendCfg<T, D>;
@@ -34,11 +38,31 @@ decode_tree_kernel(CacheView cv, TreeArgs a) {
   const int b = blockIdx.y;
   const int i = blockIdx.x / cv.H, h = blockIdx.x % cv.H;
   const int kvh = h / (cv.H / cv.Hkv);
+  const size_t bkv = (size_t)b * cv.Hkv + kvh;
+  const T* Kb = static_cast<const T*>(cv.K) + bkv * cv.slab_rows * D;
+  const T* Vb = static_cast<const T*>(cv.V) + bkv * cv.slab_rows * D;
+  const int64_t first = (int64_t)warp * C::KEYS_WARP, step = (int64_t)NW * C::KEYS_WARP;
+  int64_t m_b = 0;
+  AttendBatch<T, D> pre;
+  bool have_pre = false;
+  if (PREFETCH) {
+    m_b = cv.m_dev[b];
+    if (first < m_b) {
+      attend_load<T, D>(Kb, Vb, D, first, 0, m_b, -1, nullptr, nullptr, lane, INT64_MAX, 0,
+                        pre);
+      have_pre = true;
+    }
+  }
   griddep_wait();
   griddep_launch_dependents();
-  if (i >= live_nodes(a.counts, b, a.nodes, cv.err)) return;
+  if (!PREFETCH) m_b = cv.m_dev[b];
+  const int64_t t_b = cv.t_dev[(size_t)b * cv.H + h];
   const int64_t n = cv.n;
-  if (threadIdx.x == 0) {
+  const size_t qrow = ((size_t)b * a.nodes + i) * cv.H + h;
+  if (i >= live_nodes(a.counts, b, a.nodes, cv.err)) return;
+  float qf[C::EPL];
+  load_q_frag<T, D>(static_cast<const T*>(a.q) + qrow * D, lane, qf);
+  if (threadIdx.x == (NW - 1) * 32) {
     // Parents come before their children, so the walk ends; a parent that
     // does not is flagged and taken as none.
     const int32_t* par = a.parents + (size_t)b * a.nodes;
@@ -54,19 +78,14 @@ decode_tree_kernel(CacheView cv, TreeArgs a) {
     s_len = len;
     s_depth = depth;
   }
-  __syncthreads();
-  const int64_t m_b = cv.m_dev[b], t_b = cv.t_dev[(size_t)b * cv.H + h];
-  const int len = s_len;
-  const size_t bkv = (size_t)b * cv.Hkv + kvh;
-  const T* Kb = static_cast<const T*>(cv.K) + bkv * cv.slab_rows * D;
-  const T* Vb = static_cast<const T*>(cv.V) + bkv * cv.slab_rows * D;
-  const int64_t first = (int64_t)warp * C::KEYS_WARP, step = (int64_t)NW * C::KEYS_WARP;
-  const size_t qrow = ((size_t)b * a.nodes + i) * cv.H + h;
-  float qf[C::EPL];
-  load_q_frag<T, D>(static_cast<const T*>(a.q) + qrow * D, lane, qf);
+  __syncwarp();
   SoftmaxState<C::EPL> st;
   st.init();
-  attend_range<T, D>(qf, Kb, Vb, D, 0, m_b, first, step, -1, nullptr, nullptr, lane, st);
+  if (have_pre) attend_consume<T, D>(qf, pre, st);
+  attend_range<T, D>(qf, Kb, Vb, D, 0, m_b, have_pre ? first + step : first, step, -1, nullptr,
+                     nullptr, lane, st);
+  __syncthreads();
+  const int len = s_len;
   const int64_t j_lo = max((int64_t)0, t_b + s_depth - n + 1);
   if (j_lo < t_b) {
     const T* Kr = Kb + cv.m_cap * D;
@@ -151,26 +170,49 @@ commit_tree_kernel(CacheView cv, const T* k, const T* v, int nodes, const int32_
 }
 
 template <typename T, int D>
-cudaError_t launch_tree_t(const CacheView& cv, const TreeArgs& a, cudaStream_t s) {
-  return launch_dependent(decode_tree_kernel<T, D>,
+cudaError_t launch_tree_t(const CacheView& cv, const TreeArgs& a, bool prefetch,
+                          cudaStream_t s) {
+  return launch_dependent(prefetch ? decode_tree_kernel<T, D, true>
+                                   : decode_tree_kernel<T, D, false>,
                           dim3((unsigned)a.nodes * cv.H, (unsigned)cv.B),
                           dim3(kTreeWarps * 32), 0, s, cv, a);
 }
 
 }  // namespace
 
+// Small work is done sooner on the CUDA cores, whose kernel takes 3.4 us and the
+// larger of 7.1 ns a key (while its CTAs fit the SMs twice) and 65 ps for each
+// pair of a query row and a key; the tensor-core kernel takes 11 us while a
+// unit's keys are few and 15 and more where it cuts them.  bf16, d 128, 10 heads,
+// us on the CUDA / tensor cores: 16 nodes 7.8 / 10.9 at 416 keys, 17.0 / 15.6 at
+// 1184; 32 nodes 12.9 / 10.8 at 416; 1 node 11.2 / 16.6 at 1184, 34 / 16 at 4256.
+// The keys are the cache's capacity: the host does not know the live ones.
+constexpr int64_t kCudaCorePairs = 110000, kCudaCoreKeys = 1200;
+
+static bool small_work(const CacheView& cv, int nodes) {
+  const int64_t keys = cv.m_cap + cv.n;
+  return keys <= kCudaCoreKeys && (int64_t)cv.B * cv.H * nodes * keys <= kCudaCorePairs;
+}
+
+bool decode_tree_use_tc(const CacheView& cv, int nodes) {
+  return !small_work(cv, nodes) && decode_tree_tc_supported(cv, nodes);
+}
+
 size_t decode_tree_workspace(const CacheView& cv, int nodes) {
-  return decode_tree_tc_supported(cv, nodes) ? decode_tree_tc_workspace(cv, nodes) : 256;
+  // For any count of nodes that may come, not only those the kernel takes: a
+  // workspace for more nodes serves fewer.
+  if (small_work(cv, nodes) || cv.dtype != RSWA_BF16 || cv.H / cv.Hkv > 128) return 256;
+  return decode_tree_tc_workspace(cv, nodes);
 }
 
 cudaError_t launch_decode_tree(const CacheView& cv, const TreeArgs& a, const SlabMaps* maps,
-                               bool, cudaStream_t s) {
-  if (decode_tree_tc_supported(cv, a.nodes)) return launch_decode_tree_tc(cv, a, *maps, s);
+                               bool prefetch, cudaStream_t s) {
+  if (decode_tree_use_tc(cv, a.nodes)) return launch_decode_tree_tc(cv, a, *maps, s);
   if (cv.dtype == RSWA_F32)
-    return cv.d == 64 ? launch_tree_t<float, 64>(cv, a, s)
-                      : launch_tree_t<float, 128>(cv, a, s);
-  return cv.d == 64 ? launch_tree_t<__nv_bfloat16, 64>(cv, a, s)
-                    : launch_tree_t<__nv_bfloat16, 128>(cv, a, s);
+    return cv.d == 64 ? launch_tree_t<float, 64>(cv, a, prefetch, s)
+                      : launch_tree_t<float, 128>(cv, a, prefetch, s);
+  return cv.d == 64 ? launch_tree_t<__nv_bfloat16, 64>(cv, a, prefetch, s)
+                    : launch_tree_t<__nv_bfloat16, 128>(cv, a, prefetch, s);
 }
 
 cudaError_t launch_commit_tree(const CacheView& cv, const void* k, const void* v, int nodes,

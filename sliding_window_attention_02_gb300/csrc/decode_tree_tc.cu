@@ -108,7 +108,7 @@ constexpr uint64_t kWaitLimitNs = 1000000000ull;
 // first tile carries the unit's start and end as well.  A CTA's share is never
 // below kMinCost, so that it holds a tile at least and no join is made for less
 // work than it costs.
-constexpr int kUnitCost = 2, kMinCost = 7;
+constexpr int kUnitCost = 2, kMinCost = 3;
 static_assert(kMinCost >= 1 + kUnitCost, "a share holds a tile");
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x,
@@ -527,11 +527,12 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     const int per = (cv.B + 31) / 32;
     const int b_lo = min(lane * per, cv.B), b_hi = min(b_lo + per, cv.B);
     Seq sq;
-    int mine = 0;
+    int mine = 0, my_units = 0;
 #pragma unroll 2
     for (int b = b_lo; b < b_hi; ++b) {
       sq.load(cv, a, sh, b);
       mine += sq.cost(flat) * sq.units;
+      my_units += sq.units;
     }
     int inc = mine;
 #pragma unroll
@@ -540,10 +541,23 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       if (lane >= off) inc += x;
     }
     const int total = __shfl_sync(0xffffffffu, inc, 31);
-    // CTA c takes the tiles that begin in [from(c), from(c + 1)).
-    const int ctas = min(grid, max(1, flat ? total : total / kMinCost));
+    const int units = __reduce_add_sync(0xffffffffu, my_units);
+    // CTA c takes the tiles that begin in [from(c), from(c + 1)).  Few units have
+    // the same number of CTAs each, if they are alike: their ends meet CTAs' ends.
+    int ctas = min(grid, max(1, flat ? total : total / kMinCost));
+    if (units > 0 && units < ctas) ctas -= ctas % units;
+    const bool small = total < 1 << 22;          // c * total fits 32 bits
     const int each = total / ctas, rem = total - each * ctas;
-    auto from = [&](int c) { return c * each + min(c, rem); };
+    auto from = [&](int c) {
+      return small ? (int)((uint32_t)c * (uint32_t)total / (uint32_t)ctas)
+                   : c * each + min(c, rem);
+    };
+    // The last CTA that begins at or before cost x.
+    auto owner = [&](int x) {
+      if (small) return (int)(((uint32_t)(x + 1) * (uint32_t)ctas - 1) / (uint32_t)total);
+      const int cut = rem * (each + 1);
+      return min(ctas - 1, x < cut ? x / (each + 1) : rem + (x - cut) / each);
+    };
     JoinDesc jd = {0, 0, 0, -1, 0, {0, 0, 0}};
     int k = 0;
     if (cta < ctas && total > 0) {
@@ -617,10 +631,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         // nodes: their buffers are free later than those.
         if (k == 0) queries(w);
         if (j0 == 0 && !w.whole) {       // begun here, ended by the CTA of its last tile
-          const int x = ubase + sq.before(sq.tl - 1, flat), cut = rem * (each + 1);
-          jd = {b, w.node0, w.kvh,
-                min(ctas - 1, x < cut ? x / (each + 1) : rem + (x - cut) / each), sq.cnt,
-                {0, 0, 0}};
+          jd = {b, w.node0, w.kvh, owner(ubase + sq.before(sq.tl - 1, flat)), sq.cnt, {0, 0, 0}};
         }
         // Depths and ancestors of the unit's nodes, where the segment's ring
         // and tree tiles ask for them.
@@ -849,9 +860,10 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
           tc_fence_before();
         }
         started = true;
-        if (kind == kTree && keys % 16 != 0 && (warp & 3) == 0) {
-          // Value rows keys .. up to the next 16 belong to nodes past the
-          // count, or to the next sequence, and may hold anything: zero.
+        if (keys % 16 != 0 && (warp & 3) == 0) {
+          // Value rows keys .. up to the next 16 are no keys of any row (of the
+          // tree, nodes past the count or the next sequence's) and may hold
+          // anything: zero, as 0 x NaN is NaN.
           const uint32_t vi = 2u * (uint32_t)(w.tiles + j - w.j0) + 1u;
           if (__all_sync(0xffffffffu, wait_for(bar(SM::B_FULL + vi % NS), (vi / NS) & 1,
                                                 abort_flag, wait_ns))) {
@@ -973,45 +985,51 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
 
 // Joins the partials of the units that the CTAs' ranges cut.  Block (x, y, z):
 // the x-th CTA that begins a unit and does not end it, rows 32 y .. 32 y + 31
-// of that unit (lane = row), 16 columns (4 a warp).  Few threads and registers,
-// so that blocks are resident beside the first kernel's CTAs before those end.
+// of that unit (lane = row).  MANY: few units are cut into many parts; the block
+// joins float4 z of the rows, each of its four warps every fourth partial, up to
+// four at a time, so that the reads of 16 parts are one round trip.  Else many
+// units are cut into two or three: the warps take a float4 each, 4 z + warp, and
+// all the partials (a block for every float4 would be 38912 blocks and 35 us for
+// 152 units of 256 rows).
 constexpr int kJoinWarps = 4;
 
-template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32, 10)
+template <int D, bool MANY>
+__global__ void __launch_bounds__(kJoinWarps * 32, 8)
 join_tree_kernel(CacheView cv, TreeArgs a, Shape sh, int ctas) {
+  __shared__ float sm[kJoinWarps][6][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_wait();
   griddep_launch_dependents();
   const JoinDesc* desc = static_cast<const JoinDesc*>(a.ws);
   int c = -1;
-  for (int c0 = 0, skip = blockIdx.x; c0 < ctas; c0 += 256) {
-    int last[8];
+  for (int c0 = 0, skip = blockIdx.x; c < 0 && c0 < ctas; c0 += 160) {
+    int last[5];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 5; ++i) {
       const int x = c0 + 32 * i + lane;
       last[i] = x < ctas ? desc[x].last : -1;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 5; ++i) {
       const uint32_t on = __ballot_sync(0xffffffffu, last[i] >= 0);
       const int cnt = __popc(on);
       if (c < 0 && skip < cnt) c = c0 + 32 * i + (int)__fns(on, 0, skip + 1);
       skip -= cnt;
     }
-    if (c >= 0) break;
   }
   if (c < 0) return;
   const JoinDesc jd = desc[c];
   const int prow = blockIdx.y * 32 + lane, prows = BM << sh.pair;
   const int r = prow & (BM - 1), rg = r / sh.G;
   const int node = jd.node0 + (prow >= BM ? sh.npt : 0) + rg;
-  if (rg >= sh.npt || node >= jd.cnt) return;
-  const int col4 = blockIdx.z * kJoinWarps + warp;       // float4 of the row
-  constexpr int PB = 4;                                  // partials read at a time
+  const bool live = rg < sh.npt && node < jd.cnt;
+  if (!__syncthreads_or(live)) return;
+  constexpr int PB = 4;                                  // partials of a warp at a time
+  constexpr int kStep = MANY ? kJoinWarps : 1;
+  const int col4 = MANY ? (int)blockIdx.z : (int)blockIdx.z * kJoinWarps + warp;
   float M = -INFINITY, L = 0.f;
   float x[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int p0 = c; p0 <= jd.last; p0 += PB) {
+  for (int p0 = MANY ? c + warp : c; p0 <= jd.last; p0 += PB * kStep) {
     float m[PB], l[PB];
     float4 v[PB];
 #pragma unroll
@@ -1019,8 +1037,8 @@ join_tree_kernel(CacheView cv, TreeArgs a, Shape sh, int ctas) {
       m[i] = -INFINITY;
       l[i] = 0.f;
       v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      const int p = p0 + i;
-      if (p <= jd.last) {
+      const int p = p0 + i * kStep;
+      if (p <= jd.last && live) {
         const float* part = partial_at(a.ws, ctas, 2 * p + (p == c ? 1 : 0), D, sh.pair);
         m[i] = __ldcg(part + (size_t)prows * D + prow);
         l[i] = __ldcg(part + (size_t)prows * (D + 1) + prow);
@@ -1046,7 +1064,26 @@ join_tree_kernel(CacheView cv, TreeArgs a, Shape sh, int ctas) {
       x[3] += v[i].w * s;
     }
   }
-  const float inv = 1.f / L;                       // self is visible: L > 0
+  if (MANY) {
+    sm[warp][0][lane] = M;
+    sm[warp][1][lane] = L;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sm[warp][2 + e][lane] = x[e];
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) {
+      const float m = sm[w][0][lane], mn = fmaxf(M, m);    // warp 0 has the first partial
+      const float s0 = fast_exp2(M - (mn == -INFINITY ? 0.f : mn));
+      const float s1 = fast_exp2(m - (mn == -INFINITY ? 0.f : mn));
+      M = mn;
+      L = L * s0 + sm[w][1][lane] * s1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = x[e] * s0 + sm[w][2 + e][lane] * s1;
+    }
+  }
+  if (!live) return;
+  const float inv = 1.f / L;                             // self is visible: L > 0
   const size_t orow =
       ((size_t)jd.b * a.nodes + node) * cv.H + (size_t)jd.kvh * sh.G + (r - rg * sh.G);
   reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + orow * D)[col4] =
@@ -1080,7 +1117,7 @@ int64_t most_cost(const CacheView& cv, int nodes, const Shape& sh) {
 
 // Units of up to this many tiles, no more of them than SMs, have a CTA each:
 // the second kernel would take longer than what cutting them saves.
-constexpr int kFlatTiles = 8;
+constexpr int kFlatTiles = 6;
 
 // CTAs of the launch: one per SM, no more than the largest list could feed.
 int grid_of(const CacheView& cv, int nodes, const Shape& sh) {
@@ -1115,8 +1152,12 @@ cudaError_t launch_d(const CacheView& cv, const TreeArgs& a, const SlabMaps& map
   if (e != cudaSuccess) return e;
   if (sh.flat) return cudaSuccess;
   const int rows = PAIR ? 2 * BM : std::min(a.nodes, sh.npt) * sh.G;
-  return launch_dependent(join_tree_kernel<D>,
-                          dim3(sh.joins, (rows + 31) / 32, D / (4 * kJoinWarps)),
+  // More CTAs than units: many parts to a unit.
+  if (sh.joins < grid)
+    return launch_dependent(join_tree_kernel<D, true>, dim3(sh.joins, (rows + 31) / 32, D / 4),
+                            dim3(kJoinWarps * 32), 0, s, cv, a, sh, grid);
+  return launch_dependent(join_tree_kernel<D, false>,
+                          dim3(sh.joins, (rows + 31) / 32, D / 4 / kJoinWarps),
                           dim3(kJoinWarps * 32), 0, s, cv, a, sh, grid);
 }
 

@@ -175,8 +175,9 @@ struct TreeArgs {
 };
 constexpr int kMaxTreeNodes = 1024;
 size_t decode_tree_workspace(const CacheView& cv, int nodes);
-// bf16, at most 128 query heads per KV head: on the tensor cores
-// (decode_tree_tc.cu); the rest on the CUDA cores.
+// bf16, at most 128 query heads per KV head, and work enough: on the tensor
+// cores (decode_tree_tc.cu); the rest on the CUDA cores.
+bool decode_tree_use_tc(const CacheView& cv, int nodes);
 bool decode_tree_tc_supported(const CacheView& cv, int nodes);
 size_t decode_tree_tc_workspace(const CacheView& cv, int nodes);
 // Its tensor maps of the cache slabs (boxes of 128 and of 16 rows): the slabs
@@ -191,7 +192,7 @@ cudaError_t launch_decode_tree_tc(const CacheView& cv, const TreeArgs& a, const 
 // box_rows rows, 128-byte swizzle.
 bool make_tmap_heads_bf16(CUtensorMap* map, const void* base, uint64_t d, uint64_t heads,
                           uint64_t rows, uint32_t box_heads, uint32_t box_rows);
-// maps: of decode_tree_tc_supported shapes, else unused.
+// maps: of decode_tree_use_tc shapes, else unused.
 cudaError_t launch_decode_tree(const CacheView& cv, const TreeArgs& a, const SlabMaps* maps,
                                bool prefetch, cudaStream_t s);
 cudaError_t launch_commit_tree(const CacheView& cv, const void* k, const void* v, int nodes,

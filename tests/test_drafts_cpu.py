@@ -135,7 +135,7 @@ def test_norm_rope_takes_what_it_should(rswa):
     (dict(q=0x10008), 1), (dict(k=0x10002), 1), (dict(q_out=0x10008), 1),
     (dict(k_out=0x10008), 1), (dict(positions=0x10004), 1), (dict(q_stride=1279), 1),
     (dict(q_stride=1284), 1), (dict(k_stride=1272), 1), (dict(k_stride=-1280), 1),
-    (dict(q_stride=1 << 41), 1),
+    (dict(q_stride=1 << 41), 1), (dict(rows=1 << 31), 1),
 ])
 def test_norm_rope_refuses_arguments(rswa, kw, status):
     assert _norm_rope(rswa, _rope(rswa), **kw) == status

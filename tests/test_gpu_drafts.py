@@ -394,25 +394,35 @@ def test_decode_tree(cuda_lib, m, t, n, H, Hkv, d, N, dtype):
     run_tree(cuda_lib, m, t, n, H, Hkv, d, N, dtype, 50)
 
 
-@pytest.mark.parametrize("dtype", [BF, F32])
+# A prefix capacity above 1200 keys takes small work to the tensor cores too.
+WIDE = 1300
+
+
+@pytest.mark.parametrize("m,t,n,H,Hkv,d,N,dtype", [c for c in TREE_CASES if c[7] is BF])
+def test_decode_tree_with_room_in_the_cache(cuda_lib, m, t, n, H, Hkv, d, N, dtype):
+    run_tree(cuda_lib, m, t, n, H, Hkv, d, N, dtype, 55, cap=max(m) + WIDE)
+
+
+@pytest.mark.parametrize("dtype,cap", [(BF, None), (BF, 300 + WIDE), (F32, None)])
 @pytest.mark.parametrize("H,Hkv,d,N", [(4, 4, 128, 40), (8, 2, 128, 70), (8, 2, 64, 70)])
-def test_decode_tree_ragged_counts(cuda_lib, H, Hkv, d, N, dtype):
+def test_decode_tree_ragged_counts(cuda_lib, H, Hkv, d, N, dtype, cap):
     """Padded trees: rows past the count are left, whatever the padding holds;
     an empty sequence and a whole one among them, and all of them empty."""
     counts = [N, 0, 1, 17, N - 1, 33]
     m, t = [200, 10, 0, 129, 300, 5], [0, 4, 50, 140, 9, 64]
-    run_tree(cuda_lib, m, t, 64, H, Hkv, d, N, dtype, 60, counts)
-    run_tree(cuda_lib, m[:2], t[:2], 64, H, Hkv, d, N, dtype, 61, [0, 0])
+    run_tree(cuda_lib, m, t, 64, H, Hkv, d, N, dtype, 60, counts, cap)
+    run_tree(cuda_lib, m[:2], t[:2], 64, H, Hkv, d, N, dtype, 61, [0, 0], cap)
 
 
+@pytest.mark.parametrize("cap", [40, 40 + WIDE])
 @pytest.mark.parametrize("d", [64, 128])
-def test_decode_tree_deep_chain_and_star(cuda_lib, d):
+def test_decode_tree_deep_chain_and_star(cuda_lib, d, cap):
     """Depth beyond the window (ancestors and the ring fall out of it), and all
     nodes at depth 0."""
     N = 150
-    run_tree(cuda_lib, [40], [60], 48, 2, 2, d, N, BF, 70, parents=[list(range(-1, N - 1))])
-    run_tree(cuda_lib, [40], [60], 48, 2, 2, d, N, BF, 71, parents=[[-1] * N])
-    run_tree(cuda_lib, [40], [60], 48, 2, 2, d, N, BF, 72, parents=[[-1] + [0] * (N - 1)])
+    run_tree(cuda_lib, [40], [60], 48, 2, 2, d, N, BF, 70, cap=cap, parents=[list(range(-1, N - 1))])
+    run_tree(cuda_lib, [40], [60], 48, 2, 2, d, N, BF, 71, cap=cap, parents=[[-1] * N])
+    run_tree(cuda_lib, [40], [60], 48, 2, 2, d, N, BF, 72, cap=cap, parents=[[-1] + [0] * (N - 1)])
 
 
 def test_decode_tree_1024_nodes(cuda_lib):
@@ -430,14 +440,15 @@ def test_decode_tree_large_logits(cuda_lib):
     run_tree(cuda_lib, [300], [20], 16, 2, 2, 64, 20, F32, 76, std=40.0)
 
 
-@pytest.mark.parametrize("d,dtype", [(128, BF), (64, BF), (64, F32)])
-def test_decode_tree_counts_its_keys(cuda_lib, d, dtype):
+@pytest.mark.parametrize("d,dtype,cap", [(128, BF, None), (128, BF, 200 + WIDE), (64, BF, None),
+                                         (64, BF, 200 + WIDE), (64, F32, None)])
+def test_decode_tree_counts_its_keys(cuda_lib, d, dtype, cap):
     """q = 0 weighs every visible key alike, and with it exactly: lse is the
     logarithm of their number, and with values 1 for the tree's nodes and 0 in
     the cache o is the share of ancestors."""
     rswa = cuda_lib
     m, t, n, H, N = 200, 90, 50, 2, 140
-    cache, states = make_cache(rswa, [m], [t], n, H, H, d, dtype, 80)
+    cache, states = make_cache(rswa, [m], [t], n, H, H, d, dtype, 80, cap)
     Ks, Vs = cache.slabs()
     Vs.zero_()
     cache.set_t([t])
@@ -461,8 +472,8 @@ def test_decode_tree_bad_parents_and_counts(cuda_lib):
     the flag; the parent counts as -1, the count as the nearest in range."""
     rswa = cuda_lib
     m, t, n, H, d, N = [50, 60], [5, 6], 16, 2, 128, 12
-    for dtype in (BF, F32):
-        cache, states = make_cache(rswa, m, t, n, H, H, d, dtype, 85)
+    for dtype, cap in ((BF, None), (BF, 60 + WIDE), (F32, None)):
+        cache, states = make_cache(rswa, m, t, n, H, H, d, dtype, 85, cap)
         q, k, v = (normal((2, N, H, d), 86 + i, dtype) for i in range(3))
         good = [random_tree(N, 88), random_tree(N, 89)]
         good[0][3], good[0][4], good[1][5], good[1][11] = -1, -1, -1, -1
@@ -535,6 +546,94 @@ def test_decode_tree_refusals(cuda_lib):
     rswa.rswa_debug_fail_next_cuda(1)
     assert lib.rswa_decode_tree(h, *good) == 5
     assert lib.rswa_decode_tree(h, *good) == 0
+    assert cache.sync_status() == 0
+
+
+def test_decode_tree_ignores_what_is_no_key(cuda_lib):
+    """NaN in prefix rows past m_b and in ring slots that hold no output yet (a
+    caller's own writes into the slabs) does not reach any row."""
+    rswa = cuda_lib
+    m, t, n, H, d, N = [200, 5], [3, 0], 40, 2, 128, 20
+    for dtype, cap in ((BF, None), (BF, 200 + WIDE), (F32, None)):
+        cache, states = make_cache(rswa, m, t, n, H, H, d, dtype, 240, cap)
+        for slab in cache.slabs():
+            for b in range(2):
+                slab[b, :, m[b]:cache.m] = float("nan")
+                slab[b, :, cache.m + t[b]:] = float("nan")
+        cache.set_t(t)
+        q, k, v = (normal((2, N, H, d), 241 + i, dtype) for i in range(3))
+        par = [random_tree(N, 244), random_tree(N, 245)]
+        o, lse = torch.empty_like(q), torch.empty(2, N, H, device="cuda")
+        cache.decode_tree(q, k, v, torch.tensor(par, dtype=torch.int32).cuda(), o, lse)
+        for b in range(2):
+            check_tree(o[b], lse[b], q[b], k[b], v[b], states[b], par[b], n, f"{dtype} {b}")
+
+
+def test_decode_tree_wait_runs_out_then_recovers(cuda_lib):
+    """The tensor-core kernel with its waits bounded to 1 ns gives up, reports
+    RSWA_EDEVICE and leaves the cache usable: the next call is right (cut units,
+    a pair of query tiles, and a CTA for every unit)."""
+    rswa = cuda_lib
+    for m, H, Hkv, N, cap in ((3000, 2, 2, 20, None), (1500, 8, 2, 64, None), (100, 8, 2, 200, 500)):
+        cache, states = make_cache(rswa, [m], [70], 64, H, Hkv, 128, BF, 250, cap)
+        q, k, v = normal((1, N, H, 128), 251), normal((1, N, Hkv, 128), 252), normal((1, N, Hkv, 128), 253)
+        par = [random_tree(N, 254)]
+        dev = torch.tensor(par, dtype=torch.int32).cuda()
+        o, lse = torch.empty_like(q), torch.empty(1, N, H, device="cuda")
+        rswa.rswa_debug_set_wait_limit_ns(1)
+        try:
+            cache.decode_tree(q, k, v, dev, o, lse)
+        finally:
+            rswa.rswa_debug_set_wait_limit_ns(0)
+        assert cache.sync_status() == RSWA_EDEVICE
+        assert cache.sync_status() == 0
+        cache.decode_tree(q, k, v, dev, o, lse)
+        assert cache.sync_status() == 0
+        check_tree(o[0], lse[0], q[0], k[0], v[0], states[0], par[0], 64, "after the timeout")
+
+
+def test_decode_tree_workspaces(cuda_lib):
+    """A workspace for more nodes serves fewer; what it holds does not matter."""
+    rswa = cuda_lib
+    m, t, n, H, Hkv, d = [1400], [30], 64, 8, 2, 128
+    cache, states = make_cache(rswa, m, t, n, H, Hkv, d, BF, 260)
+    ws = cache.tree_workspace(300)
+    sizes = [rswa.rswa_decode_tree_workspace(cache.handle, x) for x in (1, 5, 32, 33, 64, 65, 300, 1024)]
+    assert sizes == sorted(sizes) and sizes[0] >= 256
+    for N in (300, 40, 3, 32):
+        ws.fill_(0xff)
+        q, k, v = normal((1, N, H, d), 261), normal((1, N, Hkv, d), 262), normal((1, N, Hkv, d), 263)
+        par = [random_tree(N, 264)]
+        o, lse = torch.empty_like(q), torch.empty(1, N, H, device="cuda")
+        cache.decode_tree(q, k, v, torch.tensor(par, dtype=torch.int32).cuda(), o, lse, workspace=ws)
+        check_tree(o[0], lse[0], q[0], k[0], v[0], states[0], par[0], n, f"{N} nodes")
+
+
+def test_decode_tree_back_to_back_and_after_other_calls(cuda_lib):
+    """Calls queued without a wait, each on inputs of its own, between appends
+    and decode steps (programmatic dependents that start early)."""
+    rswa = cuda_lib
+    m, n, H, Hkv, d, N = [1300, 40], 32, 8, 2, 128, 33
+    cache, states = make_cache(rswa, m, [10, 0], n, H, Hkv, d, BF, 270)
+    par = [random_tree(N, 271), random_tree(N, 272)]
+    dev = torch.tensor(par, dtype=torch.int32).cuda()
+    rounds = []
+    torch.cuda.synchronize()
+    for r in range(4):
+        q, k, v = normal((2, N, H, d), 280 + r), normal((2, N, Hkv, d), 290 + r), normal((2, N, Hkv, d), 300 + r)
+        q1, k1, v1 = normal((2, H, d), 310 + r), normal((2, Hkv, d), 320 + r), normal((2, Hkv, d), 330 + r)
+        o, lse, o1 = torch.empty_like(q), torch.empty(2, N, H, device="cuda"), torch.empty_like(q1)
+        rounds.append((q, k, v, q1, k1, v1, o, lse, o1))
+    torch.cuda.synchronize()
+    for q, k, v, q1, k1, v1, o, lse, o1 in rounds:
+        cache.decode_tree(q, k, v, dev, o, lse)
+        cache.decode_step_fused(q1, k1, v1, o1)
+    for r, (q, k, v, q1, k1, v1, o, lse, o1) in enumerate(rounds):
+        for b in range(2):
+            check_tree(o[b], lse[b], q[b], k[b], v[b], states[b], par[b], n, f"round {r}")
+            states[b], ref, _ = oracle.decode_step_fused(states[b], f64(q1[b]), f64(k1[b]), f64(v1[b]), n)
+            assert np.abs(f64(o1[b]) - ref).max() <= 2e-2
+    check_ring(cache, states, n)
     assert cache.sync_status() == 0
 
 
