@@ -103,13 +103,14 @@ constexpr float kRescaleThreshold = 8.0f;      // log2 units
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
 // The work list is cut by cost.  Every key tile costs 1, a partial one too: a
-// step takes as long as its chain of matrix products and softmax (2600 cycles,
-// about the time in which an SM's share of HBM brings a whole tile).  A unit's
-// first tile carries the unit's start and end as well.  A CTA's share is never
-// below kMinCost, so that it holds a tile at least and no join is made for less
-// work than it costs.
-constexpr int kUnitCost = 2, kMinCost = 3;
-static_assert(kMinCost >= 1 + kUnitCost, "a share holds a tile");
+// step takes as long as its chain of matrix products and softmax, about the time
+// in which an SM's share of HBM brings a whole tile.  A unit's first tile carries
+// the unit's start and end as well.  Fitted over the CTAs of a launch (time from
+// the dependency wait to the end): 64 sequences of 10 heads and 32 nodes 1.1 us a
+// tile and 3.0 us a segment, 64 of 32 / 8 heads and 64 nodes (pairs) 2.05 and 5.2
+// us.  A CTA's share is never below kMinCost, so that it holds a tile at least.
+constexpr int kUnitCost = 3, kPairUnitCost = 2, kMinCost = 4;
+static_assert(kMinCost >= 1 + kUnitCost && kUnitCost >= kPairUnitCost, "a share holds a tile");
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x,
                                             int32_t y, int32_t z, uint32_t bar) {
@@ -167,7 +168,7 @@ struct Shape {
 struct Seq {
   int cnt, m_b, ring;
   int64_t t_b;
-  int np, nr, tl, units;
+  int np, nr, tl, units, extra;
   __device__ __forceinline__ void load(const CacheView& cv, const TreeArgs& a, const Shape& sh,
                                        int b) {
     const int c = a.counts ? a.counts[b] : a.nodes;
@@ -179,17 +180,18 @@ struct Seq {
     np = (m_b + BN - 1) / BN;
     nr = (ring + BN - 1) / BN;
     tl = np + nr + (cnt + BN - 1) / BN;
+    extra = sh.pair ? kPairUnitCost : kUnitCost;
     const int per = sh.npt << sh.pair;
     units = (cnt + per - 1) / per * cv.Hkv;
   }
-  __device__ int cost(bool flat) const { return flat ? 1 : tl + kUnitCost; }   // of a unit
+  __device__ int cost(bool flat) const { return flat ? 1 : tl + extra; }   // of a unit
   // Cost of a unit's tiles before tile j, and the first tile that begins at or
   // after cost x (tl: none).  Where no unit is cut, a unit costs 1 as a whole.
   __device__ int before(int j, bool flat) const {
-    return j > 0 ? (flat ? 1 : j + kUnitCost) : 0;
+    return j > 0 ? (flat ? 1 : j + extra) : 0;
   }
   __device__ int at(int x, bool flat) const {
-    return x <= 0 ? 0 : (flat ? tl : min(max(x - kUnitCost, 1), tl));
+    return x <= 0 ? 0 : (flat ? tl : min(max(x - extra, 1), tl));
   }
 };
 
@@ -983,112 +985,175 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
   if (threadIdx.x == 0 && *abort_flag) flag_error(cv.err, kErrWaitTimeout);
 }
 
-// Joins the partials of the units that the CTAs' ranges cut.  Block (x, y, z):
-// the x-th CTA that begins a unit and does not end it, rows 32 y .. 32 y + 31
-// of that unit (lane = row).  MANY: few units are cut into many parts; the block
-// joins float4 z of the rows, each of its four warps every fourth partial, up to
-// four at a time, so that the reads of 16 parts are one round trip.  Else many
-// units are cut into two or three: the warps take a float4 each, 4 z + warp, and
-// all the partials (a block for every float4 would be 38912 blocks and 35 us for
-// 152 units of 256 rows).
-constexpr int kJoinWarps = 4;
+// The joins of the units that the CTAs' ranges cut.
 
-template <int D, bool MANY>
-__global__ void __launch_bounds__(kJoinWarps * 32, 8)
-join_tree_kernel(CacheView cv, TreeArgs a, Shape sh, int ctas) {
-  __shared__ float sm[kJoinWarps][6][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  griddep_wait();
-  griddep_launch_dependents();
-  const JoinDesc* desc = static_cast<const JoinDesc*>(a.ws);
+// The x-th CTA that begins a unit and does not end it; -1: there are fewer.
+// Called by whole warps.
+__device__ __forceinline__ int join_owner(const JoinDesc* desc, int ctas, int x) {
+  const int lane = threadIdx.x & 31;
   int c = -1;
-  for (int c0 = 0, skip = blockIdx.x; c < 0 && c0 < ctas; c0 += 160) {
+  for (int c0 = 0; c < 0 && c0 < ctas; c0 += 160) {
     int last[5];
 #pragma unroll
     for (int i = 0; i < 5; ++i) {
-      const int x = c0 + 32 * i + lane;
-      last[i] = x < ctas ? desc[x].last : -1;
+      const int y = c0 + 32 * i + lane;
+      last[i] = y < ctas ? desc[y].last : -1;
     }
 #pragma unroll
     for (int i = 0; i < 5; ++i) {
       const uint32_t on = __ballot_sync(0xffffffffu, last[i] >= 0);
       const int cnt = __popc(on);
-      if (c < 0 && skip < cnt) c = c0 + 32 * i + (int)__fns(on, 0, skip + 1);
-      skip -= cnt;
+      if (c < 0 && x < cnt) c = c0 + 32 * i + (int)__fns(on, 0, x + 1);
+      x -= cnt;
     }
   }
+  return c;
+}
+
+// A row of a cut unit: row y of the workspace's partials.
+struct JoinRow {
+  int prow, prows;
+  bool live;
+  size_t orow;                     // of o and lse
+  __device__ JoinRow(const CacheView& cv, const TreeArgs& a, const Shape& sh, const JoinDesc& jd,
+                     int y) {
+    prow = y;
+    prows = BM << sh.pair;
+    const int r = y & (BM - 1), rg = r / sh.G;
+    const int node = jd.node0 + (y >= BM ? sh.npt : 0) + rg;
+    live = rg < sh.npt && node < jd.cnt;
+    orow = ((size_t)jd.b * a.nodes + node) * cv.H + (size_t)jd.kvh * sh.G + (r - rg * sh.G);
+  }
+};
+
+// State of a row over the partials seen: reference, sum and NV float4 of o.
+template <int NV>
+struct JoinState {
+  float M = -INFINITY, L = 0.f;
+  float4 x[NV];
+  __device__ JoinState() {
+#pragma unroll
+    for (int e = 0; e < NV; ++e) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ void add(float m, float l, const float4* v) {
+    const float mn = fmaxf(M, m), ref = (mn == -INFINITY) ? 0.f : mn;
+    const float s0 = fast_exp2(M - ref), s1 = fast_exp2(m - ref);
+    M = mn;
+    L = L * s0 + l * s1;
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+      x[e].x = x[e].x * s0 + v[e].x * s1;
+      x[e].y = x[e].y * s0 + v[e].y * s1;
+      x[e].z = x[e].z * s0 + v[e].z * s1;
+      x[e].w = x[e].w * s0 + v[e].w * s1;
+    }
+  }
+  // float4 col4 .. col4 + NV - 1 of the row, and its lse; self is visible: L > 0.
+  template <int D>
+  __device__ void store(const TreeArgs& a, size_t orow, int col4) const {
+    const float inv = 1.f / L;
+    uint2* dst =
+        reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + orow * D) + col4;
+#pragma unroll
+    for (int e = 0; e < NV; ++e)
+      dst[e] = make_uint2(pack_bf16(x[e].x * inv, x[e].y * inv),
+                          pack_bf16(x[e].z * inv, x[e].w * inv));
+    if (col4 == 0 && a.lse) a.lse[orow] = (M + log2f(L)) * kLn2;
+  }
+};
+
+// Reads partial p's part of a row: m, l and NV float4 from col4 on.
+template <int D, int NV>
+__device__ __forceinline__ void read_partial(const TreeArgs& a, const Shape& sh, int ctas, int p,
+                                             bool first, const JoinRow& w, int col4, float& m,
+                                             float& l, float4* v) {
+  const float* part = partial_at(a.ws, ctas, 2 * p + (first ? 1 : 0), D, sh.pair);
+  m = __ldcg(part + (size_t)w.prows * D + w.prow);
+  l = __ldcg(part + (size_t)w.prows * (D + 1) + w.prow);
+#pragma unroll
+  for (int e = 0; e < NV; ++e)
+    v[e] = __ldcg(reinterpret_cast<const float4*>(part) + (size_t)(col4 + e) * w.prows + w.prow);
+}
+
+constexpr int kJoinWarps = 4;
+
+// Few units cut into many parts.  Block (x, y, z): unit x, rows 32 y .. 32 y + 31
+// (lane = row), float4 z; each of the four warps takes every fourth partial, up
+// to four at a time, so that the reads of 16 parts are one round trip.
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+join_many_kernel(CacheView cv, TreeArgs a, Shape sh, int ctas) {
+  __shared__ float sm[kJoinWarps][6][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  griddep_wait();
+  griddep_launch_dependents();
+  const JoinDesc* desc = static_cast<const JoinDesc*>(a.ws);
+  const int c = join_owner(desc, ctas, blockIdx.x);
   if (c < 0) return;
   const JoinDesc jd = desc[c];
-  const int prow = blockIdx.y * 32 + lane, prows = BM << sh.pair;
-  const int r = prow & (BM - 1), rg = r / sh.G;
-  const int node = jd.node0 + (prow >= BM ? sh.npt : 0) + rg;
-  const bool live = rg < sh.npt && node < jd.cnt;
-  if (!__syncthreads_or(live)) return;
-  constexpr int PB = 4;                                  // partials of a warp at a time
-  constexpr int kStep = MANY ? kJoinWarps : 1;
-  const int col4 = MANY ? (int)blockIdx.z : (int)blockIdx.z * kJoinWarps + warp;
-  float M = -INFINITY, L = 0.f;
-  float x[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int p0 = MANY ? c + warp : c; p0 <= jd.last; p0 += PB * kStep) {
+  const JoinRow w(cv, a, sh, jd, blockIdx.y * 32 + lane);
+  if (!__syncthreads_or(w.live)) return;
+  constexpr int PB = 4;
+  JoinState<1> st;
+  for (int p0 = c + warp; p0 <= jd.last; p0 += PB * kJoinWarps) {
     float m[PB], l[PB];
     float4 v[PB];
 #pragma unroll
     for (int i = 0; i < PB; ++i) {
+      const int p = p0 + i * kJoinWarps;
       m[i] = -INFINITY;
       l[i] = 0.f;
       v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      const int p = p0 + i * kStep;
-      if (p <= jd.last && live) {
-        const float* part = partial_at(a.ws, ctas, 2 * p + (p == c ? 1 : 0), D, sh.pair);
-        m[i] = __ldcg(part + (size_t)prows * D + prow);
-        l[i] = __ldcg(part + (size_t)prows * (D + 1) + prow);
-        v[i] = __ldcg(reinterpret_cast<const float4*>(part) + (size_t)col4 * prows + prow);
-      }
+      if (p <= jd.last && w.live)
+        read_partial<D, 1>(a, sh, ctas, p, p == c, w, blockIdx.z, m[i], l[i], &v[i]);
     }
-    float mn = M;
 #pragma unroll
-    for (int i = 0; i < PB; ++i) mn = fmaxf(mn, m[i]);
-    const float ref = (mn == -INFINITY) ? 0.f : mn;
-    const float s0 = fast_exp2(M - ref);
-    M = mn;
-    L *= s0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] *= s0;
-#pragma unroll
-    for (int i = 0; i < PB; ++i) {
-      const float s = fast_exp2(m[i] - ref);
-      L += l[i] * s;
-      x[0] += v[i].x * s;
-      x[1] += v[i].y * s;
-      x[2] += v[i].z * s;
-      x[3] += v[i].w * s;
-    }
+    for (int i = 0; i < PB; ++i) st.add(m[i], l[i], &v[i]);
   }
-  if (MANY) {
-    sm[warp][0][lane] = M;
-    sm[warp][1][lane] = L;
+  sm[warp][0][lane] = st.M;
+  sm[warp][1][lane] = st.L;
+  sm[warp][2][lane] = st.x[0].x;
+  sm[warp][3][lane] = st.x[0].y;
+  sm[warp][4][lane] = st.x[0].z;
+  sm[warp][5][lane] = st.x[0].w;
+  __syncthreads();
+  if (warp > 0 || !w.live) return;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sm[warp][2 + e][lane] = x[e];
-    __syncthreads();
-    if (warp > 0) return;
-#pragma unroll
-    for (int w = 1; w < kJoinWarps; ++w) {
-      const float m = sm[w][0][lane], mn = fmaxf(M, m);    // warp 0 has the first partial
-      const float s0 = fast_exp2(M - (mn == -INFINITY ? 0.f : mn));
-      const float s1 = fast_exp2(m - (mn == -INFINITY ? 0.f : mn));
-      M = mn;
-      L = L * s0 + sm[w][1][lane] * s1;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = x[e] * s0 + sm[w][2 + e][lane] * s1;
-    }
+  for (int k = 1; k < kJoinWarps; ++k) {
+    const float4 v = make_float4(sm[k][2][lane], sm[k][3][lane], sm[k][4][lane], sm[k][5][lane]);
+    st.add(sm[k][0][lane], sm[k][1][lane], &v);
   }
-  if (!live) return;
-  const float inv = 1.f / L;                             // self is visible: L > 0
-  const size_t orow =
-      ((size_t)jd.b * a.nodes + node) * cv.H + (size_t)jd.kvh * sh.G + (r - rg * sh.G);
-  reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + orow * D)[col4] =
-      make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
-  if (col4 == 0 && a.lse) a.lse[orow] = (M + log2f(L)) * kLn2;
+  st.template store<D>(a, w.orow, blockIdx.z);
+}
+
+// Many units cut into two or three parts.  Block (x, y, z): unit x, rows 32 y ..
+// 32 y + 31 (lane = row), NV float4 a warp, two partials read at a time: all
+// columns of the rows where there are many rows (152 units of 256 rows: 1216
+// blocks; with NV 1 they were 9728 and took 22 us), a quarter of them otherwise.
+// Bound by the partials' traffic through L2.
+template <int D, int NV>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+join_few_kernel(CacheView cv, TreeArgs a, Shape sh, int ctas) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  griddep_wait();
+  griddep_launch_dependents();
+  const JoinDesc* desc = static_cast<const JoinDesc*>(a.ws);
+  const int c = join_owner(desc, ctas, blockIdx.x);
+  if (c < 0) return;
+  const JoinDesc jd = desc[c];
+  const JoinRow w(cv, a, sh, jd, blockIdx.y * 32 + lane);
+  if (!w.live) return;
+  const int col4 = ((int)blockIdx.z * kJoinWarps + warp) * NV;
+  JoinState<NV> st;
+  for (int p = c; p <= jd.last; p += 2) {
+    float m0, l0, m1, l1;
+    float4 v0[NV], v1[NV];
+    read_partial<D, NV>(a, sh, ctas, p, p == c, w, col4, m0, l0, v0);
+    if (p < jd.last) read_partial<D, NV>(a, sh, ctas, p + 1, false, w, col4, m1, l1, v1);
+    st.add(m0, l0, v0);
+    if (p < jd.last) st.add(m1, l1, v1);
+  }
+  st.template store<D>(a, w.orow, col4);
 }
 
 // A cache of more than this is streamed: half of L2.
@@ -1154,10 +1219,11 @@ cudaError_t launch_d(const CacheView& cv, const TreeArgs& a, const SlabMaps& map
   const int rows = PAIR ? 2 * BM : std::min(a.nodes, sh.npt) * sh.G;
   // More CTAs than units: many parts to a unit.
   if (sh.joins < grid)
-    return launch_dependent(join_tree_kernel<D, true>, dim3(sh.joins, (rows + 31) / 32, D / 4),
+    return launch_dependent(join_many_kernel<D>, dim3(sh.joins, (rows + 31) / 32, D / 4),
                             dim3(kJoinWarps * 32), 0, s, cv, a, sh, grid);
-  return launch_dependent(join_tree_kernel<D, false>,
-                          dim3(sh.joins, (rows + 31) / 32, D / 4 / kJoinWarps),
+  constexpr int NV = D / 4 / kJoinWarps / (PAIR ? 1 : 4);
+  return launch_dependent(join_few_kernel<D, NV>,
+                          dim3(sh.joins, (rows + 31) / 32, D / 4 / kJoinWarps / NV),
                           dim3(kJoinWarps * 32), 0, s, cv, a, sh, grid);
 }
 
