@@ -637,6 +637,35 @@ def test_decode_tree_back_to_back_and_after_other_calls(cuda_lib):
     assert cache.sync_status() == 0
 
 
+@pytest.mark.parametrize("H,Hkv,N", [(2, 2, 12), (8, 2, 60)])
+def test_decode_tree_after_commits_that_move_the_plan(cuda_lib, H, Hkv, N):
+    """Commits and trees queued without a wait while t_b crosses tile boundaries
+    of the ring: what a tree call reads before its dependency wait is stale."""
+    rswa = cuda_lib
+    m, t, n, d, P, rounds = [1300, 700, 20], [100, 120, 0], 300, 128, 6, 50
+    cache, states = make_cache(rswa, m, t, n, H, Hkv, d, BF, 340)
+    par = [random_tree(N, 341 + b) for b in range(3)]
+    dev = torch.tensor(par, dtype=torch.int32).cuda()
+    path = torch.tensor([[0, 1, 3, 5, 7, 9]] * 3, dtype=torch.int32).cuda()
+    accs = [[6, 5, 6 if r % 2 else 0] for r in range(rounds)]
+    accd = [torch.tensor(x, dtype=torch.int32).cuda() for x in accs]
+    k, v = normal((3, N, Hkv, d), 344), normal((3, N, Hkv, d), 345)
+    q = normal((3, N, H, d), 346)
+    out = [(torch.empty_like(q), torch.empty(3, N, H, device="cuda")) for _ in range(rounds)]
+    cache.decode_tree(q, k, v, dev, *out[0])
+    torch.cuda.synchronize()
+    for r in range(rounds):
+        cache.commit_tree(k, v, path, accd[r])
+        cache.decode_tree(q, k, v, dev, *out[r])
+    assert cache.sync_status() == 0
+    for r in range(rounds):
+        for b in range(3):
+            states[b] = drafts.commit_tree(states[b], f64(k[b]), f64(v[b]), path[b, :accs[r][b]].tolist(), n)
+            if r % 7 == 0 or any(states[b]["t"] - x <= 6 for x in (128, 256)):
+                check_tree(out[r][0][b], out[r][1][b], q[b], k[b], v[b], states[b], par[b], n, f"round {r}")
+    check_ring(cache, states, n)
+
+
 # ---------------------------------------------------------------------------
 # commit
 # ---------------------------------------------------------------------------
