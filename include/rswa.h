@@ -375,7 +375,9 @@ RSWA_API int rswa_decode_tree_workspace(rswa_cache* cache, int64_t nodes,
  * A parent or a count outside its range sets the device flag (RSWA_EDEVICE of
  * rswa_sync_status); the parent is then taken as -1 and the count as the
  * nearest in range.  The ordering rule of rswa_decode_step for the prefix
- * rows holds here too.
+ * rows holds here too.  After a wait that ran out (RSWA_EDEVICE), o and lse are
+ * undefined: call rswa_cache_set_t with the same t_b, which clears the counters
+ * that CTAs of one unit meet on, before the next decode call.
  * Errors: RSWA_EHANDLE, RSWA_EINVAL, RSWA_ECAPACITY (workspace too small),
  * RSWA_ECUDA.
  */

@@ -17,10 +17,16 @@
 // the other, unit after unit, form one list, which the CTAs (one per SM) cut
 // into equal ranges.  A CTA streams its range through one TMA ring without
 // draining between units; a unit that a range covers whole is written out at
-// once, of another the CTA leaves a partial (m, l, O) in the workspace, and a
-// second, dependent kernel joins the partials of every cut unit.  Each CTA
-// leaves at most two: of the unit that a CTA before it began, and of the one
-// that it begins and does not end.
+// once, of another the CTA leaves a partial (m, l, O) in the workspace.  Each
+// CTA leaves at most two: of the unit that a CTA before it began, and of the one
+// that it begins and does not end.  The partials of a cut unit are joined
+//   pairs, in many units: by the last of the unit's CTAs, from its own
+//     accumulators where it is the one that began the unit (64 sequences of
+//     32 / 8 heads and 64 nodes: 123.7 us, with the second kernel 128.8; a
+//     launch without pairs has a quarter to an eighth of the partials, and gets
+//     slower by the code: 84.2 -> 84.7 and 21.8 -> 22.8 us)
+//   otherwise: by a second, dependent kernel.
+// The order of a unit's partials is the same whoever joins it last.
 //
 // Roles (352 threads): warps 0-3 / 4-7 softmax and epilogue of half 0 / 1
 // (thread r owns row r = TMEM lane r), warp 8 TMA producer, warp 9 TMEM
@@ -36,6 +42,14 @@
 // to the next multiple of 16, and value rows of nodes past the count are
 // zeroed first (0 x NaN is NaN).  Every wait is bounded; on a timeout the CTA
 // drains its copies and MMAs, frees TMEM and sets the cache's device flag.
+//
+// What bounds it: for many sequences (64 with 640..928 prefix and 512 ring
+// rows) the issue slots of the softmax, two exchanges of 128 x 128 scores and
+// weights with TMEM a tile and half, and one product at a time: 10 heads and 32
+// nodes take 84.2 us where the bytes take 57.6 at the copy rate and the launch
+// without softmax and products 73; 32 / 8 heads and 64 nodes 123.7, bytes 57.0,
+// products alone 41.  For one long sequence (40 pages) latency: 21.8 us, of
+// which 4.6 are state, plan and first keys, and 4.6 the second kernel.
 #include <cuda.h>
 
 #include <algorithm>
@@ -90,8 +104,11 @@ struct Smem {
   static constexpr int B_SEG = B_FIN + 1;          // NSEG segments handed over
   static constexpr int B_NODE = B_SEG + NSEG;      // 2 segments' nodes handed over
   static constexpr int B_NFREE = B_NODE + 2;       // and read by every row
-  static constexpr int NBAR = B_NFREE + 2;
-  static_assert(8 * NBAR + 16 <= 512, "barriers");
+  static constexpr int B_CUT = B_NFREE + 2;        // a cut unit's partial is written
+  static constexpr int B_JOIN = B_CUT + 1;         // and who joins it is known
+  static constexpr int B_ASK = B_JOIN + 1;         // the same before it is written
+  static constexpr int NBAR = B_ASK + 1;
+  static_assert(8 * NBAR + 24 <= 512, "barriers");
 };
 
 __host__ __device__ constexpr uint32_t tm_s(int half) { return half ? 128u : 0u; }
@@ -154,13 +171,21 @@ __device__ __forceinline__ bool wait_for(uint32_t b, uint32_t phase, volatile in
   return mbar_try_wait(b, phase) || wait_on(b, phase, abort_flag, ns);
 }
 
+__device__ __forceinline__ int load_acquire(const int32_t* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // The shape of a launch.
 struct Shape {
   int npt;      // nodes of a query tile
+  int box;      // nodes of its loads: fewer where no tree has so many
   int pair;     // 1: units of two query tiles
   int G;        // query heads of a KV head
   int evict;    // 1: cache tiles are loaded evict-first
   int flat;     // 1: a CTA for every unit, no unit is cut
+  int inl;      // 1: the last CTA of a cut unit joins it, no second kernel
   int joins;    // units of the launch, or its CTAs where those are fewer
 };
 
@@ -204,7 +229,8 @@ struct Segment {
   int np, nr;             // the unit's prefix and ring tiles, then come the tree's
   int m_b, ring;          // prefix rows, filled ring slots
   int newest, age;        // ring slot of output t_b - 1, and t_b - 1 (clamped)
-  int split, whole, begins;
+  uint8_t split, whole, begins, pad;
+  int first, last;        // the CTAs that a cut unit begins and ends in
   int tiles;              // the CTA's key tiles before the segment
   // Kind of key tile j, its index among its kind, and its keys.
   __device__ void tile(int j, int& kind, int& i, int& keys) const {
@@ -260,6 +286,67 @@ __device__ __forceinline__ float* partial_at(void* ws, int grid, int slot, int D
          (size_t)slot * partial_floats(D, pair);
 }
 
+// 32 columns of a row, times inv.
+__device__ __forceinline__ void store_columns(__nv_bfloat16* to, const float* x, float inv) {
+  uint4* dst = reinterpret_cast<uint4*>(to);
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    dst[e] = make_uint4(pack_bf16(x[8 * e] * inv, x[8 * e + 1] * inv),
+                        pack_bf16(x[8 * e + 2] * inv, x[8 * e + 3] * inv),
+                        pack_bf16(x[8 * e + 4] * inv, x[8 * e + 5] * inv),
+                        pack_bf16(x[8 * e + 6] * inv, x[8 * e + 7] * inv));
+}
+
+// x += wp times the partial's columns 32 c .. 32 c + 31 of the row.
+template <int D, bool PAIR>
+__device__ __forceinline__ void add_partial(const float* part, int prow, int c, float wp,
+                                            float* x) {
+  constexpr int prows = BM << (PAIR ? 1 : 0);
+  const float4* src = reinterpret_cast<const float4*>(part) + prow;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float4 v = __ldcg(src + (size_t)(c * 8 + e) * prows);
+    x[4 * e] = fmaf(v.x, wp, x[4 * e]);
+    x[4 * e + 1] = fmaf(v.y, wp, x[4 * e + 1]);
+    x[4 * e + 2] = fmaf(v.z, wp, x[4 * e + 2]);
+    x[4 * e + 3] = fmaf(v.w, wp, x[4 * e + 3]);
+  }
+}
+
+// A row's columns from the partials of CTAs first .. last, as the CTA that begins
+// a unit joins them to its own O, term by term in the same order.
+template <int D, bool PAIR>
+__device__ __noinline__ void join_row(void* ws, int grid, int first, int last, int prow, int c_lo,
+                                      int c_hi, __nv_bfloat16* orow, float* lse) {
+  constexpr int prows = BM << (PAIR ? 1 : 0);
+  auto part = [&](int p) { return partial_at(ws, grid, 2 * p + (p == first ? 1 : 0), D, PAIR); };
+  auto m_of = [&](int p) { return __ldcg(part(p) + (size_t)prows * D + prow); };
+  float top = m_of(first);
+  for (int p = first + 1; p <= last; ++p) top = fmaxf(top, m_of(p));
+  const float wf = ex2(m_of(first) - top);
+  float L = __ldcg(part(first) + (size_t)prows * (D + 1) + prow) * wf;
+  for (int p = first + 1; p <= last; ++p)
+    L = fmaf(__ldcg(part(p) + (size_t)prows * (D + 1) + prow), ex2(m_of(p) - top), L);
+#pragma unroll 1
+  for (int c = c_lo; c < c_hi; ++c) {
+    float x[32];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(part(first)) + prow +
+                              (size_t)(c * 8 + e) * prows);
+      x[4 * e] = v.x * wf;
+      x[4 * e + 1] = v.y * wf;
+      x[4 * e + 2] = v.z * wf;
+      x[4 * e + 3] = v.w * wf;
+    }
+#pragma unroll 1
+    for (int p = first + 1; p <= last; ++p)
+      add_partial<D, PAIR>(part(p), prow, c, ex2(m_of(p) - top), x);
+    store_columns(orow + c * 32, x, 1.f / L);
+  }
+  if (lse) *lse = (top + log2f(L)) * kLn2;
+}
+
 template <int D, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -285,6 +372,8 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::OFF_BAR + 8 * NBAR);
   volatile int* abort_flag =
       reinterpret_cast<volatile int*>(smem + SM::OFF_BAR + 8 * NBAR + 4);
+  // Whether this CTA joins a cut unit: two it counted itself in, one it asked for.
+  volatile int* joiner = reinterpret_cast<volatile int*>(smem + SM::OFF_BAR + 8 * NBAR + 12);
   volatile int* never = reinterpret_cast<volatile int*>(smem + SM::OFF_BAR + 8 * NBAR + 8);
   const Segment* segs = reinterpret_cast<const Segment*>(smem + SM::OFF_SEG);
   int32_t* nodes_smem = reinterpret_cast<int32_t*>(smem + SM::OFF_NODE);
@@ -296,7 +385,9 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     for (int k = 0; k < NBAR; ++k)
       mbar_init(bar(k), k == SM::B_P || k == SM::B_P + 1
                            ? 128u
-                           : (k == SM::B_F || k == SM::B_ML || k >= SM::B_NFREE ? 256u : 1u));
+                           : (k == SM::B_F || k == SM::B_ML || (k >= SM::B_NFREE && k <= SM::B_CUT)
+                                  ? 256u
+                                  : 1u));
     *abort_flag = 0;
     *never = 0;
     fence_mbar_init();
@@ -377,7 +468,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     // ------------------------------------------------------------ MMA issuer
     // One lane issues.  Step s: PV of step s - 2, then QK of step s, both of half
     // s & 1.  What the lane does between the products holds the tensor core up
-    // (2700 cycles a step with 1350 of them in products), so waits are made
+    // (2400 cycles a step with 1200 of them in products), so waits are made
     // where their answer can be new only, descriptors advance by constants, and
     // the rare paths are out of line.
     if (lane == 0) {
@@ -426,7 +517,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       const uint64_t qdesc = desc_sw128(sb + SM::OFF_Q, 16, 1024);
       const uint64_t kdesc = desc_sw128(sb + SM::OFF_RING, 16, 1024);
       const uint64_t vdesc = desc_sw128(sb + SM::OFF_RING, kSub, 1024);
-      int np = pmore ? segs[0].np - segs[0].j0 : 0, tl = pc.left;   // see `whole` below
+      int np = pmore ? segs[0].np - segs[0].j0 : 0, tl = pc.left;
 #pragma unroll 1
       for (uint32_t s = 0; pmore; ++s) {
         const uint32_t half = s & 1;
@@ -514,7 +605,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                                                            abort_flag, wait_ns)))
           return false;
         if (lane == 0) {
-          mbar_arrive_expect_tx(bar(SM::B_QF + s), (uint32_t)NSUB * sh.npt * sh.G * 128u);
+          mbar_arrive_expect_tx(bar(SM::B_QF + s), (uint32_t)NSUB * sh.box * sh.G * 128u);
 #pragma unroll
           for (int c = 0; c < NSUB; ++c)
             tma_load_3d(sb + SM::OFF_Q + s * kTile + c * kSub, &tmQ, c * 64, w.kvh * sh.G,
@@ -620,6 +711,11 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         w.split = !PAIR || w.node0 + sh.npt >= sq.cnt;
         w.whole = j0 == 0 && w.j1 == sq.tl;
         w.begins = j0 == 0;
+        w.first = w.last = cta;
+        if (!w.whole) {
+          w.first = owner(ubase);
+          w.last = owner(ubase + sq.before(sq.tl - 1, flat));
+        }
         w.tiles = tiles;
         tiles += w.j1 - j0;
         // Slot k % NSEG was segment k - 4's: all roles had left it when the
@@ -632,9 +728,8 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         // The first segment's queries come at once, a later one's after its
         // nodes: their buffers are free later than those.
         if (k == 0) queries(w);
-        if (j0 == 0 && !w.whole) {       // begun here, ended by the CTA of its last tile
-          jd = {b, w.node0, w.kvh, owner(ubase + sq.before(sq.tl - 1, flat)), sq.cnt, {0, 0, 0}};
-        }
+        if (j0 == 0 && !w.whole && !sh.inl)  // begun here, ended by the CTA of its last tile
+          jd = {b, w.node0, w.kvh, w.last, sq.cnt, {0, 0, 0}};
         // Depths and ancestors of the unit's nodes, where the segment's ring
         // and tree tiles ask for them.
         const bool ask = w.j1 > sq.np;
@@ -679,7 +774,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     if (lane == 0) {
       out[k % NSEG].j1 = 0;              // no more segments
       mbar_arrive(bar(SM::B_SEG + k % NSEG));
-      if (!flat) static_cast<JoinDesc*>(a.ws)[cta] = jd;
+      if (!flat && !sh.inl) static_cast<JoinDesc*>(a.ws)[cta] = jd;
       // Drain: every copy issued has landed before the CTA may exit.
       for (int x = max(qi - NQ, 0); x < qi; ++x)
         wait_for(bar(SM::B_QF + x % NQ), (x / NQ) & 1, never, kWaitLimitNs);
@@ -698,6 +793,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     float* ml = reinterpret_cast<float*>(smem + SM::OFF_ML);
     uint32_t step = 0, turns = 0;                       // steps before; this half's among them
     uint32_t o_phase0 = 0, o_phase1 = 0, ml_phase = 0;  // segments with steps of each half; split
+    uint32_t cut_phase = 0;                             // cut units left to a join (at most 2)
     bool ok = true;
     Segment w;
     for (int k = 0;; ++k) {
@@ -888,6 +984,19 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       auto wait_all = [&](int b, uint32_t phase) {
         return __all_sync(0xffffffffu, wait_for(bar(b), phase & 1, abort_flag, wait_ns)) != 0;
       };
+      // A cut unit is joined by the last of its CTAs to get here (inl; else by the
+      // second kernel): the one that begins it, as a rule, as the others come to
+      // it at the start of their ranges.  It then takes their partials from L2 to
+      // its own O as it writes the rows, and leaves none itself.  It asks early:
+      // the answer comes while the other half's last step runs.
+      const bool counted = PAIR && sh.inl && !w.whole;
+      int32_t* count = cv.cnt_bh + (size_t)w.b * cv.H + (size_t)w.kvh * sh.G +
+                       w.node0 / (sh.npt << sh.pair);
+      const bool ask = ok && counted && w.begins;
+      if (ask && threadIdx.x == 0) {                    // once a launch: its last unit
+        joiner[2] = load_acquire(count) == w.last - w.first;
+        mbar_arrive(bar(SM::B_ASK));
+      }
       // Weights of the two halves' O, the row's reference and sum.
       float a0 = 1.f, a1 = 0.f, M = m_run, L = l_run;
       if (split) {
@@ -908,21 +1017,46 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         }
         ++ml_phase;
       }
+      constexpr int prows = BM << (PAIR ? 1 : 0);
+      const int prow = (split ? 0 : half * BM) + r;
+      auto partial_of = [&](int p) {
+        return partial_at(a.ws, grid, 2 * p + (p == w.first ? 1 : 0), D, PAIR);
+      };
+      bool joins = false;
+      float m1 = -INFINITY, l1 = 0.f;          // state of the next CTA's partial
+      if (ask) {
+        ok = wait_all(SM::B_ASK, 0);
+        joins = ok && joiner[2] != 0;
+        if (joins && live) {
+          m1 = __ldcg(partial_of(cta + 1) + (size_t)prows * D + prow);
+          l1 = __ldcg(partial_of(cta + 1) + (size_t)prows * (D + 1) + prow);
+        }
+      }
       if (ok && own > 0) ok = wait_all(SM::B_O + half, half ? o_phase1 : o_phase0);
       if (ok && split && other > 0) ok = wait_all(SM::B_O + 1 - half, half ? o_phase0 : o_phase1);
       if (!ok) break;
       tc_fence_after();
+      const size_t orow = ((size_t)w.b * a.nodes + node) * cv.H + (size_t)w.kvh * sh.G + hg;
+      __nv_bfloat16* orow_p = static_cast<__nv_bfloat16*>(a.o) + orow * D;
+      // Split: each half writes half of the columns of the joined row.
+      const int c_lo = split ? half * (D / 64) : 0, c_hi = split ? c_lo + D / 64 : D / 32;
+      const bool final_rows = w.whole || joins;
       if (any) {
-        const int slot = 2 * cta + w.begins;
-        float* part = partial_at(a.ws, grid, slot, D, sh.pair);
-        const int prow = (split ? 0 : half * BM) + r;
-        const int prows = BM << sh.pair;
+        float* part = partial_of(cta);
+        float ws = 1.f;
+        float top = M;
+        if (joins && live) {
+          top = fmaxf(M, m1);
+          for (int p = cta + 2; p <= w.last; ++p)
+            top = fmaxf(top, __ldcg(partial_of(p) + (size_t)prows * D + prow));
+          ws = ex2(M - top);
+          L = fmaf(l1, ex2(m1 - top), L * ws);
+          for (int p = cta + 2; p <= w.last; ++p)
+            L = fmaf(__ldcg(partial_of(p) + (size_t)prows * (D + 1) + prow),
+                     ex2(__ldcg(partial_of(p) + (size_t)prows * D + prow) - top), L);
+          M = top;
+        }
         const float inv = 1.f / L;
-        const bool whole = w.whole != 0;
-        const size_t orow = ((size_t)w.b * a.nodes + node) * cv.H + (size_t)w.kvh * sh.G + hg;
-        __nv_bfloat16* orow_p = static_cast<__nv_bfloat16*>(a.o) + orow * D;
-        // Split: each half writes half of the columns of the joined row.
-        const int c_lo = split ? half * (D / 64) : 0, c_hi = split ? c_lo + D / 64 : D / 32;
         const bool use0 = own > 0, use1 = split && other > 0;
 #pragma unroll 1
         for (int c = c_lo; c < c_hi; ++c) {
@@ -940,14 +1074,16 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(ov[e]), a1, x[e]);
           }
-          if (live && whole) {
-            uint4* dst = reinterpret_cast<uint4*>(orow_p + c * 32);
+          if (live && joins) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dst[e] = make_uint4(pack_bf16(x[8 * e] * inv, x[8 * e + 1] * inv),
-                                  pack_bf16(x[8 * e + 2] * inv, x[8 * e + 3] * inv),
-                                  pack_bf16(x[8 * e + 4] * inv, x[8 * e + 5] * inv),
-                                  pack_bf16(x[8 * e + 6] * inv, x[8 * e + 7] * inv));
+            for (int e = 0; e < 32; ++e) x[e] *= ws;
+            add_partial<D, PAIR>(partial_of(cta + 1), prow, c, ex2(m1 - M), x);
+            for (int p = cta + 2; p <= w.last; ++p)
+              add_partial<D, PAIR>(partial_of(p), prow, c,
+                                   ex2(__ldcg(partial_of(p) + (size_t)prows * D + prow) - M), x);
+          }
+          if (live && final_rows) {
+            store_columns(orow_p + c * 32, x, inv);
           } else if (live) {
             float4* dst = reinterpret_cast<float4*>(part) + prow;
 #pragma unroll
@@ -959,7 +1095,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         tc_fence_before();
         mbar_arrive(bar(SM::B_F));
         if (live && (!split || half == 0)) {
-          if (!whole) {
+          if (!final_rows) {
             part[(size_t)prows * D + prow] = M;
             part[(size_t)prows * (D + 1) + prow] = L;
           } else if (a.lse) {
@@ -970,6 +1106,22 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         tc_fence_before();
         mbar_arrive(bar(SM::B_F));
       }
+      if (counted && !joins) {
+        mbar_arrive(bar(SM::B_CUT));
+        if (threadIdx.x == 0 && wait_for(bar(SM::B_CUT), cut_phase & 1, abort_flag, wait_ns)) {
+          joiner[cut_phase & 1] = arrive_acq_rel(count) == w.last - w.first;
+          mbar_arrive(bar(SM::B_JOIN));
+        }
+        if (!wait_all(SM::B_JOIN, cut_phase)) break;
+        joins = joiner[cut_phase & 1] != 0;
+        ++cut_phase;
+        if (joins && live) {
+          // The last after all, with its O given up.
+          join_row<D, PAIR>(a.ws, grid, w.first, w.last, prow, c_lo, c_hi, orow_p,
+                            a.lse && (!split || half == 0) ? a.lse + orow : nullptr);
+        }
+      }
+      if (joins && threadIdx.x == 0) *count = 0;        // ready for the next call
       if ((half ? other : own) > 0) ++o_phase0;
       if ((half ? own : other) > 0) ++o_phase1;
       step += split ? nseg : 2 * nseg;
@@ -1164,7 +1316,8 @@ Shape shape_of(const CacheView& cv, int nodes) {
   sh.G = cv.H / cv.Hkv;
   sh.npt = BM / sh.G;
   sh.pair = nodes > sh.npt ? 1 : 0;
-  sh.evict = sh.joins = sh.flat = 0;
+  sh.box = std::min(sh.npt, nodes);
+  sh.evict = sh.joins = sh.flat = sh.inl = 0;
   return sh;
 }
 
@@ -1199,7 +1352,7 @@ cudaError_t launch_d(const CacheView& cv, const TreeArgs& a, const SlabMaps& map
   const uint64_t trows = (uint64_t)cv.B * a.nodes;
   const uint64_t crows = (uint64_t)cv.B * cv.Hkv * cv.slab_rows;
   CUtensorMap mq, mkt, mvt, mkt16, mvt16;
-  if (!make_tmap_heads_bf16(&mq, a.q, D, cv.H, trows, sh.G, sh.npt) ||
+  if (!make_tmap_heads_bf16(&mq, a.q, D, cv.H, trows, sh.G, sh.box) ||
       !make_tmap_rows_bf16(&mkt, a.k, (uint64_t)cv.Hkv * D, trows) ||
       !make_tmap_rows_bf16(&mvt, a.v, (uint64_t)cv.Hkv * D, trows) ||
       !make_tmap_rows_bf16(&mkt16, a.k, (uint64_t)cv.Hkv * D, trows, 16) ||
@@ -1207,6 +1360,10 @@ cudaError_t launch_d(const CacheView& cv, const TreeArgs& a, const SlabMaps& map
     return cudaErrorInvalidValue;
   sh.evict = crows * D * 4 > kEvictBytes;
   sh.joins = (int)std::min<int64_t>(most_units(cv, a.nodes, sh), grid);
+  // Many units, cut into few parts each, and a counter for each (the cache has
+  // one a query head).
+  sh.inl = PAIR && !sh.flat && sh.joins == grid &&
+           most_units(cv, a.nodes, sh) <= (int64_t)cv.B * cv.Hkv * sh.G;
   // Per device (the attribute belongs to the current device's context).
   cudaError_t e = cudaFuncSetAttribute(decode_tree_tc_kernel<D, PAIR>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, PAIR>::kBytes);
@@ -1215,7 +1372,7 @@ cudaError_t launch_d(const CacheView& cv, const TreeArgs& a, const SlabMaps& map
                        maps.k, maps.v, mkt, mvt, maps.k16, maps.v16, mkt16, mvt16, cv, a, sh,
                        phase_wait_limit_ns());
   if (e != cudaSuccess) return e;
-  if (sh.flat) return cudaSuccess;
+  if (sh.flat || sh.inl) return cudaSuccess;
   const int rows = PAIR ? 2 * BM : std::min(a.nodes, sh.npt) * sh.G;
   // More CTAs than units: many parts to a unit.
   if (sh.joins < grid)

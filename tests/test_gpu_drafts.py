@@ -571,8 +571,9 @@ def test_decode_tree_ignores_what_is_no_key(cuda_lib):
 
 def test_decode_tree_wait_runs_out_then_recovers(cuda_lib):
     """The tensor-core kernel with its waits bounded to 1 ns gives up, reports
-    RSWA_EDEVICE and leaves the cache usable: the next call is right (cut units,
-    a pair of query tiles, and a CTA for every unit)."""
+    RSWA_EDEVICE and leaves the cache usable: after rswa_cache_set_t the next
+    call is right (few units cut into many parts, a pair of query tiles, a CTA
+    for every unit)."""
     rswa = cuda_lib
     for m, H, Hkv, N, cap in ((3000, 2, 2, 20, None), (1500, 8, 2, 64, None), (100, 8, 2, 200, 500)):
         cache, states = make_cache(rswa, [m], [70], 64, H, Hkv, 128, BF, 250, cap)
@@ -587,6 +588,7 @@ def test_decode_tree_wait_runs_out_then_recovers(cuda_lib):
             rswa.rswa_debug_set_wait_limit_ns(0)
         assert cache.sync_status() == RSWA_EDEVICE
         assert cache.sync_status() == 0
+        cache.set_t([70])                           # the documented way back
         cache.decode_tree(q, k, v, dev, o, lse)
         assert cache.sync_status() == 0
         check_tree(o[0], lse[0], q[0], k[0], v[0], states[0], par[0], 64, "after the timeout")
@@ -664,6 +666,44 @@ def test_decode_tree_after_commits_that_move_the_plan(cuda_lib, H, Hkv, N):
             if r % 7 == 0 or any(states[b]["t"] - x <= 6 for x in (128, 256)):
                 check_tree(out[r][0][b], out[r][1][b], q[b], k[b], v[b], states[b], par[b], n, f"round {r}")
     check_ring(cache, states, n)
+
+
+@pytest.mark.parametrize("B,H,Hkv,N,d", [(40, 6, 6, 20, 128), (40, 12, 3, 60, 128), (60, 4, 4, 9, 64)])
+def test_decode_tree_many_units(cuda_lib, B, H, Hkv, N, d):
+    """More units than SMs: units cut between two CTAs and joined by the last of
+    them, call after call on the same counters, and the same bits every time;
+    then a wait that runs out, and the way back."""
+    rswa = cuda_lib
+    g = np.random.default_rng(350)
+    m, t = [int(x) for x in g.integers(0, 700, B)], [int(x) for x in g.integers(0, 150, B)]
+    counts = [int(x) for x in g.integers(0, N + 1, B)]
+    cache, states = make_cache(rswa, m, t, 100, H, Hkv, d, BF, 351, 1400)
+    q, k, v = normal((B, N, H, d), 352), normal((B, N, Hkv, d), 353), normal((B, N, Hkv, d), 354)
+    par = [random_tree(N, 355 + b) for b in range(B)]
+    dev = torch.tensor(par, dtype=torch.int32).cuda()
+    cnt = torch.tensor(counts, dtype=torch.int32).cuda()
+    outs = []
+    for _ in range(6):
+        outs.append((torch.zeros_like(q), torch.zeros(B, N, H, device="cuda")))
+        cache.decode_tree(q, k, v, dev, *outs[-1], counts=cnt)
+    assert cache.sync_status() == 0
+    o, lse = outs[0]
+    for o2, l2 in outs[1:]:
+        assert torch.equal(o, o2) and torch.equal(lse, l2)
+    for b in list(range(0, B, 7)) + [B - 1]:
+        c = counts[b]
+        check_tree(o[b, :c], lse[b, :c], q[b, :c], k[b, :c], v[b, :c], states[b], par[b][:c], 100, f"{b}")
+    rswa.rswa_debug_set_wait_limit_ns(1)
+    try:
+        cache.decode_tree(q, k, v, dev, torch.zeros_like(q), torch.zeros_like(lse), counts=cnt)
+    finally:
+        rswa.rswa_debug_set_wait_limit_ns(0)
+    assert cache.sync_status() == RSWA_EDEVICE
+    cache.set_t(t)
+    o2, l2 = torch.zeros_like(q), torch.zeros_like(lse)
+    cache.decode_tree(q, k, v, dev, o2, l2, counts=cnt)
+    assert cache.sync_status() == 0
+    assert torch.equal(o, o2) and torch.equal(lse, l2)
 
 
 # ---------------------------------------------------------------------------
