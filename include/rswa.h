@@ -467,7 +467,7 @@ RSWA_API void rswa_debug_fail_next_cuda(int count);
 /*
  * Test hook: bound, in nanoseconds, on each wait for a pipeline phase (a
  * tile landing, a tensor core result, a softmax hand-off) of the pipelined
- * kernels - the tensor-core prefill, block decode and grouped-head decode,
+ * kernels - the tensor-core prefill, block, tree and grouped-head decode,
  * and the shared-memory streaming decode; 0 restores the default of one
  * second.
  * Kernels launched with a bound that runs out stop, drain their own copies

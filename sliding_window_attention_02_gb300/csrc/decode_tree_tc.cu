@@ -43,8 +43,8 @@
 // zeroed first (0 x NaN is NaN).  Every wait is bounded; on a timeout the CTA
 // drains its copies and MMAs, frees TMEM and sets the cache's device flag.
 //
-// What bounds it: for many sequences (64 with 640..928 prefix and 512 ring
-// rows) the issue slots of the softmax, two exchanges of 128 x 128 scores and
+// What bounds it: for many sequences (64 with prefixes of 256..2048 rows,
+// n 128) the issue slots of the softmax, two exchanges of 128 x 128 scores and
 // weights with TMEM a tile and half, and one product at a time: 10 heads and 32
 // nodes take 84.2 us where the bytes take 57.6 at the copy rate and the launch
 // without softmax and products 73; 32 / 8 heads and 64 nodes 123.7, bytes 57.0,
