@@ -321,7 +321,7 @@ RSWA_API int rswa_qk_norm_rope(const rswa_rope* rope, const void* q,
  * rswa_decode_step_fused (tokens = 1), rswa_decode_block, and rswa_decode_tree
  * (offsets = the nodes' depths).  Heads, head_dim and dtype are the cache's.
  * m_b and t_b are read on the device; the cache is not changed.
- * tokens >= 1, B * tokens < 2^31.
+ * 1 <= tokens <= 2^24, B * tokens < 2^31.
  * Errors: RSWA_EHANDLE, RSWA_EINVAL, RSWA_ECUDA.
  */
 RSWA_API int rswa_qk_norm_rope_cached(rswa_cache* cache, const rswa_rope* rope,

@@ -158,6 +158,13 @@ def _ptr(t):
     return t.data_ptr()
 
 
+def _row_ptr(t):
+    """Device pointer of a CUDA tensor of rows with a stride."""
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    return t.data_ptr()
+
+
 def _stream(stream):
     if stream is None:
         import torch
@@ -356,7 +363,7 @@ def rswa_qk_norm_rope_cached(handle, rope, q, q_stride, k, k_stride, offsets, to
     """Pointers as tensors, strides in elements; RswaCache.qk_norm_rope checks
     shapes and types."""
     _check(load().rswa_qk_norm_rope_cached(
-        handle, rope.ref, q.data_ptr(), q_stride, k.data_ptr(), k_stride,
+        handle, rope.ref, _row_ptr(q), q_stride, _row_ptr(k), k_stride,
         _ptr(offsets), tokens, _ptr(q_out), _ptr(k_out),
         _stream_of(stream, _device_index(q))), "rswa_qk_norm_rope_cached")
 
@@ -366,8 +373,8 @@ def rswa_append_kv_rope(handle, rope, q, q_stride, k, k_stride, v, v_stride, q_o
     """Pointers as tensors, strides in elements; RswaCache.append_kv_rope
     checks shapes and types."""
     _check(load().rswa_append_kv_rope(
-        handle, rope.ref, q.data_ptr(), q_stride, k.data_ptr(), k_stride,
-        v.data_ptr(), v_stride, _ptr(q_out), _stream_of(stream, _device_index(q))),
+        handle, rope.ref, _row_ptr(q), q_stride, _row_ptr(k), k_stride,
+        _row_ptr(v), v_stride, _ptr(q_out), _stream_of(stream, _device_index(q))),
         "rswa_append_kv_rope")
 
 
@@ -594,6 +601,8 @@ class RswaCache:
         cp = None if counts is None else _dense(counts, (B,), i32, ix, "counts")
         if workspace is None:
             workspace = self._own_workspace(nodes)
+        elif workspace.get_device() != ix:
+            raise ValueError(f"workspace: expected a tensor on CUDA device {ix}")
         status = load().rswa_decode_tree(
             self.handle, qp, kp, vp, pp, cp, nodes, op, lp, _ptr(workspace),
             workspace.numel(), _stream_of(stream, ix))

@@ -222,8 +222,8 @@ constexpr int kRopeBatch = 2;                  // head groups a warp has in flig
 // head groups (HPW heads, queries then keys).  Bound by HBM: every head is read
 // and written once.  Many small CTAs (8 an SM, 64 registers a thread) hide each
 // other's start: 32768 rows of 10 + 10 heads, d 128, bf16 take 57.3 us (5.9
-// TB/s, 86 % of a plain copy's) so, 63.6 with 4 CTAs of an SM and five groups in flight, 72 with CTAs of
-// 8 warps that held the entries in registers.
+// TB/s, 86 % of a plain copy's) so, 63.6 with 4 CTAs of an SM and five groups in
+// flight, 72 with CTAs of 8 warps that held the entries in registers.
 template <typename T, int D, bool IL>
 __global__ void __launch_bounds__(kRopeThreads, 8)
 norm_rope_kernel(rswa_rope rp, RopeRows rr, CacheView cv, int R) {

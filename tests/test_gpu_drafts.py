@@ -940,6 +940,29 @@ def test_capture_needs_a_workspace(cuda_lib):
     assert cache.sync_status() == 0
 
 
+def test_calls_by_handle_refuse_cpu_tensors(cuda_lib):
+    rswa = cuda_lib
+    H, Hkv, d = 4, 2, 128
+    cache, _ = make_cache(rswa, [9], [0], 8, H, Hkv, d, BF, 190)
+    rope = rswa.RswaRope(inv_freq(d))
+    q, k, v = normal((1, H, d), 191), normal((1, Hkv, d), 192), normal((1, Hkv, d), 193)
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    for bad in ((q.cpu(), k, v), (q, k.cpu(), v)):
+        with pytest.raises(ValueError):
+            rswa.rswa_qk_norm_rope_cached(cache.handle, rope, bad[0], H * d, bad[1], Hkv * d,
+                                          None, 1, qo, ko)
+    for bad in ((q.cpu(), k, v), (q, k.cpu(), v), (q, k, v.cpu())):
+        with pytest.raises(ValueError):
+            rswa.rswa_append_kv_rope(cache.handle, rope, bad[0], H * d, bad[1], Hkv * d,
+                                     bad[2], Hkv * d, qo)
+    o = torch.empty(1, 1, H, d, dtype=BF, device="cuda")
+    par = torch.full((1, 1), -1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        cache.decode_tree(q[None], k[None], v[None], par, o,
+                          workspace=cache.tree_workspace(1).cpu())
+    assert cache.sync_status() == 0 and cache.get_t(0) == 0
+
+
 def test_two_caches_on_two_streams(cuda_lib):
     """Calls on different caches overlap; each has its own workspace."""
     rswa = cuda_lib
