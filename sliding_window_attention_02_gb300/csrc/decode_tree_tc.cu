@@ -115,7 +115,6 @@ __host__ __device__ constexpr uint32_t tm_s(int half) { return half ? 128u : 0u;
 __host__ __device__ constexpr uint32_t tm_o(int half) { return half ? 384u : 256u; }
 constexpr uint32_t TM_COLS = 512;
 constexpr int kTurnUnroll = 1;                 // rolled softmax loop
-constexpr int kMmaUnroll = 8;
 constexpr float kRescaleThreshold = 8.0f;      // log2 units
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
@@ -1011,7 +1010,9 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
           const float ref = (M == -INFINITY) ? 0.f : M;
           a0 = ex2(m_run - ref);
           a1 = ex2(m1 - ref);
-          L = l_run * a0 + l1 * a1;
+          // The same bits in both halves (no fma): a join from the partials
+          // takes half 0's, one from the accumulators each half's own.
+          L = __fadd_rn(__fmul_rn(l_run, a0), __fmul_rn(l1, a1));
         } else {
           ok = false;
         }

@@ -706,6 +706,49 @@ def test_decode_tree_many_units(cuda_lib, B, H, Hkv, N, d):
     assert torch.equal(o, o2) and torch.equal(lse, l2)
 
 
+@pytest.mark.parametrize("B,H,Hkv,N,d", [(60, 12, 3, 60, 128), (40, 8, 2, 100, 128), (40, 4, 4, 200, 64),
+                                         (40, 4, 4, 300, 128), (20, 64, 8, 17, 64)])
+def test_decode_tree_many_pairs(cuda_lib, B, H, Hkv, N, d):
+    """As many units of two query tiles as SMs or more (one unit or two a key
+    head, some of them with one tile's rows only): the same bits call after call
+    and in a graph, and a decode step after them as on a cache that saw none."""
+    rswa = cuda_lib
+    g = np.random.default_rng(360)
+    m, t = [int(x) for x in g.integers(0, 500, B)], [int(x) for x in g.integers(0, 150, B)]
+    counts = [int(x) for x in g.integers(0, N + 1, B)]
+    counts[0], counts[1], m[2], t[2] = N, 0, 0, 0
+    cache, states = make_cache(rswa, m, t, 100, H, Hkv, d, BF, 361, 600)
+    other, _ = make_cache(rswa, m, t, 100, H, Hkv, d, BF, 361, 600)
+    q, k, v = normal((B, N, H, d), 362), normal((B, N, Hkv, d), 363), normal((B, N, Hkv, d), 364)
+    par = [random_tree(N, 365 + b) for b in range(B)]
+    dev = torch.tensor(par, dtype=torch.int32).cuda()
+    cnt = torch.tensor(counts, dtype=torch.int32).cuda()
+    o, lse = torch.zeros_like(q), torch.zeros(B, N, H, device="cuda")
+    o2, l2 = torch.zeros_like(o), torch.zeros_like(lse)
+    cache.decode_tree(q, k, v, dev, o, lse, counts=cnt)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(4):
+            cache.decode_tree(q, k, v, dev, o2, l2, counts=cnt)
+    for _ in range(3):
+        o2.zero_()
+        l2.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, o2) and torch.equal(lse, l2)
+    assert cache.sync_status() == 0
+    for b in [0, 1, 2] + list(range(3, B, 9)):
+        c = counts[b]
+        check_tree(o[b, :c], lse[b, :c], q[b, :c], k[b, :c], v[b, :c], states[b], par[b][:c], 100, f"{b}")
+        assert not o[b, c:].any()
+    q1, k1, v1 = normal((B, H, d), 370), normal((B, Hkv, d), 371), normal((B, Hkv, d), 372)
+    steps = torch.empty_like(q1), torch.empty_like(q1)
+    for c, out in zip((cache, other), steps):
+        c.decode_step_fused(q1, k1, v1, out)
+        assert c.sync_status() == 0
+    assert torch.equal(*steps)
+
+
 # ---------------------------------------------------------------------------
 # commit
 # ---------------------------------------------------------------------------
