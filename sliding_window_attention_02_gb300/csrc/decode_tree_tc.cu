@@ -192,7 +192,7 @@ struct Shape {
 struct Seq {
   int cnt, m_b, ring;
   int64_t t_b;
-  int np, nr, tl, units, extra;
+  int p16, r16, tl, units, extra;
   __device__ __forceinline__ void load(const CacheView& cv, const TreeArgs& a, const Shape& sh,
                                        int b) {
     const int c = a.counts ? a.counts[b] : a.nodes;
@@ -201,9 +201,9 @@ struct Seq {
     cnt = min(max(c, 0), a.nodes);
     if (c != cnt) flag_error(cv.err, kErrBadTree);
     ring = (int)min(min(cv.n, t_b), (int64_t)1 << 30);
-    np = (m_b + BN - 1) / BN;
-    nr = (ring + BN - 1) / BN;
-    tl = np + nr + (cnt + BN - 1) / BN;
+    p16 = (m_b + 15) & ~15;
+    r16 = (ring + 15) & ~15;
+    tl = (p16 + r16 + cnt + BN - 1) / BN;
     extra = sh.pair ? kPairUnitCost : kUnitCost;
     const int per = sh.npt << sh.pair;
     units = (cnt + per - 1) / per * cv.Hkv;
@@ -219,35 +219,20 @@ struct Seq {
   }
 };
 
-enum TileKind { kPrefix = 0, kRing = 1, kTree = 2 };
-
 // A segment as the planner hands it over.
 struct Segment {
   int b, kvh, node0, cnt;
   int j0, j1;             // key tiles of the unit inside the range; j1 = 0: no more segments
-  int np, nr;             // the unit's prefix and ring tiles, then come the tree's
+  int p16, t0;            // where the ring's and the tree's keys begin
   int m_b, ring;          // prefix rows, filled ring slots
   int newest, age;        // ring slot of output t_b - 1, and t_b - 1 (clamped)
   uint8_t split, whole, begins, pad;
   int first, last;        // the CTAs that a cut unit begins and ends in
   int tiles;              // the CTA's key tiles before the segment
-  // Kind of key tile j, its index among its kind, and its keys.
-  __device__ void tile(int j, int& kind, int& i, int& keys) const {
-    if (j < np) {
-      kind = kPrefix;
-      i = j;
-      keys = m_b;
-    } else if (j < np + nr) {
-      kind = kRing;
-      i = j - np;
-      keys = ring;
-    } else {
-      kind = kTree;
-      i = j - np - nr;
-      keys = cnt;
-    }
-    keys = min(BN, keys - i * BN);
-  }
+  // Key x of the unit: prefix row x from 0, ring slot x - p16 from p16, node
+  // x - t0 from t0 to the end; p16 and t0 are multiples of 16.
+  __device__ int end() const { return t0 + cnt; }
+  __device__ int keys(int j) const { return min(BN, end() - j * BN); }   // of tile j
 };
 static_assert(sizeof(Segment) <= 64, "segment");
 
@@ -356,7 +341,9 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmKc16,
                       const __grid_constant__ CUtensorMap tmVc16,
                       const __grid_constant__ CUtensorMap tmKt16,
-                      const __grid_constant__ CUtensorMap tmVt16, CacheView cv, TreeArgs a,
+                      const __grid_constant__ CUtensorMap tmVt16,
+                      const __grid_constant__ CUtensorMap tmKc64,
+                      const __grid_constant__ CUtensorMap tmVc64, CacheView cv, TreeArgs a,
                       Shape sh, uint64_t wait_ns) {
   using SM = Smem<D, PAIR>;
   constexpr int NSUB = SM::NSUB, NS = SM::NS, NQ = SM::NQ, NODES = SM::NODES;
@@ -418,6 +405,8 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       prefetch_tmap(&tmVt16);
       prefetch_tmap(&tmKc16);
       prefetch_tmap(&tmVc16);
+      prefetch_tmap(&tmKc64);
+      prefetch_tmap(&tmVc64);
       const uint64_t normal = evict_normal_policy();
       const uint64_t stream = sh.evict ? evict_first_policy() : normal;
       uint32_t gi = 0;                           // loads issued
@@ -426,14 +415,10 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       for (int k = 0; ok && segment(k, w) && w.j1 > 0; ++k) {
         const int64_t slab0 = ((int64_t)w.b * cv.Hkv + w.kvh) * cv.slab_rows;
         for (int j = w.j0; ok && j < w.j1; ++j) {
-          int kind, i, keys;
-          w.tile(j, kind, i, keys);
-          const int boxes = (keys + 15) / 16;
-          const uint64_t pol = kind == kTree ? normal : stream;
-          const int x0 = kind == kTree ? w.kvh * D : 0;
-          const int y0 = kind == kTree
-                             ? w.b * a.nodes + i * BN
-                             : (int)(slab0 + (kind == kRing ? cv.m_cap : 0) + (int64_t)i * BN);
+          const int x0 = j * BN, boxes = (w.keys(j) + 15) / 16;
+          // one box of 128 keys where they have one source, or boxes of 64 and 16
+          const bool whole = boxes == BN / 16 && (x0 + BN <= w.p16 || x0 >= w.t0 ||
+                                                  (x0 >= w.p16 && x0 + BN <= w.t0));
 #pragma unroll 1
           for (int isv = 0; isv < 2; ++isv, ++gi) {
             const uint32_t s = gi % NS;
@@ -444,18 +429,26 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
             }
             const uint32_t dst = sb + SM::OFF_RING + s * kTile;
             mbar_arrive_expect_tx(bar(SM::B_FULL + s), (uint32_t)NSUB * boxes * 2048u);
-            // one box of 128 keys, or one for every 16
-            const bool whole = boxes == BN / 16;
-            const CUtensorMap* map =
-                whole ? (kind == kTree ? (isv ? &tmVt : &tmKt) : (isv ? &tmVc : &tmKc))
-                      : (kind == kTree ? (isv ? &tmVt16 : &tmKt16) : (isv ? &tmVc16 : &tmKc16));
-            const int parts = whole ? 1 : boxes;
 #pragma unroll 1
-            for (int r = 0; r < parts; ++r)
+            for (int r = 0; r < boxes;) {
+              const int x = x0 + 16 * r;
+              const bool tree = x >= w.t0;
+              const int groups =                         // of 16 keys
+                  whole ? BN / 16
+                        : (!tree && r + 4 <= boxes && x + 64 <= (x < w.p16 ? w.p16 : w.t0)) ? 4 : 1;
+              const CUtensorMap* map =
+                  whole ? (tree ? (isv ? &tmVt : &tmKt) : (isv ? &tmVc : &tmKc))
+                        : tree ? (isv ? &tmVt16 : &tmKt16)
+                               : groups == 4 ? (isv ? &tmVc64 : &tmKc64) : (isv ? &tmVc16 : &tmKc16);
+              const int col = tree ? w.kvh * D : 0;
+              const int row = tree ? w.b * a.nodes + x - w.t0
+                                   : (int)(slab0 + (x < w.p16 ? x : cv.m_cap + x - w.p16));
 #pragma unroll
               for (int c = 0; c < NSUB; ++c)
-                tma_load_2d_pol(dst + c * kSub + r * 2048, map, x0 + c * 64, y0 + 16 * r,
-                                bar(SM::B_FULL + s), pol);
+                tma_load_2d_pol(dst + c * kSub + r * 2048, map, col + c * 64, row,
+                                bar(SM::B_FULL + s), tree ? normal : stream);
+              r += groups;
+            }
           }
         }
       }
@@ -516,7 +509,8 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       const uint64_t qdesc = desc_sw128(sb + SM::OFF_Q, 16, 1024);
       const uint64_t kdesc = desc_sw128(sb + SM::OFF_RING, 16, 1024);
       const uint64_t vdesc = desc_sw128(sb + SM::OFF_RING, kSub, 1024);
-      int np = pmore ? segs[0].np - segs[0].j0 : 0, tl = pc.left;
+      // The segment's tiles, and of these, from the first on, those of 128 keys.
+      int nf = pmore ? segs[0].end() / BN - segs[0].j0 : 0, tl = pc.left;
 #pragma unroll 1
       for (uint32_t s = 0; pmore; ++s) {
         const uint32_t half = s & 1;
@@ -530,17 +524,14 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
           if (!pc.second && !wait(SM::B_FULL + pc.slot, pc.phase)) break;
           tc_fence_after();
           const uint64_t vd = vdesc + (uint64_t)(pc.slot * (kTile >> 4));
-          // Tile tl - left of the segment holds 128 keys if a prefix tile comes
-          // after it.
-          if (tl - pc.left + 1 < np) {
+          if (tl - pc.left < nf) {
 #pragma unroll
             for (int k = 0; k < BN / 16; ++k)
               mma_bf16_ts(tmem + tm_o(half), tmem + tm_s(half) + k * 8, vd + k * 128, idesc_pv,
                           k > 0 ? 1u : (first ? 0u : 1u));
           } else {
             const Segment& w = segs[pc.k % NSEG];
-            int kind, i, keys;
-            w.tile(w.j1 - pc.left, kind, i, keys);
+            const int keys = w.keys(w.j1 - pc.left);
 #pragma unroll 1
             for (int k = 0; 16 * k < keys; ++k)
               mma_bf16_ts(tmem + tm_o(half), tmem + tm_s(half) + k * 8, vd + k * 128, idesc_pv,
@@ -552,7 +543,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
           pmore = advance(pc);
           if (pc.k != at) {
             pfresh = pc.split && pc.left == 1 ? 1 : 2;
-            np = segs[pc.k % NSEG].np - segs[pc.k % NSEG].j0;
+            nf = segs[pc.k % NSEG].end() / BN - segs[pc.k % NSEG].j0;
             tl = pc.left;
           }
         }
@@ -696,8 +687,8 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         w.cnt = sq.cnt;
         w.j0 = j0;
         w.j1 = sq.at(x1 - ubase, flat);
-        w.np = sq.np;
-        w.nr = sq.nr;
+        w.p16 = sq.p16;
+        w.t0 = sq.p16 + sq.r16;
         w.m_b = sq.m_b;
         w.ring = sq.ring;
         w.age = (int)min(sq.t_b - 1, (int64_t)1 << 30);
@@ -731,7 +722,7 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
           jd = {b, w.node0, w.kvh, w.last, sq.cnt, {0, 0, 0}};
         // Depths and ancestors of the unit's nodes, where the segment's ring
         // and tree tiles ask for them.
-        const bool ask = w.j1 > sq.np;
+        const bool ask = w.j1 * BN > sq.p16;
         if (ask && par_b != b) {
           __syncwarp();
           for (int i = lane; i < sq.cnt; i += 32) par[i] = a.parents[(size_t)b * a.nodes + i];
@@ -817,20 +808,66 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       bool started = false;
       for (int j = w.j0; j < w.j1; ++j) {
         if (split && ((step + (uint32_t)(j - w.j0)) & 1) != (uint32_t)half) continue;
-        int kind, i, keys;
-        w.tile(j, kind, i, keys);
-        const int k0 = i * BN;
-        const bool full = kind == kPrefix && keys == BN;
+        const int x0 = j * BN;
+        const bool full = x0 + BN <= w.m_b;              // every column is a key of every row
+        if (x0 + BN > w.p16 && !nodes()) {
+          ok = false;
+          break;
+        }
+        // The row's keys among the tile's columns, while S is on its way.
+        uint32_t see0 = 0u, see1 = 0u, see2 = 0u, see3 = 0u;
+        if (any && !full) {
+          // Ring slot s is a key iff its age (r0 - s) mod n is at most lim.
+          const int rc = w.p16 - x0, tc = w.t0 - x0;     // columns of slot 0 and node 0
+          int a1 = 0, b1 = -1, a2 = 0, b2 = -1;
+          if (x0 < w.t0 && x0 + BN > w.p16) {
+            const int lim = min(w.age, n - 2 - (live ? nd[ni] : 0));
+            if (lim >= 0) {
+              a1 = max(r0 - lim, 0) + rc;
+              b1 = r0 + rc;
+              if (r0 < lim) {
+                a2 = r0 - lim + n + rc;
+                b2 = n - 1 + rc;
+              }
+            }
+          }
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t see = 0u;
+            if (32 * c < w.m_b - x0) see = range_mask(0, w.m_b - 1 - x0, c);
+            if (32 * c + 32 > rc && 32 * c < tc)
+              see |= range_mask(a1, b1, c) | range_mask(a2, b2, c);
+            const int c0 = 32 * c - tc;                  // the chunk's first node
+            if (live && c0 > -32 && c0 < w.cnt) {
+              if (c0 + 32 <= BN * NTT) {
+                const int i = c0 >> 5;                   // -1: nodes from column 16 on
+                const uint32_t lo = i < 0 ? 0u : (uint32_t)nd[(1 + i) * NODES + ni];
+                const uint32_t hi = c0 & 31 ? (uint32_t)nd[(2 + i) * NODES + ni] : 0u;
+                see |= __funnelshift_r(lo, hi, c0 & 31);
+              } else {
+                // far nodes of a large tree: walk up from the row's
+                const int32_t* par = a.parents + (size_t)w.b * a.nodes;
+                int up = 0;
+                for (int x = node; x >= c0 && up < n; ++up) {
+                  if (x < c0 + 32) see |= 1u << (x - c0);
+                  const int p = par[x];
+                  if (p >= x) break;
+                  x = p;
+                }
+              }
+            }
+            see0 = see1;
+            see1 = see2;
+            see2 = see3;
+            see3 = see;
+          }
+        }
         if (!__all_sync(0xffffffffu,
                         wait_for(bar(SM::B_S + half), turns & 1, abort_flag, wait_ns))) {
           ok = false;
           break;
         }
         ++turns;
-        if (kind != kPrefix && !nodes()) {
-          ok = false;
-          break;
-        }
         tc_fence_after();
         if (any) {
           // Pass 1: the row's maximum; scores of columns that are no keys of it
@@ -859,41 +896,12 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
             }
             tmem_wait_ld32(va);                          // columns 0-31, for pass 2
           } else {
-            // Ring: slot s is a key iff its age (r0 - s) mod n is at most lim.
-            int a1 = 0, b1 = keys - 1, a2 = 1, b2 = 0;
-            if (kind == kRing) {
-              const int lim = min(w.age, n - 2 - (live ? nd[ni] : 0));
-              if (lim < 0) {
-                b1 = -1;
-              } else if (r0 >= lim) {
-                a1 = r0 - lim - k0;
-                b1 = r0 - k0;
-              } else {
-                b1 = r0 - k0;
-                a2 = r0 - lim + n - k0;
-                b2 = n - 1 - k0;
-              }
-            }
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-              uint32_t see = range_mask(a1, b1, c) | range_mask(a2, b2, c);
-              if (kind == kTree) {
-                see = 0u;
-                if (live && i < NTT) {
-                  see = (uint32_t)nd[(1 + 4 * i + c) * NODES + ni];
-                } else if (live) {
-                  // a further tile of a large tree: walk up from the node
-                  const int32_t* par = a.parents + (size_t)w.b * a.nodes;
-                  const int c0 = k0 + 32 * c;
-                  int up = 0;
-                  for (int x = node; x >= c0 && up < n; ++up) {
-                    if (x < c0 + 32) see |= 1u << (x - c0);
-                    const int p = par[x];
-                    if (p >= x) break;
-                    x = p;
-                  }
-                }
-              }
+              const uint32_t see = see0;
+              see0 = see1;
+              see1 = see2;
+              see2 = see3;
               tmem_ld32_sync(s_addr + 32 * c, va);
 #pragma unroll
               for (int e = 0; e < 32; ++e)
@@ -957,18 +965,28 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
           tc_fence_before();
         }
         started = true;
-        if (keys % 16 != 0 && (warp & 3) == 0) {
-          // Value rows keys .. up to the next 16 are no keys of any row (of the
-          // tree, nodes past the count or the next sequence's) and may hold
-          // anything: zero, as 0 x NaN is NaN.
+        // Value rows from key e, a source's end, to the next multiple of 16 are no
+        // keys of any row (of the tree, nodes past the count or the next
+        // sequence's) and may hold anything: zero, as 0 x NaN is NaN.
+        const int e1 = w.p16 + w.ring, e2 = w.end();
+        auto ends = [&](int e) { return (e & 15) != 0 && e >> 7 == j; };
+        if ((warp & 3) == 0 && (ends(w.m_b) || ends(e1) || ends(e2))) {
           const uint32_t vi = 2u * (uint32_t)(w.tiles + j - w.j0) + 1u;
           if (__all_sync(0xffffffffu, wait_for(bar(SM::B_FULL + vi % NS), (vi / NS) & 1,
                                                 abort_flag, wait_ns))) {
-            const int rows = 16 - keys % 16;
-            uint8_t* v = smem + SM::OFF_RING + (vi % NS) * kTile + keys * 128;
-            for (int x = lane; x < rows * 8 * NSUB; x += 32)
-              *reinterpret_cast<uint4*>(v + x / (rows * 8) * kSub + x % (rows * 8) * 16) =
-                  make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+            for (int i = 0; i < 3; ++i) {
+              const int e = i == 0 ? w.m_b : i == 1 ? e1 : e2;
+              if (!ends(e)) continue;
+              uint8_t* v = smem + SM::OFF_RING + (vi % NS) * kTile + (e & 112) * 128 + lane * 16;
+#pragma unroll
+              for (int x = 0; x < 16; x += 4)            // a row is 8 lanes
+                if (x + (lane >> 3) >= (e & 15)) {
+#pragma unroll
+                  for (int c = 0; c < NSUB; ++c)
+                    *reinterpret_cast<uint4*>(v + x * 128 + c * kSub) = make_uint4(0, 0, 0, 0);
+                }
+            }
             fence_proxy_async_smem();
           }
         }
@@ -1328,7 +1346,7 @@ int64_t most_units(const CacheView& cv, int nodes, const Shape& sh) {
   return (int64_t)cv.B * cv.Hkv * ((nodes + per - 1) / per);
 }
 int64_t most_tiles(const CacheView& cv, int nodes) {
-  return (cv.m_cap + BN - 1) / BN + (cv.n + BN - 1) / BN + (nodes + BN - 1) / BN;
+  return ((cv.m_cap + 15) / 16 * 16 + (cv.n + 15) / 16 * 16 + nodes + BN - 1) / BN;
 }
 int64_t most_cost(const CacheView& cv, int nodes, const Shape& sh) {
   return most_units(cv, nodes, sh) * (most_tiles(cv, nodes) + kUnitCost);
@@ -1370,7 +1388,8 @@ cudaError_t launch_d(const CacheView& cv, const TreeArgs& a, const SlabMaps& map
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, PAIR>::kBytes);
   if (e != cudaSuccess) return e;
   e = launch_dependent(decode_tree_tc_kernel<D, PAIR>, dim3(grid), dim3(kThreads), Smem<D, PAIR>::kBytes, s, mq,
-                       maps.k, maps.v, mkt, mvt, maps.k16, maps.v16, mkt16, mvt16, cv, a, sh,
+                       maps.k, maps.v, mkt, mvt, maps.k16, maps.v16, mkt16, mvt16, maps.k64,
+                       maps.v64, cv, a, sh,
                        phase_wait_limit_ns());
   if (e != cudaSuccess) return e;
   if (sh.flat || sh.inl) return cudaSuccess;
@@ -1406,7 +1425,9 @@ bool make_slab_maps(const CacheView& cv, SlabMaps* maps) {
   return make_tmap_rows_bf16(&maps->k, cv.K, cv.d, rows) &&
          make_tmap_rows_bf16(&maps->v, cv.V, cv.d, rows) &&
          make_tmap_rows_bf16(&maps->k16, cv.K, cv.d, rows, 16) &&
-         make_tmap_rows_bf16(&maps->v16, cv.V, cv.d, rows, 16);
+         make_tmap_rows_bf16(&maps->v16, cv.V, cv.d, rows, 16) &&
+         make_tmap_rows_bf16(&maps->k64, cv.K, cv.d, rows, 64) &&
+         make_tmap_rows_bf16(&maps->v64, cv.V, cv.d, rows, 64);
 }
 
 cudaError_t launch_decode_tree_tc(const CacheView& cv, const TreeArgs& a, const SlabMaps& maps,

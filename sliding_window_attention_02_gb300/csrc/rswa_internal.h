@@ -180,10 +180,10 @@ size_t decode_tree_workspace(const CacheView& cv, int nodes);
 bool decode_tree_use_tc(const CacheView& cv, int nodes);
 bool decode_tree_tc_supported(const CacheView& cv, int nodes);
 size_t decode_tree_tc_workspace(const CacheView& cv, int nodes);
-// Its tensor maps of the cache slabs (boxes of 128 and of 16 rows): the slabs
+// Its tensor maps of the cache slabs (boxes of 128, 64 and 16 rows): the slabs
 // stay where they are, so a handle makes them once.
 struct SlabMaps {
-  CUtensorMap k, v, k16, v16;
+  CUtensorMap k, v, k16, v16, k64, v64;
 };
 bool make_slab_maps(const CacheView& cv, SlabMaps* maps);
 cudaError_t launch_decode_tree_tc(const CacheView& cv, const TreeArgs& a, const SlabMaps& maps,
