@@ -184,11 +184,12 @@ cudaError_t launch_tree_t(const CacheView& cv, const TreeArgs& a, bool prefetch,
 
 // Small work is done sooner on the CUDA cores, whose kernel takes 3.4 us and the
 // larger of 7.1 ns a key (while its CTAs fit the SMs twice) and 65 ps for each
-// pair of a query row and a key; the tensor-core kernel takes 11 us while a
-// unit's keys are few and 13.5 and more where it cuts them.  bf16, d 128, 10
-// heads, us on the CUDA / tensor cores: 16 nodes 7.8 / 10.8 at 416 keys, 17.0 /
-// 13.5 at 1184; 32 nodes 12.9 / 10.7 at 416; 1 node 11.2 / 14 at 1184, 34 / 16 at
-// 4256.
+// pair of a query row and a key; the tensor-core kernel takes 7 us and 1 for a
+// tile of 128 keys while its units are few, 13.5 and more where it cuts them, and
+// 3 more for every further unit of an SM.  bf16, d 128, 10 heads, us on the CUDA /
+// tensor cores: 16 nodes 5.8 / 8.4 at 192 keys, 7.8 / 10.1 at 416, 17.0 / 14.6 at
+// 1184; 32 nodes 9.4 / 9.0 at 192, 12.8 / 10.3 at 416; 1 node 11.2 / 14 at 1184,
+// 34 / 16 at 4256; 51 sequences of at most 120 keys: 1 node 7.7 / 24.6.
 // The keys are the cache's capacity: the host does not know the live ones.
 constexpr int64_t kCudaCorePairs = 110000, kCudaCoreKeys = 1200;
 

@@ -13,18 +13,25 @@
 // where the trees have more rows than that, a pair of query tiles, one for
 // each half, that read every key tile once between them.
 //
-// Work: the key tiles of a unit (prefix, ring, tree; 128 keys each) one after
-// the other, unit after unit, form one list, which the CTAs (one per SM) cut
-// into equal ranges.  A CTA streams its range through one TMA ring without
-// draining between units; a unit that a range covers whole is written out at
-// once, of another the CTA leaves a partial (m, l, O) in the workspace.  Each
-// CTA leaves at most two: of the unit that a CTA before it began, and of the one
-// that it begins and does not end.  The partials of a cut unit are joined
+// Keys: a unit's prefix rows, its ring slots and its nodes follow each other,
+// each from a multiple of 16 on, and are cut into tiles of 128: a tile costs the
+// same however many of its keys are real, and only those that lie in the prefix
+// whole need no masks (tiles of one source each: 64 sequences 84.2 us for 80.8,
+// 64 grouped 123.7 for 113.8, 51 sequences of 85 keys 26.5 for 16.4).  A tile of
+// several sources is loaded in boxes of 64 and 16 keys.
+//
+// Work: the key tiles of a unit one after the other, unit after unit, form one
+// list, which the CTAs (one per SM) cut into equal ranges.  A CTA streams its
+// range through one TMA ring without draining between units; a unit that a range
+// covers whole is written out at once, of another the CTA leaves a partial (m, l,
+// O) in the workspace.  Each CTA leaves at most two: of the unit that a CTA before
+// it began, and of the one that it begins and does not end.  The partials of a cut
+// unit are joined
 //   pairs, in many units: by the last of the unit's CTAs, from its own
 //     accumulators where it is the one that began the unit (64 sequences of
-//     32 / 8 heads and 64 nodes: 123.7 us, with the second kernel 128.8; a
-//     launch without pairs has a quarter to an eighth of the partials, and gets
-//     slower by the code: 84.2 -> 84.7 and 21.8 -> 22.8 us)
+//     32 / 8 heads and 64 nodes: 4 % less time than with the second kernel; a
+//     launch without pairs has a quarter to an eighth of the partials and gains
+//     nothing)
 //   otherwise: by a second, dependent kernel.
 // The order of a unit's partials is the same whoever joins it last.
 //
@@ -38,18 +45,18 @@
 // PV(0) QK(2) PV(1) QK(3) ..., so the tensor core works on one half while the
 // other half's softmax runs.  TMEM: S0 | S1 | O0 | O1, P over S.  O is
 // rescaled lazily (threshold 2^8, exact because O and l share the reference).
-// A key tile's PV takes only the 16-key steps that hold keys; keys are loaded
-// to the next multiple of 16, and value rows of nodes past the count are
-// zeroed first (0 x NaN is NaN).  Every wait is bounded; on a timeout the CTA
-// drains its copies and MMAs, frees TMEM and sets the cache's device flag.
+// A key tile's PV takes only the 16-key steps that hold keys; value rows between
+// a source's end and the next multiple of 16 are zeroed first (0 x NaN is NaN).
+// Every wait is bounded; on a timeout the CTA drains its copies and MMAs, frees
+// TMEM and sets the cache's device flag.
 //
 // What bounds it: for many sequences (64 with prefixes of 256..2048 rows,
 // n 128) the issue slots of the softmax, two exchanges of 128 x 128 scores and
 // weights with TMEM a tile and half, and one product at a time: 10 heads and 32
-// nodes take 84.2 us where the bytes take 57.6 at the copy rate and the launch
-// without softmax and products 73; 32 / 8 heads and 64 nodes 123.7, bytes 57.0,
-// products alone 41.  For one long sequence (40 pages) latency: 21.8 us, of
-// which 4.6 are state, plan and first keys, and 4.6 the second kernel.
+// nodes take 80.8 us where the bytes take 57.6 at the copy rate; 32 / 8 heads and
+// 64 nodes 113.8, bytes 57.0, products alone 41.  For one long sequence (40 pages)
+// latency: 22.8 us, of which 4.6 are state, plan and first keys, and 4.6 the
+// second kernel.
 #include <cuda.h>
 
 #include <algorithm>
@@ -1352,9 +1359,17 @@ int64_t most_cost(const CacheView& cv, int nodes, const Shape& sh) {
   return most_units(cv, nodes, sh) * (most_tiles(cv, nodes) + kUnitCost);
 }
 
-// Units of up to this many tiles, no more of them than SMs, have a CTA each:
-// the second kernel would take longer than what cutting them saves.
-constexpr int kFlatTiles = 6;
+// Units, no more of them than SMs, have a CTA each where cutting them would save
+// less than the second kernel and the starts of their parts take: at most
+// kFlatTiles tiles, of which an even cut would leave a CTA units / SMs.  us for a
+// CTA each / cut: 70 units of 9 tiles 15.3 / 21.7, 46 of 7 13.6 / 19.2, 16 pairs
+// of 7 24.8 / 28.5, 32 of 10 17.7 / 19.3, but 10 of 10 17.0 / 13.5.
+constexpr int kFlatTiles = 10, kFlatSaved = 8;
+
+bool flat_of(const CacheView& cv, int nodes, const Shape& sh) {
+  const int64_t units = most_units(cv, nodes, sh), tiles = most_tiles(cv, nodes);
+  return units <= cv.sms && tiles <= kFlatTiles && tiles * (cv.sms - units) <= kFlatSaved * cv.sms;
+}
 
 // CTAs of the launch: one per SM, no more than the largest list could feed.
 int grid_of(const CacheView& cv, int nodes, const Shape& sh) {
@@ -1366,7 +1381,7 @@ template <int D, bool PAIR>
 cudaError_t launch_d(const CacheView& cv, const TreeArgs& a, const SlabMaps& maps,
                      cudaStream_t s) {
   Shape sh = shape_of(cv, a.nodes);
-  sh.flat = most_units(cv, a.nodes, sh) <= cv.sms && most_tiles(cv, a.nodes) <= kFlatTiles;
+  sh.flat = flat_of(cv, a.nodes, sh);
   const int grid = grid_of(cv, a.nodes, sh);
   const uint64_t trows = (uint64_t)cv.B * a.nodes;
   const uint64_t crows = (uint64_t)cv.B * cv.Hkv * cv.slab_rows;
