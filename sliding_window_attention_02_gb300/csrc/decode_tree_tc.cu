@@ -16,9 +16,9 @@
 // Keys: a unit's prefix rows, its ring slots and its nodes follow each other,
 // each from a multiple of 16 on, and are cut into tiles of 128: a tile costs the
 // same however many of its keys are real, and only those that lie in the prefix
-// whole need no masks (tiles of one source each: 64 sequences 84.2 us for 80.8,
-// 64 grouped 123.7 for 113.8, 51 sequences of 85 keys 26.5 for 16.4).  A tile of
-// several sources is loaded in boxes of 64 and 16 keys.
+// whole need no masks (64 sequences 84.2 -> 80.8 us, 64 grouped 123.7 -> 113.8, 51
+// sequences of 85 keys 26.5 -> 16.4 when tiles of one source each gave way to
+// this).  A tile of several sources is loaded in boxes of 64 and 16 keys.
 //
 // Work: the key tiles of a unit one after the other, unit after unit, form one
 // list, which the CTAs (one per SM) cut into equal ranges.  A CTA streams its
@@ -54,7 +54,7 @@
 // n 128) the issue slots of the softmax, two exchanges of 128 x 128 scores and
 // weights with TMEM a tile and half, and one product at a time: 10 heads and 32
 // nodes take 80.8 us where the bytes take 57.6 at the copy rate; 32 / 8 heads and
-// 64 nodes 113.8, bytes 57.0, products alone 41.  For one long sequence (40 pages)
+// 64 nodes 111.4, bytes 57.0, products alone 41.  For one long sequence (40 pages)
 // latency: 22.8 us, of which 4.6 are state, plan and first keys, and 4.6 the
 // second kernel.
 #include <cuda.h>
@@ -277,15 +277,26 @@ __device__ __forceinline__ float* partial_at(void* ws, int grid, int slot, int D
          (size_t)slot * partial_floats(D, pair);
 }
 
-// 32 columns of a row, times inv.
+// 32 columns of a row, times inv, 32 bytes an instruction where o is aligned to
+// that: the rows of a warp lie 256 bytes or more apart, and 16 at a time write
+// every sector twice (64 grouped sequences 113.8 us for 111.4).
 __device__ __forceinline__ void store_columns(__nv_bfloat16* to, const float* x, float inv) {
-  uint4* dst = reinterpret_cast<uint4*>(to);
+  uint32_t p[16];
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    dst[e] = make_uint4(pack_bf16(x[8 * e] * inv, x[8 * e + 1] * inv),
-                        pack_bf16(x[8 * e + 2] * inv, x[8 * e + 3] * inv),
-                        pack_bf16(x[8 * e + 4] * inv, x[8 * e + 5] * inv),
-                        pack_bf16(x[8 * e + 6] * inv, x[8 * e + 7] * inv));
+  for (int e = 0; e < 16; ++e) p[e] = pack_bf16(x[2 * e] * inv, x[2 * e + 1] * inv);
+  if ((reinterpret_cast<uintptr_t>(to) & 31) == 0) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to + 16 * e),
+                   "r"(p[8 * e]), "r"(p[8 * e + 1]), "r"(p[8 * e + 2]), "r"(p[8 * e + 3]),
+                   "r"(p[8 * e + 4]), "r"(p[8 * e + 5]), "r"(p[8 * e + 6]), "r"(p[8 * e + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      reinterpret_cast<uint4*>(to)[e] =
+          make_uint4(p[4 * e], p[4 * e + 1], p[4 * e + 2], p[4 * e + 3]);
+  }
 }
 
 // x += wp times the partial's columns 32 c .. 32 c + 31 of the row.

@@ -749,6 +749,25 @@ def test_decode_tree_many_pairs(cuda_lib, B, H, Hkv, N, d):
     assert torch.equal(*steps)
 
 
+@pytest.mark.parametrize("B,H,Hkv,N,d", [(2, 10, 10, 40, 128), (2, 8, 2, 60, 64), (40, 16, 4, 60, 128)])
+def test_decode_tree_output_at_16_bytes(cuda_lib, B, H, Hkv, N, d):
+    """o 16 and not 32 bytes aligned, lse 4: the same bits."""
+    rswa = cuda_lib
+    cache, _ = make_cache(rswa, [300 + 7 * b for b in range(B)], [90 + b for b in range(B)], 64, H, Hkv, d, BF, 380,
+                          700)
+    q, k, v = normal((B, N, H, d), 381), normal((B, N, Hkv, d), 382), normal((B, N, Hkv, d), 383)
+    dev = torch.tensor([random_tree(N, 384 + b) for b in range(B)], dtype=torch.int32).cuda()
+    o, lse = torch.zeros_like(q), torch.zeros(B, N, H, device="cuda")
+    cache.decode_tree(q, k, v, dev, o, lse)
+    buf, lbuf = torch.zeros(q.numel() + 24, dtype=BF, device="cuda"), torch.zeros(lse.numel() + 2, device="cuda")
+    o2, l2 = buf[8:8 + q.numel()].view(q.shape), lbuf[1:1 + lse.numel()].view(lse.shape)
+    assert o2.data_ptr() % 32 == 16
+    cache.decode_tree(q, k, v, dev, o2, l2)
+    assert cache.sync_status() == 0
+    assert torch.equal(o, o2) and torch.equal(lse, l2)
+    assert not buf[:8].any() and not buf[-16:].any() and lbuf[0] == 0 and lbuf[-1] == 0
+
+
 # ---------------------------------------------------------------------------
 # commit
 # ---------------------------------------------------------------------------
