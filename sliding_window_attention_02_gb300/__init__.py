@@ -196,7 +196,17 @@ def _current_stream(index: int):
     return _raw_stream(index)
 
 
-_raw_stream = None
+def _current_device():
+    """torch.cuda.current_device(), without its test for an initialised CUDA
+    (0.2 us of a call): the caller has a CUDA tensor."""
+    global _get_device
+    if _get_device is None:
+        import torch
+        _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _get_device()
+
+
+_raw_stream = _get_device = None
 
 
 def _rows(t, shape, dtype, index, name):
@@ -331,11 +341,12 @@ def rswa_qk_norm_rope(rope, q, k, positions, q_out, k_out, stream=None) -> None:
     """rope: RswaRope; q, k: [rows][heads][d], the rows possibly part of longer
     ones (a fused projection's output); positions: int64 [rows]; q_out, k_out:
     contiguous, or q and k themselves."""
-    if q.dim() != 3 or k.dim() != 3:
+    shape, k_shape = q.shape, k.shape
+    if len(shape) != 3 or len(k_shape) != 3:
         raise ValueError("q, k: expected [rows][heads][d]")
     index, dt, torch = q.get_device(), q.dtype, rope.torch
-    rows, heads, d = shape = q.shape
-    kv_heads = k.shape[1]
+    rows, heads, d = shape
+    kv_heads = k_shape[1]
     k_shape = (rows, kv_heads, d)
     if index < 0:
         raise ValueError("q: expected a CUDA tensor")
@@ -349,7 +360,7 @@ def rswa_qk_norm_rope(rope, q, k, positions, q_out, k_out, stream=None) -> None:
             _dense(positions, (rows,), torch.int64, index, "positions"), rows, heads, kv_heads,
             d, code, _dense(q_out, shape, dt, index, "q_out"),
             _dense(k_out, k_shape, dt, index, "k_out"), _stream_of(stream, index))
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = load().rswa_qk_norm_rope(*args)
     else:
         with torch.cuda.device(index):
