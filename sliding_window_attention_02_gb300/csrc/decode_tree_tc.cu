@@ -1413,10 +1413,9 @@ cudaError_t launch_d(const CacheView& cv, const TreeArgs& a, const SlabMaps& map
   cudaError_t e = cudaFuncSetAttribute(decode_tree_tc_kernel<D, PAIR>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, PAIR>::kBytes);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(decode_tree_tc_kernel<D, PAIR>, dim3(grid), dim3(kThreads), Smem<D, PAIR>::kBytes, s, mq,
-                       maps.k, maps.v, mkt, mvt, maps.k16, maps.v16, mkt16, mvt16, maps.k64,
-                       maps.v64, cv, a, sh,
-                       phase_wait_limit_ns());
+  e = launch_dependent(decode_tree_tc_kernel<D, PAIR>, dim3(grid), dim3(kThreads),
+                       Smem<D, PAIR>::kBytes, s, mq, maps.k, maps.v, mkt, mvt, maps.k16, maps.v16,
+                       mkt16, mvt16, maps.k64, maps.v64, cv, a, sh, phase_wait_limit_ns());
   if (e != cudaSuccess) return e;
   if (sh.flat || sh.inl) return cudaSuccess;
   const int rows = PAIR ? 2 * BM : std::min(a.nodes, sh.npt) * sh.G;

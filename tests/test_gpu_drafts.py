@@ -749,6 +749,63 @@ def test_decode_tree_many_pairs(cuda_lib, B, H, Hkv, N, d):
     assert torch.equal(*steps)
 
 
+@pytest.mark.parametrize("H,Hkv,N,d,n", [(2, 2, 21, 128, 40), (4, 2, 50, 64, 40), (8, 2, 70, 128, 33)])
+def test_decode_tree_sources_meet_inside_a_tile(cuda_lib, H, Hkv, N, d, n):
+    """Prefix, ring and nodes that end before, at and past multiples of 16 and of
+    128; NaN in every row of the slabs that is no key, and in dead nodes."""
+    rswa = cuda_lib
+    g = np.random.default_rng(400)
+    m = [x for x in (0, 1, 15, 16, 17, 95, 96, 111, 112, 113, 127, 128, 129, 144) for _ in range(4)]
+    t = [x for _ in range(14) for x in (0, 16, 31, 3 * n + 5)]
+    B = len(m)
+    cache, states = make_cache(rswa, m, t, n, H, Hkv, d, BF, 401, 147)
+    Ks, Vs = cache.slabs()
+    rows = torch.arange(147 + n, device="cuda")
+    for b in range(B):
+        dead = (rows >= m[b]) & (rows < 147) | (rows >= 147 + min(n, t[b]))
+        Ks[b, :, dead] = float("nan")
+        Vs[b, :, dead] = float("nan")
+    counts = [int(x) for x in g.choice([1, 15, 16, 17, N - 1, N], B)]
+    q, k, v = normal((B, N, H, d), 402), normal((B, N, Hkv, d), 403), normal((B, N, Hkv, d), 404)
+    for b in range(B):
+        for x in (q, k, v):
+            x[b, counts[b]:] = float("nan")
+    par = [random_tree(N, 405 + b) for b in range(B)]
+    o, lse = torch.zeros_like(q), torch.zeros(B, N, H, device="cuda")
+    cache.decode_tree(q, k, v, torch.tensor(par, dtype=torch.int32).cuda(), o, lse,
+                      counts=torch.tensor(counts, dtype=torch.int32).cuda())
+    assert cache.sync_status() == 0
+    for b in range(B):
+        c = counts[b]
+        check_tree(o[b, :c], lse[b, :c], q[b, :c], k[b, :c], v[b, :c], states[b], par[b][:c], n, f"{b}")
+        assert not o[b, c:].any() and not lse[b, c:].any()
+
+
+def test_decode_tree_many_pairs_wait_runs_out_then_recovers(cuda_lib):
+    """Units whose CTAs meet on the cache's counters: cleared by set_t."""
+    rswa = cuda_lib
+    B, H, Hkv, N, d = 60, 12, 3, 60, 128
+    m, t = [100 + 9 * b for b in range(B)], [3 * b for b in range(B)]
+    cache, _ = make_cache(rswa, m, t, 100, H, Hkv, d, BF, 390, 700)
+    q, k, v = normal((B, N, H, d), 391), normal((B, N, Hkv, d), 392), normal((B, N, Hkv, d), 393)
+    dev = torch.tensor([random_tree(N, 394 + b) for b in range(B)], dtype=torch.int32).cuda()
+    want = torch.zeros_like(q), torch.zeros(B, N, H, device="cuda")
+    cache.decode_tree(q, k, v, dev, *want)
+    assert cache.sync_status() == 0
+    for _ in range(3):
+        rswa.rswa_debug_set_wait_limit_ns(1)
+        try:
+            cache.decode_tree(q, k, v, dev, torch.zeros_like(q))
+        finally:
+            rswa.rswa_debug_set_wait_limit_ns(0)
+        assert cache.sync_status() == RSWA_EDEVICE
+        cache.set_t(t)
+        got = torch.zeros_like(q), torch.zeros(B, N, H, device="cuda")
+        cache.decode_tree(q, k, v, dev, *got)
+        assert cache.sync_status() == 0
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
 @pytest.mark.parametrize("B,H,Hkv,N,d", [(2, 10, 10, 40, 128), (2, 8, 2, 60, 64), (40, 16, 4, 60, 128)])
 def test_decode_tree_output_at_16_bytes(cuda_lib, B, H, Hkv, N, d):
     """o 16 and not 32 bytes aligned, lse 4: the same bits."""
