@@ -196,6 +196,14 @@ def _current_stream(index: int):
     return _raw_stream(index)
 
 
+def _torch_stream(handle: int, index: int):
+    """The torch stream of a handle (0 and cudaStreamLegacy: the default one)."""
+    import torch
+    if handle in (0, 1):
+        return torch.cuda.default_stream(index)
+    return torch.cuda.ExternalStream(handle, device=index)
+
+
 def _current_device():
     """torch.cuda.current_device(), without its test for an initialised CUDA
     (0.2 us of a call): the caller has a CUDA tensor."""
@@ -518,8 +526,8 @@ class RswaCache:
                        torch.float32 if dtype == RSWA_F32 else torch.bfloat16,
                        self.buf.get_device())
         self._int32, self._float32 = torch.int32, torch.float32
-        # decode_tree's own workspaces, by node count; all stay, as captured
-        # graphs hold them
+        # decode_tree's own workspaces, by node count and stream; all stay, as
+        # captured graphs hold them
         self._tree_ws = {}
 
     def close(self):
@@ -589,7 +597,8 @@ class RswaCache:
             raise RswaError(status, "rswa_append_kv_rope")
 
     def tree_workspace(self, nodes):
-        """A workspace for decode_tree calls of up to `nodes` nodes."""
+        """A workspace for decode_tree calls of up to `nodes` nodes, like any
+        tensor made on torch's current stream."""
         import torch
         return torch.empty(rswa_decode_tree_workspace(self.handle, nodes),
                            dtype=torch.uint8, device=self.buf.device)
@@ -598,8 +607,8 @@ class RswaCache:
                     stream=None):
         """Attention of a tree of drafted tokens per sequence over the cache
         (see rswa_decode_tree).  workspace: from tree_workspace; None: one the
-        cache keeps, which has to exist before a stream capture (by a call
-        outside it) and serves calls that do not overlap."""
+        cache keeps for the stream; a capture takes one that a call before it
+        has made."""
         B, H, Hkv, d, dt, ix = self._shape
         nodes = q.shape[1]
         i32 = self._int32
@@ -610,30 +619,43 @@ class RswaCache:
         op = _dense(o, (B, nodes, H, d), dt, ix, "o")
         lp = None if lse is None else _dense(lse, (B, nodes, H), self._float32, ix, "lse")
         cp = None if counts is None else _dense(counts, (B,), i32, ix, "counts")
+        at = _stream_of(stream, ix)
         if workspace is None:
-            workspace = self._own_workspace(nodes)
+            workspace = self._own_workspace(nodes, at)
         elif workspace.get_device() != ix:
             raise ValueError(f"workspace: expected a tensor on CUDA device {ix}")
         status = load().rswa_decode_tree(
             self.handle, qp, kp, vp, pp, cp, nodes, op, lp, _ptr(workspace),
-            workspace.numel(), _stream_of(stream, ix))
+            workspace.numel(), at)
         if status:
             raise RswaError(status, "rswa_decode_tree")
 
-    def _own_workspace(self, nodes):
-        """The cache's workspace for trees of `nodes` nodes, made by the first
-        call that needs it (or a larger one)."""
-        have = self._tree_ws.get(nodes)
-        if have is None:
-            import torch
-            if torch.cuda.is_current_stream_capturing():
-                raise ValueError("decode_tree: no workspace of the cache's own yet: call it "
-                                 "once before the capture, or pass one")
-            need = rswa_decode_tree_workspace(self.handle, nodes)
-            have = next((w for w in self._tree_ws.values() if w.numel() >= need), None)
+    def _own_workspace(self, nodes, stream):
+        """The cache's workspace for trees of `nodes` nodes on a stream (handle):
+        made by the first call there that needs one (or a larger one), from the
+        stream's own pool, so that torch's allocator neither hands the cache a
+        block that other queued work still uses nor, once the cache is gone,
+        others one that the stream's queued calls do.  A capture takes one made
+        before it: calls on one cache are ordered, so it need not be its own."""
+        stream = getattr(stream, "value", stream) or 0
+        have = self._tree_ws.get((nodes, stream))
+        if have is not None:
+            return have
+        import torch
+        need = rswa_decode_tree_workspace(self.handle, nodes)
+        capturing = torch.cuda.is_current_stream_capturing()
+        with torch.cuda.stream(_torch_stream(stream, self.buf.get_device())):
+            if capturing or torch.cuda.is_current_stream_capturing():
+                have = next((w for w in self._tree_ws.values() if w.numel() >= need), None)
+                if have is None:
+                    raise ValueError("decode_tree: no workspace of the cache's own yet: call it "
+                                     "once before the capture, or pass one")
+                return have
+            have = next((w for (_, at), w in self._tree_ws.items()
+                         if at == stream and w.numel() >= need), None)
             if have is None:
                 have = self.tree_workspace(nodes)
-            self._tree_ws[nodes] = have
+        self._tree_ws[nodes, stream] = have
         return have
 
     def commit_tree(self, k, v, path, accepted, stream=None):

@@ -1100,6 +1100,74 @@ def test_two_caches_on_two_streams(cuda_lib):
         check_tree(out[i][0][0], out[i][1][0], *(a[0] for a in x[i]), made[i][1][0], par[i], 64, f"cache {i}")
 
 
+def test_own_workspaces_belong_to_their_streams(cuda_lib):
+    """The workspace that a cache makes for itself comes from the pool of the
+    stream that the call runs on (named, or torch's current one), whose queued
+    work orders its use and its release."""
+    rswa = cuda_lib
+    cache, states = make_cache(rswa, [1500], [40], 64, 8, 2, 128, BF, 410)
+    q, k, v = normal((1, 60, 8, 128), 411), normal((1, 60, 2, 128), 412), normal((1, 60, 2, 128), 413)
+    par = [random_tree(60, 414)]
+    dev = torch.tensor(par, dtype=torch.int32).cuda()
+    default, named, current = torch.cuda.current_stream(), torch.cuda.Stream(), torch.cuda.Stream()
+    outs = [(torch.empty_like(q), torch.empty(1, 60, 8, device="cuda")) for _ in range(4)]
+
+    def pool(w):
+        at, size = w.data_ptr(), w.numel()
+        assert size > 1 << 20                    # of the tensor-core kernel
+        return [s["stream"] for s in torch.cuda.memory_snapshot()
+                if s["address"] <= at and at + size <= s["address"] + s["total_size"]]
+
+    torch.cuda.synchronize()
+    cache.decode_tree(q, k, v, dev, *outs[0], stream=named)
+    current.wait_stream(named)
+    with torch.cuda.stream(current):
+        cache.decode_tree(q, k, v, dev, *outs[1])
+    default.wait_stream(current)
+    cache.decode_tree(q, k, v, dev, *outs[2])
+    cache.decode_tree(q[:, :9].contiguous(), k[:, :9].contiguous(), v[:, :9].contiguous(),
+                      dev[:, :9].contiguous(), outs[3][0][:, :9].contiguous())   # fewer: the same one
+    torch.cuda.synchronize()
+    used = sorted({w.data_ptr(): pool(w) for w in cache._tree_ws.values()}.values())
+    assert used == sorted([s.cuda_stream] for s in (named, current, default))
+    for o, lse in outs[:3]:
+        check_tree(o[0], lse[0], q[0], k[0], v[0], states[0], par[0], 64, "on three streams")
+        assert torch.equal(o, outs[0][0])
+    assert cache.sync_status() == 0
+
+
+def test_own_workspace_and_a_capture_on_a_named_stream(cuda_lib):
+    """Whether a call is part of a capture goes by the stream that it names."""
+    rswa = cuda_lib
+    cache, states = make_cache(rswa, [1500], [40], 64, 2, 2, 128, BF, 415)
+    q, k, v = (normal((1, 20, 2, 128), 416 + i) for i in range(3))
+    par = [random_tree(20, 419)]
+    dev = torch.tensor(par, dtype=torch.int32).cuda()
+    o, lse = torch.empty_like(q), torch.empty(1, 20, 2, device="cuda")
+    side, away = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        other = torch.cuda.current_stream()
+        side.wait_stream(other)
+        with torch.cuda.stream(away):
+            with pytest.raises(ValueError):      # side is part of the capture, the current one not
+                cache.decode_tree(q, k, v, dev, o, lse, stream=side)
+        other.wait_stream(side)
+    assert not cache._tree_ws
+    cache.decode_tree(q, k, v, dev, o, lse)
+    o.zero_(), lse.zero_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.decode_tree(q, k, v, dev, o, lse)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert len({w.data_ptr() for w in cache._tree_ws.values()}) == 1
+    check_tree(o[0], lse[0], q[0], k[0], v[0], states[0], par[0], 64, "replayed")
+    assert cache.sync_status() == 0
+
+
 def test_decode_tree_is_deterministic(cuda_lib):
     rswa = cuda_lib
     _, _, (q, k, v, par, o, lse) = run_tree(rswa, [1500], [90], 64, 4, 2, 128, 30, BF, 200)
