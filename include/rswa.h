@@ -300,7 +300,9 @@ typedef struct rswa_rope {
  *   positions    device array of `rows` positions (any int64 value).
  *   q_out, k_out [rows][heads][d] and [rows][kv_heads][d], contiguous.  q_out
  *                may be q and k_out may be k where the stride is the row's own
- *                length; they must not overlap the inputs in another way.
+ *                length, or there is one row.  A result that shares memory
+ *                with an input in another way, or with the other result, is
+ *                RSWA_EINVAL.
  * 0 <= rows < 2^31, heads and kv_heads 1 .. 4096.  Needs no cache; runs on the
  * current device, to which the stream and all
  * pointers belong.  All pointers 16-byte aligned (positions and inv_freq
@@ -336,7 +338,8 @@ RSWA_API int rswa_qk_norm_rope_cached(rswa_cache* cache, const rswa_rope* rope,
  * t_b mod n takes the normed and rotated k and the v as it is, and t_b
  * advances by one.  rswa_decode_step(q_out) follows.  q, k, v: B rows with the
  * strides of rswa_qk_norm_rope; q_out: [B][H][d], may be q where q_stride is
- * H * d.  Errors: RSWA_EHANDLE, RSWA_EINVAL, RSWA_ECUDA.
+ * H * d or B is 1, and shares no other memory with q, k and v (RSWA_EINVAL).
+ * Errors: RSWA_EHANDLE, RSWA_EINVAL, RSWA_ECUDA.
  */
 RSWA_API int rswa_append_kv_rope(rswa_cache* cache, const rswa_rope* rope,
                                  const void* q, int64_t q_stride,

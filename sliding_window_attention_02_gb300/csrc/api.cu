@@ -102,6 +102,40 @@ bool valid_rows(const void* p, int64_t stride, int64_t len, int64_t rows, int dt
   return rows < 2 || (stride >= len && stride * elt % 16 == 0);
 }
 
+// Rows of heads as a norm and rotation reads them.
+struct InRows {
+  const void* p;
+  int64_t stride, len;                         // elements
+};
+
+// Whether the rows share a byte with the `bytes` bytes at out.
+bool rows_meet(const InRows& in, int64_t rows, int64_t elt, const void* out, int64_t bytes) {
+  const int64_t len = in.len * elt, step = rows < 2 ? len : in.stride * elt;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(in.p), o = reinterpret_cast<uintptr_t>(out);
+  // the first row that ends behind out's first byte
+  const int64_t r = o >= a + len ? (int64_t)((o - a - len) / step) + 1 : 0;
+  return r < rows && a + r * step < o + bytes;
+}
+
+// Whether dense result rows at `out` may be written while `in` is read: apart,
+// or row on row of `own` (in place).  Rows are done in any order.
+bool out_apart(const void* out, int64_t bytes, const InRows& in, int64_t rows, int64_t elt,
+               bool own) {
+  if (own && out == in.p && (rows < 2 || in.stride == in.len)) return true;
+  return !rows_meet(in, rows, elt, out, bytes);
+}
+
+// The results of rswa_qk_norm_rope(_cached): each apart from the other and from
+// the other's input, in place or apart from its own.
+bool valid_outputs(const InRows& q, const InRows& k, int64_t rows, int dtype, const void* q_out,
+                   const void* k_out) {
+  const int64_t elt = dtype == RSWA_F32 ? 4 : 2;
+  const int64_t qb = rows * q.len * elt, kb = rows * k.len * elt;
+  return out_apart(q_out, qb, q, rows, elt, true) && out_apart(q_out, qb, k, rows, elt, false) &&
+         out_apart(k_out, kb, q, rows, elt, false) && out_apart(k_out, kb, k, rows, elt, true) &&
+         !rows_meet(InRows{q_out, q.len, q.len}, rows, elt, k_out, kb);
+}
+
 struct Layout {
   size_t m_off, t_off, err_off, k_off, v_off, part_off, cnt_bh_off;
   size_t total;
@@ -492,7 +526,9 @@ int rswa_qk_norm_rope(const rswa_rope* rope, const void* q, int64_t q_stride,
   if (!positions || !aligned8(positions) || !q_out || !k_out || !aligned16(q_out) ||
       !aligned16(k_out) ||
       !valid_rows(q, q_stride, (int64_t)heads * head_dim, rows, dtype) ||
-      !valid_rows(k, k_stride, (int64_t)kv_heads * head_dim, rows, dtype))
+      !valid_rows(k, k_stride, (int64_t)kv_heads * head_dim, rows, dtype) ||
+      !valid_outputs({q, q_stride, (int64_t)heads * head_dim},
+                     {k, k_stride, (int64_t)kv_heads * head_dim}, rows, dtype, q_out, k_out))
     return RSWA_EINVAL;
   if (injected_failure()) return RSWA_ECUDA;
   RopeRows rr{};
@@ -523,7 +559,9 @@ int rswa_qk_norm_rope_cached(rswa_cache* cache, const rswa_rope* rope, const voi
   if (rows >= (int64_t(1) << 31)) return RSWA_EINVAL;
   if (!aligned4(offsets) || !q_out || !k_out || !aligned16(q_out) || !aligned16(k_out) ||
       !valid_rows(q, q_stride, (int64_t)cv.H * cv.d, rows, cv.dtype) ||
-      !valid_rows(k, k_stride, (int64_t)cv.Hkv * cv.d, rows, cv.dtype))
+      !valid_rows(k, k_stride, (int64_t)cv.Hkv * cv.d, rows, cv.dtype) ||
+      !valid_outputs({q, q_stride, (int64_t)cv.H * cv.d}, {k, k_stride, (int64_t)cv.Hkv * cv.d},
+                     rows, cv.dtype, q_out, k_out))
     return RSWA_EINVAL;
   if (injected_failure()) return RSWA_ECUDA;
   DeviceGuard g(cache->device);
@@ -553,6 +591,12 @@ int rswa_append_kv_rope(rswa_cache* cache, const rswa_rope* rope, const void* q,
       !valid_rows(q, q_stride, (int64_t)cv.H * cv.d, cv.B, cv.dtype) ||
       !valid_rows(k, k_stride, (int64_t)cv.Hkv * cv.d, cv.B, cv.dtype) ||
       !valid_rows(v, v_stride, (int64_t)cv.Hkv * cv.d, cv.B, cv.dtype))
+    return RSWA_EINVAL;
+  const int64_t elt = cv.dtype == RSWA_F32 ? 4 : 2, q_len = (int64_t)cv.H * cv.d,
+                k_len = (int64_t)cv.Hkv * cv.d, bytes = cv.B * q_len * elt;
+  if (!out_apart(q_out, bytes, {q, q_stride, q_len}, cv.B, elt, true) ||
+      !out_apart(q_out, bytes, {k, k_stride, k_len}, cv.B, elt, false) ||
+      !out_apart(q_out, bytes, {v, v_stride, k_len}, cv.B, elt, false))
     return RSWA_EINVAL;
   if (injected_failure()) return RSWA_ECUDA;
   DeviceGuard g(cache->device);

@@ -141,6 +141,34 @@ def test_norm_rope_refuses_arguments(rswa, kw, status):
     assert _norm_rope(rswa, _rope(rswa), **kw) == status
 
 
+# Rows of 1280 bf16 elements: 2560 bytes, 4 of them dense 10240 (0x2800).
+@pytest.mark.parametrize("kw,status", [
+    # in place, rows side by side or only one row
+    (dict(q_out=0x10000), 5), (dict(k_out=0x20000), 5),
+    (dict(rows=1, q_stride=3840, q_out=0x10000), 5), (dict(rows=1, q_stride=0, q_out=0x10000), 5),
+    # in place, rows part of longer ones: a row of the result is another's input
+    (dict(q_stride=3840, q_out=0x10000), 1), (dict(k_stride=1288, k_out=0x20000), 1),
+    (dict(rows=2, q_stride=3840, q_out=0x10000), 1),
+    # shifted
+    (dict(q_out=0x10010), 1), (dict(q_out=0x10000 - 16), 1), (dict(q_out=0x10000 + 0x2800 - 16), 1),
+    (dict(q_out=0x10000 + 0x2800), 5), (dict(q_out=0x10000 - 0x2800), 5),
+    (dict(k_out=0x20000 - 0x2800 + 16), 1), (dict(rows=1, q_out=0x10010), 1),
+    # over the other's input, and over each other
+    (dict(q_out=0x20000), 1), (dict(k_out=0x10000), 1), (dict(k_out=0x40000), 1),
+    (dict(k_out=0x40000 + 0x2800), 5), (dict(q_out=0x50000 - 16), 1),
+    # in and beside the gaps of packed rows (queries, keys, values: 7680 bytes apart)
+    (dict(k=0x10000 + 2560, q_stride=3840, k_stride=3840, rows=1, q_out=0x10000 + 5120), 5),
+    (dict(k=0x10000 + 2560, q_stride=3840, k_stride=3840, rows=2, q_out=0x10000 + 5120), 1),
+    (dict(q_stride=1 << 20, q_out=0x10000 + 2560), 5), (dict(q_stride=1 << 20, q_out=0x10000 + 2544), 1),
+    (dict(q_stride=1 << 20, k=0x2000000, q_out=0x10000 + 3 * (2 << 20) - 0x2800), 5),
+    (dict(q_stride=1 << 20, k=0x2000000, q_out=0x10000 + 3 * (2 << 20) - 0x2800 + 16), 1),
+    (dict(q_stride=1 << 20, k=0x2000000, q_out=0x10000 + 3 * (2 << 20) + 2560), 5),
+    (dict(q_stride=1 << 20, k=0x2000000, q_out=0x10000 + 3 * (2 << 20) + 2544), 1),
+])
+def test_norm_rope_refuses_results_over_inputs(rswa, kw, status):
+    assert _norm_rope(rswa, _rope(rswa), **kw) == status
+
+
 @pytest.mark.parametrize("kw", [
     dict(rotary_dim=-16), dict(rotary_dim=144), dict(rotary_dim=24), dict(rotary_dim=2),
     dict(inv_freq=None), dict(inv_freq=0x1004), dict(q_weight=0x1008), dict(k_weight=0x1002),

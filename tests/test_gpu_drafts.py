@@ -185,6 +185,52 @@ def test_norm_rope_refusals(cuda_lib):
             rswa.rswa_qk_norm_rope(*bad)
 
 
+def test_results_over_inputs_are_refused(cuda_lib):
+    """A result over rows that other CTAs have yet to read: refused by all three
+    calls, with nothing written; in place is taken where rows lie side by side."""
+    rswa = cuda_lib
+    B, H, Hkv, d, n = 4, 4, 2, 64, 8
+    cache, states = make_cache(rswa, [9] * B, [3] * B, n, H, Hkv, d, BF, 16)
+    rope = rswa.RswaRope(inv_freq(d), weight(d, 17, BF), weight(d, 18, BF))
+    flat = normal((B * (H + 2 * Hkv) * d,), 19)
+    before = flat.clone()
+    qkv = flat.view(B, H + 2 * Hkv, d)
+    q, k, v = qkv[:, :H], qkv[:, H:H + Hkv], qkv[:, H + Hkv:]
+    over_q, over_k = flat[:B * H * d].view(B, H, d), flat[H * d:][:B * Hkv * d].view(B, Hkv, d)
+    qo, ko = torch.empty_like(over_q), torch.empty_like(over_k)
+    pos = torch.arange(B).cuda()
+    both = torch.empty(B * (H + Hkv) * d - 8, dtype=BF, device="cuda")
+    for a, b in ((over_q, ko), (qo, over_k),
+                 (both[:B * H * d].view(B, H, d), both[-B * Hkv * d:].view(B, Hkv, d))):
+        for call in (lambda: rswa.rswa_qk_norm_rope(rope, q, k, pos, a, b),
+                     lambda: cache.qk_norm_rope(rope, q, k, a, b)):
+            with pytest.raises(rswa.RswaError) as e:
+                call()
+            assert e.value.status == 1
+    for a in (over_q, flat[-B * H * d:].view(B, H, d), flat[H * d:][:B * H * d].view(B, H, d)):
+        with pytest.raises(rswa.RswaError) as e:
+            cache.append_kv_rope(rope, q, k, v, a)
+        assert e.value.status == 1
+    torch.cuda.synchronize()
+    assert torch.equal(flat, before)
+    check_ring(cache, states, n)
+    # in place
+    q1, k1 = q.contiguous(), k.contiguous()
+    cache.qk_norm_rope(rope, q1, k1, q1, k1)
+    check_rope(q1, q, rope.q_weight, [12] * B, rope, "q")
+    check_rope(k1, k, rope.k_weight, [12] * B, rope, "k")
+    q1 = q.contiguous()
+    cache.append_kv_rope(rope, q1, k, v, q1)
+    check_rope(q1, q, rope.q_weight, [12] * B, rope, "q")
+    one = flat[:(H + 2 * Hkv) * d].view(1, H + 2 * Hkv, d)      # one row: beside its own key
+    want = torch.empty(1, H, d, dtype=BF, device="cuda"), torch.empty(1, Hkv, d, dtype=BF, device="cuda")
+    rswa.rswa_qk_norm_rope(rope, one[:, :H], one[:, H:H + Hkv], pos[:1], *want)
+    rswa.rswa_qk_norm_rope(rope, one[:, :H], one[:, H:H + Hkv], pos[:1],
+                           flat[:H * d].view(1, H, d), flat[H * d:(H + Hkv) * d].view(1, Hkv, d))
+    assert torch.equal(one[:, :H], want[0]) and torch.equal(one[:, H:H + Hkv], want[1])
+    assert cache.sync_status() == 0
+
+
 # ---------------------------------------------------------------------------
 # caches
 # ---------------------------------------------------------------------------
