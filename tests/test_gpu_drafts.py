@@ -657,6 +657,34 @@ def test_decode_tree_workspaces(cuda_lib):
         check_tree(o[0], lse[0], q[0], k[0], v[0], states[0], par[0], n, f"{N} nodes")
 
 
+@pytest.mark.parametrize("m,n,B,H,Hkv,d,most,fewer", [
+    (704, 128, 1, 10, 10, 128, 257, (256, 40)), (800, 128, 2, 10, 10, 128, 300, (256, 129)),
+    (1000, 128, 3, 64, 8, 64, 40, (32, 33)), (900, 100, 1, 32, 8, 128, 193, (192, 65)),
+    (250, 200, 1, 10, 10, 128, 800, (768, 257)), (100, 8, 1, 2, 2, 64, 1024, (300, 1))])
+def test_decode_tree_workspace_serves_fewer_nodes(cuda_lib, m, n, B, H, Hkv, d, most, fewer):
+    """Shapes where more nodes take the launch form that cuts no unit, and uses no
+    workspace, and fewer nodes, of fewer units, the one that does."""
+    rswa = cuda_lib
+    cache, states = make_cache(rswa, [m] * B, [30] * B, n, H, Hkv, d, BF, 420)
+    sizes = [rswa.rswa_decode_tree_workspace(cache.handle, x) for x in range(1, 1025)]
+    assert sizes == sorted(sizes) and sizes[0] >= 256
+    ws = cache.tree_workspace(most)
+    ws.fill_(0xff)
+    for N in (most,) + fewer:
+        q, k, v = normal((B, N, H, d), 421), normal((B, N, Hkv, d), 422), normal((B, N, Hkv, d), 423)
+        par = [random_tree(N, 424 + b) for b in range(B)]
+        dev = torch.tensor(par, dtype=torch.int32).cuda()
+        o, lse = torch.zeros_like(q), torch.zeros(B, N, H, device="cuda")
+        cache.decode_tree(q, k, v, dev, o, lse, workspace=ws)
+        assert cache.sync_status() == 0
+        c = min(N, 40)                           # nodes come before their children
+        check_tree(o[-1, :c], lse[-1, :c], q[-1, :c], k[-1, :c], v[-1, :c], states[-1], par[-1][:c],
+                   n, f"{N} nodes")
+        o2, l2 = torch.zeros_like(o), torch.zeros_like(lse)
+        cache.decode_tree(q, k, v, dev, o2, l2)
+        assert torch.equal(o, o2) and torch.equal(lse, l2)
+
+
 def test_decode_tree_back_to_back_and_after_other_calls(cuda_lib):
     """Calls queued without a wait, each on inputs of its own, between appends
     and decode steps (programmatic dependents that start early)."""
