@@ -616,8 +616,7 @@ int rswa_decode_tree(rswa_cache* cache, const void* q, const void* k, const void
                      const int32_t* parents, const int32_t* counts, int64_t nodes, void* o,
                      float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   if (!live(cache)) return RSWA_EHANDLE;
-  // grid limits of the CUDA-core kernel: B on grid.y, nodes * H on grid.x
-  if (nodes < 1 || nodes > kMaxTreeNodes || cache->cv.B > 65535) return RSWA_EINVAL;
+  if (nodes < 1 || nodes > kMaxTreeNodes) return RSWA_EINVAL;
   if (!q || !k || !v || !o || !parents || !workspace || !aligned16(q) || !aligned16(k) ||
       !aligned16(v) || !aligned16(o) || !aligned4(parents) || !aligned4(counts) ||
       !aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0)
@@ -647,8 +646,7 @@ int rswa_commit_tree(rswa_cache* cache, const void* k, const void* v, int64_t no
                      const int32_t* path, const int32_t* accepted, int64_t max_path,
                      void* stream) {
   if (!live(cache)) return RSWA_EHANDLE;
-  if (nodes < 1 || nodes > kMaxTreeNodes || max_path < 1 || max_path > kMaxTreeNodes ||
-      cache->cv.B > 65535)
+  if (nodes < 1 || nodes > kMaxTreeNodes || max_path < 1 || max_path > kMaxTreeNodes)
     return RSWA_EINVAL;
   if (!k || !v || !path || !accepted || !aligned16(k) || !aligned16(v) || !aligned4(path) ||
       !aligned4(accepted))

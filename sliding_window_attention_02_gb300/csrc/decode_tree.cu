@@ -36,7 +36,8 @@ decode_tree_kernel(CacheView cv, TreeArgs a) {
   __shared__ float s_m[NW], s_l[NW];
   __shared__ float s_acc[NW][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = blockIdx.y;
+  const int b = blockIdx.z * gridDim.y + blockIdx.y;
+  if (b >= cv.B) return;
   const int i = blockIdx.x / cv.H, h = blockIdx.x % cv.H;
   const int kvh = h / (cv.H / cv.Hkv);
   const size_t bkv = (size_t)b * cv.Hkv + kvh;
@@ -174,9 +175,10 @@ commit_tree_kernel(CacheView cv, const T* k, const T* v, int nodes, const int32_
 template <typename T, int D>
 cudaError_t launch_tree_t(const CacheView& cv, const TreeArgs& a, bool prefetch,
                           cudaStream_t s) {
+  const unsigned y = (unsigned)std::min(cv.B, 65535);          // the grid's limit
   return launch_dependent(prefetch ? decode_tree_kernel<T, D, true>
                                    : decode_tree_kernel<T, D, false>,
-                          dim3((unsigned)a.nodes * cv.H, (unsigned)cv.B),
+                          dim3((unsigned)a.nodes * cv.H, y, (unsigned)(cv.B + y - 1) / y),
                           dim3(kTreeWarps * 32), 0, s, cv, a);
 }
 

@@ -1432,7 +1432,9 @@ cudaError_t launch_d(const CacheView& cv, const TreeArgs& a, const SlabMaps& map
 }  // namespace
 
 bool decode_tree_tc_supported(const CacheView& cv, int nodes) {
-  if (cv.dtype != RSWA_BF16 || cv.H / cv.Hkv > BM) return false;
+  // The planner steps over sequences without live nodes one by one (65533 of them
+  // in 10.8 ms): so many at most keep that far below the bound of its readers' waits.
+  if (cv.dtype != RSWA_BF16 || cv.H / cv.Hkv > BM || cv.B > 65535) return false;
   return most_cost(cv, nodes, shape_of(cv, nodes)) < (int64_t(1) << 31) &&
          (int64_t)cv.B * nodes < (int64_t(1) << 30) &&
          (int64_t)cv.B * cv.Hkv * cv.slab_rows + cv.n < (int64_t(1) << 31);

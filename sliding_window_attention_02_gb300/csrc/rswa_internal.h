@@ -175,8 +175,8 @@ struct TreeArgs {
 };
 constexpr int kMaxTreeNodes = 1024;
 size_t decode_tree_workspace(const CacheView& cv, int nodes);
-// bf16, at most 128 query heads per KV head, and work enough: on the tensor
-// cores (decode_tree_tc.cu); the rest on the CUDA cores.
+// bf16, at most 128 query heads per KV head and 65535 sequences, and work
+// enough: on the tensor cores (decode_tree_tc.cu); the rest on the CUDA cores.
 bool decode_tree_use_tc(const CacheView& cv, int nodes);
 bool decode_tree_tc_supported(const CacheView& cv, int nodes);
 size_t decode_tree_tc_workspace(const CacheView& cv, int nodes);

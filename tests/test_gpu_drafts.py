@@ -1242,6 +1242,52 @@ def test_own_workspace_and_a_capture_on_a_named_stream(cuda_lib):
     assert cache.sync_status() == 0
 
 
+@pytest.mark.parametrize("dtype,N", [(BF, 2), (BF, 33), (F32, 2)])
+def test_more_sequences_than_a_grid_dimension(cuda_lib, dtype, N):
+    """66000 sequences: trees, the accepted nodes and the rotated append of all
+    of them."""
+    rswa = cuda_lib
+    B, m, n, d = 66000, 2, 2, 64
+    code = rswa.RSWA_BF16 if dtype is BF else rswa.RSWA_F32
+    K, V = normal((B * (m + 1), 1, d), 430, dtype), normal((B * (m + 1), 1, d), 431, dtype)
+    cache = rswa.RswaCache(m, n, 1, d, B, code)
+    cache.prefill(None, K, V, None, [m] * B, 1)
+    q, k, v = (normal((B, N, 1, d), 432 + i, dtype) for i in range(3))
+    par = random_tree(N, 435)
+    dev = torch.tensor([par], dtype=torch.int32).expand(B, N).contiguous().cuda()
+    counts = (torch.arange(B, dtype=torch.int32) % (N + 1)).cuda()
+    counts[65534:65538] = N
+    o, lse = torch.full_like(q, 7.0), torch.full((B, N, 1), 7.0, device="cuda")
+    cache.decode_tree(q, k, v, dev, o, lse, counts=counts)
+    assert cache.sync_status() == 0
+    at = [0, N, 65534, 65535, 65536, 65537, B - 1]
+    for b in at:
+        sl, c = slice(b * (m + 1), (b + 1) * (m + 1)), int(counts[b])
+        state = oracle.prefill_cache(f64(K[sl]), f64(V[sl]), m, n, 1)
+        check_tree(o[b, :c], lse[b, :c], q[b, :c], k[b, :c], v[b, :c], state, par[:c], n, f"{b}")
+    live = torch.arange(N, device="cuda") < counts[:, None]
+    assert torch.equal((o == 7).all(-1)[..., 0], ~live) and torch.equal(lse[..., 0] == 7, ~live)
+    path = torch.zeros(B, 1, dtype=torch.int32, device="cuda")
+    acc = (counts > 0).int()
+    cache.commit_tree(k, v, path, acc)
+    rope = rswa.RswaRope(inv_freq(d), None, weight(d, 436, dtype))
+    qkv = normal((B, 3, d), 437, dtype)
+    qo = torch.empty(B, 1, d, dtype=dtype, device="cuda")
+    cache.append_kv_rope(rope, qkv[:, :1], qkv[:, 1:2], qkv[:, 2:], qo)
+    assert cache.sync_status() == 0
+    Ks, Vs = cache.slabs()
+    for b in at:
+        a = int(acc[b])
+        slot = m + (1 + a) % n                   # of the appended token
+        assert cache.get_t(b) == 2 + a
+        check_rope(qo[b:b + 1], qkv[b:b + 1, :1], None, [m + 1 + a], rope, f"q {b}")
+        check_rope(Ks[b:b + 1, :, slot], qkv[b:b + 1, 1:2], rope.k_weight, [m + 1 + a], rope, f"k {b}")
+        same(Vs[b, :, slot], f64(qkv[b, 2:]))
+        if a:
+            same(Ks[b, :, m + 1], f64(k[b, 0]))
+            same(Vs[b, :, m + 1], f64(v[b, 0]))
+
+
 def test_decode_tree_is_deterministic(cuda_lib):
     rswa = cuda_lib
     _, _, (q, k, v, par, o, lse) = run_tree(rswa, [1500], [90], 64, 4, 2, 128, 30, BF, 200)
