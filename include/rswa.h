@@ -360,6 +360,8 @@ RSWA_API int rswa_decode_tree_workspace(rswa_cache* cache, int64_t nodes,
  * Attention of a tree of drafted tokens per sequence over the cache, to
  * verify several drafts in one call; the cache is not changed.
  *   q, o       [B][nodes][H][d]; k, v [B][nodes][H_kv][d]; 1 <= nodes <= 1024.
+ *              o may be q; o, lse and the workspace share no other memory with
+ *              each other or with an input (RSWA_EINVAL).
  *   parents    device int32 [B][nodes]: the node before, -1 <= parents[b][i]
  *              < i; -1 for a node that follows the last output directly.
  *   counts     device int32 [B], the live nodes of each sequence, 0 <=

@@ -102,6 +102,16 @@ bool valid_rows(const void* p, int64_t stride, int64_t len, int64_t rows, int dt
   return rows < 2 || (stride >= len && stride * elt % 16 == 0);
 }
 
+// Bytes that a call reads or writes.
+struct Span {
+  const void* p;
+  int64_t bytes;
+  bool meets(const Span& x) const {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(x.p);
+    return a < b + x.bytes && b < a + bytes;
+  }
+};
+
 // Rows of heads as a norm and rotation reads them.
 struct InRows {
   const void* p;
@@ -622,6 +632,22 @@ int rswa_decode_tree(rswa_cache* cache, const void* q, const void* k, const void
       !aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0)
     return RSWA_EINVAL;
   if (workspace_bytes < decode_tree_workspace(cache->cv, (int)nodes)) return RSWA_ECAPACITY;
+  {
+    // What is written shares no byte with anything else, but o may be q: a row's
+    // query is read before its result is written.
+    const CacheView& cv = cache->cv;
+    const int64_t rows = nodes * cv.B, elt = cv.dtype == RSWA_F32 ? 4 : 2;
+    const int64_t qo = rows * cv.H * cv.d * elt, kv = rows * cv.Hkv * cv.d * elt;
+    const Span out[3] = {{o, qo}, {lse, lse ? rows * cv.H * 4 : 0},
+                         {workspace, (int64_t)decode_tree_workspace(cv, (int)nodes)}};
+    const Span in[5] = {{q, qo}, {k, kv}, {v, kv}, {parents, rows * 4}, {counts, counts ? cv.B * 4 : 0}};
+    for (int i = 0; i < 3; ++i) {
+      for (int j = 0; j < 5; ++j)
+        if (out[i].meets(in[j]) && !(i == 0 && j == 0 && o == q)) return RSWA_EINVAL;
+      for (int j = 0; j < i; ++j)
+        if (out[i].meets(out[j])) return RSWA_EINVAL;
+    }
+  }
   if (injected_failure()) return RSWA_ECUDA;
   DeviceGuard g(cache->device);
   if (!g.ok) return RSWA_ECUDA;

@@ -595,6 +595,67 @@ def test_decode_tree_refusals(cuda_lib):
     assert cache.sync_status() == 0
 
 
+def test_decode_tree_refuses_results_over_inputs(cuda_lib):
+    """o, lse or the workspace over what other CTAs still read: refused, with
+    nothing written."""
+    rswa = cuda_lib
+    B, H, Hkv, d, N = 2, 4, 2, 64, 6
+    cache, _ = make_cache(rswa, [9] * B, [2] * B, 8, H, Hkv, d, BF, 440)
+    need = rswa.rswa_decode_tree_workspace(cache.handle, N)
+    mem = normal((1 << 20,), 441)
+    base, before = mem.data_ptr(), mem.clone()
+    assert base % 256 == 0 and need <= 4096
+    qb, kb = B * N * H * d * 2, B * N * Hkv * d * 2
+    at = dict(q=0, k=0x10000, v=0x20000, par=0x30000, cnt=0x40000, o=0x50000, lse=0x60000, ws=0x70000)
+    for name, x in (("par", [-1] * (B * N)), ("cnt", [N, N])):
+        x = torch.tensor(x, dtype=torch.int32).cuda().view(BF)
+        mem[at[name] // 2:][:x.numel()] = x
+    before = mem.clone()
+
+    def call(**kw):
+        p = {x: base + y for x, y in dict(at, **kw).items()}
+        return rswa.load().rswa_decode_tree(cache.handle, p["q"], p["k"], p["v"], p["par"], p["cnt"], N,
+                                            p["o"], p["lse"], p["ws"], need, None)
+
+    for bad in (dict(o=16), dict(o=qb - 16), dict(q=16, o=0), dict(o=at["k"]), dict(o=at["k"] - qb + 16),
+                dict(o=at["v"] + kb - 16), dict(o=at["par"]), dict(o=at["cnt"]), dict(lse=0),
+                dict(lse=at["k"] + kb - 4), dict(lse=at["o"] + qb - 4), dict(lse=at["par"]),
+                dict(ws=0), dict(ws=at["v"]), dict(ws=at["par"]), dict(ws=at["cnt"]), dict(ws=at["o"]),
+                dict(ws=at["lse"]), dict(o=at["ws"]), dict(lse=at["ws"] + need - 4)):
+        assert call(**bad) == 1, bad
+    torch.cuda.synchronize()
+    assert torch.equal(mem.view(torch.int16), before.view(torch.int16))
+    assert call(k=at["q"], v=at["q"]) == 0                 # inputs may be one tensor
+    assert call(o=at["k"] + kb, lse=at["o"] + qb) == 0     # side by side
+    assert cache.sync_status() == 0
+
+
+@pytest.mark.parametrize("m,H,Hkv,d,N,dtype", [(200, 4, 2, 64, 9, F32), (200, 4, 4, 128, 5, BF),
+                                               (3000, 2, 2, 128, 20, BF), (1500, 32, 8, 128, 60, BF),
+                                               (400, 4, 2, 64, 300, BF)])
+def test_decode_tree_in_place(cuda_lib, m, H, Hkv, d, N, dtype):
+    """o may be q, with NaN in dead nodes: the same bits (CUDA cores; one query
+    tile and pairs, cut and whole)."""
+    rswa = cuda_lib
+    B, n = 40, 48
+    ms, ts = [max(0, m - 31 * b) for b in range(B)], [5 * b for b in range(B)]
+    cache, _ = make_cache(rswa, ms, ts, n, H, Hkv, d, dtype, 445)
+    for B_live in (B, 1):
+        counts = torch.tensor([(N - b % 3 if b < B_live else 0) for b in range(B)], dtype=torch.int32).cuda()
+        q, k, v = normal((B, N, H, d), 446, dtype), normal((B, N, Hkv, d), 447, dtype), normal((B, N, Hkv, d), 448, dtype)
+        dead = torch.arange(N, device="cuda") >= counts[:, None]
+        q[dead] = float("nan")
+        par = torch.tensor([random_tree(N, 449 + b) for b in range(B)], dtype=torch.int32).cuda()
+        o, lse, l2 = torch.full_like(q, float("nan")), torch.zeros(B, N, H, device="cuda"), torch.zeros(B, N, H, device="cuda")
+        cache.decode_tree(q, k, v, par, o, lse, counts=counts)
+        for _ in range(3):
+            x = q.clone()
+            cache.decode_tree(x, k, v, par, x, l2, counts=counts)
+            assert torch.equal(x[~dead], o[~dead]) and torch.equal(l2, lse)
+            assert torch.isnan(x[dead]).all()
+    assert cache.sync_status() == 0
+
+
 def test_decode_tree_ignores_what_is_no_key(cuda_lib):
     """NaN in prefix rows past m_b and in ring slots that hold no output yet (a
     caller's own writes into the slabs) does not reach any row."""
