@@ -941,6 +941,69 @@ def test_decode_tree_many_pairs_wait_runs_out_then_recovers(cuda_lib):
         assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
 
 
+def arrivals(cache, B, H):
+    """The cache's arrival counters, [B][H]: the last words before the keys."""
+    keys = cache.slabs()[0].data_ptr() - cache.buf.data_ptr()
+    return cache.buf[keys - -(-4 * B * H // 256) * 256:][:4 * B * H].view(torch.int32)
+
+
+@pytest.mark.parametrize("B,H,Hkv,N,d,m", [(60, 12, 3, 60, 128, 300), (160, 8, 1, 20, 64, 200)])
+def test_set_t_clears_the_counters_that_joins_meet_on(cuda_lib, B, H, Hkv, N, d, m):
+    """The counters are zero after a call whose CTAs join cut units; words that a
+    call which gave up may have left there are cleared by set_t, and the next
+    call has the same bits."""
+    rswa = cuda_lib
+    ms, ts = [m + 9 * b for b in range(B)], [3 * b % 110 for b in range(B)]
+    cache, states = make_cache(rswa, ms, ts, 100, H, Hkv, d, BF, 460, m + 9 * B)
+    q, k, v = normal((B, N, H, d), 461), normal((B, N, Hkv, d), 462), normal((B, N, Hkv, d), 463)
+    par = [random_tree(N, 464 + b) for b in range(B)]
+    dev = torch.tensor(par, dtype=torch.int32).cuda()
+    want = torch.zeros_like(q), torch.zeros(B, N, H, device="cuda")
+    cache.decode_tree(q, k, v, dev, *want)
+    assert cache.sync_status() == 0
+    cnt = arrivals(cache, B, H)
+    assert not cnt.any()
+    for left in (1, 2, 7):
+        cnt.fill_(left)
+        cache.set_t(ts)
+        assert not cnt.any()
+        got = torch.zeros_like(q), torch.zeros(B, N, H, device="cuda")
+        cache.decode_tree(q, k, v, dev, *got)
+        assert cache.sync_status() == 0 and not cnt.any()
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    for b in (0, B // 2, B - 1):
+        check_tree(want[0][b], want[1][b], q[b], k[b], v[b], states[b], par[b], 100, f"{b}")
+
+
+@pytest.mark.parametrize("live", [{7: 20}, {0: 20, 159: 17}, {3: 20, 80: 1, 81: 19}, {158: 33}, {}])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_tree_few_live_sequences_of_many(cuda_lib, live, d):
+    """A launch of pairs planned for 160 units of which a few are live: each is
+    cut into many parts, which the CTA that arrives last joins alone."""
+    rswa = cuda_lib
+    B, H, N, n = 160, 8, 33, 100
+    m, t = [6000 - 500 * (b % 3) if b in live else 0 for b in range(B)], [70 + b if b in live else 0 for b in range(B)]
+    cache, states = make_cache(rswa, m, t, n, H, 1, d, BF, 470, 6000)
+    counts = [live.get(b, 0) for b in range(B)]
+    q, k, v = normal((B, N, H, d), 471), normal((B, N, 1, d), 472), normal((B, N, 1, d), 473)
+    for b in range(B):
+        for x in (q, k, v):
+            x[b, counts[b]:] = float("nan")
+    par = [random_tree(N, 474 + b) for b in range(B)]
+    dev = torch.tensor(par, dtype=torch.int32).cuda()
+    cnt = torch.tensor(counts, dtype=torch.int32).cuda()
+    outs = [(torch.full_like(q, 7.0), torch.full((B, N, H), 7.0, device="cuda")) for _ in range(5)]
+    o, lse = outs[0]
+    for o2, l2 in outs:
+        cache.decode_tree(q, k, v, dev, o2, l2, counts=cnt)
+        assert cache.sync_status() == 0 and not arrivals(cache, B, H).any()
+        assert torch.equal(o, o2) and torch.equal(lse, l2)
+    for b, c in live.items():
+        check_tree(o[b, :c], lse[b, :c], q[b, :c], k[b, :c], v[b, :c], states[b], par[b][:c], n, f"{b}")
+    for b in range(B):
+        assert (o[b, counts[b]:] == 7).all() and (lse[b, counts[b]:] == 7).all()
+
+
 @pytest.mark.parametrize("B,H,Hkv,N,d", [(2, 10, 10, 40, 128), (2, 8, 2, 60, 64), (40, 16, 4, 60, 128)])
 def test_decode_tree_output_at_16_bytes(cuda_lib, B, H, Hkv, N, d):
     """o 16 and not 32 bytes aligned, lse 4: the same bits."""
