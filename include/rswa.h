@@ -25,7 +25,11 @@
  *     caller.  The library allocates no device memory: the cache lives in a
  *     caller-provided buffer of rswa_cache_footprint() bytes.
  *   - dtype is RSWA_F32 (float) or RSWA_BF16 (bfloat16) and applies to every
- *     Q/K/V/O tensor of a cache; arithmetic is float32 in both cases.
+ *     Q/K/V/O tensor of a cache.  Sums, products and softmax statistics are
+ *     float32 in both cases, with one exception: the tensor-core kernels of
+ *     bf16 caches (prefill; blocks of 64 tokens and more and grouped decode at
+ *     head_dim 128; trees but the smallest) round each softmax weight to bf16
+ *     (by 2^-8 of it at most) for its product with V, not for the sum.
  *   - Token-major tensors: a "[rows][H][d]" tensor is contiguous with d
  *     fastest.  Per-step tensors q, k, v, o are "[B][H][d]".
  *   - Work is enqueued on the caller's stream (a cudaStream_t passed as
@@ -375,7 +379,11 @@ RSWA_API int rswa_decode_tree_workspace(rswa_cache* cache, int64_t nodes,
  * stands for output t_b + depth(i): it attends to the prefix, to the cached
  * outputs j > t_b + depth(i) - n, and to itself and its ancestors a with
  * depth(i) - depth(a) < n - what rswa_decode_block would give for the chain
- * that ends in it.  Keys and values of live nodes and of the cache must be
+ * that ends in it.  Of a bf16 cache the softmax weights are float32 where the
+ * work is small (the cache's m + n at most 1200, and B * H * nodes * (m + n) at
+ * most 110000), for more than 128 query heads per KV head and for more than
+ * 65535 sequences, and otherwise rounded to bf16 for their product with the
+ * values.  Keys and values of live nodes and of the cache must be
  * finite.  Accepted nodes are stored with rswa_commit_tree.
  * A parent or a count outside its range sets the device flag (RSWA_EDEVICE of
  * rswa_sync_status); the parent is then taken as -1 and the count as the

@@ -949,7 +949,10 @@ decode_tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
               tmem_st32(o_addr + c, vb);
             }
           }
-          // Pass 2: P, over columns of S already read, and its sum.
+          // Pass 2: P, over columns of S already read, and its sum.  P is rounded to
+          // bf16 for the product with V, whose two operands are of one 16-bit type;
+          // l sums it unrounded.  64 sequences of 10 heads and 32 nodes: o is off
+          // by 0.0023 relative to 64 bits, 0.0017 of it o's own rounding.
           const float nref = (m_run == -INFINITY) ? 0.f : -m_run;
           const uint64_t sl2x2 = f2_pack(sl2, sl2), nref2 = f2_pack(nref, nref);
           uint64_t ps2 = 0;
