@@ -279,10 +279,14 @@ RSWA_API int rswa_decode_step_fused_static(rswa_cache* cache, const void* q,
  *     (a, b) -> (a cos - b sin, b cos + a sin),
  *   with (a, b) = (y[i], y[i + rotary_dim/2]), or (y[2i], y[2i+1]) when
  *   `interleaved` is not 0; the other elements stay.
- * The result is rounded once, to the tensors' dtype.  The angle is held as a
- * 64-bit fraction of a turn, so that it is as exact at position 10^6 as at 1
- * (its error is below position * 2^-52 turns).  Scaled and extended rotations
- * are a matter of inv_freq.
+ * The result is rounded once, to the tensors' dtype.  The angle is reduced to a
+ * fraction of a turn in 64-bit integers and its sine and cosine are taken of that
+ * fraction in float32: it is off by at most 2^-26 + 2^-32 turns (1e-7 radians) plus
+ * abs(position) * max(1, abs(inv_freq[i])) * 2^-63 turns: as exact at position
+ * 10^6 as at 1.  Scaled and interpolated frequencies are a matter of inv_freq; a
+ * factor on cosine and sine, as some extended rotations have it, is not: it may
+ * be multiplied into the weights of the rotated elements.  A head's sum of
+ * squares has to be in float32's range.
  */
 typedef struct rswa_rope {
   const void* q_weight;   /* [d], dtype of the heads; NULL: queries not normed */

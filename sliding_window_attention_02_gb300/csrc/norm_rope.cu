@@ -16,9 +16,10 @@
 // Angles: pos f_i / (2 pi) turns, of which only the fraction matters.  f_i /
 // (2 pi) is taken as a 64-bit fraction of a turn, by an integer product of f_i's
 // mantissa with 2^64 / (2 pi); its product with the position modulo 2^64 is the
-// phase, off by less than position * 2^-60 turns - a 32-bit float angle would be
-// off by 0.006 at position 10^5, and 64-bit floats are slow here.  The phase's
-// top 32 bits go to sincospi.
+// phase, off by at most |pos| max(1, |f_i|) 2^-63 turns (2^64 / (2 pi) is cut to an
+// integer, and so is the step) - a 32-bit float angle would be off by 0.006 at
+// position 10^5, and 64-bit floats are slow here.  The phase's top 32 bits (2^-32
+// turns) are rounded to a float of half turns (2^-26 turns) for sincospi.
 //
 // Angles and weights depend on the row and the pair, not on the head, so a CTA
 // first puts, for each row and for queries and keys,

@@ -135,6 +135,40 @@ def test_norm_rope_far_and_negative_positions(cuda_lib):
     same(qo[:0], f64(q[:0]))
 
 
+def test_rotation_angles_are_as_exact_as_stated(cuda_lib):
+    """Cosine and sine of angles at near and far positions and of small and huge
+    frequencies, against exact integer arithmetic (2^200 / (2 pi) as an integer).
+    The angle: 2^-26 + 2^-32 + |pos| max(1, |f|) 2^-63 turns.  Sine and cosine of
+    it: 4 half steps of 1; the rotation's products with 1 and 0 and the norm are
+    exact or left out."""
+    from fractions import Fraction
+    rswa = cuda_lib
+    two_pi = Fraction(628318530717958647692528676655900576839433879875021164194988918461563281257,
+                      10 ** 74)
+    freqs = [1.0, -1.0, 0.75, 2 ** -20 / 3, 1e-9, 1e-30, 5e-324, 0.0, 10000 ** -0.3, 3.0, -1e3, 1e6,
+             123456.789, 2.0 ** 52 + 1, 2.0 ** 100, -1e300, 2 * np.pi, np.pi / 2, 1e-3, 7.0]
+    freqs += [10000.0 ** (-i / 20) for i in range(32 - len(freqs))]
+    pos = [0, 1, -1, 2, 77, 1000, -77777, 999_983, 2 ** 31 + 5, -2 ** 40 - 3]
+    q = torch.zeros(len(pos), 1, 64, device="cuda")
+    q[..., :32] = 1.0                            # pairs (1, 0): cosine, sine
+    rope = rswa.RswaRope(torch.tensor(freqs, dtype=torch.float64).cuda())
+    qo, ko = torch.empty_like(q), torch.empty_like(q)
+    rswa.rswa_qk_norm_rope(rope, q, q, torch.tensor(pos).cuda(), qo, ko)
+    got = f64(qo)[:, 0]
+    assert np.array_equal(got, f64(ko)[:, 0])
+    for r, p in enumerate(pos):
+        for i, f in enumerate(freqs):
+            bound = 2.0 ** -26 + 2.0 ** -32 + abs(p) * max(1.0, abs(f)) * 2.0 ** -63
+            if bound > 2.0 ** -10:
+                continue                         # the statement says little there
+            turn = Fraction(f) * p / two_pi
+            turn -= int(turn)
+            tol = 2 * np.pi * bound + 4 * 2.0 ** -24
+            assert abs(got[r, i] - np.cos(2 * np.pi * float(turn))) <= tol, (p, f)
+            assert abs(got[r, 32 + i] - np.sin(2 * np.pi * float(turn))) <= tol, (p, f)
+    assert np.abs(got).max() <= 1 + 4 * 2.0 ** -24
+
+
 def test_norm_rope_in_place_and_only_one_norm(cuda_lib):
     rswa = cuda_lib
     q, k = normal((50, 4, 64), 8), normal((50, 2, 64), 9)
