@@ -358,8 +358,9 @@ RSWA_API int rswa_append_kv_rope(rswa_cache* cache, const rswa_rope* rope,
 /*
  * Device bytes of workspace that rswa_decode_tree needs for trees of up to
  * `nodes` nodes on this cache (at least 256).  The workspace need not be
- * initialised and keeps nothing between calls; calls that may overlap on the
- * GPU need one each.  Host-only.  Errors: RSWA_EHANDLE, RSWA_EINVAL.
+ * initialised and keeps nothing between calls.  Calls on one cache, which are
+ * ordered, may share it; calls on several caches that may overlap on the GPU need
+ * one each.  Host-only.  Errors: RSWA_EHANDLE, RSWA_EINVAL.
  */
 RSWA_API int rswa_decode_tree_workspace(rswa_cache* cache, int64_t nodes,
                                         size_t* out_bytes);

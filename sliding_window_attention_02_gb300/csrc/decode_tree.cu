@@ -11,12 +11,21 @@
 #include <algorithm>
 
 #include "attend.cuh"
-#include "decode_tree.cuh"
+#include "rswa_device.cuh"
 
 namespace rswa {
 namespace {
 
 constexpr int kTreeWarps = 8;
+
+// Live nodes of sequence b; a count outside 0..nodes is flagged and clamped.
+__device__ __forceinline__ int live_nodes(const int32_t* counts, int b, int nodes,
+                                          int32_t* err) {
+  if (!counts) return nodes;
+  const int c = counts[b];
+  if (c < 0 || c > nodes) flag_error(err, kErrBadTree);
+  return min(max(c, 0), nodes);
+}
 
 // One CTA of 8 warps per (node, query head, sequence): the warps split every
 // key segment between them and merge in shared memory.  A node past the

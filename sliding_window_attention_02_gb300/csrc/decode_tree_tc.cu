@@ -61,7 +61,6 @@
 
 #include <algorithm>
 
-#include "decode_tree.cuh"
 #include "rswa_device.cuh"
 #include "tc_ptx.cuh"
 
@@ -202,7 +201,7 @@ struct Seq {
   int p16, r16, tl, units, extra;
   __device__ __forceinline__ void load(const CacheView& cv, const TreeArgs& a, const Shape& sh,
                                        int b) {
-    const int c = a.counts ? a.counts[b] : a.nodes;
+    const int c = a.counts ? a.counts[b] : a.nodes;        // one round trip with m_b and t_b
     m_b = cv.m_dev[b];
     t_b = cv.t_dev[(size_t)b * cv.H];
     cnt = min(max(c, 0), a.nodes);
