@@ -1446,6 +1446,78 @@ def test_more_sequences_than_a_grid_dimension(cuda_lib, dtype, N):
             same(Vs[b, :, m + 1], f64(v[b, 0]))
 
 
+@pytest.mark.parametrize("dtype,cap", [(BF, 20_000_000), (F32, 10_000_000)])
+def test_offsets_beyond_32_bits(cuda_lib, dtype, cap):
+    """A cache whose second sequence begins more than 2^32 bytes, and in bf16
+    2^31 elements, behind the first: append, tree (tensor and CUDA cores) and
+    commit of the same node twice."""
+    rswa = cuda_lib
+    m, t, n, H, d, N = [300, 170], [20, 65], 64, 2, 128, 21
+    cache, states = make_cache(rswa, m, t, n, H, 1, d, dtype, 480, cap)
+    Ks, Vs = cache.slabs()
+    assert Ks[1].data_ptr() - Ks[0].data_ptr() > 2 ** 32
+    rope = rswa.RswaRope(inv_freq(d), weight(d, 481, dtype), weight(d, 482, dtype))
+    qkv = normal((2, H + 2, d), 483, dtype)
+    qo = torch.empty(2, H, d, dtype=dtype, device="cuda")
+    cache.append_kv_rope(rope, qkv[:, :H], qkv[:, H:H + 1], qkv[:, H + 1:], qo)
+    pos = [a + b for a, b in zip(m, t)]
+    check_rope(qo, qkv[:, :H], rope.q_weight, pos, rope, "q")
+    for b in range(2):
+        stored = Ks[b, :, cap + t[b] % n]
+        check_rope(stored[None], qkv[b:b + 1, H:H + 1], rope.k_weight, pos[b:b + 1], rope, "k")
+        states[b] = oracle.append_kv(states[b], f64(stored), f64(qkv[b, H + 1:]), n)
+    q, k, v = normal((2, N, H, d), 484, dtype), normal((2, N, 1, d), 485, dtype), normal((2, N, 1, d), 486, dtype)
+    par = [random_tree(N, 487), random_tree(N, 488)]
+    path = torch.tensor([[0, 5, 5], [20, 20, 1]], dtype=torch.int32).cuda()
+    acc = torch.tensor([3, 2], dtype=torch.int32).cuda()
+    o, lse = torch.empty_like(q), torch.empty(2, N, H, device="cuda")
+    cache.decode_tree(q, k, v, torch.tensor(par, dtype=torch.int32).cuda(), o, lse)
+    cache.commit_tree(k, v, path, acc)
+    assert cache.sync_status() == 0
+    for b in range(2):
+        check_tree(o[b], lse[b], q[b], k[b], v[b], states[b], par[b], n, f"{b}")
+        states[b] = drafts.commit_tree(states[b], f64(k[b]), f64(v[b]), path[b, :int(acc[b])].tolist(), n)
+        assert cache.get_t(b) == states[b]["t"]
+        for slab, name in ((Ks, "Kr"), (Vs, "Vr")):
+            got = f64(slab[b, :, cap:]).transpose(1, 0, 2)
+            filled = sorted(oracle.ring_outputs(states[b]["t"], n))
+            np.testing.assert_array_equal(got[filled], states[b][name][filled])
+
+
+def test_two_graphs_share_a_workspace(cuda_lib):
+    """Two captured calls of one cache, of different trees, replayed in turn on
+    the workspace that the cache keeps."""
+    rswa = cuda_lib
+    m, n, H, Hkv, d = [1500, 900], 64, 8, 2, 128
+    cache, states = make_cache(rswa, m, [40, 3], n, H, Hkv, d, BF, 490)
+    calls = []
+    for N in (60, 17):
+        q, k, v = normal((2, N, H, d), 491 + N), normal((2, N, Hkv, d), 492 + N), normal((2, N, Hkv, d), 493 + N)
+        par = [random_tree(N, 494), random_tree(N, 495)]
+        calls.append((q, k, v, torch.tensor(par, dtype=torch.int32).cuda(), torch.empty_like(q),
+                      torch.empty(2, N, H, device="cuda"), par))
+    for c in calls:
+        cache.decode_tree(*c[:6])
+    graphs = []
+    for c in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            cache.decode_tree(*c[:6])
+            cache.decode_tree(*c[:6])
+    want = [(c[4].clone(), c[5].clone()) for c in calls]
+    for _ in range(4):
+        for c in calls:
+            c[4].zero_(), c[5].zero_()
+        for g in graphs:
+            g.replay()
+        for c, (o, lse) in zip(calls, want):
+            assert torch.equal(c[4], o) and torch.equal(c[5], lse)
+    for q, k, v, _, o, lse, par in calls:
+        for b in range(2):
+            check_tree(o[b], lse[b], q[b], k[b], v[b], states[b], par[b], n, f"{b}")
+    assert cache.sync_status() == 0
+
+
 def test_decode_tree_is_deterministic(cuda_lib):
     rswa = cuda_lib
     _, _, (q, k, v, par, o, lse) = run_tree(rswa, [1500], [90], 64, 4, 2, 128, 30, BF, 200)
