@@ -29,12 +29,16 @@ __device__ __forceinline__ int live_nodes(const int32_t* counts, int b, int node
 
 // One CTA of 8 warps per (node, query head, sequence): the warps split every
 // key segment between them and merge in shared memory.  A node past the
-// sequence's count is left alone.  Bound by latency for the few nodes it is
-// used for: the walk to the root runs in one lane while the warps are at the
-// prefix, whose first rows are requested before the dependency wait where the
-// preceding kernel of the stream writes no prefix row (PREFETCH, the handle's
-// flag).  16 nodes of 10 heads over 288 + 128 keys, bf16: 7.8 us, 0.34 by
-// the bytes.
+// sequence's count is left alone.  Bound by latency for a few nodes, a chain of
+// reads, merge and store: the walk to the root runs in one lane while the warps
+// are at the prefix, whose first rows are requested before the dependency wait
+// where the preceding kernel of the stream writes no prefix row (PREFETCH, the
+// handle's flag).  Beyond some 50000 pairs of a query row and a key bound by
+// those: every CTA reads all keys of its row through L2 for itself, with no reuse
+// between nodes or heads, bf16 71 ps a pair at d 128 and 57 at d 64, float32 78 and
+// 47, 4.5 to 7 TFLOP/s.  In deep trees by the walk, a load a level.
+// 16 nodes of 10 heads over 288 + 128 keys, bf16: 7.8 us (34 MB through L2),
+// 0.34 by the 2.3 MB of data.
 template <typename T, int D, bool PREFETCH>
 __global__ void __launch_bounds__(kTreeWarps * 32)
 decode_tree_kernel(CacheView cv, TreeArgs a) {
@@ -193,15 +197,26 @@ cudaError_t launch_tree_t(const CacheView& cv, const TreeArgs& a, bool prefetch,
 
 }  // namespace
 
-// Small work is done sooner on the CUDA cores, whose kernel takes 3.4 us and the
-// larger of 7.1 ns a key (while its CTAs fit the SMs twice) and 65 ps for each
-// pair of a query row and a key; the tensor-core kernel takes 7 us and 1 for a
-// tile of 128 keys while its units are few, 13.5 and more where it cuts them, and
-// 3 more for every further unit of an SM.  bf16, d 128, 10 heads, us on the CUDA /
-// tensor cores: 16 nodes 5.8 / 8.4 at 192 keys, 7.8 / 10.1 at 416, 17.0 / 14.6 at
-// 1184; 32 nodes 9.4 / 9.0 at 192, 12.8 / 10.3 at 416; 1 node 11.2 / 14 at 1184,
-// 34 / 16 at 4256; 51 sequences of at most 120 keys: 1 node 7.7 / 24.6.
-// The keys are the cache's capacity: the host does not know the live ones.
+// Small work is done sooner on the CUDA cores, whose kernel takes the larger of
+// 2.1 us and 7 ns a key (d 64: 2.4 and 3.4 ns) and, once its CTAs fill the SMs, of
+// 2.7 us and 71 ps for each pair of a query row and a key (d 64: 2.2 and 57 ps);
+// the tensor-core kernel takes 7 us and 1 for a tile of 128 keys while its units
+// are few, 13.5 and more where it cuts them, and 3 more for every further unit of
+// an SM.  One sequence, bf16, us on the CUDA / tensor cores, d 128 and then d 64,
+// at 192 keys (m 64, n 128), 416 and 1184:
+//   heads   nodes       192                      416                     1184
+//   10        1                         5.0/10.2, 3.9/9.2     10.4/14.7, 6.5/13.0
+//   10       16   4.8/7.8, 3.7/7.6      7.0/9.9, 4.7/9.0      16.0/14.2, 8.9/12.6
+//   10       32   8.0/8.0, 6.7/8.0     11.2/10.1, 8.3/9.1
+//   32 / 8    4   3.7/7.9, 3.3/7.3      5.3/10.2, 4.2/9.2     10.7/14.6, 6.8/12.7
+//   32 / 8   16   8.8/7.8, 6.9/7.6     13.9/10.0, 9.1/9.0
+//   16 / 2   16   4.9/8.4, 3.9/8.0      7.2/10.6, 4.7/9.5
+//   16 / 2   32   9.2/12.6, 7.4/11.4   14.0/15.6, 9.4/13.9
+//   40        4   4.6/8.2, 3.7/7.7      7.1/10.6, 4.7/9.6     15.9/17.1, 8.9/14.9
+// and 10 heads, d 128: 1 node 34/16 at 4256; 51 sequences of at most 120 keys, 1
+// node 7.7/24.6.  At d 64, and with few KV heads, the CUDA cores stay ahead to
+// twice the pairs and more; the bound is that of 10 heads at d 128.  The keys are
+// the cache's capacity: the host does not know the live ones.
 constexpr int64_t kCudaCorePairs = 110000, kCudaCoreKeys = 1200;
 
 static bool small_work(const CacheView& cv, int nodes) {
