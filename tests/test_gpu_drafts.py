@@ -590,6 +590,31 @@ def test_decode_tree_equals_block_on_a_chain(cuda_lib):
     assert cache.get_t(0) == t[0] + N
 
 
+@pytest.mark.parametrize("H,Hkv,d,dtype", [(2, 2, 128, BF), (8, 2, 64, BF), (96, 1, 128, BF), (2, 1, 64, F32)])
+def test_decode_tree_deepest_chain(cuda_lib, H, Hkv, d, dtype):
+    """1024 nodes in one chain inside the window (every node walks to the root):
+    a block of 1024 outputs.  Both are off by the bounds above, with sum |q k| at
+    most the product of the lengths and |o| at most the largest value."""
+    rswa = cuda_lib
+    m, t, n, N = [150], [900], 2000, 1024
+    cache, _ = make_cache(rswa, m, t, n, H, Hkv, d, dtype, 500)
+    q, k, v = normal((1, N, H, d), 501, dtype), normal((1, N, Hkv, d), 502, dtype), normal((1, N, Hkv, d), 503, dtype)
+    par = torch.arange(-1, N - 1, dtype=torch.int32)[None].cuda()
+    o, ob = torch.empty_like(q), torch.empty_like(q)
+    lse, lb = torch.empty(1, N, H, device="cuda"), torch.empty(1, N, H, device="cuda")
+    cache.decode_tree(q, k, v, par, o, lse)
+    cache.decode_block(q, k, v, ob, lb)
+    assert cache.sync_status() == 0
+    logit = (q.float().norm(dim=-1).max() * k.float().norm(dim=-1).max()).item() / d ** 0.5
+    half = 2.0 ** -24 * (1 if dtype is F32 else 2)
+    rel = (d + 8) * half * logit + 2 * (m[0] + n) * half + 2.0 ** -21
+    assert (lse - lb).abs().max().item() <= 2 * rel + 4 * half * (1 + lb.abs().max().item())
+    big = v.float().abs().max().item()
+    tol = 2 * (2 * rel + half + (2 * HALF[dtype] if dtype is BF else 0)) * big
+    assert (o.float() - ob.float()).abs().max().item() <= tol
+    assert cache.get_t(0) == t[0] + N
+
+
 def test_decode_tree_refusals(cuda_lib):
     rswa = cuda_lib
     H, Hkv, d, N = 4, 2, 128, 6
