@@ -529,6 +529,7 @@ class RswaCache:
         # decode_tree's own workspaces, by node count and stream; all stay, as
         # captured graphs hold them
         self._tree_ws = {}
+        self._tree_at = {}              # and their pointers and sizes
 
     def close(self):
         if self.handle is not None:
@@ -621,27 +622,25 @@ class RswaCache:
         cp = None if counts is None else _dense(counts, (B,), i32, ix, "counts")
         at = _stream_of(stream, ix)
         if workspace is None:
-            workspace = self._own_workspace(nodes, at)
+            wp, size = self._tree_at.get((nodes, at)) or self._own_workspace(nodes, at)
         elif workspace.get_device() != ix:
             raise ValueError(f"workspace: expected a tensor on CUDA device {ix}")
+        else:
+            wp, size = _ptr(workspace), workspace.numel()
         status = load().rswa_decode_tree(
-            self.handle, qp, kp, vp, pp, cp, nodes, op, lp, _ptr(workspace),
-            workspace.numel(), at)
+            self.handle, qp, kp, vp, pp, cp, nodes, op, lp, wp, size, at)
         if status:
             raise RswaError(status, "rswa_decode_tree")
 
     def _own_workspace(self, nodes, stream):
-        """The cache's workspace for trees of `nodes` nodes on a stream (handle):
-        made by the first call there that needs one (or a larger one), from the
+        """(pointer, bytes) of the cache's workspace for trees of `nodes` nodes on a
+        stream (handle): made by the first call there that needs one (or a larger one), from the
         stream's own pool, so that torch's allocator neither hands the cache a
         block that other queued work still uses nor, once the cache is gone,
         others one that the stream's queued calls do.  A capture takes one made
         before it: calls on one cache are ordered, so it need not be its own."""
-        stream = getattr(stream, "value", stream) or 0
-        have = self._tree_ws.get((nodes, stream))
-        if have is not None:
-            return have
         import torch
+        stream = getattr(stream, "value", stream) or 0
         need = rswa_decode_tree_workspace(self.handle, nodes)
         capturing = torch.cuda.is_current_stream_capturing()
         with torch.cuda.stream(_torch_stream(stream, self.buf.get_device())):
@@ -650,13 +649,14 @@ class RswaCache:
                 if have is None:
                     raise ValueError("decode_tree: no workspace of the cache's own yet: call it "
                                      "once before the capture, or pass one")
-                return have
+                return have.data_ptr(), have.numel()
             have = next((w for (_, at), w in self._tree_ws.items()
                          if at == stream and w.numel() >= need), None)
             if have is None:
                 have = self.tree_workspace(nodes)
         self._tree_ws[nodes, stream] = have
-        return have
+        self._tree_at[nodes, stream] = have.data_ptr(), have.numel()
+        return self._tree_at[nodes, stream]
 
     def commit_tree(self, k, v, path, accepted, stream=None):
         """Append the accepted nodes path[b][:accepted[b]] of a tree."""

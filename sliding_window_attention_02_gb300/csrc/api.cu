@@ -122,6 +122,7 @@ struct InRows {
 bool rows_meet(const InRows& in, int64_t rows, int64_t elt, const void* out, int64_t bytes) {
   const int64_t len = in.len * elt, step = rows < 2 ? len : in.stride * elt;
   const uintptr_t a = reinterpret_cast<uintptr_t>(in.p), o = reinterpret_cast<uintptr_t>(out);
+  if (o + bytes <= a || o >= a + (uintptr_t)(rows - 1) * step + len) return false;
   // the first row that ends behind out's first byte
   const int64_t r = o >= a + len ? (int64_t)((o - a - len) / step) + 1 : 0;
   return r < rows && a + r * step < o + bytes;
@@ -631,7 +632,8 @@ int rswa_decode_tree(rswa_cache* cache, const void* q, const void* k, const void
       !aligned16(v) || !aligned16(o) || !aligned4(parents) || !aligned4(counts) ||
       !aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0)
     return RSWA_EINVAL;
-  if (workspace_bytes < decode_tree_workspace(cache->cv, (int)nodes)) return RSWA_ECAPACITY;
+  const size_t need = decode_tree_workspace(cache->cv, (int)nodes);
+  if (workspace_bytes < need) return RSWA_ECAPACITY;
   {
     // What is written shares no byte with anything else, but o may be q: a row's
     // query is read before its result is written.
@@ -639,7 +641,7 @@ int rswa_decode_tree(rswa_cache* cache, const void* q, const void* k, const void
     const int64_t rows = nodes * cv.B, elt = cv.dtype == RSWA_F32 ? 4 : 2;
     const int64_t qo = rows * cv.H * cv.d * elt, kv = rows * cv.Hkv * cv.d * elt;
     const Span out[3] = {{o, qo}, {lse, lse ? rows * cv.H * 4 : 0},
-                         {workspace, (int64_t)decode_tree_workspace(cv, (int)nodes)}};
+                         {workspace, (int64_t)need}};
     const Span in[5] = {{q, qo}, {k, kv}, {v, kv}, {parents, rows * 4}, {counts, counts ? cv.B * 4 : 0}};
     for (int i = 0; i < 3; ++i) {
       for (int j = 0; j < 5; ++j)
