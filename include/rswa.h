@@ -72,8 +72,9 @@ enum rswa_status {
   RSWA_EHANDLE = 4,   /* NULL, destroyed or foreign handle */
   RSWA_ECUDA = 5,     /* a CUDA runtime call or launch failed */
   RSWA_EDEVICE = 6    /* a kernel flagged an error (bounded wait ran out, a
-                        launch shape that does not cover its work, or a draft
-                        tree or accepted path that is not one) */
+                        launch shape that does not cover its work, a draft
+                        tree or accepted path that is not one, or a batch whose
+                        rows, lengths or pages are out of range) */
 };
 
 enum rswa_dtype { RSWA_F32 = 0, RSWA_BF16 = 1 };
@@ -421,6 +422,164 @@ RSWA_API int rswa_commit_tree(rswa_cache* cache, const void* k, const void* v,
                               int64_t nodes, const int32_t* path,
                               const int32_t* accepted, int64_t max_path,
                               void* stream);
+
+/*
+ * Paged cache.  Keys and values live in a pool of pages; a table names the pages
+ * of each sequence, so that sequences of unlike lengths share one buffer, come and
+ * go, and may share pages that none of them writes.  The mask is the method's: a
+ * token sees the sequence's first m_b tokens (the reference prefix, or a few that
+ * stay visible) and the last n, itself included, all causally; n of every token's
+ * number makes it plain causal attention.
+ *
+ * The pool is [pages][kv_heads][page_size][head_dim], for keys and for values.
+ * Token x of sequence b is row x % page_size of page table[b][x / page_size].
+ * Unlike a cache's, the lengths belong to the caller: one description of a step
+ * (rswa_batch) serves every layer, each with a pool of its own.
+ */
+typedef struct rswa_pages rswa_pages;
+
+/*
+ * The sequences of a call (host struct; its arrays are on the pool's device and
+ * are read by the kernels, so that a captured graph replays with what they hold
+ * then).  Calls with a chunk take `rows` rows of q, k, v, o: sequence b has
+ * T_b = starts[b + 1] - starts[b] of them, from row starts[b] on, and they are the
+ * last T_b of its lens[b] tokens: lens counts the chunk.  Rows that no sequence
+ * has are neither read nor written.
+ * A row range outside 0 .. rows or of negative length, a length outside 0 ..
+ * max_pages * page_size or below T_b sets the device flag (RSWA_EDEVICE of
+ * rswa_pages_sync_status), and the sequence is taken as empty.  A page outside
+ * the pool sets the flag where it is read or written; a write is left out, results
+ * that depend on a read are undefined.  Only the entries of pages that hold a
+ * token which is read or written are looked at: others may hold anything.
+ */
+typedef struct rswa_batch {
+  const int32_t* table;   /* [batch][max_pages] */
+  const int32_t* lens;    /* [batch] tokens of each sequence, the chunk's included */
+  const int32_t* prefix;  /* [batch] first tokens that stay visible, m_b (clamped to
+                             0 .. lens[b]); NULL: none */
+  const int32_t* starts;  /* [batch + 1]; NULL: rows / batch rows each */
+  int64_t max_pages;      /* >= 1; max_pages * page_size at most 2^30 */
+  int64_t window;         /* n >= 1; 2^30 and more: every token */
+  int batch;              /* 1 .. 2^20 */
+} rswa_batch;
+
+/*
+ * Bytes of device memory of a pool, and its creation over the caller's buffer
+ * (256-byte aligned, owned by the caller, outlives the handle).  page_size is 16,
+ * 32, 64, 128 or 256; `heads` query heads share kv_heads, of which pages *
+ * page_size * kv_heads is at most 2^30; head_dim and dtype as for a cache.  The
+ * pages keep what the buffer holds: rows that are no tokens may be any bits.
+ * Creation zeroes the device flag (synchronous).
+ * Errors: RSWA_EINVAL, RSWA_EDTYPE, RSWA_ECAPACITY, RSWA_ECUDA.
+ */
+RSWA_API int rswa_pages_footprint(int64_t pages, int page_size, int heads, int kv_heads,
+                                  int head_dim, int dtype, size_t* out_bytes);
+RSWA_API int rswa_pages_create(int64_t pages, int page_size, int heads, int kv_heads,
+                               int head_dim, int dtype, void* device_buf, size_t buf_bytes,
+                               rswa_pages** out);
+
+/* Free the host handle (not the buffer).  Later use returns RSWA_EHANDLE. */
+RSWA_API int rswa_pages_destroy(rswa_pages* pages);
+
+/*
+ * Store the chunk's keys and values in the sequences' pages.  k, v: `rows` rows of
+ * [kv_heads][head_dim] elements, k_stride and v_stride elements apart (multiples
+ * of 16 bytes, at least the row's own length), apart from the pool.
+ * 0 <= rows, rows * heads < 2^31 (here and below); rows = 0 does nothing.
+ * Calls that write pages which others read or write are to be ordered by the
+ * caller; calls on one pool may overlap otherwise.
+ * Errors: RSWA_EHANDLE, RSWA_EINVAL, RSWA_ECUDA.
+ */
+RSWA_API int rswa_pages_append(rswa_pages* pages, const rswa_batch* batch, int64_t rows,
+                               const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                               void* stream);
+
+/*
+ * Device bytes of workspace of rswa_pages_attend for up to `rows` rows.  The
+ * workspace is zero before its first call; every call leaves it fit for the next
+ * one, of any size that it is large enough for.  Calls that may overlap on the GPU
+ * need one each.  After a call that reported RSWA_EDEVICE because a wait ran out,
+ * zero it again.  Host-only.  Errors: RSWA_EHANDLE, RSWA_EINVAL.
+ */
+RSWA_API int rswa_pages_attend_workspace(rswa_pages* pages, int64_t rows, int batch,
+                                         size_t* out_bytes);
+
+/*
+ * Attention of the chunk over the pages, which hold its own keys and values
+ * (rswa_pages_append comes first).  Token a sees token j <= a when j < m_b or
+ * j > a - n.
+ *   q          `rows` rows of [heads][head_dim], q_stride elements apart.
+ *   o          [rows][heads][head_dim]; may be q where q_stride is heads *
+ *              head_dim or rows is 1.  o, lse and the workspace share no other
+ *              memory with each other, with an input or with the pool.
+ *   lse        [rows][heads] float32 natural-log log-sum-exp of the scaled
+ *              logits, or NULL.
+ *   workspace  of rswa_pages_attend_workspace bytes, 256-byte aligned.
+ * Tokens that a row sees must be finite; every other row of a page may hold
+ * anything.  On the tensor cores (bf16 but for small work) the softmax weights are
+ * rounded to bf16 for their product with the values, not for the sum.
+ * Errors: RSWA_EHANDLE, RSWA_EINVAL, RSWA_ECAPACITY (workspace too small),
+ * RSWA_ECUDA.
+ */
+RSWA_API int rswa_pages_attend(rswa_pages* pages, const rswa_batch* batch, int64_t rows,
+                               const void* q, int64_t q_stride, void* o, float* lse,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Accumulate the attention weight that each cached token receives from the chunk:
+ *   weights[b][h][x] = decay * weights[b][h][x]
+ *                      + sum of exp(logit - lse) over the chunk's rows that see
+ *                        token x and the query heads of KV head h,
+ * for x < lens[b]; entries behind stay as they are.
+ *   lse      [rows][heads] as rswa_pages_attend gives it for these rows.
+ *   weights  float32 [batch][kv_heads][max_pages * page_size].
+ *   decay    0 .. 1; at 0 the old entries are not read.
+ * A row's own sums are float32, added in a fixed order: the result does not vary
+ * from call to call.  The chunk may be the last rows of a longer one only.
+ * Errors: RSWA_EHANDLE, RSWA_EINVAL, RSWA_ECUDA.
+ */
+RSWA_API int rswa_pages_weigh(rswa_pages* pages, const rswa_batch* batch, int64_t rows,
+                              const void* q, int64_t q_stride, const float* lse, float* weights,
+                              float decay, void* stream);
+
+/*
+ * Device bytes of workspace of rswa_pages_evict (it need not be initialised; calls
+ * that may overlap need one each).  Host-only.  Errors: RSWA_EHANDLE, RSWA_EINVAL.
+ */
+RSWA_API int rswa_pages_evict_workspace(rswa_pages* pages, int batch, int64_t budget,
+                                        size_t* out_bytes);
+
+/*
+ * Cut every sequence down to `budget` tokens: in each KV head stay the first
+ * `first`, the last `last` and, of those between, the ones of most weight (of
+ * equals the lower index; a NaN weighs least), budget - first - last of them.  They
+ * take the sequence's first places in their order, as do their weights; weights_out
+ * is 0 behind them.  A sequence of at most `budget` tokens stays whole.  The
+ * caller's next lens[b] is min(lens[b], budget); starts, prefix and window are not
+ * looked at.  1 <= budget <= 2^30, first + last <= budget.
+ *   weights      float32 [batch][kv_heads][max_pages * page_size].
+ *   table_out    [batch][max_pages] pages that the kept tokens go to, none of them
+ *                a page of `table`; NULL or batch->table: in place.  Pages that
+ *                other sequences share are not to be cut in place.
+ *   weights_out  as weights; may be weights.
+ *   kept         int32 [batch][kv_heads][budget], the kept tokens' former indices,
+ *                -1 behind the last; or NULL.
+ *   workspace    of rswa_pages_evict_workspace bytes, 256-byte aligned.
+ * What is written shares no other memory with an input or with each other.
+ * Errors: RSWA_EHANDLE, RSWA_EINVAL, RSWA_ECAPACITY, RSWA_ECUDA.
+ */
+RSWA_API int rswa_pages_evict(rswa_pages* pages, const rswa_batch* batch, const float* weights,
+                              int64_t budget, int64_t first, int64_t last,
+                              const int32_t* table_out, float* weights_out, int32_t* kept,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Byte offsets of the K and V pools inside the buffer.  Host-only.
+ * Errors: RSWA_EINVAL, RSWA_EHANDLE. */
+RSWA_API int rswa_pages_kv_offsets(rswa_pages* pages, size_t* k_offset, size_t* v_offset);
+
+/* rswa_sync_status of a pool: waits for the device, reports and clears the first
+ * error that a kernel flagged (RSWA_EDEVICE). */
+RSWA_API int rswa_pages_sync_status(rswa_pages* pages);
 
 /*
  * Live cache size of sequence b in bytes: C(t_b) * H_kv * d * 2 (K and V) *

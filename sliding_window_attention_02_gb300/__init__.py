@@ -28,7 +28,11 @@ __all__ = [
     "rswa_debug_set_wait_limit_ns", "rswa_cache_kv_offsets",
     "rswa_qk_norm_rope", "rswa_qk_norm_rope_cached", "rswa_append_kv_rope",
     "rswa_decode_tree_workspace", "rswa_decode_tree", "rswa_commit_tree",
-    "RswaRope", "RswaCache",
+    "rswa_pages_footprint", "rswa_pages_create", "rswa_pages_destroy",
+    "rswa_pages_append", "rswa_pages_attend_workspace", "rswa_pages_attend",
+    "rswa_pages_weigh", "rswa_pages_evict_workspace", "rswa_pages_evict",
+    "rswa_pages_kv_offsets", "rswa_pages_sync_status",
+    "RswaRope", "RswaCache", "RswaBatch", "RswaPages",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -51,6 +55,15 @@ class _RopeStruct(ctypes.Structure):
 
 
 _c_rope = ctypes.POINTER(_RopeStruct)
+
+
+class _BatchStruct(ctypes.Structure):
+    """struct rswa_batch of include/rswa.h."""
+    _fields_ = [("table", _c_vp), ("lens", _c_vp), ("prefix", _c_vp), ("starts", _c_vp),
+                ("max_pages", _c_i64), ("window", _c_i64), ("batch", _c_int)]
+
+
+_c_batch = ctypes.POINTER(_BatchStruct)
 
 _SIGNATURES = {
     "rswa_strerror": (ctypes.c_char_p, [_c_int]),
@@ -96,6 +109,25 @@ _SIGNATURES = {
                                   _c_vp, _c_vp, _c_vp, _c_size, _c_vp]),
     "rswa_commit_tree": (_c_int, [_c_vp, _c_vp, _c_vp, _c_i64, _c_vp, _c_vp, _c_i64,
                                   _c_vp]),
+    "rswa_pages_footprint": (_c_int, [_c_i64, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                      ctypes.POINTER(_c_size)]),
+    "rswa_pages_create": (_c_int, [_c_i64, _c_int, _c_int, _c_int, _c_int, _c_int, _c_vp,
+                                   _c_size, ctypes.POINTER(_c_vp)]),
+    "rswa_pages_destroy": (_c_int, [_c_vp]),
+    "rswa_pages_append": (_c_int, [_c_vp, _c_batch, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64,
+                                   _c_vp]),
+    "rswa_pages_attend_workspace": (_c_int, [_c_vp, _c_i64, _c_int,
+                                             ctypes.POINTER(_c_size)]),
+    "rswa_pages_attend": (_c_int, [_c_vp, _c_batch, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp,
+                                   _c_vp, _c_size, _c_vp]),
+    "rswa_pages_weigh": (_c_int, [_c_vp, _c_batch, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp,
+                                  ctypes.c_float, _c_vp]),
+    "rswa_pages_evict_workspace": (_c_int, [_c_vp, _c_int, _c_i64, ctypes.POINTER(_c_size)]),
+    "rswa_pages_evict": (_c_int, [_c_vp, _c_batch, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp,
+                                  _c_vp, _c_vp, _c_size, _c_vp]),
+    "rswa_pages_kv_offsets": (_c_int, [_c_vp, ctypes.POINTER(_c_size),
+                                       ctypes.POINTER(_c_size)]),
+    "rswa_pages_sync_status": (_c_int, [_c_vp]),
     "rswa_sync_status": (_c_int, [_c_vp]),
     "rswa_cache_kv_offsets": (_c_int, [_c_vp, ctypes.POINTER(_c_size),
                                        ctypes.POINTER(_c_size)]),
@@ -421,6 +453,84 @@ def rswa_commit_tree(handle, k, v, path, accepted, stream=None) -> None:
         int(path.shape[1]), _stream_of(stream, _device_index(k))), "rswa_commit_tree")
 
 
+def rswa_pages_footprint(pages, page_size, heads, kv_heads, head_dim, dtype) -> int:
+    out = _c_size(0)
+    _check(load().rswa_pages_footprint(pages, page_size, heads, kv_heads, head_dim, dtype,
+                                       ctypes.byref(out)), "rswa_pages_footprint")
+    return out.value
+
+
+def rswa_pages_create(pages, page_size, heads, kv_heads, head_dim, dtype, buf):
+    """Create a pool over the uint8 CUDA tensor ``buf``; returns the handle."""
+    h = _c_vp()
+    _check(load().rswa_pages_create(pages, page_size, heads, kv_heads, head_dim, dtype,
+                                    _ptr(buf), buf.numel() * buf.element_size(),
+                                    ctypes.byref(h)), "rswa_pages_create")
+    return h.value
+
+
+def rswa_pages_destroy(handle) -> None:
+    _check(load().rswa_pages_destroy(handle), "rswa_pages_destroy")
+
+
+def rswa_pages_append(handle, batch, k, k_stride, v, v_stride, stream=None) -> None:
+    """batch: RswaBatch; pointers as tensors, strides in elements;
+    RswaPages.append checks shapes and types."""
+    _check(load().rswa_pages_append(
+        handle, batch.ref, int(k.shape[0]), _row_ptr(k), k_stride, _row_ptr(v), v_stride,
+        _stream_of(stream, _device_index(k))), "rswa_pages_append")
+
+
+def rswa_pages_attend_workspace(handle, rows: int, batch: int) -> int:
+    out = _c_size(0)
+    _check(load().rswa_pages_attend_workspace(handle, rows, batch, ctypes.byref(out)),
+           "rswa_pages_attend_workspace")
+    return out.value
+
+
+def rswa_pages_attend(handle, batch, q, q_stride, o, workspace, lse=None, stream=None) -> None:
+    """RswaPages.attend checks shapes and types; workspace: zeroed uint8 tensor."""
+    _check(load().rswa_pages_attend(
+        handle, batch.ref, int(q.shape[0]), _row_ptr(q), q_stride, _ptr(o), _ptr(lse),
+        _ptr(workspace), workspace.numel(), _stream_of(stream, _device_index(q))),
+        "rswa_pages_attend")
+
+
+def rswa_pages_weigh(handle, batch, q, q_stride, lse, weights, decay=1.0, stream=None) -> None:
+    """RswaPages.weigh checks shapes and types."""
+    _check(load().rswa_pages_weigh(
+        handle, batch.ref, int(q.shape[0]), _row_ptr(q), q_stride, _ptr(lse), _ptr(weights),
+        decay, _stream_of(stream, _device_index(weights))), "rswa_pages_weigh")
+
+
+def rswa_pages_evict_workspace(handle, batch: int, budget: int) -> int:
+    out = _c_size(0)
+    _check(load().rswa_pages_evict_workspace(handle, batch, budget, ctypes.byref(out)),
+           "rswa_pages_evict_workspace")
+    return out.value
+
+
+def rswa_pages_evict(handle, batch, weights, budget, first, last, weights_out, workspace,
+                     table_out=None, kept=None, stream=None) -> None:
+    """RswaPages.evict checks shapes and types."""
+    _check(load().rswa_pages_evict(
+        handle, batch.ref, _ptr(weights), budget, first, last, _ptr(table_out),
+        _ptr(weights_out), _ptr(kept), _ptr(workspace), workspace.numel(),
+        _stream_of(stream, _device_index(weights))), "rswa_pages_evict")
+
+
+def rswa_pages_kv_offsets(handle):
+    ko, vo = _c_size(0), _c_size(0)
+    _check(load().rswa_pages_kv_offsets(handle, ctypes.byref(ko), ctypes.byref(vo)),
+           "rswa_pages_kv_offsets")
+    return ko.value, vo.value
+
+
+def rswa_pages_sync_status(handle) -> int:
+    """Returns the status code (does not raise)."""
+    return load().rswa_pages_sync_status(handle)
+
+
 def rswa_cache_bytes(handle, b: int) -> int:
     out = _c_size(0)
     _check(load().rswa_cache_bytes(handle, b, ctypes.byref(out)),
@@ -696,3 +806,212 @@ class RswaCache:
         Kt = self.buf[ko:ko + nb].view(tdt).view(B, H, R, d)
         Vt = self.buf[vo:vo + nb].view(tdt).view(B, H, R, d)
         return Kt, Vt
+
+
+class RswaBatch:
+    """The sequences of the calls on a paged cache (struct rswa_batch), with the
+    tensors it points to: int32 CUDA tensors that the calls read when they run, so
+    that a step may rewrite them in place.
+
+    table: [B][max_pages], the page of each page_size tokens; lens: [B] tokens,
+    the chunk's included; starts: [B + 1], the rows of the chunk that each sequence
+    has, or None for the same number each; prefix: [B] first tokens that stay
+    visible, or None; window: tokens that a token sees back, itself included, or
+    None for all.
+    """
+
+    def __init__(self, table, lens, starts=None, prefix=None, window=None):
+        import torch
+        if table.dim() != 2:
+            raise ValueError("table: expected [batch][max_pages]")
+        B = table.shape[0]
+        index = _device_index(table)
+        self.table, self.lens, self.starts, self.prefix = table, lens, starts, prefix
+        self.shape, self.index = (B, table.shape[1]), index
+
+        def ints(t, shape, name):
+            return None if t is None else _dense(t, shape, torch.int32, index, name)
+
+        if window is not None and window < 1:
+            raise ValueError("window: expected at least 1")
+        self._struct = _BatchStruct(
+            ints(table, self.shape, "table"), ints(lens, (B,), "lens"),
+            ints(prefix, (B,), "prefix"), ints(starts, (B + 1,), "starts"), table.shape[1],
+            1 << 30 if window is None else min(int(window), 1 << 30), B)
+        self.ref = ctypes.byref(self._struct)
+
+
+class _Workspaces:
+    """A handle's own workspaces: one for each stream that a call runs on, made (or
+    made larger) by the first call there that needs it, from the stream's own pool,
+    so that torch's allocator neither hands out a block that other queued work still
+    uses nor, once the handle is gone, gives others one that the stream's queued
+    calls do.  All stay, as captured graphs hold them."""
+
+    def __init__(self, index, what):
+        self.index, self.what = index, what
+        self.all = []                   # (stream, tensor)
+        self.at = {}                    # stream: (pointer, bytes) of its largest
+
+    def get(self, stream, need):
+        """(pointer, bytes) of one of at least `need` bytes for a stream (handle)."""
+        stream = getattr(stream, "value", stream) or 0
+        have = self.at.get(stream)
+        if have is not None and have[1] >= need:
+            return have
+        import torch
+        capturing = torch.cuda.is_current_stream_capturing()
+        with torch.cuda.stream(_torch_stream(stream, self.index)):
+            if capturing or torch.cuda.is_current_stream_capturing():
+                raise ValueError(f"{self.what}: no workspace of its own for this stream yet: "
+                                 f"call it there once before the capture, or pass one")
+            w = torch.zeros(need, dtype=torch.uint8, device=torch.device("cuda", self.index))
+        self.all.append((stream, w))
+        self.at[stream] = (w.data_ptr(), w.numel())
+        return self.at[stream]
+
+
+class RswaPages:
+    """A paged cache: a pool of pages plus the torch-allocated buffer behind it."""
+
+    def __init__(self, pages, page_size, heads, head_dim, dtype, device="cuda", kv_heads=None):
+        import torch
+        self.pages, self.page_size, self.heads, self.head_dim = pages, page_size, heads, head_dim
+        self.kv_heads = heads if kv_heads is None else kv_heads
+        self.dtype, self.handle = dtype, None
+        nbytes = rswa_pages_footprint(pages, page_size, heads, self.kv_heads, head_dim, dtype)
+        self.buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ix = self.buf.get_device()
+        with torch.cuda.device(ix):
+            self.handle = rswa_pages_create(pages, page_size, heads, self.kv_heads, head_dim,
+                                            dtype, self.buf)
+        self._shape = (heads, self.kv_heads, head_dim,
+                       torch.float32 if dtype == RSWA_F32 else torch.bfloat16, ix)
+        self._int32, self._float32 = torch.int32, torch.float32
+        self._attend_ws = _Workspaces(ix, "attend")
+        self._evict_ws = _Workspaces(ix, "evict")
+        self._attend_need, self._evict_need = {}, {}
+
+    def close(self):
+        if self.handle is not None:
+            rswa_pages_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _check_batch(self, batch):
+        if batch.index != self._shape[4]:
+            raise ValueError("batch: on another device than the pages")
+
+    def append(self, batch, k, v, stream=None):
+        """Store the chunk's keys and values: k, v of [rows][kv_heads][d] rows
+        (possibly part of longer ones)."""
+        H, Hkv, d, dt, ix = self._shape
+        rows = k.shape[0]
+        self._check_batch(batch)
+        kp, ks = _rows(k, (rows, Hkv, d), dt, ix, "k")
+        vp, vs = _rows(v, (rows, Hkv, d), dt, ix, "v")
+        status = load().rswa_pages_append(self.handle, batch.ref, rows, kp, ks, vp, vs,
+                                          _stream_of(stream, ix))
+        if status:
+            raise RswaError(status, "rswa_pages_append")
+
+    def attend_workspace(self, rows, batch):
+        """A workspace for attend calls of up to `rows` rows of `batch` sequences,
+        like any tensor made on torch's current stream."""
+        import torch
+        return torch.zeros(rswa_pages_attend_workspace(self.handle, rows, batch),
+                           dtype=torch.uint8, device=self.buf.device)
+
+    def attend(self, batch, q, o, lse=None, workspace=None, stream=None):
+        """Attention of the chunk's rows over the pages (see rswa_pages_attend): q
+        of [rows][heads][d] rows (possibly part of longer ones), o contiguous, lse
+        float32 [rows][heads] or None.  workspace: from attend_workspace; None: one
+        kept for the stream; a capture takes one that a call there has made."""
+        H, Hkv, d, dt, ix = self._shape
+        rows = q.shape[0]
+        self._check_batch(batch)
+        qp, qs = _rows(q, (rows, H, d), dt, ix, "q")
+        op = _dense(o, (rows, H, d), dt, ix, "o")
+        lp = None if lse is None else _dense(lse, (rows, H), self._float32, ix, "lse")
+        at = _stream_of(stream, ix)
+        if workspace is None:
+            key = (rows, batch.shape[0])
+            need = self._attend_need.get(key)
+            if need is None:
+                need = self._attend_need[key] = rswa_pages_attend_workspace(self.handle, *key)
+            wp, size = self._attend_ws.get(at, need)
+        elif workspace.get_device() != ix:
+            raise ValueError(f"workspace: expected a tensor on CUDA device {ix}")
+        else:
+            wp, size = _ptr(workspace), workspace.numel()
+        status = load().rswa_pages_attend(self.handle, batch.ref, rows, qp, qs, op, lp, wp, size,
+                                          at)
+        if status:
+            raise RswaError(status, "rswa_pages_attend")
+
+    def _weights(self, t, batch, name):
+        B, width = batch.shape
+        return _dense(t, (B, self.kv_heads, width * self.page_size), self._float32,
+                      self._shape[4], name)
+
+    def weigh(self, batch, q, lse, weights, decay=1.0, stream=None):
+        """Add the attention weights that the cached tokens receive from the
+        chunk's rows: weights float32 [B][kv_heads][max_pages * page_size] =
+        decay * weights + what they receive; lse as attend gave it."""
+        H, Hkv, d, dt, ix = self._shape
+        rows = q.shape[0]
+        self._check_batch(batch)
+        qp, qs = _rows(q, (rows, H, d), dt, ix, "q")
+        status = load().rswa_pages_weigh(
+            self.handle, batch.ref, rows, qp, qs, _dense(lse, (rows, H), self._float32, ix, "lse"),
+            self._weights(weights, batch, "weights"), decay, _stream_of(stream, ix))
+        if status:
+            raise RswaError(status, "rswa_pages_weigh")
+
+    def evict(self, batch, weights, budget, first=0, last=0, table_out=None, weights_out=None,
+              kept=None, workspace=None, stream=None):
+        """Cut every sequence down to `budget` tokens: its first and last ones and
+        the heaviest of the others, in their order (see rswa_pages_evict).  In
+        place, or to the pages of table_out; weights_out: weights itself where
+        None; kept: int32 [B][kv_heads][budget] for the tokens' former indices."""
+        ix = self._shape[4]
+        B, width = batch.shape
+        self._check_batch(batch)
+        wp = self._weights(weights, batch, "weights")
+        wo = wp if weights_out is None else self._weights(weights_out, batch, "weights_out")
+        tp = None if table_out is None else _dense(table_out, (B, width), self._int32, ix,
+                                                   "table_out")
+        kp = None if kept is None else _dense(kept, (B, self.kv_heads, budget), self._int32, ix,
+                                              "kept")
+        at = _stream_of(stream, ix)
+        if workspace is None:
+            need = self._evict_need.get((B, budget))
+            if need is None:
+                need = rswa_pages_evict_workspace(self.handle, B, budget)
+                self._evict_need[B, budget] = need
+            sp, size = self._evict_ws.get(at, need)
+        elif workspace.get_device() != ix:
+            raise ValueError(f"workspace: expected a tensor on CUDA device {ix}")
+        else:
+            sp, size = _ptr(workspace), workspace.numel()
+        status = load().rswa_pages_evict(self.handle, batch.ref, wp, budget, first, last, tp, wo,
+                                         kp, sp, size, at)
+        if status:
+            raise RswaError(status, "rswa_pages_evict")
+
+    def sync_status(self):
+        return rswa_pages_sync_status(self.handle)
+
+    def slabs(self):
+        """(K, V) views of the pools [pages][kv_heads][page_size][d]."""
+        H, Hkv, d, tdt, ix = self._shape
+        shape = (self.pages, Hkv, self.page_size, d)
+        nb = self.pages * Hkv * self.page_size * d * (4 if self.dtype == RSWA_F32 else 2)
+        ko, vo = rswa_pages_kv_offsets(self.handle)
+        return (self.buf[ko:ko + nb].view(tdt).view(shape),
+                self.buf[vo:vo + nb].view(tdt).view(shape))

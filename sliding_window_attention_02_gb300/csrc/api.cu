@@ -8,6 +8,7 @@
 #include <unordered_set>
 #include <vector>
 
+#include "api_util.h"
 #include "rswa_internal.h"
 
 using namespace rswa;
@@ -33,47 +34,10 @@ std::unordered_set<rswa_cache*> g_live;
 std::atomic<int> g_fail_next{0};
 std::atomic<uint64_t> g_wait_limit_ns{0};      // 0: the default bound
 
-constexpr size_t kAlign = 256;
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
 bool live(rswa_cache* c) {
   std::lock_guard<std::mutex> lk(g_mu);
   return c != nullptr && g_live.count(c) != 0;
 }
-
-// Test hook: simulated CUDA failure before anything is launched.
-bool injected_failure() {
-  int v = g_fail_next.load();
-  while (v > 0) {
-    if (g_fail_next.compare_exchange_weak(v, v - 1)) return true;
-  }
-  return false;
-}
-
-bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
-
-int status_of(cudaError_t e) { return e == cudaSuccess ? RSWA_OK : RSWA_ECUDA; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-// Makes the cache's device current for the duration of a call.
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = true;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) {
-      ok = false;
-      return;
-    }
-    if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
-  }
-  ~DeviceGuard() {
-    int cur;
-    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev)
-      cudaSetDevice(prev);
-  }
-};
 
 // Runs a decode launch with the handle's permission to read prefix rows and
 // m_b before the dependency wait.  Only a launch that succeeded counts as the
@@ -93,47 +57,6 @@ bool valid_rope(const rswa_rope* r, int head_dim) {
   if (r->rotary_dim < 0 || r->rotary_dim > head_dim || r->rotary_dim % 16 != 0) return false;
   if (r->rotary_dim > 0 && (!r->inv_freq || !aligned8(r->inv_freq))) return false;
   return aligned16(r->q_weight) && aligned16(r->k_weight);
-}
-
-// `rows` rows of `len` elements, `stride` apart, of 16-byte vectors.
-bool valid_rows(const void* p, int64_t stride, int64_t len, int64_t rows, int dtype) {
-  const int64_t elt = dtype == RSWA_F32 ? 4 : 2;
-  if (!p || !aligned16(p) || stride < 0 || stride > (int64_t(1) << 40)) return false;
-  return rows < 2 || (stride >= len && stride * elt % 16 == 0);
-}
-
-// Bytes that a call reads or writes.
-struct Span {
-  const void* p;
-  int64_t bytes;
-  bool meets(const Span& x) const {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(x.p);
-    return a < b + x.bytes && b < a + bytes;
-  }
-};
-
-// Rows of heads as a norm and rotation reads them.
-struct InRows {
-  const void* p;
-  int64_t stride, len;                         // elements
-};
-
-// Whether the rows share a byte with the `bytes` bytes at out.
-bool rows_meet(const InRows& in, int64_t rows, int64_t elt, const void* out, int64_t bytes) {
-  const int64_t len = in.len * elt, step = rows < 2 ? len : in.stride * elt;
-  const uintptr_t a = reinterpret_cast<uintptr_t>(in.p), o = reinterpret_cast<uintptr_t>(out);
-  if (o + bytes <= a || o >= a + (uintptr_t)(rows - 1) * step + len) return false;
-  // the first row that ends behind out's first byte
-  const int64_t r = o >= a + len ? (int64_t)((o - a - len) / step) + 1 : 0;
-  return r < rows && a + r * step < o + bytes;
-}
-
-// Whether dense result rows at `out` may be written while `in` is read: apart,
-// or row on row of `own` (in place).  Rows are done in any order.
-bool out_apart(const void* out, int64_t bytes, const InRows& in, int64_t rows, int64_t elt,
-               bool own) {
-  if (own && out == in.p && (rows < 2 || in.stride == in.len)) return true;
-  return !rows_meet(in, rows, elt, out, bytes);
 }
 
 // The results of rswa_qk_norm_rope(_cached): each apart from the other and from
@@ -252,6 +175,14 @@ Layout make_layout(int64_t m, int64_t n, int heads, int kv_heads, int head_dim,
 }
 
 }  // namespace
+
+bool rswa::injected_failure() {
+  int v = g_fail_next.load();
+  while (v > 0) {
+    if (g_fail_next.compare_exchange_weak(v, v - 1)) return true;
+  }
+  return false;
+}
 
 uint64_t rswa::phase_wait_limit_ns() {
   const uint64_t ns = g_wait_limit_ns.load();

@@ -1,0 +1,270 @@
+// Attention of a chunk of tokens over a paged cache, on the CUDA cores: float32
+// caches, groups too large for the tensor cores' tiles, and small work, where
+// latency counts.
+//
+//   o = sum_j exp(s_j - lse) v_j,  s_j = q . k_j / sqrt(d),  lse = log sum_j exp(s_j)
+// over the tokens j that the row's token sees (paged.cuh).
+//
+// A unit is up to R rows (token, query head of the group) of one KV head: every
+// key and value is loaded once for all of them.  Its keys, packed, are cut into
+// tiles that the launch's CTAs share evenly (PagedPlan); the eight warps of a CTA
+// take turns on a tile's keys, each lane group with its own running maximum, sum
+// and output (online softmax), merged at the end of the unit's part.  Units cut
+// over several CTAs leave partials, which the last of the CTAs merges in the
+// order of the CTAs, so that a result does not depend on who is last.
+#include <algorithm>
+
+#include "attend.cuh"
+#include "paged.cuh"
+
+namespace rswa {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kTile = 128;                     // keys
+
+using Plan = PagedPlan<kTile, false, 0, 1>;
+
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kWarps * 32)
+paged_attend_kernel(PagesView pv, BatchArgs ba, AttendArgs a) {
+  constexpr int U = R == 1 ? 8 : 4;
+  using C = AttendCfg<T, D, U>;
+  constexpr int EPL = C::EPL, LPK = C::LPK, KPW = C::KPW;
+  __shared__ PagedUnit s_unit;
+  __shared__ int s_more, s_last;
+  __shared__ float s_m[kWarps][R], s_l[kWarps][R];
+  __shared__ float s_acc[kWarps][R][D];
+  __shared__ float s_M[R], s_L[R];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int grp = lane / LPK, col = (lane % LPK) * EPL;
+  const int cta = blockIdx.x, G = pv.G;
+  const float sl2 = rsqrtf((float)D) * kLog2e;
+  griddep_wait();
+  griddep_launch_dependents();
+  Plan plan(pv, ba, R);
+  if (warp == 0) {
+    const bool more = plan.start(cta, gridDim.x);
+    if (lane == 0) {
+      s_more = more;
+      if (more) s_unit = plan.u;
+    }
+  }
+  __syncthreads();
+  while (s_more) {
+    const PagedUnit& u = s_unit;
+    const int rows = min(R, u.seq.T * G - u.f0);
+    const int b = u.b, kvh = u.kvh, m = u.seq.m, n = ba.window;
+    const int tok0 = u.seq.L - u.seq.T;
+    const Hull hull = u.hull;
+    const int x0 = u.j0 * kTile, x1 = min(u.j1 * kTile, hull.keys());
+    const int skip = hull.w0 - hull.p;
+    // Rows of q and o: row f of the unit is query head kvh * G + f % G of chunk
+    // row f / G.
+    auto row_of = [&](int r, int& head) {
+      const int f = u.f0 + r;
+      head = kvh * G + f % G;
+      return u.seq.row0 + f / G;
+    };
+    float qf[R][EPL];
+    int tok[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      int head;
+      const int64_t row = row_of(min(r, rows - 1), head);
+      tok[r] = tok0 + (u.f0 + min(r, rows - 1)) / G;
+      Elt<T>::widen(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
+                                                    row * a.q_stride + (int64_t)head * D + col),
+                    qf[r]);
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) qf[r][e] *= sl2;
+    }
+    SoftmaxState<EPL> st[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) st[r].init();
+    for (int base = x0 + warp * C::KEYS_WARP; base < x1; base += kWarps * C::KEYS_WARP) {
+      uint4 kr[U], vr[U];
+      int t[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int x = base + i * KPW + grp;
+        const int y = x < x1 ? x : x0;         // any key of the part
+        const int tk = y < hull.p ? y : y + skip;
+        const size_t at =
+            (((size_t)page_at(pv, ba, b, tk >> pv.log2P) * pv.Hkv + kvh) * pv.P +
+             (tk & (pv.P - 1))) * D + col;
+        kr[i] = ld_stream16(static_cast<const T*>(pv.K) + at);
+        vr[i] = ld_stream16(static_cast<const T*>(pv.V) + at);
+        t[i] = x < x1 ? tk : INT32_MAX;        // not a key: after every token
+      }
+      float s[R][U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        float kf[EPL];
+        Elt<T>::widen(kr[i], kf);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float x = 0.f;
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) x = fmaf(qf[r][e], kf[e], x);
+          s[r][i] = x;
+        }
+      }
+#pragma unroll
+      for (int off = LPK / 2; off > 0; off >>= 1)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int i = 0; i < U; ++i) s[r][i] += __shfl_xor_sync(0xffffffffu, s[r][i], off);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float mx = st[r].m;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          if (t[i] > tok[r] || (t[i] >= m && t[i] <= tok[r] - n)) s[r][i] = -INFINITY;
+          mx = fmaxf(mx, s[r][i]);
+        }
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        const float alpha = fast_exp2(st[r].m - ref);
+        st[r].l *= alpha;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) st[r].acc[e] *= alpha;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          s[r][i] = fast_exp2(s[r][i] - ref);
+          st[r].l += s[r][i];
+        }
+        st[r].m = mx;
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        float vf[EPL];
+        Elt<T>::widen(vr[i], vf);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) st[r].acc[e] = fmaf(s[r][i], vf[e], st[r].acc[e]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      merge_groups<T, D>(st[r]);
+      if (lane < LPK) {
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) s_acc[warp][r][col + e] = st[r].acc[e];
+        if (lane == 0) {
+          s_m[warp][r] = st[r].m;
+          s_l[warp][r] = st[r].l;
+        }
+      }
+    }
+    __syncthreads();
+    // The CTA's result of row r, column c: over the warps.
+    const size_t pf = (size_t)R * (D + 2);
+    float* part = paged_partial(a.ws, cta, u.first, pf);
+    const bool whole = u.whole();
+    for (int i = threadIdx.x; i < rows * D; i += kWarps * 32) {
+      const int r = i / D, c = i % D;
+      float M = -INFINITY, L = 0.f, A = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][r]);
+      const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float sc = fast_exp2(s_m[w][r] - ref);
+        L += s_l[w][r] * sc;
+        A += s_acc[w][r][c] * sc;
+      }
+      if (whole) {
+        int head;
+        const int64_t row = row_of(r, head), oi = row * pv.H + head;
+        static_cast<T*>(a.o)[oi * D + c] = (T)(A / L);   // a token sees itself: L > 0
+        if (c == 0 && a.lse) a.lse[oi] = (ref + log2f(L)) * kLn2;
+      } else {
+        part[i] = A;
+        if (c == 0) {
+          part[R * D + r] = M;
+          part[R * D + R + r] = L;
+        }
+      }
+    }
+    if (!whole) {
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        int32_t* count = paged_counter(a.ws, u.first);
+        s_last = arrive_acq_rel(count) == u.last - u.first;
+        if (s_last) *count = 0;                // ready for the next call
+      }
+      __syncthreads();
+      if (s_last) {
+        for (int r = warp; r < rows; r += kWarps) {
+          float M = -INFINITY;
+          for (int p = u.first + lane; p <= u.last; p += 32)
+            M = fmaxf(M, __ldcg(paged_partial(a.ws, p, u.first, pf) + R * D + r));
+          M = warp_max(M);
+          float L = 0.f;
+          for (int p = u.first + lane; p <= u.last; p += 32) {
+            const float* P = paged_partial(a.ws, p, u.first, pf) + R * D + r;
+            L += __ldcg(P + R) * fast_exp2(__ldcg(P) - M);
+          }
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+          if (lane == 0) {
+            s_M[r] = M;
+            s_L[r] = L;
+          }
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < rows * D; i += kWarps * 32) {
+          const int r = i / D, c = i % D;
+          const float M = s_M[r], L = s_L[r];
+          float A = 0.f;
+#pragma unroll 4
+          for (int p = u.first; p <= u.last; ++p) {
+            const float* P = paged_partial(a.ws, p, u.first, pf);
+            A = fmaf(__ldcg(P + i), fast_exp2(__ldcg(P + R * D + r) - M), A);
+          }
+          int head;
+          const int64_t row = row_of(r, head), oi = row * pv.H + head;
+          static_cast<T*>(a.o)[oi * D + c] = (T)(A / L);
+          if (c == 0 && a.lse) a.lse[oi] = (M + log2f(L)) * kLn2;
+        }
+      }
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const bool more = plan.next();
+      if (lane == 0) {
+        s_more = more;
+        if (more) s_unit = plan.u;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+int grid_of(const PagesView& pv) { return std::min(2 * std::max(pv.sms, 1), kMaxPagedCtas); }
+
+template <typename T, int D>
+cudaError_t launch_d(const PagesView& pv, const BatchArgs& ba, const AttendArgs& a,
+                     cudaStream_t s) {
+  const bool one = (int64_t)ba.rows * pv.G <= ba.B;      // one row to a unit
+  return launch_dependent(one ? paged_attend_kernel<T, D, 1> : paged_attend_kernel<T, D, 4>,
+                          dim3(grid_of(pv)), dim3(kWarps * 32), 0, s, pv, ba, a);
+}
+
+}  // namespace
+
+size_t paged_attend_workspace(const PagesView& pv, int64_t rows, int batch) {
+  return kPagedCounterBytes + (size_t)grid_of(pv) * 2 * 4 * (pv.d + 2) * sizeof(float);
+}
+
+cudaError_t launch_paged_attend(const PagesView& pv, const BatchArgs& ba, const AttendArgs& a,
+                                cudaStream_t s) {
+  if (pv.dtype == RSWA_F32)
+    return pv.d == 64 ? launch_d<float, 64>(pv, ba, a, s) : launch_d<float, 128>(pv, ba, a, s);
+  return pv.d == 64 ? launch_d<__nv_bfloat16, 64>(pv, ba, a, s)
+                    : launch_d<__nv_bfloat16, 128>(pv, ba, a, s);
+}
+
+}  // namespace rswa

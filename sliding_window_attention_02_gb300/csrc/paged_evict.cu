@@ -1,0 +1,320 @@
+// Eviction from a paged cache: of every (sequence, KV head) the first tokens, the
+// last ones and the heaviest of the others stay, up to a budget, in their order.
+//
+// Two kernels.  The first, a CTA for each (sequence, KV head), finds the least
+// weight that stays: the weights as integers of the same order, a radix select of
+// four passes over 8 bits each, in shared memory where a sequence's fit.  Ties of
+// that weight stay from the lowest index on.  A scan of what stays gives each kept
+// token its place; the weights follow.  The second moves the rows, 64 of them a
+// CTA, every read of it in flight at once.
+//
+// In place a row's place is at or before where it comes from, so a CTA's writes
+// may meet only what CTAs of lower rows of the same head read: CTAs take their rows
+// in ticket order, read them into registers, say so, and write once the lower ones
+// whose reads reach its rows have said so too.  No CTA waits before it has read, so
+// the wait ends whatever CTAs run at a time.
+#include <algorithm>
+
+#include "paged.cuh"
+#include "tc_ptx.cuh"
+
+namespace rswa {
+namespace {
+
+constexpr int kSelectThreads = 1024;
+constexpr int kMoveRows = 64, kMoveThreads = 128;
+constexpr uint64_t kWaitLimitNs = 1000000000ull;
+// Weights of a sequence that are kept in shared memory between the passes.
+constexpr int kSelectSmem = 40 * 1024;
+
+// A float as an unsigned integer of the same order; both zeros alike, NaN lowest.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  if (x != x) return 0u;
+  const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Tokens of sequence b; a length outside its range is flagged and taken as 0.
+__device__ __forceinline__ int length_of(const PagesView& pv, const BatchArgs& ba, int b) {
+  const int L = ba.lens[b];
+  if (L >= 0 && L <= ba.cap) return L;
+  flag_error(pv.err, kErrBadBatch);
+  return 0;
+}
+
+// The workspace: a ticket, a flag for every CTA of the move, and the kept tokens
+// where the caller wants none.
+__device__ __forceinline__ int32_t* move_flags(void* ws) { return static_cast<int32_t*>(ws) + 64; }
+
+template <bool SMEM>
+__global__ void __launch_bounds__(kSelectThreads)
+evict_select_kernel(PagesView pv, BatchArgs ba, EvictArgs a, int chunks) {
+  extern __shared__ uint32_t s_key[];
+  __shared__ uint32_t s_hist[256];
+  __shared__ uint32_t s_prefix, s_need;
+  __shared__ int s_warp[2][kSelectThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t bh = blockIdx.x;
+  const int b = (int)(bh / pv.Hkv);
+  const float* w = a.weights + bh * ba.cap;
+  float* wo = a.weights_out + bh * ba.cap;
+  int32_t* kept = a.kept + bh * a.budget;
+  if (a.in_place) {
+    if (bh == 0 && tid == 0) *static_cast<int32_t*>(a.ws) = 0;
+    for (int i = tid; i < chunks; i += kSelectThreads) move_flags(a.ws)[bh * chunks + i] = 0;
+  }
+  const int L = length_of(pv, ba, b);
+  if (L <= a.budget) {
+    for (int i = tid; i < a.budget; i += kSelectThreads) kept[i] = i < L ? i : -1;
+    for (int i = tid; i < ba.cap; i += kSelectThreads) {
+      if (i >= L)
+        wo[i] = 0.f;
+      else if (wo != w)
+        wo[i] = w[i];
+    }
+    return;
+  }
+  const int lo = a.first, hi = L - a.last;               // the tokens that are weighed
+  auto key = [&](int j) { return SMEM ? s_key[j] : order_key(w[j]); };
+  if (SMEM)
+    for (int j = lo + tid; j < hi; j += kSelectThreads) s_key[j] = order_key(w[j]);
+  if (tid == 0) {
+    s_prefix = 0;
+    s_need = (uint32_t)(a.budget - a.first - a.last);
+  }
+  __syncthreads();
+  uint32_t least = 0xffffffffu;                          // no weight has this key
+  int ties = 0;                                          // of the least weight that stay
+  if (s_need > 0) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      if (tid < 256) s_hist[tid] = 0;
+      __syncthreads();
+      const uint32_t prefix = s_prefix;
+      for (int j = lo + tid; j < hi; j += kSelectThreads) {
+        const uint32_t x = key(j);
+        if (shift == 24 || (x ^ prefix) >> (shift + 8) == 0)
+          atomicAdd(&s_hist[x >> shift & 255u], 1u);
+      }
+      __syncthreads();
+      if (warp == 0) {
+        // the digit in which the needed one falls, from the highest down: lane l
+        // has digits 255 - 8 l ... 248 - 8 l
+        uint32_t c[8], mine = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mine += c[e] = s_hist[255 - 8 * lane - e];
+        uint32_t inc = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, inc, off);
+          if (lane >= off) inc += y;
+        }
+        const uint32_t need = s_need;
+        __syncwarp();
+        uint32_t above = inc - mine;
+        if (above < need && need <= inc) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (above < need && need <= above + c[e]) {
+              s_prefix = prefix | (uint32_t)(255 - 8 * lane - e) << shift;
+              s_need = need - above;
+            }
+            above += c[e];
+          }
+        }
+      }
+      __syncthreads();
+    }
+    least = s_prefix;
+    ties = (int)s_need;
+  }
+  // Thread t looks through tokens [t * per, (t + 1) * per); an odd number spreads
+  // them over the banks.
+  const int per = ((L + kSelectThreads - 1) / kSelectThreads) | 1;
+  const int j0 = min(tid * per, L), j1 = min(j0 + per, L);
+  int above = 0, equal = 0;
+  for (int j = j0; j < j1; ++j) {
+    if (j < lo || j >= hi) {
+      ++above;
+    } else {
+      const uint32_t x = key(j);
+      above += x > least;
+      equal += x == least;
+    }
+  }
+  int inc_a = above, inc_e = equal;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int ya = __shfl_up_sync(0xffffffffu, inc_a, off);
+    const int ye = __shfl_up_sync(0xffffffffu, inc_e, off);
+    if (lane >= off) {
+      inc_a += ya;
+      inc_e += ye;
+    }
+  }
+  if (lane == 31) {
+    s_warp[0][warp] = inc_a;
+    s_warp[1][warp] = inc_e;
+  }
+  __syncthreads();
+  int na = inc_a - above, ne = inc_e - equal;            // before this thread's tokens
+  for (int x = 0; x < warp; ++x) {
+    na += s_warp[0][x];
+    ne += s_warp[1][x];
+  }
+  for (int j = j0; j < j1; ++j) {
+    bool stays = j < lo || j >= hi, tie = false;
+    if (!stays) {
+      const uint32_t x = key(j);
+      stays = x > least;
+      tie = x == least;
+    }
+    if (stays || (tie && ne < ties)) kept[na + min(ne, ties)] = j;
+    na += stays;
+    ne += tie;
+  }
+  __syncthreads();
+  // The weights: in place too, a batch is read before it is written, and a later
+  // batch comes from behind what an earlier one writes.
+  for (int i0 = 0; i0 < a.budget; i0 += kSelectThreads) {
+    const int i = i0 + tid;
+    const float x = i < a.budget ? w[kept[i]] : 0.f;
+    __syncthreads();
+    if (i < a.budget) wo[i] = x;
+  }
+  __syncthreads();
+  for (int i = a.budget + tid; i < ba.cap; i += kSelectThreads) wo[i] = 0.f;
+}
+
+template <int ELT, int D>
+__global__ void __launch_bounds__(kMoveThreads)
+evict_move_kernel(PagesView pv, BatchArgs ba, EvictArgs a, int chunks) {
+  constexpr int NV = D * ELT / 16;                       // vectors of a row
+  constexpr int PASS = kMoveThreads / NV;                // rows at a time
+  constexpr int N = kMoveRows / PASS;
+  static_assert(NV <= kMoveThreads && kMoveRows % PASS == 0, "rows of a CTA");
+  __shared__ int s_ticket;
+  __shared__ int s_late;
+  const int tid = threadIdx.x;
+  griddep_wait();
+  griddep_launch_dependents();
+  int64_t id = blockIdx.x;
+  if (a.in_place) {
+    if (tid == 0) {
+      s_ticket = atomicAdd(static_cast<int32_t*>(a.ws), 1);
+      s_late = 0;
+    }
+    __syncthreads();
+    id = s_ticket;
+  }
+  const int64_t bh = id / chunks;
+  const int chunk = (int)(id % chunks), r0 = chunk * kMoveRows;
+  const int b = (int)(bh / pv.Hkv), h = (int)(bh % pv.Hkv);
+  const int L = length_of(pv, ba, b);
+  const int count = min(L, a.budget);
+  if (r0 >= count || (a.in_place && L <= a.budget)) return;    // nothing waits for it
+  const int32_t* kept = a.kept + bh * a.budget;
+  const int32_t* out = a.in_place ? ba.table : a.table_out;
+  const int col = tid % NV, row = r0 + tid / NV;
+  const uint4* K = static_cast<const uint4*>(pv.K);
+  const uint4* V = static_cast<const uint4*>(pv.V);
+  uint4 k[N], v[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const int r = row + e * PASS;
+    if (r >= count) break;
+    const int j = kept[r];
+    const size_t at = (((size_t)page_at(pv, ba, b, j >> pv.log2P) * pv.Hkv + h) * pv.P +
+                       (j & (pv.P - 1))) * NV + col;
+    // not through the read-only path: in place, rows are written in this launch
+    k[e] = __ldcg(K + at);
+    v[e] = __ldcg(V + at);
+  }
+  bool ok = true;
+  if (a.in_place) {
+    __syncthreads();                                     // the CTA has its rows
+    int32_t* flags = move_flags(a.ws) + bh * chunks;
+    if (tid == 0)
+      asm volatile("st.release.gpu.s32 [%0], 1;" ::"l"(flags + chunk) : "memory");
+    // the lower chunks whose last row comes from this one's first row or behind it
+    for (int c = chunk - 1 - tid; c >= 0; c -= kMoveThreads) {
+      if (kept[c * kMoveRows + kMoveRows - 1] < r0) break;
+      const uint64_t t0 = ptx::globaltimer_ns();
+      for (;;) {
+        int done;
+        asm volatile("ld.acquire.gpu.s32 %0, [%1];" : "=r"(done) : "l"(flags + c) : "memory");
+        if (done) break;
+        if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+          flag_error(pv.err, kErrWaitTimeout);
+          s_late = 1;
+          break;
+        }
+      }
+    }
+    __syncthreads();
+    ok = s_late == 0;
+  }
+  if (!ok) return;
+  uint4* Ko = static_cast<uint4*>(pv.K);
+  uint4* Vo = static_cast<uint4*>(pv.V);
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const int r = row + e * PASS;
+    if (r >= count) break;
+    const int page = out[(size_t)b * ba.max_pages + (r >> pv.log2P)];
+    if ((unsigned)page >= (unsigned)pv.pages) {
+      flag_error(pv.err, kErrBadBatch);
+      continue;
+    }
+    const size_t at = (((size_t)page * pv.Hkv + h) * pv.P + (r & (pv.P - 1))) * NV + col;
+    Ko[at] = k[e];
+    Vo[at] = v[e];
+  }
+}
+
+// CTAs of the move for each (sequence, KV head).
+int move_chunks(int64_t budget) { return (int)((budget + kMoveRows - 1) / kMoveRows); }
+
+template <int ELT, int D>
+cudaError_t launch_move(const PagesView& pv, const BatchArgs& ba, const EvictArgs& a, int chunks,
+                        cudaStream_t s) {
+  return launch_dependent(evict_move_kernel<ELT, D>,
+                          dim3((unsigned)((int64_t)ba.B * pv.Hkv * chunks)), dim3(kMoveThreads), 0,
+                          s, pv, ba, a, chunks);
+}
+
+}  // namespace
+
+size_t paged_evict_workspace(const PagesView& pv, int64_t batch, int64_t budget, bool kept) {
+  const size_t heads = (size_t)batch * pv.Hkv;
+  return 256 + (heads * move_chunks(budget) + (kept ? 0 : heads * budget)) * sizeof(int32_t);
+}
+
+cudaError_t launch_paged_evict(const PagesView& pv, const BatchArgs& ba, const EvictArgs& in,
+                               cudaStream_t s) {
+  EvictArgs a = in;
+  const int chunks = move_chunks(std::min(a.budget, ba.cap));
+  const int64_t heads = (int64_t)ba.B * pv.Hkv;
+  if (!a.kept) a.kept = static_cast<int32_t*>(a.ws) + 64 + heads * chunks;
+  cudaError_t e;
+  if (ba.cap <= kSelectSmem) {
+    const size_t smem = (size_t)ba.cap * 4;
+    e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSelectSmem * 4);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(evict_select_kernel<true>, dim3((unsigned)heads), dim3(kSelectThreads),
+                         smem, s, pv, ba, a, chunks);
+  } else {
+    e = launch_dependent(evict_select_kernel<false>, dim3((unsigned)heads), dim3(kSelectThreads), 0,
+                         s, pv, ba, a, chunks);
+  }
+  if (e != cudaSuccess) return e;
+  if (pv.dtype == RSWA_F32)
+    return pv.d == 64 ? launch_move<4, 64>(pv, ba, a, chunks, s)
+                      : launch_move<4, 128>(pv, ba, a, chunks, s);
+  return pv.d == 64 ? launch_move<2, 64>(pv, ba, a, chunks, s)
+                    : launch_move<2, 128>(pv, ba, a, chunks, s);
+}
+
+}  // namespace rswa

@@ -19,6 +19,7 @@ enum DeviceErr : int32_t {
   kErrWaitTimeout = 1,
   kErrLaunchShape = 2,   // a launch whose grid does not cover its work
   kErrBadTree = 3,       // a parent, count or path node outside its range
+  kErrBadBatch = 4,      // a length, row range or page outside its range
 };
 
 __device__ __forceinline__ void flag_error(int32_t* err, int32_t code) {

@@ -199,6 +199,52 @@ cudaError_t launch_commit_tree(const CacheView& cv, const void* k, const void* v
                                const int32_t* path, const int32_t* accepted, int max_path,
                                cudaStream_t s);
 
+// A pool of pages: K, V [pages][Hkv][P][d], P tokens a page (a power of two).
+struct PagesView {
+  void* K;
+  void* V;
+  int32_t* err;            // first device-side error code (0 = none)
+  int pages, P, log2P;
+  int H, Hkv, G, d, dtype; // G = H / Hkv
+  int sms;
+};
+// What a call says of its sequences (rswa_batch).
+struct BatchArgs {
+  const int32_t *table, *lens, *prefix, *starts;
+  int B, max_pages, rows;
+  int each;                // rows of every sequence where starts is NULL
+  int cap;                 // max_pages * P
+  int window;              // at most 2^30
+};
+struct AttendArgs {
+  const void* q;
+  int64_t q_stride;        // elements
+  void* o;
+  float* lse;
+  void* ws;
+};
+cudaError_t launch_paged_append(const PagesView& pv, const BatchArgs& ba, const void* k,
+                                int64_t k_stride, const void* v, int64_t v_stride,
+                                cudaStream_t s);
+size_t paged_attend_workspace(const PagesView& pv, int64_t rows, int batch);
+cudaError_t launch_paged_attend(const PagesView& pv, const BatchArgs& ba, const AttendArgs& a,
+                                cudaStream_t s);
+cudaError_t launch_paged_weigh(const PagesView& pv, const BatchArgs& ba, const void* q,
+                               int64_t q_stride, const float* lse, float* weights, float decay,
+                               cudaStream_t s);
+struct EvictArgs {
+  const float* weights;
+  float* weights_out;
+  const int32_t* table_out;
+  int32_t* kept;           // [B][Hkv][budget]
+  void* ws;
+  int budget, first, last;
+  bool in_place;
+};
+size_t paged_evict_workspace(const PagesView& pv, int64_t batch, int64_t budget, bool kept);
+cudaError_t launch_paged_evict(const PagesView& pv, const BatchArgs& ba, const EvictArgs& a,
+                               cudaStream_t s);
+
 // Programmatic stream serialization: a kernel may begin launching while the
 // previous kernel of the stream drains; each one waits (griddepcontrol) before
 // it touches memory that the previous one writes.
