@@ -255,12 +255,18 @@ cudaError_t launch_d(const PagesView& pv, const BatchArgs& ba, const AttendArgs&
 
 }  // namespace
 
-size_t paged_attend_workspace(const PagesView& pv, int64_t rows, int batch) {
-  return kPagedCounterBytes + (size_t)grid_of(pv) * 2 * 4 * (pv.d + 2) * sizeof(float);
+static bool use_tc(const PagesView& pv, int64_t rows, int batch) {
+  return paged_attend_tc_supported(pv) && rows > batch;
 }
 
-cudaError_t launch_paged_attend(const PagesView& pv, const BatchArgs& ba, const AttendArgs& a,
-                                cudaStream_t s) {
+size_t paged_attend_workspace(const PagesView& pv, int64_t rows, int batch) {
+  const size_t own = kPagedCounterBytes + (size_t)grid_of(pv) * 2 * 4 * (pv.d + 2) * sizeof(float);
+  return use_tc(pv, rows, batch) ? std::max(own, paged_attend_tc_workspace(pv)) : own;
+}
+
+cudaError_t launch_paged_attend(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
+                                const AttendArgs& a, cudaStream_t s) {
+  if (use_tc(pv, ba.rows, ba.B)) return launch_paged_attend_tc(pv, maps, ba, a, s);
   if (pv.dtype == RSWA_F32)
     return pv.d == 64 ? launch_d<float, 64>(pv, ba, a, s) : launch_d<float, 128>(pv, ba, a, s);
   return pv.d == 64 ? launch_d<__nv_bfloat16, 64>(pv, ba, a, s)

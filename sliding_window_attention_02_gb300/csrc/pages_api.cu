@@ -15,6 +15,7 @@ struct rswa_pages {
   int device;
   void* buf;
   size_t k_off, v_off;
+  PagesMaps maps;                              // of a bf16 pool
 };
 
 namespace {
@@ -140,7 +141,9 @@ int rswa_pages_create(int64_t pages, int page_size, int heads, int kv_heads, int
   p->buf = device_buf;
   p->k_off = L.k_off;
   p->v_off = L.v_off;
-  cudaError_t e = cudaMemsetAsync(device_buf, 0, kAlign, 0);
+  cudaError_t e = dtype == RSWA_BF16 && !make_pages_maps(pv, &p->maps) ? cudaErrorInvalidValue
+                                                                       : cudaSuccess;
+  if (e == cudaSuccess) e = cudaMemsetAsync(device_buf, 0, kAlign, 0);
   if (e == cudaSuccess) e = cudaStreamSynchronize(0);
   if (e != cudaSuccess) {
     delete p;
@@ -232,7 +235,7 @@ int rswa_pages_attend(rswa_pages* pages, const rswa_batch* batch, int64_t rows, 
   a.o = o;
   a.lse = lse;
   a.ws = workspace;
-  return status_of(launch_paged_attend(pv, ba, a, static_cast<cudaStream_t>(stream)));
+  return status_of(launch_paged_attend(pv, pages->maps, ba, a, static_cast<cudaStream_t>(stream)));
 }
 
 int rswa_pages_weigh(rswa_pages* pages, const rswa_batch* batch, int64_t rows, const void* q,

@@ -658,11 +658,13 @@ bool make_tmap_rows_bf16(CUtensorMap* map, const void* base, uint64_t cols,
 }
 
 bool make_tmap_heads_bf16(CUtensorMap* map, const void* base, uint64_t d, uint64_t heads,
-                          uint64_t rows, uint32_t box_heads, uint32_t box_rows) {
+                          uint64_t rows, uint32_t box_heads, uint32_t box_rows,
+                          uint64_t stride) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
-  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)(heads * d) * 2};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2,
+                                 (cuuint64_t)(stride ? stride : heads * d) * 2};
   const cuuint32_t box[3] = {64, box_heads, box_rows};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,

@@ -189,9 +189,10 @@ bool make_slab_maps(const CacheView& cv, SlabMaps* maps);
 cudaError_t launch_decode_tree_tc(const CacheView& cv, const TreeArgs& a, const SlabMaps& maps,
                                   cudaStream_t s);
 // [rows][heads][d] bf16 as a 3-D TMA map: box 64 columns x box_heads heads x
-// box_rows rows, 128-byte swizzle.
+// box_rows rows, 128-byte swizzle; rows `stride` elements apart (0: heads * d).
 bool make_tmap_heads_bf16(CUtensorMap* map, const void* base, uint64_t d, uint64_t heads,
-                          uint64_t rows, uint32_t box_heads, uint32_t box_rows);
+                          uint64_t rows, uint32_t box_heads, uint32_t box_rows,
+                          uint64_t stride = 0);
 // maps: of decode_tree_use_tc shapes, else unused.
 cudaError_t launch_decode_tree(const CacheView& cv, const TreeArgs& a, const SlabMaps* maps,
                                bool prefetch, cudaStream_t s);
@@ -226,9 +227,21 @@ struct AttendArgs {
 cudaError_t launch_paged_append(const PagesView& pv, const BatchArgs& ba, const void* k,
                                 int64_t k_stride, const void* v, int64_t v_stride,
                                 cudaStream_t s);
+// Tensor maps of a bf16 pool (boxes of a page's rows, at most 128): the pool stays
+// where it is, so a handle makes them once.
+struct PagesMaps {
+  CUtensorMap k, v;
+};
+bool make_pages_maps(const PagesView& pv, PagesMaps* maps);
+// maps: of bf16 pools, else unused.
 size_t paged_attend_workspace(const PagesView& pv, int64_t rows, int batch);
-cudaError_t launch_paged_attend(const PagesView& pv, const BatchArgs& ba, const AttendArgs& a,
-                                cudaStream_t s);
+cudaError_t launch_paged_attend(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
+                                const AttendArgs& a, cudaStream_t s);
+// On the tensor cores (paged_attend_tc.cu): bf16, at most 128 query heads per KV head.
+bool paged_attend_tc_supported(const PagesView& pv);
+size_t paged_attend_tc_workspace(const PagesView& pv);
+cudaError_t launch_paged_attend_tc(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
+                                   const AttendArgs& a, cudaStream_t s);
 cudaError_t launch_paged_weigh(const PagesView& pv, const BatchArgs& ba, const void* q,
                                int64_t q_stride, const float* lse, float* weights, float decay,
                                cudaStream_t s);
