@@ -351,13 +351,78 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       int pfresh = 2, qfresh = 2;        // steps until both halves have had one
       if (pmore && pc.split && pc.left == 1) pfresh = 1;
       if (qmore && qc.split && qc.left == 1) qfresh = 1;
-      uint32_t begun = 0;                // halves whose O holds a product of the segment
       const uint64_t qdesc = desc_sw128(sb + SM::OFF_Q, 16, 1024);
       const uint64_t kdesc = desc_sw128(sb + SM::OFF_RING, 16, 1024);
       const uint64_t vdesc = desc_sw128(sb + SM::OFF_RING, kSub, 1024);
+      uint32_t begun = 0;                // halves whose O holds a product of the segment
+      // O_h (+)= P_h V, of the steps that hold keys; S_h = Q_h K^T.
+      auto pv = [&](uint32_t half, uint32_t slot, uint32_t flags) {
+        if (!(flags >> (8 + half) & 1u)) return;
+        const uint64_t vd = vdesc + (uint64_t)(slot * (kTile >> 4));
+        uint32_t acc = begun >> half & 1u;
+        begun |= 1u << half;
+        if ((flags & 0xffu) == 0xffu) {
+#pragma unroll
+          for (int k = 0; k < BN / 16; ++k)
+            mma_bf16_ts(tmem + tm_o(half), tmem + tm_s(half) + k * 8, vd + k * 128, idesc_pv,
+                        k > 0 ? 1u : acc);
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < BN / 16; ++k)
+            if (flags >> k & 1u) {
+              mma_bf16_ts(tmem + tm_o(half), tmem + tm_s(half) + k * 8, vd + k * 128, idesc_pv,
+                          acc);
+              acc = 1u;
+            }
+        }
+      };
+      auto qk = [&](uint32_t half, uint32_t slot, uint32_t qt, uint32_t flags) {
+        if (flags >> (8 + half) & 1u) {
+          const uint64_t kd = kdesc + (uint64_t)(slot * (kTile >> 4));
+          const uint64_t qd = qdesc + (uint64_t)((qt % NQ) * (kTile >> 4));
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * kSub + (k & 3) * 32) >> 4;
+            mma_bf16_ss(tmem + tm_s(half), qd + off, kd + off, idesc_qk, k > 0);
+          }
+        }
+        mma_commit(bar(SM::B_S + half));
+      };
 #pragma unroll 1
       for (uint32_t s = 0; pmore; ++s) {
         const uint32_t half = s & 1;
+        // Inside a pair's segment: both halves' turns on a tile in a row, PV of tile
+        // t and QK of t + 1, without a question about segments, and with the waits
+        // for loads before those for the softmax.
+        if (half == 0 && s >= 2 && pfresh == 0 && qfresh == 0 && !pc.split && pc.k == qc.k &&
+            !pc.second && !qc.second && qc.left > 1) {
+          bool ok = true;
+#pragma unroll 1
+          for (; qc.left > 1; s += 2) {
+            ok = wait(SM::B_FULL + pc.slot, pc.phase) && wait(SM::B_FULL + qc.slot, qc.phase);
+            if (!ok) break;
+            const uint32_t fv = slot_flags[pc.slot], fk = slot_flags[qc.slot];
+            if (!(ok = wait(SM::B_P + 0, (s >> 1) - 1))) break;
+            tc_fence_after();
+            pv(0, pc.slot, fv);
+            qk(0, qc.slot, qc.q, fk);
+            if (!(ok = wait(SM::B_P + 1, (s >> 1) - 1))) break;
+            tc_fence_after();
+            pv(1, pc.slot, fv);
+            mma_commit(bar(SM::B_EMPTY + pc.slot));
+            qk(1, qc.slot, qc.q + 1, fk);
+            mma_commit(bar(SM::B_EMPTY + qc.slot));
+            for (Cursor* c : {&pc, &qc}) {
+              c->slot += 2;
+              if (c->slot >= (uint32_t)NS) {
+                c->slot -= NS;
+                c->phase ^= 1;
+              }
+              --c->left;
+            }
+          }
+          if (!ok) break;
+        }
         if (s >= 2) {
           const bool last = pc.left <= (pc.split ? 2 : 1);
           if (pfresh > 0) {
@@ -367,26 +432,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
           if (!wait(SM::B_P + half, (s >> 1) - 1)) break;
           if (!pc.second && !wait(SM::B_FULL + pc.slot, pc.phase)) break;
           tc_fence_after();
-          const uint64_t vd = vdesc + (uint64_t)(pc.slot * (kTile >> 4));
-          const uint32_t flags = slot_flags[pc.slot];
-          if (flags >> (8 + half) & 1u) {
-            uint32_t acc = begun >> half & 1u;
-            begun |= 1u << half;
-            if ((flags & 0xffu) == 0xffu) {
-#pragma unroll
-              for (int k = 0; k < BN / 16; ++k)
-                mma_bf16_ts(tmem + tm_o(half), tmem + tm_s(half) + k * 8, vd + k * 128, idesc_pv,
-                            k > 0 ? 1u : acc);
-            } else {
-#pragma unroll 1
-              for (int k = 0; k < BN / 16; ++k)
-                if (flags >> k & 1u) {
-                  mma_bf16_ts(tmem + tm_o(half), tmem + tm_s(half) + k * 8, vd + k * 128,
-                              idesc_pv, acc);
-                  acc = 1u;
-                }
-            }
-          }
+          pv(half, pc.slot, slot_flags[pc.slot]);
           if (pc.split || pc.second) mma_commit(bar(SM::B_EMPTY + pc.slot));
           if (last) mma_commit(bar(SM::B_O + half));
           const int at = pc.k;
@@ -405,16 +451,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
           }
           if (!qc.second && !wait(SM::B_FULL + qc.slot, qc.phase)) break;
           tc_fence_after();
-          if (slot_flags[qc.slot] >> (8 + half) & 1u) {
-            const uint64_t kd = kdesc + (uint64_t)(qc.slot * (kTile >> 4));
-            const uint64_t qd = qdesc + (uint64_t)((qt % NQ) * (kTile >> 4));
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = ((k >> 2) * kSub + (k & 3) * 32) >> 4;
-              mma_bf16_ss(tmem + tm_s(half), qd + off, kd + off, idesc_qk, k > 0);
-            }
-          }
-          mma_commit(bar(SM::B_S + half));
+          qk(half, qc.slot, qt, slot_flags[qc.slot]);
           if (qc.split || qc.second) {
             mma_commit(bar(SM::B_EMPTY + qc.slot));
             if (qc.left == 1) {
