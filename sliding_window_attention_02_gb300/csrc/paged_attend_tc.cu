@@ -76,8 +76,9 @@ struct Smem {
   static constexpr int B_QF = B_EMPTY + NS;        // NQ query tiles landed
   static constexpr int B_QE = B_QF + NQ;           // and free
   static constexpr int B_S = B_QE + NQ;            // 2 halves: S ready
-  static constexpr int B_P = B_S + 2;              // 2 halves: P written
-  static constexpr int B_O = B_P + 2;              // 2 halves: the segment's last PV done
+  static constexpr int B_P = B_S + 2;              // 2 halves: P of the first 64 keys written
+  static constexpr int B_P2 = B_P + 2;             // and of the others
+  static constexpr int B_O = B_P2 + 2;             // 2 halves: the segment's last PV done
   static constexpr int B_F = B_O + 2;              // the segment's O read out
   static constexpr int B_ML = B_F + 1;             // split: both halves' (m, l) in smem
   static constexpr int B_FIN = B_ML + 1;
@@ -186,6 +187,20 @@ __device__ __forceinline__ void landed32(uint32_t* r) {
                  "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 
+// One lane of a converged warp.  The compiler knows that a single thread runs what
+// depends on it, and keeps descriptors in uniform registers: an MMA takes about 20
+// cycles to issue so, 70 where a comparison of lane numbers chooses the thread (40
+// pages chunk 155 -> 147 us).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t on;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(on));
+  return on != 0;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -217,7 +232,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
 
   if (threadIdx.x == 0) {
     for (int k = 0; k < NBAR; ++k)
-      mbar_init(bar(k), k == SM::B_P || k == SM::B_P + 1 ? 128u
+      mbar_init(bar(k), k >= SM::B_P && k < SM::B_O ? 128u
                         : (k == SM::B_F || k == SM::B_ML || k == SM::B_CUT ||
                            (k >= SM::B_SFREE && k < SM::B_SFREE + NSEG))
                             ? 256u
@@ -308,7 +323,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     // One lane issues.  Step s: PV of step s - 2, then QK of step s, both of half
     // s & 1.  What the lane does between the products holds the tensor core up, so
     // descriptors advance by constants and the rare paths are out of line.
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idesc_qk = idesc_bf16(BM, BN, false);
       constexpr uint32_t idesc_pv = idesc_bf16(BM, D, true);
       auto wait = [&](int k, uint32_t phase) {
@@ -356,25 +371,34 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       const uint64_t vdesc = desc_sw128(sb + SM::OFF_RING, kSub, 1024);
       uint32_t begun = 0;                // halves whose O holds a product of the segment
       // O_h (+)= P_h V, of the steps that hold keys; S_h = Q_h K^T.
-      auto pv = [&](uint32_t half, uint32_t slot, uint32_t flags) {
-        if (!(flags >> (8 + half) & 1u)) return;
+      // pv waits for the two parts of P in turn; false: the wait gave up.
+      auto pv = [&](uint32_t half, uint32_t slot, uint32_t flags, uint32_t phase) {
         const uint64_t vd = vdesc + (uint64_t)(slot * (kTile >> 4));
-        uint32_t acc = begun >> half & 1u;
-        begun |= 1u << half;
-        if ((flags & 0xffu) == 0xffu) {
+        const bool used = flags >> (8 + half) & 1u;
 #pragma unroll
-          for (int k = 0; k < BN / 16; ++k)
-            mma_bf16_ts(tmem + tm_o(half), tmem + tm_s(half) + k * 8, vd + k * 128, idesc_pv,
-                        k > 0 ? 1u : acc);
-        } else {
-#pragma unroll 1
-          for (int k = 0; k < BN / 16; ++k)
-            if (flags >> k & 1u) {
+        for (int part = 0; part < 2; ++part) {
+          if (!wait((part ? SM::B_P2 : SM::B_P) + half, phase)) return false;
+          tc_fence_after();
+          if (!used) continue;
+          uint32_t acc = begun >> half & 1u;
+          if ((flags & 0xffu) == 0xffu) {
+            begun |= 1u << half;
+#pragma unroll
+            for (int k = 4 * part; k < 4 * part + 4; ++k)
               mma_bf16_ts(tmem + tm_o(half), tmem + tm_s(half) + k * 8, vd + k * 128, idesc_pv,
-                          acc);
-              acc = 1u;
-            }
+                          k > 0 ? 1u : acc);
+          } else {
+#pragma unroll 1
+            for (int k = 4 * part; k < 4 * part + 4; ++k)
+              if (flags >> k & 1u) {
+                mma_bf16_ts(tmem + tm_o(half), tmem + tm_s(half) + k * 8, vd + k * 128, idesc_pv,
+                            acc);
+                acc = 1u;
+                begun |= 1u << half;
+              }
+          }
         }
+        return true;
       };
       auto qk = [&](uint32_t half, uint32_t slot, uint32_t qt, uint32_t flags) {
         if (flags >> (8 + half) & 1u) {
@@ -402,13 +426,9 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
             ok = wait(SM::B_FULL + pc.slot, pc.phase) && wait(SM::B_FULL + qc.slot, qc.phase);
             if (!ok) break;
             const uint32_t fv = slot_flags[pc.slot], fk = slot_flags[qc.slot];
-            if (!(ok = wait(SM::B_P + 0, (s >> 1) - 1))) break;
-            tc_fence_after();
-            pv(0, pc.slot, fv);
+            if (!(ok = pv(0, pc.slot, fv, (s >> 1) - 1))) break;
             qk(0, qc.slot, qc.q, fk);
-            if (!(ok = wait(SM::B_P + 1, (s >> 1) - 1))) break;
-            tc_fence_after();
-            pv(1, pc.slot, fv);
+            if (!(ok = pv(1, pc.slot, fv, (s >> 1) - 1))) break;
             mma_commit(bar(SM::B_EMPTY + pc.slot));
             qk(1, qc.slot, qc.q + 1, fk);
             mma_commit(bar(SM::B_EMPTY + qc.slot));
@@ -429,10 +449,8 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
             --pfresh;
             if (pc.k > 0 && !wait(SM::B_F, pc.k - 1)) break;
           }
-          if (!wait(SM::B_P + half, (s >> 1) - 1)) break;
           if (!pc.second && !wait(SM::B_FULL + pc.slot, pc.phase)) break;
-          tc_fence_after();
-          pv(half, pc.slot, slot_flags[pc.slot]);
+          if (!pv(half, pc.slot, slot_flags[pc.slot], (s >> 1) - 1)) break;
           if (pc.split || pc.second) mma_commit(bar(SM::B_EMPTY + pc.slot));
           if (last) mma_commit(bar(SM::B_O + half));
           const int at = pc.k;
@@ -588,6 +606,32 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         }
         ++turns;
         tc_fence_after();
+        // Value rows that no row of the unit sees, in steps that hold others that one
+        // does (where the prefix ends, the window begins and the chunk ends): zero,
+        // as 0 x NaN is NaN.
+        const int p = w.hull.p, w0 = w.hull.w0, end = w.hull.end;
+        auto edge = [&](int e) { return (e & 15) != 0 && e >> 7 == x0 >> 7; };
+        if ((warp & 3) == 0 && ((p < w0 && (edge(p) || edge(w0))) || edge(end))) {
+          const uint32_t vi = 2u * (uint32_t)(w.tiles + j - w.j0) + 1u;
+          if (__all_sync(0xffffffffu, wait_for(bar(SM::B_FULL + vi % NS), (vi / NS) & 1,
+                                                abort_flag, wait_ns))) {
+#pragma unroll 1
+            for (int z = 0; z < 3; ++z) {
+              const int e = z == 0 ? p : z == 1 ? w0 : end;
+              if (!edge(e) || (z < 2 && p >= w0)) continue;
+              const int t = e & ~15;                     // the step's first token
+              uint8_t* v = smem + SM::OFF_RING + (vi % NS) * kTile + (t - x0) * 128 + lane * 16;
+#pragma unroll
+              for (int y = 0; y < 16; y += 4)            // a row is 8 lanes
+                if (!w.hull.has(t + y + (lane >> 3))) {
+#pragma unroll
+                  for (int c = 0; c < NSUB; ++c)
+                    *reinterpret_cast<uint4*>(v + y * 128 + c * kSub) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            fence_proxy_async_smem();
+          }
+        }
         const bool used = own_hull.meets(x0, x0 + BN);
         if (any && used) {
           uint32_t x[128];
@@ -653,6 +697,11 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
               p[e] = pack_bf16(p0, p1);
             }
             tmem_st16(s_addr + 16 * c, p);
+            if (c == 1) {                                // the product may begin
+              tmem_wait_st();
+              tc_fence_before();
+              mbar_arrive(bar(SM::B_P + half));
+            }
           }
           float s0, s1, s2, s3;
           f2_unpack(ps[0], s0, s1);
@@ -660,35 +709,11 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
           l_run += (s0 + s1) + (s2 + s3);
           tmem_wait_st();
           tc_fence_before();
+        } else {
+          mbar_arrive(bar(SM::B_P + half));
         }
         started = started || used;
-        // Value rows that no row of the unit sees, in steps that hold others that one
-        // does (where the prefix ends, the window begins and the chunk ends): zero,
-        // as 0 x NaN is NaN.
-        const int p = w.hull.p, w0 = w.hull.w0, end = w.hull.end;
-        auto edge = [&](int e) { return (e & 15) != 0 && e >> 7 == x0 >> 7; };
-        if ((warp & 3) == 0 && ((p < w0 && (edge(p) || edge(w0))) || edge(end))) {
-          const uint32_t vi = 2u * (uint32_t)(w.tiles + j - w.j0) + 1u;
-          if (__all_sync(0xffffffffu, wait_for(bar(SM::B_FULL + vi % NS), (vi / NS) & 1,
-                                                abort_flag, wait_ns))) {
-#pragma unroll 1
-            for (int z = 0; z < 3; ++z) {
-              const int e = z == 0 ? p : z == 1 ? w0 : end;
-              if (!edge(e) || (z < 2 && p >= w0)) continue;
-              const int t = e & ~15;                     // the step's first token
-              uint8_t* v = smem + SM::OFF_RING + (vi % NS) * kTile + (t - x0) * 128 + lane * 16;
-#pragma unroll
-              for (int y = 0; y < 16; y += 4)            // a row is 8 lanes
-                if (!w.hull.has(t + y + (lane >> 3))) {
-#pragma unroll
-                  for (int c = 0; c < NSUB; ++c)
-                    *reinterpret_cast<uint4*>(v + y * 128 + c * kSub) = make_uint4(0, 0, 0, 0);
-                }
-            }
-            fence_proxy_async_smem();
-          }
-        }
-        mbar_arrive(bar(SM::B_P + half));
+        mbar_arrive(bar(SM::B_P2 + half));
       }
       // ------------------------------------------------------- epilogue
       // Steps of this half and of the other in this segment.
