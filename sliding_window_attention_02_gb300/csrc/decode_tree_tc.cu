@@ -134,12 +134,6 @@ constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr int kUnitCost = 3, kPairUnitCost = 2, kMinCost = 4;
 static_assert(kMinCost >= 1 + kUnitCost && kUnitCost >= kPairUnitCost, "a share holds a tile");
 
-__device__ __forceinline__ int load_acquire(const int32_t* p) {
-  int v;
-  asm volatile("ld.acquire.gpu.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
-
 // The shape of a launch.
 struct Shape {
   int npt;      // nodes of a query tile

@@ -95,60 +95,120 @@ struct PagedUnit {
 };
 
 // The planner, run by one whole warp with the same state in every lane.  The
-// tiles of a unit after each other, unit after unit (a sequence's units KV head
-// by KV head), form one list; every tile costs 1, a unit's first one EXTRA more.
-// CTA c of `ctas` takes the tiles that begin in [from(c), from(c + 1)).
+// tiles of a unit after each other, unit after unit (sequence by sequence, its rows
+// in order, the KV heads of the same rows next to each other), form one list; every
+// tile costs 1, a unit's first one EXTRA more.  CTA c of `ctas` takes the tiles that
+// begin in [from(c), from(c + 1)).
+//
+// A group, the units of the same rows, is one entry of the sums that find a CTA's
+// range: 32 groups at a time, a lane each.  What a launch waits for before its first
+// loads is this code, run once: it is kept short (40 pages, one sequence of 16
+// groups: 2.7 us; with sums sequence by sequence and 64-bit divisions 4 to 5).
 template <int TILE, bool ALIGNED, int EXTRA, int MINCOST>
 struct PagedPlan {
   static_assert(MINCOST >= 1 + EXTRA, "a range holds a tile at least");
   using Tiles = HullTiles<TILE, ALIGNED>;
   const PagesView& pv;
   const BatchArgs& ba;
-  int unit_rows, G, n, lane;
+  int unit_rows, lane;
   int64_t total = 0, x1 = 0;
   int ctas = 1;
   PagedUnit u;
   int64_t ubase = 0;
-  int nq = 0;
 
   __device__ __forceinline__ PagedPlan(const PagesView& pv_, const BatchArgs& ba_, int rows)
-      : pv(pv_), ba(ba_), unit_rows(rows), G(pv_.G), n(ba_.window),
-        lane((int)(threadIdx.x & 31)) {}
+      : pv(pv_), ba(ba_), unit_rows(rows), lane((int)(threadIdx.x & 31)) {}
 
-  __device__ __forceinline__ Hull hull_of(const PagedSeq& s, int f0) const {
-    const int f1 = min(f0 + unit_rows, s.T * G) - 1;
-    const int a = s.L - s.T;
-    return Hull(a + f0 / G, a + f1 / G, s.m, n);
-  }
-  __device__ __forceinline__ int units_of(const PagedSeq& s) const {
-    return (s.T * G + unit_rows - 1) / unit_rows;
-  }
-  __device__ __forceinline__ int cost(const PagedSeq& s, int q) const {
-    return Tiles(hull_of(s, q * unit_rows)).nt + EXTRA;
-  }
-
-  // Cost of the units of one KV head, for the sequences of the warp's lanes:
-  // short chunks by their lane, long ones by the warp together.
-  __device__ int64_t costs(const PagedSeq& s) const {
-    const int mine = units_of(s);
-    int64_t c = 0;
-    if (mine <= 2)
-      for (int q = 0; q < mine; ++q) c += cost(s, q);
-    for (uint32_t more = __ballot_sync(0xffffffffu, mine > 2); more; more &= more - 1) {
-      const int src = __ffs(more) - 1;
-      PagedSeq x;
-      x.row0 = 0;
-      x.T = __shfl_sync(0xffffffffu, s.T, src);
-      x.L = __shfl_sync(0xffffffffu, s.L, src);
-      x.m = __shfl_sync(0xffffffffu, s.m, src);
-      const int nx = __shfl_sync(0xffffffffu, mine, src);
-      int64_t part = 0;
-      for (int q = lane; q < nx; q += 32) part += cost(x, q);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
-      if (lane == src) c = part;
+  // Finds the start of this CTA's range; false: it has none.
+  __device__ bool start(int cta, int grid) {
+    PagedSeq s = lane_seq(lane);
+    int inc = 0;                                 // groups of the block's sequences up to a lane's
+    int64_t groups = 0;
+    int64_t c0 = 0, c1 = 0;                      // inclusive costs of the first 64 groups
+    for (int b0 = 0; b0 < ba.B; b0 += 32) {
+      if (b0 > 0) s = lane_seq(b0 + lane);
+      inc = scan(groups_of(s));
+      const int count = __shfl_sync(0xffffffffu, inc, 31);
+      for (int g0 = 0; g0 < count; g0 += 32) {
+        const int64_t c = scan(group_cost(s, inc, count, g0));
+        if (b0 == 0 && g0 == 0) c0 = c;
+        if (b0 == 0 && g0 == 32) c1 = c;
+        total += __shfl_sync(0xffffffffu, c, 31);
+      }
+      groups += count;
     }
-    return c;
+    if (total == 0) return false;
+    const int64_t units = groups * pv.Hkv;
+    ctas = (int)min((int64_t)grid, max((int64_t)1, total / MINCOST));
+    // Few units have the same number of CTAs each, if they are alike: their ends
+    // meet CTAs' ends.
+    if (units < ctas) ctas -= ctas % (int)units;
+    if (cta >= ctas) return false;
+    const int64_t x0 = from(cta);
+    x1 = from(cta + 1);
+    int64_t base = 0;
+    for (int b0 = 0;; b0 += 32) {
+      if (ba.B > 32) {
+        s = lane_seq(b0 + lane);
+        inc = scan(groups_of(s));
+      }
+      const int count = __shfl_sync(0xffffffffu, inc, 31);
+      for (int g0 = 0; g0 < count; g0 += 32) {
+        const bool known = b0 == 0 && g0 < 64;
+        const int64_t c = known ? (g0 == 0 ? c0 : c1) : scan(group_cost(s, inc, count, g0));
+        const uint32_t up = __ballot_sync(0xffffffffu, base + c <= x0);   // groups before
+        if (up == 0xffffffffu) {
+          base += __shfl_sync(0xffffffffu, c, 31);
+          continue;
+        }
+        const int at = __popc(up);
+        if (at > 0) base += __shfl_sync(0xffffffffu, c, at - 1);
+        // its sequence, and its place there
+        const int g = g0 + at;
+        const int src = __popc(__ballot_sync(0xffffffffu, inc <= g));
+        take(s, b0, src);
+        const int before = src > 0 ? __shfl_sync(0xffffffffu, inc, src - 1) : 0;
+        enter(g - before);
+        u.kvh = div(x0 - base, u.nt + EXTRA);
+        ubase = base + (int64_t)u.kvh * (u.nt + EXTRA);
+        u.j0 = at_cost(x0 - ubase);
+        return u.j0 < u.nt ? clip() : next();
+      }
+    }
+  }
+
+  // The next unit of the range; false: there is none.
+  __device__ bool next() {
+    ubase += u.nt + EXTRA;
+    if (ubase >= x1) return false;
+    u.j0 = 0;
+    if (++u.kvh == pv.Hkv) {
+      u.kvh = 0;
+      int q = u.f0 / unit_rows + 1;
+      if (q * unit_rows >= u.seq.T * pv.G) {
+        q = 0;
+        // sequences without rows are passed over; there is one with some, as the
+        // list goes on
+        for (int b0 = u.b + 1; b0 < ba.B; b0 += 32) {
+          const PagedSeq s = lane_seq(b0 + lane);
+          const uint32_t live = __ballot_sync(0xffffffffu, s.T > 0);
+          if (!live) continue;
+          take(s, b0, __ffs(live) - 1);
+          break;
+        }
+      }
+      enter(q);
+    }
+    return clip();
+  }
+
+ private:
+  __device__ __forceinline__ int groups_of(const PagedSeq& s) const {
+    return (s.T * pv.G + unit_rows - 1) / unit_rows;
+  }
+  __device__ __forceinline__ Hull hull_of(int T, int L, int m, int f0) const {
+    const int f1 = min(f0 + unit_rows, T * pv.G) - 1;
+    return Hull(L - T + f0 / pv.G, L - T + f1 / pv.G, m, ba.window);
   }
   __device__ __forceinline__ PagedSeq lane_seq(int b) const {
     PagedSeq s;
@@ -158,143 +218,66 @@ struct PagedPlan {
       s.row0 = s.T = s.L = s.m = 0;
     return s;
   }
-  __device__ __forceinline__ int64_t scan(int64_t x) const {
+  template <typename X>
+  __device__ __forceinline__ X scan(X x) const {
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+      const X y = __shfl_up_sync(0xffffffffu, x, off);
       if (lane >= off) x += y;
     }
     return x;
+  }
+  // Cost of this lane's group g0 + lane of the block's `count`; inc: the groups of
+  // the sequences of the lanes up to each.
+  __device__ __forceinline__ int64_t group_cost(const PagedSeq& s, int inc, int count,
+                                                int g0) const {
+    const int g = g0 + lane;
+    int src = 0;                                 // sequences that end at or before g
+#pragma unroll
+    for (int step = 16; step > 0; step >>= 1) {
+      const int e = __shfl_sync(0xffffffffu, inc, src + step - 1);
+      if (e <= g) src += step;
+    }
+    src = min(src, 31);
+    const int e = __shfl_sync(0xffffffffu, inc, src);
+    const int T = __shfl_sync(0xffffffffu, s.T, src);
+    const int L = __shfl_sync(0xffffffffu, s.L, src);
+    const int m = __shfl_sync(0xffffffffu, s.m, src);
+    if (g >= count) return 0;
+    const int q = g - (e - (T * pv.G + unit_rows - 1) / unit_rows);
+    return (int64_t)(Tiles(hull_of(T, L, m, q * unit_rows)).nt + EXTRA) * pv.Hkv;
+  }
+  __device__ __forceinline__ void take(const PagedSeq& s, int b0, int src) {
+    u.b = b0 + src;
+    u.seq.row0 = __shfl_sync(0xffffffffu, s.row0, src);
+    u.seq.T = __shfl_sync(0xffffffffu, s.T, src);
+    u.seq.L = __shfl_sync(0xffffffffu, s.L, src);
+    u.seq.m = __shfl_sync(0xffffffffu, s.m, src);
+  }
+  __device__ __forceinline__ void enter(int q) {
+    u.f0 = q * unit_rows;
+    u.hull = hull_of(u.seq.T, u.seq.L, u.seq.m, u.f0);
+    const Tiles t(u.hull);
+    u.np = t.np;
+    u.kb = t.kb;
+    u.nt = t.nt;
+  }
+  static __device__ __forceinline__ int div(int64_t a, int64_t b) {
+    return (int)((a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b));
   }
   __device__ __forceinline__ int64_t from(int c) const {
     const int64_t p = total * c;
     return p >> 32 ? p / ctas : (int64_t)((uint32_t)p / (uint32_t)ctas);
   }
   // The last CTA whose range begins at or before cost x.
-  __device__ __forceinline__ int owner(int64_t x) const {
-    const int64_t p = (x + 1) * ctas - 1;
-    return (int)((p | total) >> 32 ? p / total : (int64_t)((uint32_t)p / (uint32_t)total));
-  }
-
-  // Finds the start of this CTA's range; false: it has none.
-  __device__ bool start(int cta, int grid) {
-    PagedSeq s0;
-    int64_t c0 = 0, inc0 = 0;                    // of the first 32 sequences
-    int64_t units = 0;
-    for (int b0 = 0; b0 < ba.B; b0 += 32) {
-      const PagedSeq s = lane_seq(b0 + lane);
-      const int64_t c = costs(s) * pv.Hkv;
-      const int64_t inc = scan(c);
-      if (b0 == 0) {
-        s0 = s;
-        c0 = c;
-        inc0 = inc;
-      }
-      total += __shfl_sync(0xffffffffu, inc, 31);
-      units += __reduce_add_sync(0xffffffffu, units_of(s)) * (int64_t)pv.Hkv;
-    }
-    if (total == 0) return false;
-    ctas = (int)min((int64_t)grid, max((int64_t)1, total / MINCOST));
-    // Few units have the same number of CTAs each, if they are alike: their ends
-    // meet CTAs' ends.
-    if (units < ctas) ctas -= ctas % (int)units;
-    if (cta >= ctas) return false;
-    const int64_t x0 = from(cta);
-    x1 = from(cta + 1);
-    int64_t base = 0;
-    int b = 0;
-    for (int b0 = 0;; b0 += 32) {
-      if (b0 > 0) {
-        s0 = lane_seq(b0 + lane);
-        c0 = costs(s0) * pv.Hkv;
-        inc0 = scan(c0);
-      }
-      const uint32_t here =
-          __ballot_sync(0xffffffffu, base + inc0 - c0 <= x0 && x0 < base + inc0);
-      if (here) {
-        const int src = __ffs(here) - 1;
-        b = b0 + src;
-        base += __shfl_sync(0xffffffffu, inc0 - c0, src);
-        u.seq.row0 = __shfl_sync(0xffffffffu, s0.row0, src);
-        u.seq.T = __shfl_sync(0xffffffffu, s0.T, src);
-        u.seq.L = __shfl_sync(0xffffffffu, s0.L, src);
-        u.seq.m = __shfl_sync(0xffffffffu, s0.m, src);
-        c0 = __shfl_sync(0xffffffffu, c0, src);
-        break;
-      }
-      base += __shfl_sync(0xffffffffu, inc0, 31);
-    }
-    u.b = b;
-    nq = units_of(u.seq);
-    const int64_t per = c0 / pv.Hkv;             // of one KV head
-    u.kvh = (int)((x0 - base) / per);
-    base += u.kvh * per;
-    for (int q0 = 0;; q0 += 32) {
-      const int64_t c = q0 + lane < nq ? cost(u.seq, q0 + lane) : 0;
-      const int64_t inc = scan(c);
-      const uint32_t here = __ballot_sync(0xffffffffu, base + inc - c <= x0 && x0 < base + inc);
-      if (here) {
-        const int src = __ffs(here) - 1;
-        base += __shfl_sync(0xffffffffu, inc - c, src);
-        enter(q0 + src, base);
-        break;
-      }
-      base += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    u.j0 = at(x0 - ubase);
-    return u.j0 < u.nt ? clip() : next();
-  }
-
-  // The next unit of the range; false: there is none.
-  __device__ bool next() {
-    const int64_t end = ubase + u.nt + EXTRA;
-    int q = u.f0 / unit_rows + 1;
-    if (q == nq) {
-      q = 0;
-      if (++u.kvh == pv.Hkv) {
-        u.kvh = 0;
-        uint32_t live = 0;
-        PagedSeq s;
-        int b0 = u.b + 1;
-        for (; b0 < ba.B; b0 += 32) {            // sequences without rows are passed over
-          s = lane_seq(b0 + lane);
-          live = __ballot_sync(0xffffffffu, s.T > 0);
-          if (live) break;
-        }
-        if (!live) return false;
-        const int src = __ffs(live) - 1;
-        u.b = b0 + src;
-        u.seq.row0 = __shfl_sync(0xffffffffu, s.row0, src);
-        u.seq.T = __shfl_sync(0xffffffffu, s.T, src);
-        u.seq.L = __shfl_sync(0xffffffffu, s.L, src);
-        u.seq.m = __shfl_sync(0xffffffffu, s.m, src);
-        nq = units_of(u.seq);
-      }
-    }
-    if (end >= x1) return false;
-    enter(q, end);
-    u.j0 = 0;
-    return clip();
-  }
-
- private:
-  __device__ __forceinline__ void enter(int q, int64_t base) {
-    u.f0 = q * unit_rows;
-    u.hull = hull_of(u.seq, u.f0);
-    const Tiles t(u.hull);
-    u.np = t.np;
-    u.kb = t.kb;
-    u.nt = t.nt;
-    ubase = base;
-  }
-  // The first tile that begins at or after cost x of the unit.
-  __device__ __forceinline__ int at(int64_t x) const {
+  __device__ __forceinline__ int owner(int64_t x) const { return div((x + 1) * ctas - 1, total); }
+  // The unit's first tile that begins at or after cost x of it.
+  __device__ __forceinline__ int at_cost(int64_t x) const {
     return x <= 0 ? 0 : (int)min(max(x - EXTRA, (int64_t)1), (int64_t)u.nt);
   }
   __device__ __forceinline__ bool clip() {
-    const int64_t b0 = ubase + (u.j0 > 0 ? u.j0 + EXTRA : 0);
-    if (b0 >= x1) return false;
-    u.j1 = at(x1 - ubase);
+    if (ubase + (u.j0 > 0 ? u.j0 + EXTRA : 0) >= x1) return false;
+    u.j1 = at_cost(x1 - ubase);
     u.first = u.last = 0;
     if (!u.whole()) {
       u.first = owner(ubase);

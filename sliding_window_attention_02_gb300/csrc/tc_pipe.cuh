@@ -49,6 +49,12 @@ __device__ __forceinline__ bool wait_for(uint32_t b, uint32_t phase, volatile in
   return mbar_try_wait(b, phase) || wait_on(b, phase, abort_flag, ns);
 }
 
+__device__ __forceinline__ int load_acquire(const int32_t* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // Bits e of word c (columns 32 c + e) with lo <= column <= hi.
 __device__ __forceinline__ uint32_t range_mask(int lo, int hi, int c) {
   const int a = max(lo - 32 * c, 0), b = min(hi - 32 * c, 31);
