@@ -255,18 +255,30 @@ cudaError_t launch_d(const PagesView& pv, const BatchArgs& ba, const AttendArgs&
 
 }  // namespace
 
-static bool use_tc(const PagesView& pv, int64_t rows, int batch) {
-  return paged_attend_tc_supported(pv) && rows > batch;
+// How a call is served.
+enum class Path { kCudaCores, kFewRows, kTiles };
+static Path path_of(const PagesView& pv, int64_t rows, int64_t batch, int64_t keys) {
+  if (!paged_attend_tc_supported(pv)) return Path::kCudaCores;
+  if (rows * pv.G <= 16 * batch) return Path::kFewRows;
+  return Path::kTiles;
 }
 
 size_t paged_attend_workspace(const PagesView& pv, int64_t rows, int batch) {
-  const size_t own = kPagedCounterBytes + (size_t)grid_of(pv) * 2 * 4 * (pv.d + 2) * sizeof(float);
-  return use_tc(pv, rows, batch) ? std::max(own, paged_attend_tc_workspace(pv)) : own;
+  size_t need = kPagedCounterBytes + (size_t)grid_of(pv) * 2 * 4 * (pv.d + 2) * sizeof(float);
+  if (paged_attend_tc_supported(pv)) {
+    need = std::max(need, paged_decode_tc_workspace(pv));
+    if (rows * pv.G > 16 * (int64_t)batch) need = std::max(need, paged_attend_tc_workspace(pv));
+  }
+  return need;
 }
 
 cudaError_t launch_paged_attend(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
                                 const AttendArgs& a, cudaStream_t s) {
-  if (use_tc(pv, ba.rows, ba.B)) return launch_paged_attend_tc(pv, maps, ba, a, s);
+  switch (path_of(pv, ba.rows, ba.B, ba.cap)) {
+    case Path::kTiles: return launch_paged_attend_tc(pv, maps, ba, a, s);
+    case Path::kFewRows: return launch_paged_decode_tc(pv, maps, ba, a, s);
+    default: break;
+  }
   if (pv.dtype == RSWA_F32)
     return pv.d == 64 ? launch_d<float, 64>(pv, ba, a, s) : launch_d<float, 128>(pv, ba, a, s);
   return pv.d == 64 ? launch_d<__nv_bfloat16, 64>(pv, ba, a, s)

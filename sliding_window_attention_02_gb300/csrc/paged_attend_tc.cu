@@ -187,20 +187,6 @@ __device__ __forceinline__ void landed32(uint32_t* r) {
                  "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 
-// One lane of a converged warp.  The compiler knows that a single thread runs what
-// depends on it, and keeps descriptors in uniform registers: an MMA takes about 20
-// cycles to issue so, 70 where a comparison of lane numbers chooses the thread (40
-// pages chunk 155 -> 147 us).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t on;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.b32 %0, 1, 0, p;\n\t}"
-      : "=r"(on));
-  return on != 0;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,

@@ -242,6 +242,10 @@ bool paged_attend_tc_supported(const PagesView& pv);
 size_t paged_attend_tc_workspace(const PagesView& pv);
 cudaError_t launch_paged_attend_tc(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
                                    const AttendArgs& a, cudaStream_t s);
+// Units of at most 16 rows (paged_decode_tc.cu).
+size_t paged_decode_tc_workspace(const PagesView& pv);
+cudaError_t launch_paged_decode_tc(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
+                                   const AttendArgs& a, cudaStream_t s);
 cudaError_t launch_paged_weigh(const PagesView& pv, const BatchArgs& ba, const void* q,
                                int64_t q_stride, const float* lse, float* weights, float decay,
                                cudaStream_t s);
