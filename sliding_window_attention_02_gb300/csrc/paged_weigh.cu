@@ -103,9 +103,11 @@ cudaError_t launch_d(const PagesView& pv, const BatchArgs& ba, const void* q, in
 
 }  // namespace
 
-cudaError_t launch_paged_weigh(const PagesView& pv, const BatchArgs& ba, const void* q,
-                               int64_t q_stride, const float* lse, float* weights, float decay,
-                               cudaStream_t s) {
+cudaError_t launch_paged_weigh(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
+                               const void* q, int64_t q_stride, const float* lse, float* weights,
+                               float decay, cudaStream_t s) {
+  if (paged_weigh_tc_supported(pv))
+    return launch_paged_weigh_tc(pv, maps, ba, q, q_stride, lse, weights, decay, s);
   if (pv.dtype == RSWA_F32)
     return pv.d == 64 ? launch_d<float, 64>(pv, ba, q, q_stride, lse, weights, decay, s)
                       : launch_d<float, 128>(pv, ba, q, q_stride, lse, weights, decay, s);

@@ -259,7 +259,7 @@ int rswa_pages_weigh(rswa_pages* pages, const rswa_batch* batch, int64_t rows, c
   if (injected_failure()) return RSWA_ECUDA;
   DeviceGuard g(pages->device);
   if (!g.ok) return RSWA_ECUDA;
-  return status_of(launch_paged_weigh(pv, ba, q, q_stride, lse, weights, decay,
+  return status_of(launch_paged_weigh(pv, pages->maps, ba, q, q_stride, lse, weights, decay,
                                       static_cast<cudaStream_t>(stream)));
 }
 

@@ -246,9 +246,14 @@ cudaError_t launch_paged_attend_tc(const PagesView& pv, const PagesMaps& maps, c
 size_t paged_decode_tc_workspace(const PagesView& pv);
 cudaError_t launch_paged_decode_tc(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
                                    const AttendArgs& a, cudaStream_t s);
-cudaError_t launch_paged_weigh(const PagesView& pv, const BatchArgs& ba, const void* q,
-                               int64_t q_stride, const float* lse, float* weights, float decay,
-                               cudaStream_t s);
+cudaError_t launch_paged_weigh(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
+                               const void* q, int64_t q_stride, const float* lse, float* weights,
+                               float decay, cudaStream_t s);
+// On the tensor cores (paged_weigh_tc.cu): bf16, at most 64 query heads per KV head.
+bool paged_weigh_tc_supported(const PagesView& pv);
+cudaError_t launch_paged_weigh_tc(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
+                                  const void* q, int64_t q_stride, const float* lse,
+                                  float* weights, float decay, cudaStream_t s);
 struct EvictArgs {
   const float* weights;
   float* weights_out;
