@@ -82,20 +82,26 @@ paged_attend_kernel(PagesView pv, BatchArgs ba, AttendArgs a) {
     SoftmaxState<EPL> st[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) st[r].init();
+    bool bad = false;                          // a page outside the pool
     for (int base = x0 + warp * C::KEYS_WARP; base < x1; base += kWarps * C::KEYS_WARP) {
       uint4 kr[U], vr[U];
-      int t[U];
+      int t[U], page[U];
+      // the pages first, then the rows: reads that do not wait for one another
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const int x = base + i * KPW + grp;
         const int y = x < x1 ? x : x0;         // any key of the part
-        const int tk = y < hull.p ? y : y + skip;
-        const size_t at =
-            (((size_t)page_at(pv, ba, b, tk >> pv.log2P) * pv.Hkv + kvh) * pv.P +
-             (tk & (pv.P - 1))) * D + col;
+        t[i] = y < hull.p ? y : y + skip;
+        page[i] = ba.table[(size_t)b * ba.max_pages + (t[i] >> pv.log2P)];
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        bad |= (unsigned)page[i] >= (unsigned)pv.pages;
+        if ((unsigned)page[i] >= (unsigned)pv.pages) page[i] = 0;
+        const size_t at = (((size_t)page[i] * pv.Hkv + kvh) * pv.P + (t[i] & (pv.P - 1))) * D + col;
         kr[i] = ld_stream16(static_cast<const T*>(pv.K) + at);
         vr[i] = ld_stream16(static_cast<const T*>(pv.V) + at);
-        t[i] = x < x1 ? tk : INT32_MAX;        // not a key: after every token
+        if (base + i * KPW + grp >= x1) t[i] = INT32_MAX;        // not a key: after every token
       }
       float s[R][U];
 #pragma unroll
@@ -158,6 +164,7 @@ paged_attend_kernel(PagesView pv, BatchArgs ba, AttendArgs a) {
         }
       }
     }
+    if (bad) flag_error(pv.err, kErrBadBatch);
     __syncthreads();
     // The CTA's result of row r, column c: over the warps.
     const size_t pf = (size_t)R * (D + 2);
@@ -259,6 +266,8 @@ cudaError_t launch_d(const PagesView& pv, const BatchArgs& ba, const AttendArgs&
 enum class Path { kCudaCores, kFewRows, kTiles };
 static Path path_of(const PagesView& pv, int64_t rows, int64_t batch, int64_t keys) {
   if (!paged_attend_tc_supported(pv)) return Path::kCudaCores;
+  // SMALL
+  if (rows * pv.G * keys <= 8192) return Path::kCudaCores;
   if (rows * pv.G <= 16 * batch) return Path::kFewRows;
   return Path::kTiles;
 }

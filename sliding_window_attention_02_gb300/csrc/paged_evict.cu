@@ -50,8 +50,8 @@ template <bool SMEM>
 __global__ void __launch_bounds__(kSelectThreads)
 evict_select_kernel(PagesView pv, BatchArgs ba, EvictArgs a, int chunks) {
   extern __shared__ uint32_t s_key[];
-  __shared__ uint32_t s_hist[256];
-  __shared__ uint32_t s_prefix, s_need;
+  __shared__ uint32_t s_hist[4][256];
+  __shared__ uint32_t s_prefix, s_need, s_whole;
   __shared__ int s_warp[2][kSelectThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_wait();
@@ -80,22 +80,36 @@ evict_select_kernel(PagesView pv, BatchArgs ba, EvictArgs a, int chunks) {
   auto key = [&](int j) { return SMEM ? s_key[j] : order_key(w[j]); };
   if (SMEM)
     for (int j = lo + tid; j < hi; j += kSelectThreads) s_key[j] = order_key(w[j]);
+  if (tid < 256)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s_hist[i][tid] = 0;
   if (tid == 0) {
     s_prefix = 0;
     s_need = (uint32_t)(a.budget - a.first - a.last);
   }
   __syncthreads();
+  // Tokens with a key above `least` stay, and the first `ties` with that key.
   uint32_t least = 0xffffffffu;                          // no weight has this key
-  int ties = 0;                                          // of the least weight that stay
+  int ties = 0;
   if (s_need > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) s_hist[tid] = 0;
-      __syncthreads();
+    for (int pass = 0;; ++pass) {
+      const int shift = 24 - 8 * pass;
       const uint32_t prefix = s_prefix;
-      for (int j = lo + tid; j < hi; j += kSelectThreads) {
-        const uint32_t x = key(j);
-        if (shift == 24 || (x ^ prefix) >> (shift + 8) == 0)
-          atomicAdd(&s_hist[x >> shift & 255u], 1u);
+      uint32_t* hist = s_hist[pass];
+      for (int j0 = lo; j0 < hi; j0 += kSelectThreads) {
+        const int j = j0 + tid;
+        const uint32_t x = j < hi ? key(j) : 0u;
+        const bool on = j < hi && (pass == 0 || (x ^ prefix) >> (shift + 8) == 0);
+        if (pass < 2) {
+          // Weights share few exponents: the lanes of a warp with one digit are
+          // counted together (10272 tokens: a pass 5 us without, as each lane's add
+          // to the same word takes its turn).
+          const uint32_t digit = on ? x >> shift & 255u : 256u;
+          const uint32_t same = __match_any_sync(0xffffffffu, digit);
+          if (on && (same & ((1u << lane) - 1u)) == 0) atomicAdd(&hist[digit], __popc(same));
+        } else if (on) {
+          atomicAdd(&hist[x >> shift & 255u], 1u);
+        }
       }
       __syncthreads();
       if (warp == 0) {
@@ -103,7 +117,7 @@ evict_select_kernel(PagesView pv, BatchArgs ba, EvictArgs a, int chunks) {
         // has digits 255 - 8 l ... 248 - 8 l
         uint32_t c[8], mine = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mine += c[e] = s_hist[255 - 8 * lane - e];
+        for (int e = 0; e < 8; ++e) mine += c[e] = hist[255 - 8 * lane - e];
         uint32_t inc = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -119,15 +133,24 @@ evict_select_kernel(PagesView pv, BatchArgs ba, EvictArgs a, int chunks) {
             if (above < need && need <= above + c[e]) {
               s_prefix = prefix | (uint32_t)(255 - 8 * lane - e) << shift;
               s_need = need - above;
+              s_whole = need - above == c[e];
             }
             above += c[e];
           }
         }
       }
       __syncthreads();
+      // Every weight with these digits stays: the lower ones need not be known.
+      if (s_whole && s_prefix != 0) {
+        least = s_prefix - 1;
+        break;
+      }
+      if (pass == 3) {
+        least = s_prefix;
+        ties = (int)s_need;
+        break;
+      }
     }
-    least = s_prefix;
-    ties = (int)s_need;
   }
   // Thread t looks through tokens [t * per, (t + 1) * per); an odd number spreads
   // them over the banks.
@@ -159,9 +182,10 @@ evict_select_kernel(PagesView pv, BatchArgs ba, EvictArgs a, int chunks) {
   }
   __syncthreads();
   int na = inc_a - above, ne = inc_e - equal;            // before this thread's tokens
-  for (int x = 0; x < warp; ++x) {
-    na += s_warp[0][x];
-    ne += s_warp[1][x];
+  {
+    int wa = lane < warp ? s_warp[0][lane] : 0, we = lane < warp ? s_warp[1][lane] : 0;
+    na += __reduce_add_sync(0xffffffffu, wa);
+    ne += __reduce_add_sync(0xffffffffu, we);
   }
   for (int j = j0; j < j1; ++j) {
     bool stays = j < lo || j >= hi, tie = false;
@@ -219,18 +243,31 @@ evict_move_kernel(PagesView pv, BatchArgs ba, EvictArgs a, int chunks) {
   const int col = tid % NV, row = r0 + tid / NV;
   const uint4* K = static_cast<const uint4*>(pv.K);
   const uint4* V = static_cast<const uint4*>(pv.V);
+  // In stages, each of reads that do not wait for one another: the kept tokens, the
+  // pages they come from and go to, the rows.
+  int j[N], from[N], to[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) j[e] = kept[min(row + e * PASS, count - 1)];
+  bool bad = false;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    from[e] = ba.table[(size_t)b * ba.max_pages + (j[e] >> pv.log2P)];
+    to[e] = out[(size_t)b * ba.max_pages + (min(row + e * PASS, count - 1) >> pv.log2P)];
+  }
   uint4 k[N], v[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    const int r = row + e * PASS;
-    if (r >= count) break;
-    const int j = kept[r];
-    const size_t at = (((size_t)page_at(pv, ba, b, j >> pv.log2P) * pv.Hkv + h) * pv.P +
-                       (j & (pv.P - 1))) * NV + col;
+    bad |= (unsigned)from[e] >= (unsigned)pv.pages || (unsigned)to[e] >= (unsigned)pv.pages;
+    const int page = (unsigned)from[e] < (unsigned)pv.pages ? from[e] : 0;
+    const size_t at =
+        (((size_t)page * pv.Hkv + h) * pv.P + (j[e] & (pv.P - 1))) * NV + col;
     // not through the read-only path: in place, rows are written in this launch
-    k[e] = __ldcg(K + at);
-    v[e] = __ldcg(V + at);
+    if (row + e * PASS < count) {
+      k[e] = __ldcg(K + at);
+      v[e] = __ldcg(V + at);
+    }
   }
+  if (bad) flag_error(pv.err, kErrBadBatch);
   bool ok = true;
   if (a.in_place) {
     __syncthreads();                                     // the CTA has its rows
@@ -262,12 +299,8 @@ evict_move_kernel(PagesView pv, BatchArgs ba, EvictArgs a, int chunks) {
   for (int e = 0; e < N; ++e) {
     const int r = row + e * PASS;
     if (r >= count) break;
-    const int page = out[(size_t)b * ba.max_pages + (r >> pv.log2P)];
-    if ((unsigned)page >= (unsigned)pv.pages) {
-      flag_error(pv.err, kErrBadBatch);
-      continue;
-    }
-    const size_t at = (((size_t)page * pv.Hkv + h) * pv.P + (r & (pv.P - 1))) * NV + col;
+    if ((unsigned)to[e] >= (unsigned)pv.pages) continue;
+    const size_t at = (((size_t)to[e] * pv.Hkv + h) * pv.P + (r & (pv.P - 1))) * NV + col;
     Ko[at] = k[e];
     Vo[at] = v[e];
   }
