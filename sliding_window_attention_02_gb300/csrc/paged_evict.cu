@@ -1,11 +1,11 @@
 // Eviction from a paged cache: of every (sequence, KV head) the first tokens, the
 // last ones and the heaviest of the others stay, up to a budget, in their order.
 //
-// Two kernels.  The first, a CTA for each (sequence, KV head), finds the least
-// weight that stays: the weights as integers of the same order, a radix select of
-// four passes over 8 bits each, in shared memory where a sequence's fit.  Ties of
-// that weight stay from the lowest index on.  A scan of what stays gives each kept
-// token its place; the weights follow.  The second moves the rows, 64 of them a
+// Two kernels.  The first, a CTA or a cluster of them for each (sequence, KV head),
+// finds the least weight that stays: the weights as integers of the same order, a
+// radix select of at most four passes over 8 bits each, in shared memory where they
+// fit.  Ties of that weight stay from the lowest index on.  Counts of what stays give
+// each kept token its place; the weights follow.  The second moves the rows, 64 of them a
 // CTA, every read of it in flight at once.
 //
 // In place a row's place is at or before where it comes from, so a CTA's writes
@@ -21,10 +21,10 @@
 namespace rswa {
 namespace {
 
-constexpr int kSelectThreads = 1024;
+constexpr int kSelectThreads = 512, kWarps = kSelectThreads / 32;
 constexpr int kMoveRows = 64, kMoveThreads = 128;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
-// Weights of a sequence that are kept in shared memory between the passes.
+// Weights of a CTA's slice that are kept in shared memory between the passes.
 constexpr int kSelectSmem = 40 * 1024;
 
 // A float as an unsigned integer of the same order; both zeros alike, NaN lowest.
@@ -46,43 +46,80 @@ __device__ __forceinline__ int length_of(const PagesView& pv, const BatchArgs& b
 // where the caller wants none.
 __device__ __forceinline__ int32_t* move_flags(void* ws) { return static_cast<int32_t*>(ws) + 64; }
 
+// Copies of the histogram, by lane: weights share few exponents, and the lanes of a
+// warp that add to one word take turns.
+constexpr int kCopies = 8;
+constexpr int kAhead = 4;                                // weights of a thread in flight
+
+// A word of CTA `rank`'s shared memory at this CTA's address p.
+__device__ __forceinline__ uint32_t peer_word(const void* p, int rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_dsmem(p, (uint32_t)rank))
+               : "memory");
+  return v;
+}
+
+// A cluster of gridDim-given size for each (sequence, KV head), whose CTAs take a
+// slice of its tokens each and add up their counts in one another's shared memory.
+// Bound by instruction issue and by the passes' barriers: what is read is small.
 template <bool SMEM>
 __global__ void __launch_bounds__(kSelectThreads)
 evict_select_kernel(PagesView pv, BatchArgs ba, EvictArgs a, int chunks) {
-  extern __shared__ uint32_t s_key[];
-  __shared__ uint32_t s_hist[4][256];
+  extern __shared__ float s_w[];                         // the slice's weights
+  __shared__ uint32_t s_hist[2][256 * kCopies];
+  __shared__ uint32_t s_total[2][256];                   // the slice's counts of a pass
+  __shared__ uint32_t s_sum[256];                        // all slices'
   __shared__ uint32_t s_prefix, s_need, s_whole;
-  __shared__ int s_warp[2][kSelectThreads / 32];
+  __shared__ int s_warp[2][kWarps], s_slice[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int peers = (int)cluster_size(), rank = (int)cluster_rank();
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t bh = blockIdx.x;
+  const int64_t bh = blockIdx.x / peers;
   const int b = (int)(bh / pv.Hkv);
   const float* w = a.weights + bh * ba.cap;
   float* wo = a.weights_out + bh * ba.cap;
   int32_t* kept = a.kept + bh * a.budget;
+  const int all_tid = rank * kSelectThreads + tid, all_threads = peers * kSelectThreads;
   if (a.in_place) {
-    if (bh == 0 && tid == 0) *static_cast<int32_t*>(a.ws) = 0;
-    for (int i = tid; i < chunks; i += kSelectThreads) move_flags(a.ws)[bh * chunks + i] = 0;
+    if (blockIdx.x == 0 && tid == 0) *static_cast<int32_t*>(a.ws) = 0;
+    for (int i = all_tid; i < chunks; i += all_threads) move_flags(a.ws)[bh * chunks + i] = 0;
   }
   const int L = length_of(pv, ba, b);
   if (L <= a.budget) {
-    for (int i = tid; i < a.budget; i += kSelectThreads) kept[i] = i < L ? i : -1;
-    for (int i = tid; i < ba.cap; i += kSelectThreads) {
+    for (int i = all_tid; i < a.budget; i += all_threads) kept[i] = i < L ? i : -1;
+    for (int i = all_tid; i < ba.cap; i += all_threads) {
       if (i >= L)
         wo[i] = 0.f;
       else if (wo != w)
         wo[i] = w[i];
     }
-    return;
+    return;                                              // as do all of the cluster
   }
+  auto meet = [&]() {
+    if (peers > 1) {
+      cluster_arrive_release();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+  };
   const int lo = a.first, hi = L - a.last;               // the tokens that are weighed
-  auto key = [&](int j) { return SMEM ? s_key[j] : order_key(w[j]); };
+  // the CTA's tokens, and its warps' of them: whole rounds of 32
+  const int span = (L + 32 * kWarps * peers - 1) / (32 * kWarps * peers) * 32;
+  const int t0 = min(rank * kWarps * span, L), t1 = min(t0 + kWarps * span, L);
   if (SMEM)
-    for (int j = lo + tid; j < hi; j += kSelectThreads) s_key[j] = order_key(w[j]);
-  if (tid < 256)
+    for (int j0 = t0 + tid; j0 < t1; j0 += kAhead * kSelectThreads) {
+      float x[kAhead];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s_hist[i][tid] = 0;
+      for (int e = 0; e < kAhead; ++e)
+        if (j0 + e * kSelectThreads < t1) x[e] = w[j0 + e * kSelectThreads];
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e)
+        if (j0 + e * kSelectThreads < t1) s_w[j0 - t0 + e * kSelectThreads] = x[e];
+    }
+  const float* from = SMEM ? s_w - t0 : w;
+  for (int i = tid; i < 256 * kCopies; i += kSelectThreads) s_hist[0][i] = 0;
   if (tid == 0) {
     s_prefix = 0;
     s_need = (uint32_t)(a.budget - a.first - a.last);
@@ -94,22 +131,32 @@ evict_select_kernel(PagesView pv, BatchArgs ba, EvictArgs a, int chunks) {
   if (s_need > 0) {
     for (int pass = 0;; ++pass) {
       const int shift = 24 - 8 * pass;
-      const uint32_t prefix = s_prefix;
-      uint32_t* hist = s_hist[pass];
-      for (int j0 = lo; j0 < hi; j0 += kSelectThreads) {
-        const int j = j0 + tid;
-        const uint32_t x = j < hi ? key(j) : 0u;
-        const bool on = j < hi && (pass == 0 || (x ^ prefix) >> (shift + 8) == 0);
-        if (pass < 2) {
-          // Weights share few exponents: the lanes of a warp with one digit are
-          // counted together (10272 tokens: a pass 5 us without, as each lane's add
-          // to the same word takes its turn).
-          const uint32_t digit = on ? x >> shift & 255u : 256u;
-          const uint32_t same = __match_any_sync(0xffffffffu, digit);
-          if (on && (same & ((1u << lane) - 1u)) == 0) atomicAdd(&hist[digit], __popc(same));
-        } else if (on) {
-          atomicAdd(&hist[x >> shift & 255u], 1u);
-        }
+      const uint32_t prefix = s_prefix, need = s_need;
+      uint32_t* hist = s_hist[pass & 1] + (lane & (kCopies - 1));
+#pragma unroll 4
+      for (int j = max(t0, lo) + tid; j < min(t1, hi); j += kSelectThreads) {
+        const uint32_t x = order_key(from[j]);
+        if (pass == 0 || (x ^ prefix) >> (shift + 8) == 0)
+          atomicAdd(hist + (x >> shift & 255u) * kCopies, 1u);
+      }
+      for (int i = tid; i < 256 * kCopies; i += kSelectThreads) s_hist[~pass & 1][i] = 0;
+      __syncthreads();
+      uint32_t* total = s_total[pass & 1];
+      if (tid < 256) {
+        const uint4* h = reinterpret_cast<const uint4*>(s_hist[pass & 1] + tid * kCopies);
+        const uint4 p = h[0], q = h[1];
+        total[tid] = ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
+      }
+      meet();
+      // two passes on, a slice's counts are written again: all have read them by then,
+      // as they meet once more in between
+      if (tid < 256) {
+        uint32_t sum = 0;
+        if (peers > 1)
+          for (int p = 0; p < peers; ++p) sum += peer_word(total + tid, p);
+        else
+          sum = total[tid];
+        s_sum[tid] = sum;
       }
       __syncthreads();
       if (warp == 0) {
@@ -117,15 +164,13 @@ evict_select_kernel(PagesView pv, BatchArgs ba, EvictArgs a, int chunks) {
         // has digits 255 - 8 l ... 248 - 8 l
         uint32_t c[8], mine = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mine += c[e] = hist[255 - 8 * lane - e];
+        for (int e = 0; e < 8; ++e) mine += c[e] = s_sum[255 - 8 * lane - e];
         uint32_t inc = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
           const uint32_t y = __shfl_up_sync(0xffffffffu, inc, off);
           if (lane >= off) inc += y;
         }
-        const uint32_t need = s_need;
-        __syncwarp();
         uint32_t above = inc - mine;
         if (above < need && need <= inc) {
 #pragma unroll
@@ -152,63 +197,72 @@ evict_select_kernel(PagesView pv, BatchArgs ba, EvictArgs a, int chunks) {
       }
     }
   }
-  // Thread t looks through tokens [t * per, (t + 1) * per); an odd number spreads
-  // them over the banks.
-  const int per = ((L + kSelectThreads - 1) / kSelectThreads) | 1;
-  const int j0 = min(tid * per, L), j1 = min(j0 + per, L);
-  int above = 0, equal = 0;
-  for (int j = j0; j < j1; ++j) {
-    if (j < lo || j >= hi) {
-      ++above;
-    } else {
-      const uint32_t x = key(j);
-      above += x > least;
-      equal += x == least;
-    }
+  // What stays, in order: a warp looks through a range of tokens, 32 at a time, once
+  // for its count and once, behind the counts of the warps before it, for the places.
+  const int j0 = min(t0 + warp * span, t1), j1 = min(j0 + span, t1);
+  auto look = [&](int j, uint32_t& stays, uint32_t& equal) {
+    const bool in = j < j1, end = in && (j < lo || j >= hi);
+    const uint32_t x = in ? order_key(from[j]) : 0u;
+    stays = __ballot_sync(0xffffffffu, end || (in && x > least));
+    equal = __ballot_sync(0xffffffffu, in && !end && x == least);
+  };
+  int na = 0, ne = 0;
+#pragma unroll 4
+  for (int j = j0; j < j1; j += 32) {
+    uint32_t stays, equal;
+    look(j + lane, stays, equal);
+    na += __popc(stays);
+    ne += __popc(equal);
   }
-  int inc_a = above, inc_e = equal;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int ya = __shfl_up_sync(0xffffffffu, inc_a, off);
-    const int ye = __shfl_up_sync(0xffffffffu, inc_e, off);
-    if (lane >= off) {
-      inc_a += ya;
-      inc_e += ye;
-    }
-  }
-  if (lane == 31) {
-    s_warp[0][warp] = inc_a;
-    s_warp[1][warp] = inc_e;
+  if (lane == 0) {
+    s_warp[0][warp] = na;
+    s_warp[1][warp] = ne;
   }
   __syncthreads();
-  int na = inc_a - above, ne = inc_e - equal;            // before this thread's tokens
+  if (warp < 2) {
+    const int sum = __reduce_add_sync(0xffffffffu, lane < kWarps ? s_warp[warp][lane] : 0);
+    if (lane == 0) s_slice[warp] = sum;
+  }
+  meet();
   {
     int wa = lane < warp ? s_warp[0][lane] : 0, we = lane < warp ? s_warp[1][lane] : 0;
-    na += __reduce_add_sync(0xffffffffu, wa);
-    ne += __reduce_add_sync(0xffffffffu, we);
-  }
-  for (int j = j0; j < j1; ++j) {
-    bool stays = j < lo || j >= hi, tie = false;
-    if (!stays) {
-      const uint32_t x = key(j);
-      stays = x > least;
-      tie = x == least;
+    if (lane < rank) {                                   // at most 8 ranks
+      wa += (int)peer_word(&s_slice[0], lane);
+      we += (int)peer_word(&s_slice[1], lane);
     }
-    if (stays || (tie && ne < ties)) kept[na + min(ne, ties)] = j;
-    na += stays;
-    ne += tie;
+    na = __reduce_add_sync(0xffffffffu, wa);
+    ne = __reduce_add_sync(0xffffffffu, we);
   }
-  __syncthreads();
-  // The weights: in place too, a batch is read before it is written, and a later
-  // batch comes from behind what an earlier one writes.
-  for (int i0 = 0; i0 < a.budget; i0 += kSelectThreads) {
-    const int i = i0 + tid;
-    const float x = i < a.budget ? w[kept[i]] : 0.f;
+  const uint32_t before = (1u << lane) - 1u;
+#pragma unroll 4
+  for (int j = j0; j < j1; j += 32) {
+    uint32_t stays, equal;
+    look(j + lane, stays, equal);
+    const int e = ne + __popc(equal & before);           // equals before this token
+    if (stays >> lane & 1u || (equal >> lane & 1u && e < ties)) {
+      const int at = na + __popc(stays & before) + min(e, ties);
+      kept[at] = j + lane;
+      // in place too: every slice has been read by now
+      if (SMEM) wo[at] = s_w[j + lane - t0];
+    }
+    na += __popc(stays);
+    ne += __popc(equal);
+  }
+  meet();                                                // peers' counts have been read
+  // The weights of a long sequence, by one CTA.  In place too: a batch is read before
+  // it is written, and a later batch comes from behind what an earlier one writes.
+  if (!SMEM && rank == 0) {
+    for (int i0 = 0; i0 < a.budget; i0 += kSelectThreads) {
+      const int i = i0 + tid;
+      const float x = i < a.budget ? w[__ldcg(kept + i)] : 0.f;
+      __syncthreads();
+      if (i < a.budget) wo[i] = x;
+    }
     __syncthreads();
-    if (i < a.budget) wo[i] = x;
+    for (int i = a.budget + tid; i < ba.cap; i += kSelectThreads) wo[i] = 0.f;
   }
-  __syncthreads();
-  for (int i = a.budget + tid; i < ba.cap; i += kSelectThreads) wo[i] = 0.f;
+  if (SMEM)
+    for (int i = a.budget + all_tid; i < ba.cap; i += all_threads) wo[i] = 0.f;
 }
 
 template <int ELT, int D>
@@ -330,18 +384,20 @@ cudaError_t launch_paged_evict(const PagesView& pv, const BatchArgs& ba, const E
   const int chunks = move_chunks(std::min(a.budget, ba.cap));
   const int64_t heads = (int64_t)ba.B * pv.Hkv;
   if (!a.kept) a.kept = static_cast<int32_t*>(a.ws) + 64 + heads * chunks;
-  cudaError_t e;
-  if (ba.cap <= kSelectSmem) {
-    const size_t smem = (size_t)ba.cap * 4;
-    e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSelectSmem * 4);
-    if (e != cudaSuccess) return e;
-    e = launch_dependent(evict_select_kernel<true>, dim3((unsigned)heads), dim3(kSelectThreads),
-                         smem, s, pv, ba, a, chunks);
-  } else {
-    e = launch_dependent(evict_select_kernel<false>, dim3((unsigned)heads), dim3(kSelectThreads), 0,
-                         s, pv, ba, a, chunks);
-  }
+  // Few heads have several CTAs each, as many as are on the SMs together, with a
+  // round of tokens for every warp at least.
+  int peers = 1;
+  while (peers < 8 && heads * peers * 2 <= 4 * (int64_t)pv.sms &&
+         ba.cap >= 2 * peers * kSelectThreads)
+    peers *= 2;
+  const int64_t slice = (ba.cap + 32 * kWarps * peers - 1) / (32 * kWarps * peers) * 32 * kWarps;
+  const bool smem = slice <= kSelectSmem;
+  auto kern = smem ? evict_select_kernel<true> : evict_select_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       smem ? kSelectSmem * 4 : 0);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent_cluster(kern, dim3((unsigned)(heads * peers)), dim3(kSelectThreads),
+                               smem ? slice * 4 : 0, s, peers, pv, ba, a, chunks);
   if (e != cudaSuccess) return e;
   if (pv.dtype == RSWA_F32)
     return pv.d == 64 ? launch_move<4, 64>(pv, ba, a, chunks, s)

@@ -286,6 +286,26 @@ inline cudaError_t launch_dependent(K kernel, dim3 grid, dim3 block, size_t smem
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// The same in clusters of `cluster` CTAs (at most 8, a divisor of the grid).
+template <typename K, typename... Args>
+inline cudaError_t launch_dependent_cluster(K kernel, dim3 grid, dim3 block, size_t smem,
+                                            cudaStream_t s, int cluster, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Fused decode step with split-K scratch in the library's static device array
 // (decode_static.cu).  Fails with cudaErrorInvalidValue when the cache needs
 // more than static_scratch_capacity() bytes of scratch.
