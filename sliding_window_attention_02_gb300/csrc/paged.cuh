@@ -288,7 +288,7 @@ struct PagedPlan {
 };
 
 // Workspace of an attention launch: counters that the CTAs of a cut unit meet
-// on, one for each CTA that may begin one (zero before the first call, and zero
+// on, one or two for each CTA that may begin one (zero before the first call, and zero
 // again after each), then two partial results for every CTA: of the unit that
 // a CTA before it began, and of the one that it begins and does not end.
 constexpr int kMaxPagedCtas = 1024;

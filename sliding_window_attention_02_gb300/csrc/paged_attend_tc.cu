@@ -84,10 +84,11 @@ struct Smem {
   static constexpr int B_FIN = B_ML + 1;
   static constexpr int B_SEG = B_FIN + 1;          // NSEG segments handed over
   static constexpr int B_SFREE = B_SEG + NSEG;     // NSEG segments left by the softmax warps
-  static constexpr int B_CUT = B_SFREE + NSEG;     // a cut unit's partial is written
-  static constexpr int B_JOIN = B_CUT + 1;         // and who joins it is known
-  static constexpr int NBAR = B_JOIN + 1;
-  static_assert(8 * NBAR + 16 + 4 * NS <= 512, "barriers");
+  static constexpr int B_CUT = B_SFREE + NSEG;     // 2 halves: a cut unit's partial is written
+  static constexpr int B_JOIN = B_CUT + 2;         // 2 halves: and who joins it is known
+  static constexpr int B_ASK = B_JOIN + 2;         // 2 halves: the same before it is written
+  static constexpr int NBAR = B_ASK + 2;
+  static_assert(8 * NBAR + 28 + 4 * NS <= 512, "barriers");
 };
 
 __host__ __device__ constexpr uint32_t tm_s(int half) { return half ? 128u : 0u; }
@@ -134,45 +135,122 @@ __device__ __forceinline__ uint32_t tile_flags(const Hull& h, int x0) {
   return f;
 }
 
-// A partial: O as [D/4][256] float4 (a warp's rows are contiguous), then m and l.
-constexpr int kPartRows = 2 * BM;
-__host__ __device__ constexpr size_t partial_floats(int D) {
-  return (size_t)kPartRows * (D + 2);
+// A partial, one of each half: O as [columns/4][128] float4 (a warp's rows are
+// contiguous), then m and l.  The halves have their own rows of a pair, and half of the
+// columns each of a split unit's; they are published and joined apart, as neither has
+// to wait for the other.
+__host__ __device__ constexpr size_t partial_floats(int D) { return (size_t)BM * (D + 2); }
+__device__ __forceinline__ float* half_partial(void* ws, int p, int first, int half, int D) {
+  return paged_partial(ws, p, first, 2 * partial_floats(D)) + half * partial_floats(D);
 }
 
-// A row's columns 32 c_lo .. 32 c_hi - 1 and lse from the partials of CTAs first ..
-// last, in their order.
+// A row's `chunks` chunks of 32 columns, and its lse, from the partials of CTAs first ..
+// last, in their order; the reads of two partials are on their way together.
 template <int D>
-__device__ __noinline__ void join_row(void* ws, int first, int last, int prow, int c_lo, int c_hi,
+__device__ __noinline__ void join_row(void* ws, int first, int last, int half, int r, int chunks,
                                       __nv_bfloat16* orow, float* lse) {
-  auto part = [&](int p) { return paged_partial(ws, p, first, partial_floats(D)); };
-  auto m_of = [&](int p) { return __ldcg(part(p) + (size_t)kPartRows * D + prow); };
-  float top = m_of(first);
-  for (int p = first + 1; p <= last; ++p) top = fmaxf(top, m_of(p));
-  float L = 0.f;
-  for (int p = first; p <= last; ++p)
-    L = fmaf(__ldcg(part(p) + (size_t)kPartRows * (D + 1) + prow), ex2(m_of(p) - top), L);
+  auto part = [&](int p) { return half_partial(ws, p, first, half, D); };
+  float M = -INFINITY, L = 0.f;
 #pragma unroll 1
-  for (int c = c_lo; c < c_hi; ++c) {
+  for (int p = first; p <= last; p += 2) {
+    const float* a = part(p) + (size_t)BM * D + r;
+    const float* b = part(min(p + 1, last)) + (size_t)BM * D + r;
+    const float m0 = __ldcg(a), l0 = __ldcg(a + BM);
+    const float m1 = p < last ? __ldcg(b) : -INFINITY, l1 = p < last ? __ldcg(b + BM) : 0.f;
+    const float mn = fmaxf(M, fmaxf(m0, m1)), ref = mn == -INFINITY ? 0.f : mn;
+    L = fmaf(l1, ex2(m1 - ref), fmaf(l0, ex2(m0 - ref), L * ex2(M - ref)));
+    M = mn;
+  }
+  const float inv = 1.f / L;
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
     float x[32];
 #pragma unroll
     for (int e = 0; e < 32; ++e) x[e] = 0.f;
 #pragma unroll 1
-    for (int p = first; p <= last; ++p) {
-      const float wp = ex2(m_of(p) - top);
-      const float4* src = reinterpret_cast<const float4*>(part(p)) + prow;
+    for (int p = first; p <= last; p += 2) {
+      const float* a = part(p);
+      const float* b = part(min(p + 1, last));
+      const float4* s0 = reinterpret_cast<const float4*>(a) + (size_t)c * 8 * BM + r;
+      const float4* s1 = reinterpret_cast<const float4*>(b) + (size_t)c * 8 * BM + r;
+      const float w0 = ex2(__ldcg(a + (size_t)BM * D + r) - M);
+      const float w1 = p < last ? ex2(__ldcg(b + (size_t)BM * D + r) - M) : 0.f;
+      float4 u[8], v[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float4 v = __ldcg(src + (size_t)(c * 8 + e) * kPartRows);
-        x[4 * e] = fmaf(v.x, wp, x[4 * e]);
-        x[4 * e + 1] = fmaf(v.y, wp, x[4 * e + 1]);
-        x[4 * e + 2] = fmaf(v.z, wp, x[4 * e + 2]);
-        x[4 * e + 3] = fmaf(v.w, wp, x[4 * e + 3]);
+        u[e] = __ldcg(s0 + (size_t)e * BM);
+        v[e] = __ldcg(s1 + (size_t)e * BM);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[4 * e] = fmaf(v[e].x, w1, fmaf(u[e].x, w0, x[4 * e]));
+        x[4 * e + 1] = fmaf(v[e].y, w1, fmaf(u[e].y, w0, x[4 * e + 1]));
+        x[4 * e + 2] = fmaf(v[e].z, w1, fmaf(u[e].z, w0, x[4 * e + 2]));
+        x[4 * e + 3] = fmaf(v[e].w, w1, fmaf(u[e].w, w0, x[4 * e + 3]));
       }
     }
-    store_columns(orow + c * 32, x, 1.f / L);
+    store_columns(orow + c * 32, x, inv);
   }
-  if (lse) *lse = (top + log2f(L)) * kLn2;
+  if (lse) *lse = (M + log2f(L)) * kLn2;
+}
+
+// The same in the CTA that begins the unit, from its own O in TMEM (t0 times a0, and t1
+// times a1 where the halves share the unit; each where it has had a tile) and the partials of the CTAs behind it.
+// Called by whole warps; M, L: of the CTA's own part.
+template <int D>
+__device__ __noinline__ void join_own(void* ws, int first, int last, int half, int r, bool live,
+                                      uint32_t t0, float a0, bool use0, uint32_t t1, float a1,
+                                      bool use1, float M, float L, int chunks,
+                                      __nv_bfloat16* orow, float* lse) {
+  auto part = [&](int p) { return half_partial(ws, p, first, half, D); };
+  const float M0 = M;
+  for (int p = first + 1; live && p <= last; ++p)
+    M = fmaxf(M, __ldcg(part(p) + (size_t)BM * D + r));
+  const float own = ex2(M0 - M);
+  L *= own;
+  for (int p = first + 1; live && p <= last; ++p) {
+    const float* a = part(p) + (size_t)BM * D + r;
+    L = fmaf(__ldcg(a + BM), ex2(__ldcg(a) - M), L);
+  }
+  a0 *= own;
+  a1 *= own;
+  const float inv = 1.f / L;
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    float x[32];
+    uint32_t ov[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] = 0.f;
+    if (use0) {
+      tmem_ld32_sync(t0 + c * 32, ov);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(ov[e]) * a0;
+    }
+    if (use1) {
+      tmem_ld32_sync(t1 + c * 32, ov);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(ov[e]), a1, x[e]);
+    }
+    if (!live) continue;
+#pragma unroll 1
+    for (int p = first + 1; p <= last; ++p) {
+      const float* a = part(p);
+      const float4* s = reinterpret_cast<const float4*>(a) + (size_t)c * 8 * BM + r;
+      const float wp = ex2(__ldcg(a + (size_t)BM * D + r) - M);
+      float4 u[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] = __ldcg(s + (size_t)e * BM);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[4 * e] = fmaf(u[e].x, wp, x[4 * e]);
+        x[4 * e + 1] = fmaf(u[e].y, wp, x[4 * e + 1]);
+        x[4 * e + 2] = fmaf(u[e].z, wp, x[4 * e + 2]);
+        x[4 * e + 3] = fmaf(u[e].w, wp, x[4 * e + 3]);
+      }
+    }
+    store_columns(orow + c * 32, x, inv);
+  }
+  if (lse && live) *lse = (M + log2f(L)) * kLn2;
 }
 
 // The registers of a TMEM load that an earlier wait has completed: no use of them
@@ -210,7 +288,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
   volatile int* joiner = reinterpret_cast<volatile int*>(smem + SM::OFF_BAR + 8 * NBAR + 12);
   // flags of the tile in each ring slot (tile_flags)
   volatile uint32_t* slot_flags =
-      reinterpret_cast<volatile uint32_t*>(smem + SM::OFF_BAR + 8 * NBAR + 16);
+      reinterpret_cast<volatile uint32_t*>(smem + SM::OFF_BAR + 8 * NBAR + 28);
   const Segment* segs = reinterpret_cast<const Segment*>(smem + SM::OFF_SEG);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -218,8 +296,8 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
 
   if (threadIdx.x == 0) {
     for (int k = 0; k < NBAR; ++k)
-      mbar_init(bar(k), k >= SM::B_P && k < SM::B_O ? 128u
-                        : (k == SM::B_F || k == SM::B_ML || k == SM::B_CUT ||
+      mbar_init(bar(k), (k >= SM::B_P && k < SM::B_O) || (k >= SM::B_CUT && k < SM::B_JOIN) ? 128u
+                        : (k == SM::B_F || k == SM::B_ML ||
                            (k >= SM::B_SFREE && k < SM::B_SFREE + NSEG))
                             ? 256u
                             : 1u);
@@ -708,6 +786,18 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       auto wait_all = [&](int b, uint32_t phase) {
         return __all_sync(0xffffffffu, wait_for(bar(b), phase & 1, abort_flag, wait_ns)) != 0;
       };
+      // The CTA that begins a cut unit comes to it at the end of its range, the others
+      // at the start of theirs: as a rule it is the last, and adds their parts to its
+      // own O as it writes the rows, without leaving one itself (half of the partials'
+      // traffic, which is what cut units cost).  It asks early: the answer comes while
+      // the last products run.
+      const bool ask = ok && !w.whole && w.j0 == 0;
+      if (ask && r == 0) {
+        int32_t* count = paged_counter(a.ws, 2 * w.first + half);
+        joiner[2 + half] = load_acquire(count) == w.last - w.first;
+        if (joiner[2 + half]) *count = 0;               // ready for the next call
+        mbar_arrive(bar(SM::B_ASK + half));
+      }
       // Weights of the two halves' O, the row's reference and sum.
       float a0w = 1.f, a1w = 0.f, M = m_run, L = l_run;
       if (split) {
@@ -729,17 +819,29 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         }
         ++ml_phase;
       }
-      const int prow = (split ? 0 : half * BM) + r;
       if (ok && own > 0) ok = wait_all(SM::B_O + half, half ? o_phase1 : o_phase0);
       if (ok && split && other > 0) ok = wait_all(SM::B_O + 1 - half, half ? o_phase0 : o_phase1);
+      bool joins = false;
+      if (ok && ask) {                                  // once a launch: its last unit
+        ok = wait_all(SM::B_ASK + half, 0);
+        joins = ok && joiner[2 + half] != 0;
+      }
       if (!ok) break;
       tc_fence_after();
       const size_t orow = ((size_t)w.row0 + i) * pv.H + (size_t)w.kvh * sh.G + hg;
       __nv_bfloat16* orow_p = static_cast<__nv_bfloat16*>(a.o) + orow * D;
       // Split: each half writes half of the columns of the joined row.
       const int c_lo = split ? half * (D / 64) : 0, c_hi = split ? c_lo + D / 64 : D / 32;
-      if (any) {
-        float* part = paged_partial(a.ws, cta, w.first, partial_floats(D));
+      if (joins) {
+        if (any)
+          join_own<D>(a.ws, w.first, w.last, half, r, live, tmem + lane_off + tm_o(half) + c_lo * 32,
+                      a0w, started, tmem + lane_off + tm_o(1 - half) + c_lo * 32, a1w,
+                      split && other > 0, M, L, c_hi - c_lo, orow_p + c_lo * 32,
+                      a.lse && (!split || half == 0) ? a.lse + orow : nullptr);
+        tc_fence_before();
+        mbar_arrive(bar(SM::B_F));
+      } else if (any) {
+        float* part = half_partial(a.ws, cta, w.first, half, D);
         const float inv = 1.f / L;
         const bool use0 = started, use1 = split && other > 0;
 #pragma unroll 1
@@ -761,20 +863,20 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
           if (live && w.whole) {
             store_columns(orow_p + c * 32, x, inv);
           } else if (live) {
-            float4* dst = reinterpret_cast<float4*>(part) + prow;
+            float4* dst = reinterpret_cast<float4*>(part) + (size_t)(c - c_lo) * 8 * BM + r;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              dst[(size_t)(c * 8 + e) * kPartRows] =
+              dst[(size_t)e * BM] =
                   make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
           }
         }
         tc_fence_before();
         mbar_arrive(bar(SM::B_F));
-        if (live && (!split || half == 0)) {
+        if (live) {
           if (!w.whole) {
-            part[(size_t)kPartRows * D + prow] = M;
-            part[(size_t)kPartRows * (D + 1) + prow] = L;
-          } else if (a.lse) {
+            part[(size_t)BM * D + r] = M;
+            part[(size_t)BM * (D + 1) + r] = L;
+          } else if (a.lse && (!split || half == 0)) {
             a.lse[orow] = (M + log2f(L)) * kLn2;
           }
         }
@@ -782,19 +884,19 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         tc_fence_before();
         mbar_arrive(bar(SM::B_F));
       }
-      if (!w.whole) {
-        mbar_arrive(bar(SM::B_CUT));
-        if (threadIdx.x == 0 && wait_for(bar(SM::B_CUT), cut_phase & 1, abort_flag, wait_ns)) {
-          int32_t* count = paged_counter(a.ws, w.first);
+      if (!w.whole && !joins) {
+        mbar_arrive(bar(SM::B_CUT + half));
+        if (r == 0 && wait_for(bar(SM::B_CUT + half), cut_phase & 1, abort_flag, wait_ns)) {
+          int32_t* count = paged_counter(a.ws, 2 * w.first + half);
           const bool last = arrive_acq_rel(count) == w.last - w.first;
           if (last) *count = 0;                         // ready for the next call
-          joiner[0] = last;
-          mbar_arrive(bar(SM::B_JOIN));
+          joiner[half] = last;
+          mbar_arrive(bar(SM::B_JOIN + half));
         }
-        if (!wait_all(SM::B_JOIN, cut_phase)) break;
+        if (!wait_all(SM::B_JOIN + half, cut_phase)) break;
         ++cut_phase;
-        if (joiner[0] && live)
-          join_row<D>(a.ws, w.first, w.last, prow, c_lo, c_hi, orow_p,
+        if (joiner[half] && live)
+          join_row<D>(a.ws, w.first, w.last, half, r, c_hi - c_lo, orow_p + c_lo * 32,
                       a.lse && (!split || half == 0) ? a.lse + orow : nullptr);
       }
       mbar_arrive(bar(SM::B_SFREE + k % NSEG));
@@ -813,7 +915,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
   if (threadIdx.x == 0 && *abort_flag) flag_error(pv.err, kErrWaitTimeout);
 }
 
-int grid_of(const PagesView& pv) { return std::min(std::max(pv.sms, 1), kMaxPagedCtas); }
+int grid_of(const PagesView& pv) { return std::min(std::max(pv.sms, 1), kMaxPagedCtas / 2); }
 
 template <int D>
 cudaError_t launch_d(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
@@ -850,7 +952,7 @@ bool paged_attend_tc_supported(const PagesView& pv) {
 }
 
 size_t paged_attend_tc_workspace(const PagesView& pv) {
-  return kPagedCounterBytes + (size_t)grid_of(pv) * 2 * partial_floats(pv.d) * sizeof(float);
+  return kPagedCounterBytes + (size_t)grid_of(pv) * 2 * 2 * partial_floats(pv.d) * sizeof(float);
 }
 
 cudaError_t launch_paged_attend_tc(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
