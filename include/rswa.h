@@ -501,8 +501,7 @@ RSWA_API int rswa_pages_append(rswa_pages* pages, const rswa_batch* batch, int64
  * need one each.  After a call that reported RSWA_EDEVICE because a wait ran out,
  * zero it again.  Host-only.  Errors: RSWA_EHANDLE, RSWA_EINVAL.
  */
-RSWA_API int rswa_pages_attend_workspace(rswa_pages* pages, int64_t rows, int batch,
-                                         size_t* out_bytes);
+RSWA_API int rswa_pages_attend_workspace(rswa_pages* pages, int64_t rows, size_t* out_bytes);
 
 /*
  * Attention of the chunk over the pages, which hold its own keys and values

@@ -116,8 +116,7 @@ _SIGNATURES = {
     "rswa_pages_destroy": (_c_int, [_c_vp]),
     "rswa_pages_append": (_c_int, [_c_vp, _c_batch, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64,
                                    _c_vp]),
-    "rswa_pages_attend_workspace": (_c_int, [_c_vp, _c_i64, _c_int,
-                                             ctypes.POINTER(_c_size)]),
+    "rswa_pages_attend_workspace": (_c_int, [_c_vp, _c_i64, ctypes.POINTER(_c_size)]),
     "rswa_pages_attend": (_c_int, [_c_vp, _c_batch, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp,
                                    _c_vp, _c_size, _c_vp]),
     "rswa_pages_weigh": (_c_int, [_c_vp, _c_batch, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp,
@@ -481,9 +480,9 @@ def rswa_pages_append(handle, batch, k, k_stride, v, v_stride, stream=None) -> N
         _stream_of(stream, _device_index(k))), "rswa_pages_append")
 
 
-def rswa_pages_attend_workspace(handle, rows: int, batch: int) -> int:
+def rswa_pages_attend_workspace(handle, rows: int) -> int:
     out = _c_size(0)
-    _check(load().rswa_pages_attend_workspace(handle, rows, batch, ctypes.byref(out)),
+    _check(load().rswa_pages_attend_workspace(handle, rows, ctypes.byref(out)),
            "rswa_pages_attend_workspace")
     return out.value
 
@@ -920,11 +919,11 @@ class RswaPages:
         if status:
             raise RswaError(status, "rswa_pages_append")
 
-    def attend_workspace(self, rows, batch):
-        """A workspace for attend calls of up to `rows` rows of `batch` sequences,
-        like any tensor made on torch's current stream."""
+    def attend_workspace(self, rows):
+        """A workspace for attend calls of up to `rows` rows, like any tensor made on
+        torch's current stream."""
         import torch
-        return torch.zeros(rswa_pages_attend_workspace(self.handle, rows, batch),
+        return torch.zeros(rswa_pages_attend_workspace(self.handle, rows),
                            dtype=torch.uint8, device=self.buf.device)
 
     def attend(self, batch, q, o, lse=None, workspace=None, stream=None):
@@ -940,10 +939,9 @@ class RswaPages:
         lp = None if lse is None else _dense(lse, (rows, H), self._float32, ix, "lse")
         at = _stream_of(stream, ix)
         if workspace is None:
-            key = (rows, batch.shape[0])
-            need = self._attend_need.get(key)
+            need = self._attend_need.get(rows)
             if need is None:
-                need = self._attend_need[key] = rswa_pages_attend_workspace(self.handle, *key)
+                need = self._attend_need[rows] = rswa_pages_attend_workspace(self.handle, rows)
             wp, size = self._attend_ws.get(at, need)
         elif workspace.get_device() != ix:
             raise ValueError(f"workspace: expected a tensor on CUDA device {ix}")

@@ -61,24 +61,17 @@ struct Hull {
   }
 };
 
-// Tiles of `TILE` keys that a hull's keys take.  ALIGNED: tiles of the tokens'
-// own numbering (tile x holds tokens x * TILE on), those that hold a key of it:
-// prefix tiles 0 .. np - 1, then band tiles kb on.  Otherwise its keys packed.
-template <int TILE, bool ALIGNED>
+// Tiles of `TILE` tokens (tile x holds tokens x * TILE on) that hold one of a hull's:
+// prefix tiles 0 .. np - 1, then band tiles kb on.
+template <int TILE>
 struct HullTiles {
   int np, kb, nt;
   __device__ __forceinline__ HullTiles() {}
   __device__ __forceinline__ explicit HullTiles(const Hull& h) {
-    if (ALIGNED) {
-      np = (h.p + TILE - 1) / TILE;
-      kb = max(h.w0 / TILE, np);
-      nt = np + max(0, (h.end + TILE - 1) / TILE - kb);
-    } else {
-      np = kb = 0;
-      nt = (h.keys() + TILE - 1) / TILE;
-    }
+    np = (h.p + TILE - 1) / TILE;
+    kb = max(h.w0 / TILE, np);
+    nt = np + max(0, (h.end + TILE - 1) / TILE - kb);
   }
-  __device__ __forceinline__ int tile(int j) const { return j < np ? j : kb + (j - np); }
 };
 
 // Where a CTA's walk over the work list stands: a unit (unit_rows rows (token,
@@ -104,10 +97,10 @@ struct PagedUnit {
 // range: 32 groups at a time, a lane each.  What a launch waits for before its first
 // loads is this code, run once: it is kept short (40 pages, one sequence of 16
 // groups: 2.7 us; with sums sequence by sequence and 64-bit divisions 4 to 5).
-template <int TILE, bool ALIGNED, int EXTRA, int MINCOST>
+template <int TILE, int EXTRA, int MINCOST>
 struct PagedPlan {
   static_assert(MINCOST >= 1 + EXTRA, "a range holds a tile at least");
-  using Tiles = HullTiles<TILE, ALIGNED>;
+  using Tiles = HullTiles<TILE>;
   const PagesView& pv;
   const BatchArgs& ba;
   int unit_rows, lane;

@@ -1,17 +1,17 @@
-// Attention of a chunk of tokens over a paged cache, on the CUDA cores: float32
-// caches, groups too large for the tensor cores' tiles, and small work, where
-// latency counts.
+// Attention of a chunk of tokens over a paged cache, on the CUDA cores: small work,
+// where latency counts, float32 caches, and groups too large for the tensor cores'
+// tiles.
 //
 //   o = sum_j exp(s_j - lse) v_j,  s_j = q . k_j / sqrt(d),  lse = log sum_j exp(s_j)
 // over the tokens j that the row's token sees (paged.cuh).
 //
-// A unit is up to R rows (token, query head of the group) of one KV head: every
-// key and value is loaded once for all of them.  Its keys, packed, are cut into
-// tiles that the launch's CTAs share evenly (PagedPlan); the eight warps of a CTA
-// take turns on a tile's keys, each lane group with its own running maximum, sum
-// and output (online softmax), merged at the end of the unit's part.  Units cut
-// over several CTAs leave partials, which the last of the CTAs merges in the
-// order of the CTAs, so that a result does not depend on who is last.
+// No list and no plan: a cluster of CTAs takes R query heads of one chunk row and KV
+// head.  Its CTAs share the row's keys evenly, the eight warps of a CTA take turns on
+// them, each lane group with its own running maximum, sum and output (online softmax);
+// they are merged in shared memory, and the CTAs hand their parts to the first through
+// distributed shared memory.  What a small call waits for is a chain of reads (the
+// row's sequence, its pages, the rows) and the join; beyond some 50000 pairs of a query
+// row and a key it is bound by those, as every CTA reads its keys through L2 for itself.
 #include <algorithm>
 
 #include "attend.cuh"
@@ -21,9 +21,6 @@ namespace rswa {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kTile = 128;                     // keys
-
-using Plan = PagedPlan<kTile, false, 0, 1>;
 
 constexpr int kMaxPeers = 8;                   // CTAs of a cluster
 
@@ -130,171 +127,6 @@ __device__ __forceinline__ void store_peer(uint32_t to, float v) {
 template <typename T, int D, int R>
 __global__ void __launch_bounds__(kWarps * 32)
 paged_attend_kernel(PagesView pv, BatchArgs ba, AttendArgs a) {
-  constexpr int U = R == 1 ? 8 : 4;
-  using C = AttendCfg<T, D, U>;
-  constexpr int EPL = C::EPL, LPK = C::LPK, KPW = C::KPW;
-  __shared__ PagedUnit s_unit;
-  __shared__ int s_more, s_last;
-  __shared__ float s_m[kWarps][R], s_l[kWarps][R];
-  __shared__ float s_acc[kWarps][R][D];
-  __shared__ float s_M[R], s_L[R];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int grp = lane / LPK, col = (lane % LPK) * EPL;
-  const int cta = blockIdx.x, G = pv.G;
-  const float sl2 = rsqrtf((float)D) * kLog2e;
-  griddep_wait();
-  griddep_launch_dependents();
-  Plan plan(pv, ba, R);
-  if (warp == 0) {
-    const bool more = plan.start(cta, gridDim.x);
-    if (lane == 0) {
-      s_more = more;
-      if (more) s_unit = plan.u;
-    }
-  }
-  __syncthreads();
-  while (s_more) {
-    const PagedUnit& u = s_unit;
-    const int rows = min(R, u.seq.T * G - u.f0);
-    const int b = u.b, kvh = u.kvh, m = u.seq.m, n = ba.window;
-    const int tok0 = u.seq.L - u.seq.T;
-    const Hull hull = u.hull;
-    const int x0 = u.j0 * kTile, x1 = min(u.j1 * kTile, hull.keys());
-    const int skip = hull.w0 - hull.p;
-    // Rows of q and o: row f of the unit is query head kvh * G + f % G of chunk
-    // row f / G.
-    auto row_of = [&](int r, int& head) {
-      const int f = u.f0 + r;
-      head = kvh * G + f % G;
-      return u.seq.row0 + f / G;
-    };
-    float qf[R][EPL];
-    int tok[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      int head;
-      const int64_t row = row_of(min(r, rows - 1), head);
-      tok[r] = tok0 + (u.f0 + min(r, rows - 1)) / G;
-      Elt<T>::widen(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
-                                                    row * a.q_stride + (int64_t)head * D + col),
-                    qf[r]);
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) qf[r][e] *= sl2;
-    }
-    SoftmaxState<EPL> st[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) st[r].init();
-    bool bad = false;                          // a page outside the pool
-    for (int base = x0 + warp * C::KEYS_WARP; base < x1; base += kWarps * C::KEYS_WARP) {
-      uint4 kr[U], vr[U];
-      int t[U], page[U];
-      // the pages first, then the rows: reads that do not wait for one another
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int x = base + i * KPW + grp;
-        const int y = x < x1 ? x : x0;         // any key of the part
-        t[i] = y < hull.p ? y : y + skip;
-        page[i] = ba.table[(size_t)b * ba.max_pages + (t[i] >> pv.log2P)];
-      }
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        bad |= (unsigned)page[i] >= (unsigned)pv.pages;
-        if ((unsigned)page[i] >= (unsigned)pv.pages) page[i] = 0;
-        const size_t at = (((size_t)page[i] * pv.Hkv + kvh) * pv.P + (t[i] & (pv.P - 1))) * D + col;
-        kr[i] = ld_stream16(static_cast<const T*>(pv.K) + at);
-        vr[i] = ld_stream16(static_cast<const T*>(pv.V) + at);
-        if (base + i * KPW + grp >= x1) t[i] = INT32_MAX;        // not a key: after every token
-      }
-      fold_keys<T, D, R, U>(
-          qf, kr, vr,
-          [&](int r, int i) { return t[i] <= tok[r] && (t[i] < m || t[i] > tok[r] - n); }, st);
-    }
-    publish_warp<T, D, R>(st, lane, warp, s_m, s_l, s_acc);
-    if (bad) flag_error(pv.err, kErrBadBatch);
-    __syncthreads();
-    // The CTA's result of row r, column c: over the warps.
-    const size_t pf = (size_t)R * (D + 2);
-    float* part = paged_partial(a.ws, cta, u.first, pf);
-    const bool whole = u.whole();
-    for (int i = threadIdx.x; i < rows * D; i += kWarps * 32) {
-      const int r = i / D, c = i % D;
-      float M, L, A;
-      merge_warps<R, D>(s_m, s_l, s_acc, r, c, M, L, A);
-      if (whole) {
-        int head;
-        const int64_t row = row_of(r, head), oi = row * pv.H + head;
-        static_cast<T*>(a.o)[oi * D + c] = (T)(A / L);   // a token sees itself: L > 0
-        if (c == 0 && a.lse) a.lse[oi] = (M + log2f(L)) * kLn2;
-      } else {
-        part[i] = A;
-        if (c == 0) {
-          part[R * D + r] = M;
-          part[R * D + R + r] = L;
-        }
-      }
-    }
-    if (!whole) {
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        int32_t* count = paged_counter(a.ws, u.first);
-        s_last = arrive_acq_rel(count) == u.last - u.first;
-        if (s_last) *count = 0;                // ready for the next call
-      }
-      __syncthreads();
-      if (s_last) {
-        for (int r = warp; r < rows; r += kWarps) {
-          float M = -INFINITY;
-          for (int p = u.first + lane; p <= u.last; p += 32)
-            M = fmaxf(M, __ldcg(paged_partial(a.ws, p, u.first, pf) + R * D + r));
-          M = warp_max(M);
-          float L = 0.f;
-          for (int p = u.first + lane; p <= u.last; p += 32) {
-            const float* P = paged_partial(a.ws, p, u.first, pf) + R * D + r;
-            L += __ldcg(P + R) * fast_exp2(__ldcg(P) - M);
-          }
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-          if (lane == 0) {
-            s_M[r] = M;
-            s_L[r] = L;
-          }
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < rows * D; i += kWarps * 32) {
-          const int r = i / D, c = i % D;
-          const float M = s_M[r], L = s_L[r];
-          float A = 0.f;
-#pragma unroll 4
-          for (int p = u.first; p <= u.last; ++p) {
-            const float* P = paged_partial(a.ws, p, u.first, pf);
-            A = fmaf(__ldcg(P + i), fast_exp2(__ldcg(P + R * D + r) - M), A);
-          }
-          int head;
-          const int64_t row = row_of(r, head), oi = row * pv.H + head;
-          static_cast<T*>(a.o)[oi * D + c] = (T)(A / L);
-          if (c == 0 && a.lse) a.lse[oi] = (M + log2f(L)) * kLn2;
-        }
-      }
-    }
-    __syncthreads();
-    if (warp == 0) {
-      const bool more = plan.next();
-      if (lane == 0) {
-        s_more = more;
-        if (more) s_unit = plan.u;
-      }
-    }
-    __syncthreads();
-  }
-}
-
-// Small work, where latency counts: no list and no plan.  A cluster of CTAs takes R
-// query heads of one chunk row and KV head; its CTAs share the row's keys evenly and
-// hand their parts to the first through distributed shared memory.  What a call waits
-// for is a chain of reads (the row's sequence, its pages, the rows) and the join.
-template <typename T, int D, int R>
-__global__ void __launch_bounds__(kWarps * 32)
-paged_attend_small_kernel(PagesView pv, BatchArgs ba, AttendArgs a) {
   constexpr int U = R <= 2 ? 8 : 4;
   using C = AttendCfg<T, D, U>;
   constexpr int EPL = C::EPL, LPK = C::LPK, KPW = C::KPW;
@@ -415,77 +247,88 @@ paged_attend_small_kernel(PagesView pv, BatchArgs ba, AttendArgs a) {
   }
 }
 
-int grid_of(const PagesView& pv) { return std::min(2 * std::max(pv.sms, 1), kMaxPagedCtas); }
-
-template <typename T, int D>
-cudaError_t launch_d(const PagesView& pv, const BatchArgs& ba, const AttendArgs& a,
-                     cudaStream_t s) {
-  const bool one = (int64_t)ba.rows * pv.G <= ba.B;      // one row to a unit
-  return launch_dependent(one ? paged_attend_kernel<T, D, 1> : paged_attend_kernel<T, D, 4>,
-                          dim3(grid_of(pv)), dim3(kWarps * 32), 0, s, pv, ba, a);
-}
-
 }  // namespace
 
-// How a call is served.
-enum class Path { kSmall, kCudaCores, kFewRows, kTiles };
-// Query heads that a CTA of the small kernel takes, and the CTAs of a launch without
-// sharing keys.
-static int small_heads(const PagesView& pv) { return pv.G >= 3 ? 4 : pv.G; }
-static int64_t small_units(const PagesView& pv, int64_t rows) {
-  const int r = small_heads(pv);
+// Query heads that a CTA of the CUDA-core kernel takes, and its launch's CTAs before any
+// share keys.
+static int core_heads(const PagesView& pv) { return pv.G >= 3 ? 4 : pv.G; }
+static int64_t core_units(const PagesView& pv, int64_t rows) {
+  const int r = core_heads(pv);
   return rows * pv.Hkv * ((pv.G + r - 1) / r);
 }
+
+// How a call is served.  The host knows the rows and what the tables can hold, not the
+// lengths.  us on the CUDA cores / in units of few rows / of tiles; bf16, d 128:
+//   sequences, rows each, heads   keys 512          2048             8192
+//    1   1   10                   4.2/9.7/12.2      6.0/10.6/19.1    17.4/14.8/29.3
+//    1   4   10                   5.7/11.6/12.4     11.7/13.7/18.8   36.3/23.9/28.7
+//    1  16   10                   11.1/13.8/12.5    35.2/15.8/19.1   127/22.1/27.8
+//    1   1   32 / 8               5.5/11.4/12.3     9.2/13.5/18.6    22.9/23.1/28.5
+//    1   8   32 / 8               9.2/13.7/12.5     23.4/16.2/18.2   76.7/24.8/26.7
+//    8   1   32 / 8               9.2/12.5/12.9     30.4/20.1/23.6   112/48.8/64.3
+//    8   4   32 / 8               24.1/15.4/13.2    101/26.3/24.2    402/68.7/64.6
+//   16  16   10 (512, 1024, 4096) 86/21/22          161/34/29        581/104/75
+//   64   1   10                   37.2/33.6/52.2    131/104/136
+//   64   4   10                   93/36.7/54.2      317/105/137
+//   64  16   10                   332/70.8/55.5     1126/200/140
+//   64   1   32 / 8               62.9/32.9/48.6    223/84/114
+// The CUDA cores' CTAs have at most so many keys, and all of them so many elements of
+// keys, before the tensor cores are ahead; units of few rows read a sequence's keys
+// again for every 8 rows, which costs little while all units have CTAs at once.
+constexpr int64_t kCoreKeys = 6144, kCoreWork = 10 << 20, kFewRows = 8, kFewUnits = 40;
+enum class Path { kCudaCores, kFewRows, kTiles };
+static bool few_rows(const PagesView& pv, int64_t rows, int64_t batch) {
+  return rows * pv.G <= kFewRows * batch ||
+         (rows * pv.G + kFewRows - 1) / kFewRows * pv.Hkv <= kFewUnits;
+}
 static Path path_of(const PagesView& pv, int64_t rows, int64_t batch, int64_t keys) {
-  // SMALL
-  if (small_units(pv, rows) <= 2 * pv.sms && keys <= 2048) return Path::kSmall;
   if (!paged_attend_tc_supported(pv)) return Path::kCudaCores;
-  if (rows * pv.G <= 16 * batch) return Path::kFewRows;
-  return Path::kTiles;
+  const int64_t units = core_units(pv, rows);
+  if (keys <= kCoreKeys && units <= 2 * pv.sms && units * keys * pv.d <= kCoreWork)
+    return Path::kCudaCores;
+  return few_rows(pv, rows, batch) ? Path::kFewRows : Path::kTiles;
 }
 
 template <typename T, int D>
-static cudaError_t launch_small_d(const PagesView& pv, const BatchArgs& ba, const AttendArgs& a,
+static cudaError_t launch_cores_d(const PagesView& pv, const BatchArgs& ba, const AttendArgs& a,
                                   cudaStream_t s) {
-  const int64_t units = small_units(pv, ba.rows);
-  // CTAs that share a row's keys: as many as fill the SMs, with 64 keys each at least
+  const int r = core_heads(pv);
+  const int64_t units = core_units(pv, ba.rows);
+  // CTAs that share a row's keys: as many as are on the SMs together (registers allow
+  // two an SM, one with four heads; clusters of 8 do not fill the groups of SMs that
+  // they have to lie in: 16 of them, one CTA an SM, take two turns), with 64 keys each
+  // at least.
+  const int64_t room = (r == 4 ? 1 : 2) * (int64_t)pv.sms;
   int peers = 1;
-  while (peers < kMaxPeers && units * peers * 2 <= 2 * (int64_t)pv.sms && ba.cap >= 128 * peers)
+  while (peers < kMaxPeers && units * peers * 2 <= (peers == 4 ? room * 5 / 8 : room) &&
+         ba.cap >= 128 * peers)
     peers *= 2;
-  const int r = small_heads(pv);
-  auto kern = r == 1   ? paged_attend_small_kernel<T, D, 1>
-              : r == 2 ? paged_attend_small_kernel<T, D, 2>
-                       : paged_attend_small_kernel<T, D, 4>;
+  auto kern = r == 1   ? paged_attend_kernel<T, D, 1>
+              : r == 2 ? paged_attend_kernel<T, D, 2>
+                       : paged_attend_kernel<T, D, 4>;
   return launch_dependent_cluster(kern, dim3((unsigned)(units * peers)), dim3(kWarps * 32), 0, s,
                                   peers, pv, ba, a);
 }
 
-size_t paged_attend_workspace(const PagesView& pv, int64_t rows, int batch) {
-  size_t need = kPagedCounterBytes + (size_t)grid_of(pv) * 2 * 4 * (pv.d + 2) * sizeof(float);
-  if (paged_attend_tc_supported(pv)) {
-    need = std::max(need, paged_decode_tc_workspace(pv));
-    if (rows * pv.G > 16 * (int64_t)batch) need = std::max(need, paged_attend_tc_workspace(pv));
-  }
-  return need;
+size_t paged_attend_workspace(const PagesView& pv, int64_t rows) {
+  if (!paged_attend_tc_supported(pv)) return 256;
+  // whatever the number of sequences: more rows never need less
+  const size_t need = paged_decode_tc_workspace(pv);
+  return few_rows(pv, rows, 0) ? need : std::max(need, paged_attend_tc_workspace(pv));
 }
 
 cudaError_t launch_paged_attend(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
                                 const AttendArgs& a, cudaStream_t s) {
   switch (path_of(pv, ba.rows, ba.B, ba.cap)) {
-    case Path::kSmall:
-      if (pv.dtype == RSWA_F32)
-        return pv.d == 64 ? launch_small_d<float, 64>(pv, ba, a, s)
-                          : launch_small_d<float, 128>(pv, ba, a, s);
-      return pv.d == 64 ? launch_small_d<__nv_bfloat16, 64>(pv, ba, a, s)
-                        : launch_small_d<__nv_bfloat16, 128>(pv, ba, a, s);
     case Path::kTiles: return launch_paged_attend_tc(pv, maps, ba, a, s);
     case Path::kFewRows: return launch_paged_decode_tc(pv, maps, ba, a, s);
     default: break;
   }
   if (pv.dtype == RSWA_F32)
-    return pv.d == 64 ? launch_d<float, 64>(pv, ba, a, s) : launch_d<float, 128>(pv, ba, a, s);
-  return pv.d == 64 ? launch_d<__nv_bfloat16, 64>(pv, ba, a, s)
-                    : launch_d<__nv_bfloat16, 128>(pv, ba, a, s);
+    return pv.d == 64 ? launch_cores_d<float, 64>(pv, ba, a, s)
+                      : launch_cores_d<float, 128>(pv, ba, a, s);
+  return pv.d == 64 ? launch_cores_d<__nv_bfloat16, 64>(pv, ba, a, s)
+                    : launch_cores_d<__nv_bfloat16, 128>(pv, ba, a, s);
 }
 
 }  // namespace rswa

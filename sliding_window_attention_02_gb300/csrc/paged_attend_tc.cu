@@ -55,7 +55,7 @@ constexpr int NSEG = 4;                        // segments handed over at a time
 
 // The list's costs: a tile 1, a unit's first one its start and end as well.
 constexpr int kUnitCost = 2, kMinCost = 4;
-using Plan = PagedPlan<BN, true, kUnitCost, kMinCost>;
+using Plan = PagedPlan<BN, kUnitCost, kMinCost>;
 
 template <int D>
 struct Smem {

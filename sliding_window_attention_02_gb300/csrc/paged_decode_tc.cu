@@ -1,10 +1,10 @@
 // Attention of a few tokens of each sequence over a paged cache on the 5th-generation
 // tensor cores (tcgen05 + TMEM + TMA), bf16, head_dim 64 and 128.
 //
-// What it computes is paged_attend_tc.cu's, for units of at most 16 rows (token, head
+// What it computes is paged_attend_tc.cu's, for units of at most 8 rows (token, head
 // of the group).  So few rows are the MMAs' N: keys fill M, S^T = K Q^T (128 keys of a
-// tile x 16 rows) and O^T += V^T P^T (d x 16 rows, K = 128 keys), with the accumulators
-// in TMEM.  A key tile is read once for all rows of the unit and takes two short
+// tile x 16 columns, the least at that M) and O^T += V^T P^T (d x 16, K = 128 keys), with
+// the accumulators in TMEM.  A key tile is read once for all rows of the unit and takes two short
 // products, so the launch runs at the rate at which tiles arrive.
 //
 // Keys are fetched page by page, without the pages in which no row sees a token; V^T
@@ -39,7 +39,8 @@ namespace {
 using namespace ptx;
 
 constexpr int BN = 128;                        // keys per tile
-constexpr int NQ = 16;                         // MMA N: rows of a unit, padded
+constexpr int NQ = 16;                         // MMA N
+constexpr int kRows = 8;                       // rows of queries and weights that are kept
 constexpr int kEpiWarp0 = 4;
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kPlanWarp = 10;
 constexpr int kThreads = 352;
@@ -49,19 +50,15 @@ constexpr float kRescaleThreshold = 8.0f;      // log2 units
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
 // A unit's start and end take about as long as a tile.
-using Plan = PagedPlan<BN, true, 1, 2>;
+using Plan = PagedPlan<BN, 1, 2>;
 
-// Two CTAs an SM; one, with a ring twice as long, for more than 8 rows, whose
-// queries and weights leave no room for two.
-template <int D, int NG>
+template <int D>
 struct Smem {
   static constexpr int NSUB = D / 64;
   static constexpr uint32_t kTile = NSUB * kSub;
-  static constexpr int kCtas = NG <= 8 ? 2 : 1;
-  static constexpr int NS = 12 / kCtas / NSUB; // ring slots (a K or a V tile)
-  // Queries and weights as the MMAs' N rows.  Of up to 8 only those are kept: the
-  // other eight are then whatever follows them here, with results that nobody reads.
-  static constexpr int kRows = NG <= 8 ? 8 : 16;
+  static constexpr int NS = 6 / NSUB;          // ring slots (a K or a V tile)
+  // Queries and weights as the MMAs' N rows: 8 are kept, the other eight are whatever
+  // follows them here, with results that nobody reads.
   static constexpr uint32_t kNAtom = kRows * 128;                 // [kRows][64] bf16
   static constexpr uint32_t OFF_RING = 0;
   static constexpr uint32_t OFF_Q = OFF_RING + NS * kTile;        // two of [kRows][D]
@@ -96,7 +93,7 @@ struct Smem {
   // at most.
   static constexpr uint32_t kAtomStep = NSUB == 2 ? kSub : 1024;
   static_assert(NSUB == 2 || OFF_Q + 1024 <= OFF_MISC, "inside the CTA's shared memory");
-  static_assert((kBytes + 1024) * kCtas <= 233472, "CTAs of an SM");
+  static_assert((kBytes + 1024) * 2 <= 233472, "two CTAs per SM");
 };
 constexpr uint32_t TM_S = 0, TM_O = 32, TM_COLS = 64;
 
@@ -113,21 +110,43 @@ struct Segment {
 };
 static_assert(sizeof(Segment) <= 128, "segment");
 
-// A partial: for each row m, l, O[D].
-__host__ __device__ constexpr size_t partial_floats(int D) { return (size_t)NQ * (D + 2); }
+// A partial: for each row O[D], then m and l (and two words, so that rows are aligned to
+// 16 bytes).
+__host__ __device__ constexpr size_t partial_floats(int D) { return (size_t)kRows * (D + 4); }
 
 struct Shape {
   int G, box;
   int64_t q_stride;
 };
 
-// NG: the most rows that a unit has (1, 2, 4, 8 or 16).
+// N consecutive floats, aligned to as many bytes as they are (16 at most), from L2.
+template <int N>
+__device__ __forceinline__ void load_columns(const float* p, float* x) {
+  if constexpr (N == 1) {
+    x[0] = __ldcg(p);
+  } else if constexpr (N == 2) {
+    const float2 v = __ldcg(reinterpret_cast<const float2*>(p));
+    x[0] = v.x;
+    x[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(p + i));
+      x[i] = v.x;
+      x[i + 1] = v.y;
+      x[i + 2] = v.z;
+      x[i + 3] = v.w;
+    }
+  }
+}
+
+// NG: the most rows that a unit has (1, 2, 4 or 8).
 template <int D, int NG>
-__global__ void __launch_bounds__(kThreads, NG <= 8 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, 2)
 paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, PagesView pv, BatchArgs ba,
                        AttendArgs a, Shape sh, uint64_t wait_ns) {
-  using SM = Smem<D, NG>;
+  using SM = Smem<D>;
   constexpr int NSUB = SM::NSUB, NS = SM::NS;
   constexpr uint32_t kTile = SM::kTile, kNAtom = SM::kNAtom;
   extern __shared__ uint8_t smem_raw[];
@@ -514,7 +533,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmK,
       }
       if (mine)
 #pragma unroll
-        for (int g = 0; g < SM::kRows; ++g)
+        for (int g = 0; g < kRows; ++g)
           *reinterpret_cast<__nv_bfloat16*>(smem + SM::OFF_Q + (s & 1) * 2 * kNAtom +
                                             sw128_off(g, e, kNAtom)) =
               g < NG ? qv[g < NG ? g : 0] : __float2bfloat16(0.f);
@@ -560,10 +579,10 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmK,
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           if (g >= rows) break;
-          if (mine) P[g * (D + 2) + 2 + e] = __uint_as_float(ov[g]);
+          if (mine) P[g * (D + 4) + e] = __uint_as_float(ov[g]);
           if (e == 0) {
-            P[g * (D + 2)] = mg[g];
-            P[g * (D + 2) + 1] = lg[g];
+            P[g * (D + 4) + D] = mg[g];
+            P[g * (D + 4) + D + 1] = lg[g];
           }
         }
         if (!end_sync()) break;
@@ -575,43 +594,54 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmK,
         }
         if (!end_sync()) break;
         if (*s_last) {
-          // parts first .. last, row by row: the reads of eight parts at a time
-          auto part = [&](int p) { return paged_partial(a.ws, p, w.first, partial_floats(D)); };
-#pragma unroll 1
-          for (int g = 0; g < rows; ++g) {
-            float M = -INFINITY, L = 0.f, A = 0.f;
-#pragma unroll 1
-            for (int p0 = w.first; p0 <= w.last; p0 += 8) {
-              float mk[8], lk[8], ak[8];
+          // Each thread has some columns of one row; of that row, the reads of kParts
+          // parts, in the order of their CTAs, are on their way together.
+          constexpr int kPer = 128 / NG, kCols = D * NG / 128 > 0 ? D * NG / 128 : 1;
+          constexpr int kParts = kCols >= 8 ? 4 : 8;
+          const int g = e / kPer, c0 = e % kPer * kCols;
+          if (g < rows && c0 < D) {
+            float M = -INFINITY, L = 0.f, A[kCols];
 #pragma unroll
-              for (int x = 0; x < 8; ++x) {
+            for (int c = 0; c < kCols; ++c) A[c] = 0.f;
+#pragma unroll 1
+            for (int p0 = w.first; p0 <= w.last; p0 += kParts) {
+              float mk[kParts], lk[kParts], ak[kParts][kCols];
+#pragma unroll
+              for (int x = 0; x < kParts; ++x) {
                 mk[x] = -INFINITY;
-                lk[x] = ak[x] = 0.f;
+                lk[x] = 0.f;
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) ak[x][c] = 0.f;
                 if (p0 + x <= w.last) {
-                  const float* P = part(p0 + x) + g * (D + 2);
-                  mk[x] = __ldcg(P);
-                  lk[x] = __ldcg(P + 1);
-                  if (mine) ak[x] = __ldcg(P + 2 + e);
+                  const float* P =
+                      paged_partial(a.ws, p0 + x, w.first, partial_floats(D)) + g * (D + 4);
+                  const float2 ml = __ldcg(reinterpret_cast<const float2*>(P + D));
+                  mk[x] = ml.x;
+                  lk[x] = ml.y;
+                  load_columns<kCols>(P + c0, ak[x]);
                 }
               }
               float mn = M;
 #pragma unroll
-              for (int x = 0; x < 8; ++x) mn = fmaxf(mn, mk[x]);
+              for (int x = 0; x < kParts; ++x) mn = fmaxf(mn, mk[x]);
               const float ref = (mn == -INFINITY) ? 0.f : mn;
               const float s0 = fast_exp2(M - ref);
               L *= s0;
-              A *= s0;
 #pragma unroll
-              for (int x = 0; x < 8; ++x) {
+              for (int c = 0; c < kCols; ++c) A[c] *= s0;
+#pragma unroll
+              for (int x = 0; x < kParts; ++x) {
                 const float wx = fast_exp2(mk[x] - ref);
                 L = fmaf(lk[x], wx, L);
-                A = fmaf(ak[x], wx, A);
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) A[c] = fmaf(ak[x][c], wx, A[c]);
               }
               M = mn;
             }
             const int64_t row = out_row(g);
-            if (mine) o[row * D + e] = __float2bfloat16(A / L);
-            if (e == 0 && a.lse) a.lse[row] = (M + log2f(L)) * kLn2;
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) o[row * D + c0 + c] = __float2bfloat16(A[c] / L);
+            if (c0 == 0 && a.lse) a.lse[row] = (M + log2f(L)) * kLn2;
           }
         }
       }
@@ -632,9 +662,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmK,
   if (tid == 0 && *abort_flag) flag_error(pv.err, kErrWaitTimeout);
 }
 
-int grid_of(const PagesView& pv, int ctas) {
-  return std::min(ctas * std::max(pv.sms, 1), kMaxPagedCtas);
-}
+int grid_of(const PagesView& pv) { return std::min(2 * std::max(pv.sms, 1), kMaxPagedCtas); }
 
 template <int D, int NG>
 cudaError_t launch_g(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
@@ -646,9 +674,9 @@ cudaError_t launch_g(const PagesView& pv, const PagesMaps& maps, const BatchArgs
   auto kern = paged_decode_tc_kernel<D, NG>;
   // Per device (the attribute belongs to the current device's context).
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Smem<D, NG>::kBytes);
+                                       Smem<D>::kBytes);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kern, dim3(grid_of(pv, Smem<D, NG>::kCtas)), dim3(kThreads), Smem<D, NG>::kBytes, s, maps.k,
+  return launch_dependent(kern, dim3(grid_of(pv)), dim3(kThreads), Smem<D>::kBytes, s, maps.k,
                           maps.v, pv, ba, a, sh, phase_wait_limit_ns());
 }
 
@@ -656,18 +684,17 @@ template <int D>
 cudaError_t launch_d(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
                      const AttendArgs& a, cudaStream_t s) {
   // the most rows of a unit, where the host knows them
-  const int64_t rows = ba.starts ? NQ : (int64_t)ba.each * pv.G;
+  const int64_t rows = ba.starts ? kRows : (int64_t)ba.each * pv.G;
   if (rows <= 1) return launch_g<D, 1>(pv, maps, ba, a, s);
   if (rows <= 2) return launch_g<D, 2>(pv, maps, ba, a, s);
   if (rows <= 4) return launch_g<D, 4>(pv, maps, ba, a, s);
-  if (rows <= 8) return launch_g<D, 8>(pv, maps, ba, a, s);
-  return launch_g<D, 16>(pv, maps, ba, a, s);
+  return launch_g<D, 8>(pv, maps, ba, a, s);
 }
 
 }  // namespace
 
 size_t paged_decode_tc_workspace(const PagesView& pv) {
-  return kPagedCounterBytes + (size_t)grid_of(pv, 2) * 2 * partial_floats(pv.d) * sizeof(float);
+  return kPagedCounterBytes + (size_t)grid_of(pv) * 2 * partial_floats(pv.d) * sizeof(float);
 }
 
 cudaError_t launch_paged_decode_tc(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,

@@ -192,10 +192,10 @@ int rswa_pages_append(rswa_pages* pages, const rswa_batch* batch, int64_t rows, 
                                        static_cast<cudaStream_t>(stream)));
 }
 
-int rswa_pages_attend_workspace(rswa_pages* pages, int64_t rows, int batch, size_t* out_bytes) {
+int rswa_pages_attend_workspace(rswa_pages* pages, int64_t rows, size_t* out_bytes) {
   if (!live(pages)) return RSWA_EHANDLE;
-  if (!out_bytes || rows < 0 || batch < 1) return RSWA_EINVAL;
-  *out_bytes = paged_attend_workspace(pages->pv, rows, batch);
+  if (!out_bytes || rows < 0 || rows >= (int64_t(1) << 31)) return RSWA_EINVAL;
+  *out_bytes = paged_attend_workspace(pages->pv, rows);
   return RSWA_OK;
 }
 
@@ -212,7 +212,7 @@ int rswa_pages_attend(rswa_pages* pages, const rswa_batch* batch, int64_t rows, 
   if (!valid_rows(q, q_stride, len, rows, pv.dtype) || !o || !aligned16(o) || !aligned4(lse) ||
       !workspace || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0)
     return RSWA_EINVAL;
-  const size_t need = paged_attend_workspace(pv, rows, ba.B);
+  const size_t need = paged_attend_workspace(pv, rows);
   if (workspace_bytes < need) return RSWA_ECAPACITY;
   const InRows qr{q, q_stride, len};
   const Span out[3] = {{o, rows * len * elt},

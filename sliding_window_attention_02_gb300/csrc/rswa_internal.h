@@ -234,7 +234,7 @@ struct PagesMaps {
 };
 bool make_pages_maps(const PagesView& pv, PagesMaps* maps);
 // maps: of bf16 pools, else unused.
-size_t paged_attend_workspace(const PagesView& pv, int64_t rows, int batch);
+size_t paged_attend_workspace(const PagesView& pv, int64_t rows);
 cudaError_t launch_paged_attend(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
                                 const AttendArgs& a, cudaStream_t s);
 // On the tensor cores (paged_attend_tc.cu): bf16, at most 128 query heads per KV head.
@@ -242,7 +242,7 @@ bool paged_attend_tc_supported(const PagesView& pv);
 size_t paged_attend_tc_workspace(const PagesView& pv);
 cudaError_t launch_paged_attend_tc(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
                                    const AttendArgs& a, cudaStream_t s);
-// Units of at most 16 rows (paged_decode_tc.cu).
+// Units of at most 8 rows (paged_decode_tc.cu).
 size_t paged_decode_tc_workspace(const PagesView& pv);
 cudaError_t launch_paged_decode_tc(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
                                    const AttendArgs& a, cudaStream_t s);

@@ -222,6 +222,76 @@ def test_attend_holes_are_not_read(cuda_lib):
         assert c.pages.sync_status() == 0
 
 
+@pytest.mark.parametrize("H,Hkv,d,P", [(10, 10, 128, 64), (32, 8, 128, 16), (16, 2, 64, 128), (8, 4, 64, 256)])
+@pytest.mark.parametrize("T", [1, 2, 0])
+def test_attend_few_rows_of_many_sequences(cuda_lib, H, Hkv, d, P, T):
+    """Prefixes, windows and lengths that meet inside tiles and 16-key steps; NaN in
+    every row of a page that no row sees, pages that nobody sees gone; T 0: one to
+    three rows each."""
+    g = np.random.default_rng(H + T)
+    B = 72
+    T = [T] * B if T else [int(x) for x in g.integers(0, 4, B)]
+    L = [int(x) for x in g.integers(4, 1500, B)]
+    prefix = [int(x) for x in g.integers(0, 700, B)]
+    window = 90
+    c = Case(cuda_lib, L, T, H, Hkv, d, P, BF, prefix, window, seed=B, hole=1 << 30, uniform=T[0] == T[1] == T[2])
+    c.m = [min(m, l) for m, l in zip(prefix, L)]
+    for b in range(B):
+        lo, hi = c.m[b], max(c.m[b], L[b] - T[b] - window + 1)
+        hi = hi if T[b] else L[b]
+        for p in range(lo // P, -(-hi // P)):
+            a, z = max(lo, p * P), min(hi, (p + 1) * P)
+            if a < z:
+                c.Kp[c.where[b][p], :, a - p * P:z - p * P] = float("nan")
+                c.Vp[c.where[b][p], :, a - p * P:z - p * P] = float("nan")
+        for p in range(-(-lo // P), hi // P):
+            c.table[b, p] = -3
+    check_attend(c, *c.attend())
+    assert c.pages.sync_status() == 0
+
+
+@pytest.mark.parametrize("H,Hkv,d,P,L,T,m,n", [
+    (10, 10, 128, 64, [1], [1], None, None), (32, 8, 128, 32, [2600], [1], None, None),
+    (16, 2, 128, 16, [7000, 6500], [1, 1], [300, 0], 129), (10, 10, 128, 16, [7000], [8], None, None),
+    (32, 8, 64, 64, [9000], [3], [5], 4000), (12, 4, 128, 128, [6700, 3], [9, 3], None, None),
+])
+def test_attend_wide_tables(cuda_lib, H, Hkv, d, P, L, T, m, n):
+    """Tables that could hold long caches: few sequences on the tensor cores, units cut
+    over many CTAs."""
+    c = Case(cuda_lib, L, T, H, Hkv, d, P, BF, m, n, seed=5, spare=700)
+    check_attend(c, *c.attend())
+    assert c.pages.sync_status() == 0
+
+
+@pytest.mark.parametrize("H,Hkv,d,T", [(10, 10, 128, 1), (32, 8, 128, 1), (32, 8, 128, 70), (10, 10, 64, 300)])
+def test_waits_that_run_out(cuda_lib, H, Hkv, d, T):
+    """A bound of 1 ns on every wait: the kernels give up, the flag says so, and with
+    zeroed workspaces and the usual bound the next call is right."""
+    rswa = cuda_lib
+    c = Case(rswa, [900] * 40, [T] * 40, H, Hkv, d, 32, seed=1, uniform=True)
+    ws = c.pages.attend_workspace(40 * T)
+    w = torch.zeros(40, Hkv, c.width * 32, device="cuda")
+    _, lse = c.attend(workspace=ws)
+    for call in (lambda: c.attend(workspace=ws), lambda: c.pages.weigh(c.batch, c.q, lse, w)):
+        rswa.rswa_debug_set_wait_limit_ns(1)
+        try:
+            call()
+        finally:
+            rswa.rswa_debug_set_wait_limit_ns(0)
+        assert c.pages.sync_status() == RSWA_EDEVICE
+        assert c.pages.sync_status() == 0
+    ws.zero_()
+    o, lse = c.attend(workspace=ws)
+    c.L, c.T = c.L, [T] + [0] * 39
+    check_attend(c, o, lse, rows_of=[0, T - 1])
+    w.zero_()
+    c.pages.weigh(c.batch, c.q, lse, w, 0.0)
+    c.L = c.L[:1]
+    c.T = c.T[:1]
+    check_weigh(c, lse, torch.zeros_like(w), w, 0.0)
+    assert c.pages.sync_status() == 0
+
+
 def test_attend_strided_queries_in_place_and_streams(cuda_lib):
     c = Case(cuda_lib, [200, 90], [30, 3], 10, 10, 128, 32, seed=2)
     qkv = torch.full((33, 30, 128), float("nan"), dtype=BF, device="cuda")
@@ -602,14 +672,14 @@ def test_two_layers_share_a_batch_and_calls_overlap(cuda_lib):
 def test_workspaces(cuda_lib):
     c = Case(cuda_lib, [900, 40], [1, 30], 32, 8, 128, 32, seed=1)
     want, _ = c.attend()
-    ws = c.pages.attend_workspace(31, 2)
+    ws = c.pages.attend_workspace(31)
     for _ in range(3):
         o, _ = c.attend(workspace=ws)
         assert torch.equal(o, want)
     with pytest.raises(cuda_lib.RswaError) as e:
         c.attend(workspace=ws[:256])
     assert e.value.status == 2
-    big = c.pages.attend_workspace(5000, 9)            # serves fewer rows
+    big = c.pages.attend_workspace(5000)            # serves fewer rows
     assert torch.equal(c.attend(workspace=big)[0], want)
     with pytest.raises(ValueError):                    # a capture makes none
         s = torch.cuda.Stream()

@@ -118,7 +118,7 @@ def test_bad_handles(rswa):
     for handle in (None, ctypes.c_void_p(0x1234)):
         assert lib.rswa_pages_destroy(handle) == 4
         assert lib.rswa_pages_append(handle, ref, 1, 16, 0, 16, 0, None) == 4
-        assert lib.rswa_pages_attend_workspace(handle, 1, 1, ctypes.byref(size)) == 4
+        assert lib.rswa_pages_attend_workspace(handle, 1, ctypes.byref(size)) == 4
         assert lib.rswa_pages_attend(handle, ref, 1, 16, 0, 16, None, 256, 1 << 20, None) == 4
         assert lib.rswa_pages_weigh(handle, ref, 1, 16, 0, 16, 16, 1.0, None) == 4
         assert lib.rswa_pages_evict_workspace(handle, 1, 1, ctypes.byref(size)) == 4
