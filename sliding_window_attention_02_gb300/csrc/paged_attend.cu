@@ -310,6 +310,18 @@ static cudaError_t launch_cores_d(const PagesView& pv, const BatchArgs& ba, cons
                                   peers, pv, ba, a);
 }
 
+// float32 with many rows: tiles of 64 rows, which read keys once for all of them, take
+// 0.145 us a key (d 64: 0.083) and turn of CTAs, one an SM (d 64: two); the kernel above
+// 90 ps for a pair of row and key (d 64: 45), 55 (26) where four heads share keys.  us
+// here / in tiles at 512 keys: 1 sequence of 64 rows of 10 heads 40.6/75.7, of 256 106/75.6,
+// 8 of 16 rows 69.5/74.6, of 64 246/75.9, 64 of 8 286/369, of 16 552/370; of 32 / 8
+// heads 1 of 64 rows 66/75.7, 8 of 16 127/75.9.
+static bool f32_tiles(const PagesView& pv, const BatchArgs& ba) {
+  const int64_t rows = ba.rows, room = (pv.d == 64 ? 2 : 1) * (int64_t)pv.sms;
+  const int64_t units = std::max((rows * pv.G + 63) / 64, (int64_t)ba.B) * pv.Hkv;
+  return rows * pv.H > (pv.G >= 3 ? 2900 : 1700) * ((units + room - 1) / room);
+}
+
 size_t paged_attend_workspace(const PagesView& pv, int64_t rows) {
   if (!paged_attend_tc_supported(pv)) return 256;
   // whatever the number of sequences: more rows never need less
@@ -324,6 +336,7 @@ cudaError_t launch_paged_attend(const PagesView& pv, const PagesMaps& maps, cons
     case Path::kFewRows: return launch_paged_decode_tc(pv, maps, ba, a, s);
     default: break;
   }
+  if (paged_f32_supported(pv, ba) && f32_tiles(pv, ba)) return launch_paged_attend_f32(pv, ba, a, s);
   if (pv.dtype == RSWA_F32)
     return pv.d == 64 ? launch_cores_d<float, 64>(pv, ba, a, s)
                       : launch_cores_d<float, 128>(pv, ba, a, s);

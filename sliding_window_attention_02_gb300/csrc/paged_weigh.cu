@@ -108,6 +108,11 @@ cudaError_t launch_paged_weigh(const PagesView& pv, const PagesMaps& maps, const
                                float decay, cudaStream_t s) {
   if (paged_weigh_tc_supported(pv))
     return launch_paged_weigh_tc(pv, maps, ba, q, q_stride, lse, weights, decay, s);
+  // float32 with 16 rows (token, head of the group) of a sequence and more: in tiles of
+  // 64 (us here / in tiles at 512 keys: 8 sequences of 10 heads and 8 rows 22.4/28.1, 16
+  // rows 36.3/28.5; 64 of 32 / 8 heads and 2 rows 113/146, 4 rows 182/148).
+  if (paged_f32_supported(pv, ba) && (int64_t)ba.rows * pv.G >= 16 * (int64_t)ba.B)
+    return launch_paged_weigh_f32(pv, ba, q, q_stride, lse, weights, decay, s);
   if (pv.dtype == RSWA_F32)
     return pv.d == 64 ? launch_d<float, 64>(pv, ba, q, q_stride, lse, weights, decay, s)
                       : launch_d<float, 128>(pv, ba, q, q_stride, lse, weights, decay, s);

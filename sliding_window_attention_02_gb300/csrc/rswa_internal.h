@@ -254,6 +254,13 @@ bool paged_weigh_tc_supported(const PagesView& pv);
 cudaError_t launch_paged_weigh_tc(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
                                   const void* q, int64_t q_stride, const float* lse,
                                   float* weights, float decay, cudaStream_t s);
+// float32 caches with many rows (paged_f32.cu).
+bool paged_f32_supported(const PagesView& pv, const BatchArgs& ba);
+cudaError_t launch_paged_attend_f32(const PagesView& pv, const BatchArgs& ba, const AttendArgs& a,
+                                    cudaStream_t s);
+cudaError_t launch_paged_weigh_f32(const PagesView& pv, const BatchArgs& ba, const void* q,
+                                   int64_t q_stride, const float* lse, float* weights, float decay,
+                                   cudaStream_t s);
 struct EvictArgs {
   const float* weights;
   float* weights_out;

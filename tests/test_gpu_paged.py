@@ -263,6 +263,30 @@ def test_attend_wide_tables(cuda_lib, H, Hkv, d, P, L, T, m, n):
     assert c.pages.sync_status() == 0
 
 
+@pytest.mark.parametrize("H,Hkv,d,P", [(10, 10, 128, 16), (12, 4, 64, 128), (20, 2, 128, 256), (6, 6, 64, 32)])
+@pytest.mark.parametrize("T,prefix,window", [([300, 1, 0, 129], None, None), ([200, 90, 64, 3], [30, 0, 200, 5], 70)])
+def test_float32_with_many_rows(cuda_lib, H, Hkv, d, P, T, prefix, window):
+    """Tiles of 64 rows and keys; NaN in rows that nobody sees."""
+    L = [433, 257, 90, 200]
+    c = Case(cuda_lib, L, T, H, Hkv, d, P, F32, prefix, window, seed=H, hole=1 << 30)
+    if window:
+        for b in range(4):
+            lo, hi = c.m[b], L[b] - T[b] - window + 1
+            for j in range(lo, hi):
+                c.Kp[c.where[b][j // P], :, j % P] = float("nan")
+                c.Vp[c.where[b][j // P], :, j % P] = float("nan")
+    o, lse = c.attend()
+    check_attend(c, o, lse, rows_of=[0, 1, 20, 63, 64, 127, 128, 199, 299])
+    old = torch.rand(4, Hkv, c.width * P, device="cuda")
+    w = old.clone()
+    c.pages.weigh(c.batch, c.q, lse, w, 0.5)
+    check_weigh(c, lse, old, w, 0.5)
+    q = c.q.clone()
+    c.pages.attend(c.batch, q, q)
+    assert torch.equal(q, o)
+    assert c.pages.sync_status() == 0
+
+
 @pytest.mark.parametrize("H,Hkv,d,T", [(10, 10, 128, 1), (32, 8, 128, 1), (32, 8, 128, 70), (10, 10, 64, 300)])
 def test_waits_that_run_out(cuda_lib, H, Hkv, d, T):
     """A bound of 1 ns on every wait: the kernels give up, the flag says so, and with
