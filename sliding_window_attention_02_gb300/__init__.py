@@ -870,6 +870,9 @@ class _Workspaces:
         return self.at[stream]
 
 
+_NO_WORKSPACE = (None, 0, -1)
+
+
 class RswaPages:
     """A paged cache: a pool of pages plus the torch-allocated buffer behind it."""
 
@@ -889,7 +892,9 @@ class RswaPages:
         self._int32, self._float32 = torch.int32, torch.float32
         self._attend_ws = _Workspaces(ix, "attend")
         self._evict_ws = _Workspaces(ix, "evict")
-        self._attend_need, self._evict_need = {}, {}
+        self._attend_at = {}            # stream: (pointer, bytes, most rows) of attend's
+        self._evict_need = {}
+        self._lib = load()
 
     def close(self):
         if self.handle is not None:
@@ -914,8 +919,8 @@ class RswaPages:
         self._check_batch(batch)
         kp, ks = _rows(k, (rows, Hkv, d), dt, ix, "k")
         vp, vs = _rows(v, (rows, Hkv, d), dt, ix, "v")
-        status = load().rswa_pages_append(self.handle, batch.ref, rows, kp, ks, vp, vs,
-                                          _stream_of(stream, ix))
+        status = self._lib.rswa_pages_append(self.handle, batch.ref, rows, kp, ks, vp, vs,
+                                             _stream_of(stream, ix))
         if status:
             raise RswaError(status, "rswa_pages_append")
 
@@ -939,16 +944,17 @@ class RswaPages:
         lp = None if lse is None else _dense(lse, (rows, H), self._float32, ix, "lse")
         at = _stream_of(stream, ix)
         if workspace is None:
-            need = self._attend_need.get(rows)
-            if need is None:
-                need = self._attend_need[rows] = rswa_pages_attend_workspace(self.handle, rows)
-            wp, size = self._attend_ws.get(at, need)
+            # what is enough for these rows, if a call on this stream has had as many
+            wp, size, most = self._attend_at.get(at, _NO_WORKSPACE)
+            if rows > most:
+                wp, size = self._attend_ws.get(at, rswa_pages_attend_workspace(self.handle, rows))
+                self._attend_at[at] = wp, size, rows
         elif workspace.get_device() != ix:
             raise ValueError(f"workspace: expected a tensor on CUDA device {ix}")
         else:
             wp, size = _ptr(workspace), workspace.numel()
-        status = load().rswa_pages_attend(self.handle, batch.ref, rows, qp, qs, op, lp, wp, size,
-                                          at)
+        status = self._lib.rswa_pages_attend(self.handle, batch.ref, rows, qp, qs, op, lp, wp,
+                                             size, at)
         if status:
             raise RswaError(status, "rswa_pages_attend")
 
@@ -965,7 +971,7 @@ class RswaPages:
         rows = q.shape[0]
         self._check_batch(batch)
         qp, qs = _rows(q, (rows, H, d), dt, ix, "q")
-        status = load().rswa_pages_weigh(
+        status = self._lib.rswa_pages_weigh(
             self.handle, batch.ref, rows, qp, qs, _dense(lse, (rows, H), self._float32, ix, "lse"),
             self._weights(weights, batch, "weights"), decay, _stream_of(stream, ix))
         if status:
@@ -997,8 +1003,8 @@ class RswaPages:
             raise ValueError(f"workspace: expected a tensor on CUDA device {ix}")
         else:
             sp, size = _ptr(workspace), workspace.numel()
-        status = load().rswa_pages_evict(self.handle, batch.ref, wp, budget, first, last, tp, wo,
-                                         kp, sp, size, at)
+        status = self._lib.rswa_pages_evict(self.handle, batch.ref, wp, budget, first, last, tp,
+                                            wo, kp, sp, size, at)
         if status:
             raise RswaError(status, "rswa_pages_evict")
 

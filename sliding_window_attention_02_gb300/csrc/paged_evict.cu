@@ -151,12 +151,11 @@ evict_select_kernel(PagesView pv, BatchArgs ba, EvictArgs a, int chunks) {
       // two passes on, a slice's counts are written again: all have read them by then,
       // as they meet once more in between
       if (tid < 256) {
-        uint32_t sum = 0;
-        if (peers > 1)
-          for (int p = 0; p < peers; ++p) sum += peer_word(total + tid, p);
-        else
-          sum = total[tid];
-        s_sum[tid] = sum;
+        uint32_t c[8];                                   // reads on their way together
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          c[p] = p >= peers ? 0u : peers > 1 ? peer_word(total + tid, p) : total[tid];
+        s_sum[tid] = ((c[0] + c[1]) + (c[2] + c[3])) + ((c[4] + c[5]) + (c[6] + c[7]));
       }
       __syncthreads();
       if (warp == 0) {
