@@ -89,17 +89,17 @@ struct PagedUnit {
 
 // The planner, run by one whole warp with the same state in every lane.  The
 // tiles of a unit after each other, unit after unit (sequence by sequence, its rows
-// in order, the KV heads of the same rows next to each other), form one list; every
-// tile costs 1, a unit's first one EXTRA more.  CTA c of `ctas` takes the tiles that
-// begin in [from(c), from(c + 1)).
+// in order, the KV heads of the same rows next to each other), form one list; a tile
+// costs COST, or SPLIT in units with half of the rows or fewer, a unit's first one EXTRA
+// more.  CTA c of `ctas` takes the tiles that begin in [from(c), from(c + 1)).
 //
 // A group, the units of the same rows, is one entry of the sums that find a CTA's
 // range: 32 groups at a time, a lane each.  What a launch waits for before its first
 // loads is this code, run once: it is kept short (40 pages, one sequence of 16
 // groups: 2.7 us; with sums sequence by sequence and 64-bit divisions 4 to 5).
-template <int TILE, int EXTRA, int MINCOST>
+template <int TILE, int COST, int SPLIT, int EXTRA, int MINCOST>
 struct PagedPlan {
-  static_assert(MINCOST >= 1 + EXTRA, "a range holds a tile at least");
+  static_assert(MINCOST >= COST + EXTRA && COST >= SPLIT, "a range holds a tile at least");
   using Tiles = HullTiles<TILE>;
   const PagesView& pv;
   const BatchArgs& ba;
@@ -108,6 +108,7 @@ struct PagedPlan {
   int ctas = 1;
   PagedUnit u;
   int64_t ubase = 0;
+  bool half = false;                             // the unit's tiles cost SPLIT
 
   __device__ __forceinline__ PagedPlan(const PagesView& pv_, const BatchArgs& ba_, int rows)
       : pv(pv_), ba(ba_), unit_rows(rows), lane((int)(threadIdx.x & 31)) {}
@@ -162,8 +163,8 @@ struct PagedPlan {
         take(s, b0, src);
         const int before = src > 0 ? __shfl_sync(0xffffffffu, inc, src - 1) : 0;
         enter(g - before);
-        u.kvh = div(x0 - base, u.nt + EXTRA);
-        ubase = base + (int64_t)u.kvh * (u.nt + EXTRA);
+        u.kvh = div(x0 - base, unit_cost());
+        ubase = base + (int64_t)u.kvh * unit_cost();
         u.j0 = at_cost(x0 - ubase);
         return u.j0 < u.nt ? clip() : next();
       }
@@ -172,7 +173,7 @@ struct PagedPlan {
 
   // The next unit of the range; false: there is none.
   __device__ bool next() {
-    ubase += u.nt + EXTRA;
+    ubase += unit_cost();
     if (ubase >= x1) return false;
     u.j0 = 0;
     if (++u.kvh == pv.Hkv) {
@@ -196,6 +197,14 @@ struct PagedPlan {
   }
 
  private:
+  // Whether the unit from row f0 on has half of the rows or fewer.
+  __device__ __forceinline__ bool is_half(int T, int f0) const {
+    return 2 * (T * pv.G - f0) <= unit_rows;
+  }
+  __device__ __forceinline__ int tile_cost() const { return COST != SPLIT && half ? SPLIT : COST; }
+  __device__ __forceinline__ int64_t unit_cost() const {
+    return (int64_t)u.nt * tile_cost() + EXTRA;
+  }
   __device__ __forceinline__ int groups_of(const PagedSeq& s) const {
     return (s.T * pv.G + unit_rows - 1) / unit_rows;
   }
@@ -238,7 +247,8 @@ struct PagedPlan {
     const int m = __shfl_sync(0xffffffffu, s.m, src);
     if (g >= count) return 0;
     const int q = g - (e - (T * pv.G + unit_rows - 1) / unit_rows);
-    return (int64_t)(Tiles(hull_of(T, L, m, q * unit_rows)).nt + EXTRA) * pv.Hkv;
+    const int64_t tiles = Tiles(hull_of(T, L, m, q * unit_rows)).nt;
+    return (tiles * (is_half(T, q * unit_rows) ? SPLIT : COST) + EXTRA) * pv.Hkv;
   }
   __device__ __forceinline__ void take(const PagedSeq& s, int b0, int src) {
     u.b = b0 + src;
@@ -254,6 +264,7 @@ struct PagedPlan {
     u.np = t.np;
     u.kb = t.kb;
     u.nt = t.nt;
+    half = is_half(u.seq.T, u.f0);
   }
   static __device__ __forceinline__ int div(int64_t a, int64_t b) {
     return (int)((a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b));
@@ -266,15 +277,17 @@ struct PagedPlan {
   __device__ __forceinline__ int owner(int64_t x) const { return div((x + 1) * ctas - 1, total); }
   // The unit's first tile that begins at or after cost x of it.
   __device__ __forceinline__ int at_cost(int64_t x) const {
-    return x <= 0 ? 0 : (int)min(max(x - EXTRA, (int64_t)1), (int64_t)u.nt);
+    return x <= 0 ? 0
+           : x <= EXTRA ? 1
+                        : min(div(x - EXTRA + tile_cost() - 1, tile_cost()), u.nt);
   }
   __device__ __forceinline__ bool clip() {
-    if (ubase + (u.j0 > 0 ? u.j0 + EXTRA : 0) >= x1) return false;
+    if (ubase + (u.j0 > 0 ? u.j0 * (int64_t)tile_cost() + EXTRA : 0) >= x1) return false;
     u.j1 = at_cost(x1 - ubase);
     u.first = u.last = 0;
     if (!u.whole()) {
       u.first = owner(ubase);
-      u.last = owner(ubase + (u.nt > 1 ? u.nt - 1 + EXTRA : 0));
+      u.last = owner(ubase + (u.nt > 1 ? (u.nt - 1) * (int64_t)tile_cost() + EXTRA : 0));
     }
     return true;
   }

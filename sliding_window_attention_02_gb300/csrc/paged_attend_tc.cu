@@ -53,9 +53,10 @@ constexpr int kProducerWarp = 8, kMmaWarp = 9, kPlanWarp = 10;
 constexpr uint32_t kSub = BM * 64 * 2;         // [128][64] bf16, 128B-swizzled
 constexpr int NSEG = 4;                        // segments handed over at a time
 
-// The list's costs: a tile 1, a unit's first one its start and end as well.
-constexpr int kUnitCost = 2, kMinCost = 4;
-using Plan = PagedPlan<BN, kUnitCost, kMinCost>;
+// The list's costs, in units of about 1100 cycles: a tile of a pair 3, of a split unit 2,
+// a unit's first tile its start and end as well.
+constexpr int kTileCost = 3, kSplitCost = 2, kUnitCost = 6, kMinCost = 9;
+using Plan = PagedPlan<BN, kTileCost, kSplitCost, kUnitCost, kMinCost>;
 
 template <int D>
 struct Smem {
@@ -203,12 +204,25 @@ __device__ __noinline__ void join_own(void* ws, int first, int last, int half, i
                                       bool use1, float M, float L, int chunks,
                                       __nv_bfloat16* orow, float* lse) {
   auto part = [&](int p) { return half_partial(ws, p, first, half, D); };
+  const float* next = part(first + 1);         // there is one part behind, mostly no more
+  auto columns = [&](const float* p, int c) {
+    return reinterpret_cast<const float4*>(p) + (size_t)c * 8 * BM + r;
+  };
+  // its columns of the chunk at hand, asked for a chunk ahead
+  float4 u[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    u[e] = live ? __ldcg(columns(next, 0) + (size_t)e * BM) : make_float4(0.f, 0.f, 0.f, 0.f);
+  const float m1 = live ? __ldcg(next + (size_t)BM * D + r) : -INFINITY;
+  const float l1 = live ? __ldcg(next + (size_t)BM * (D + 1) + r) : 0.f;
   const float M0 = M;
-  for (int p = first + 1; live && p <= last; ++p)
+  M = fmaxf(M, m1);
+  for (int p = first + 2; live && p <= last; ++p)
     M = fmaxf(M, __ldcg(part(p) + (size_t)BM * D + r));
-  const float own = ex2(M0 - M);
-  L *= own;
-  for (int p = first + 1; live && p <= last; ++p) {
+  const float ref = M == -INFINITY ? 0.f : M;
+  const float own = ex2(M0 - ref), w1 = ex2(m1 - ref);
+  L = fmaf(l1, w1, L * own);
+  for (int p = first + 2; live && p <= last; ++p) {
     const float* a = part(p) + (size_t)BM * D + r;
     L = fmaf(__ldcg(a + BM), ex2(__ldcg(a) - M), L);
   }
@@ -219,6 +233,12 @@ __device__ __noinline__ void join_own(void* ws, int first, int last, int half, i
   for (int c = 0; c < chunks; ++c) {
     float x[32];
     uint32_t ov[32];
+    float4 v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[e] = u[e];
+      if (live && c + 1 < chunks) u[e] = __ldcg(columns(next, c + 1) + (size_t)e * BM);
+    }
 #pragma unroll
     for (int e = 0; e < 32; ++e) x[e] = 0.f;
     if (use0) {
@@ -232,21 +252,22 @@ __device__ __noinline__ void join_own(void* ws, int first, int last, int half, i
       for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(ov[e]), a1, x[e]);
     }
     if (!live) continue;
-#pragma unroll 1
-    for (int p = first + 1; p <= last; ++p) {
-      const float* a = part(p);
-      const float4* s = reinterpret_cast<const float4*>(a) + (size_t)c * 8 * BM + r;
-      const float wp = ex2(__ldcg(a + (size_t)BM * D + r) - M);
-      float4 u[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) u[e] = __ldcg(s + (size_t)e * BM);
+    auto add = [&](const float4* w, float wp) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[4 * e] = fmaf(u[e].x, wp, x[4 * e]);
-        x[4 * e + 1] = fmaf(u[e].y, wp, x[4 * e + 1]);
-        x[4 * e + 2] = fmaf(u[e].z, wp, x[4 * e + 2]);
-        x[4 * e + 3] = fmaf(u[e].w, wp, x[4 * e + 3]);
+        x[4 * e] = fmaf(w[e].x, wp, x[4 * e]);
+        x[4 * e + 1] = fmaf(w[e].y, wp, x[4 * e + 1]);
+        x[4 * e + 2] = fmaf(w[e].z, wp, x[4 * e + 2]);
+        x[4 * e + 3] = fmaf(w[e].w, wp, x[4 * e + 3]);
       }
+    };
+    add(v, w1);
+#pragma unroll 1
+    for (int p = first + 2; p <= last; ++p) {
+      const float wp = ex2(__ldcg(part(p) + (size_t)BM * D + r) - M);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __ldcg(columns(part(p), c) + (size_t)e * BM);
+      add(v, wp);
     }
     store_columns(orow + c * 32, x, inv);
   }

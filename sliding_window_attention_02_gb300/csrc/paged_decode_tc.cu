@@ -50,7 +50,7 @@ constexpr float kRescaleThreshold = 8.0f;      // log2 units
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
 // A unit's start and end take about as long as a tile.
-using Plan = PagedPlan<BN, 1, 2>;
+using Plan = PagedPlan<BN, 1, 1, 1, 2>;
 
 template <int D>
 struct Smem {
