@@ -31,7 +31,8 @@
 // on a key tile) alternate between the halves through the whole range; the MMA
 // order is QK(0) QK(1) PV(0) QK(2) PV(1) QK(3) ..., so the tensor core works on one
 // half while the other half's softmax runs.  TMEM: S0 | S1 | O0 | O1, P over S.  A
-// row of S is read once, into registers.  O is rescaled lazily (threshold 2^8, exact
+// row of S is read twice, 32 columns at a time: for its maximum, then for the
+// exponentials.  O is rescaled lazily (threshold 2^8, exact
 // because O and l share the reference).  Every wait is bounded; on a timeout the
 // CTA drains its copies and MMAs, frees TMEM and sets the pool's device flag.
 #include <cuda.h>
@@ -272,18 +273,6 @@ __device__ __noinline__ void join_own(void* ws, int first, int last, int half, i
     store_columns(orow + c * 32, x, inv);
   }
   if (lse && live) *lse = (M + log2f(L)) * kLn2;
-}
-
-// The registers of a TMEM load that an earlier wait has completed: no use of them
-// moves above this.
-__device__ __forceinline__ void landed32(uint32_t* r) {
-  asm volatile(""
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
-                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]),
-                 "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 
 template <int D>
@@ -719,33 +708,53 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         }
         const bool used = own_hull.meets(x0, x0 + BN);
         if (any && used) {
-          uint32_t x[128];
-          tmem_ld32(s_addr, x);
-          tmem_ld32(s_addr + 32, x + 32);
-          tmem_ld32(s_addr + 64, x + 64);
-          tmem_ld32(s_addr + 96, x + 96);
-          tmem_wait_ld32(x);
-          landed32(x + 32);
-          landed32(x + 64);
-          landed32(x + 96);
-          if (!full) {
+          // In loops of 64 columns: with the row in registers and all 128 columns
+          // unrolled the warps waited for instructions (74.1 us for 24 ragged chunks
+          // behind their prefixes, 67 in loops; one loop of 32 columns: 67.7, but a
+          // chunk behind 20K tokens 146.6 instead of 137).
+          float mx[2] = {-INFINITY, -INFINITY};
+          uint32_t va[32], vb[32];
+          auto maxima = [&](const uint32_t* v) {
 #pragma unroll
-            for (int e = 0; e < 128; ++e)
-              if (!(see[e >> 5] >> (e & 31) & 1u)) x[e] = 0xff800000u;
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            for (int e = 0; e < 32; e += 4) {
+              mx[0] = fmax3(mx[0], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+              mx[1] = fmax3(mx[1], __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+            }
+          };
+          if (full) {
+            tmem_ld32(s_addr, va);
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 64) {
+              tmem_wait_ld32(va);
+              tmem_ld32(s_addr + c + 32, vb);
+              maxima(va);
+              tmem_wait_ld32(vb);
+              tmem_ld32(s_addr + ((c + 64) & 127), va);
+              maxima(vb);
+            }
+            tmem_wait_ld32(va);
+          } else {                                       // masked scores: -inf, back in S
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t m4 = see[0];
+              see[0] = see[1];
+              see[1] = see[2];
+              see[2] = see[3];
+              tmem_ld32_sync(s_addr + 32 * c, va);
 #pragma unroll
-          for (int e = 0; e < 128; e += 8) {
-            mx[0] = fmax3(mx[0], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-            mx[1] = fmax3(mx[1], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
-            mx[2] = fmax3(mx[2], __uint_as_float(x[e + 4]), __uint_as_float(x[e + 5]));
-            mx[3] = fmax3(mx[3], __uint_as_float(x[e + 6]), __uint_as_float(x[e + 7]));
+              for (int e = 0; e < 32; ++e)
+                if (!(m4 >> e & 1u)) va[e] = 0xff800000u;
+              tmem_st32(s_addr + 32 * c, va);
+              maxima(va);
+            }
+            tmem_wait_st();
+            tmem_ld32_sync(s_addr, va);
           }
           // The reference of a row's exponentials stays until a score exceeds
           // it by more than 2^8 (any reference gives the same o and lse); then O
           // and l are rescaled.  O_h is stable here: S_h of this step completing
           // implies that the half's PV before it has.
-          const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+          const float tmax = fmaxf(mx[0], mx[1]) * sl2;
           const bool over = tmax > m_run + kRescaleThreshold;      // also where m_run is -inf
           if (__any_sync(0xffffffffu, over)) {
             const float alpha = over ? ex2(m_run - tmax) : 1.f;
@@ -766,32 +775,38 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
           // whose two operands are of one 16-bit type; l sums it unrounded.
           const float nref = (m_run == -INFINITY) ? 0.f : -m_run;
           const uint64_t sl2x2 = f2_pack(sl2, sl2), nref2 = f2_pack(nref, nref);
-          uint64_t ps[2] = {0, 0};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          uint64_t ps2 = 0;
+          auto exponentials = [&](const uint32_t* v, uint32_t to) {
             uint32_t p[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              float y0, y1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(x[32 * c + 2 * e]),
-                                       __uint_as_float(x[32 * c + 2 * e + 1])),
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
                                sl2x2, nref2),
-                        y0, y1);
-              const float p0 = ex2(y0), p1 = ex2(y1);
-              ps[e & 1] = f2_add(ps[e & 1], f2_pack(p0, p1));
+                        x0, x1);
+              const float p0 = ex2(x0), p1 = ex2(x1);
+              ps2 = f2_add(ps2, f2_pack(p0, p1));
               p[e] = pack_bf16(p0, p1);
             }
-            tmem_st16(s_addr + 16 * c, p);
-            if (c == 1) {                                // the product may begin
+            tmem_st16(to, p);
+          };
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            tmem_ld32(s_addr + 64 * c + 32, vb);
+            exponentials(va, s_addr + 32 * c);
+            tmem_wait_ld32(vb);
+            if (c == 0) tmem_ld32(s_addr + 64, va);
+            exponentials(vb, s_addr + 32 * c + 16);
+            tmem_wait_ld32(va);
+            if (c == 0) {
               tmem_wait_st();
               tc_fence_before();
               mbar_arrive(bar(SM::B_P + half));
             }
           }
-          float s0, s1, s2, s3;
-          f2_unpack(ps[0], s0, s1);
-          f2_unpack(ps[1], s2, s3);
-          l_run += (s0 + s1) + (s2 + s3);
+          float s0, s1;
+          f2_unpack(ps2, s0, s1);
+          l_run += s0 + s1;
           tmem_wait_st();
           tc_fence_before();
         } else {
