@@ -12,6 +12,15 @@
 
 namespace rswa {
 
+__device__ __forceinline__ int operator/(int x, const Divisor& by) {
+  return (int)(__umulhi((uint32_t)x << 1, by.m) >> by.s);
+}
+__device__ __forceinline__ int operator%(int x, const Divisor& by) { return x - x / by * by.d; }
+// a / b, a >= 0, b > 0; both mostly fit 32 bits, where a division is far shorter.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // A sequence of the batch.  One that the batch describes wrongly (rows or a
 // length outside their range, more rows than tokens) is flagged and taken as empty.
 struct PagedSeq {
@@ -74,7 +83,7 @@ struct HullTiles {
   }
 };
 
-// Where a CTA's walk over the work list stands: a unit (unit_rows rows (token,
+// Where a CTA's walk over the work list stands: a unit (a number of rows (token,
 // head of the group) of one KV head) and its tiles [j0, j1) in the CTA's range.
 struct PagedUnit {
   int b, kvh;
@@ -103,15 +112,16 @@ struct PagedPlan {
   using Tiles = HullTiles<TILE>;
   const PagesView& pv;
   const BatchArgs& ba;
-  int unit_rows, lane;
+  const Divisor& unit;                           // rows of a unit
+  int lane;
   int64_t total = 0, x1 = 0;
   int ctas = 1;
   PagedUnit u;
   int64_t ubase = 0;
   bool half = false;                             // the unit's tiles cost SPLIT
 
-  __device__ __forceinline__ PagedPlan(const PagesView& pv_, const BatchArgs& ba_, int rows)
-      : pv(pv_), ba(ba_), unit_rows(rows), lane((int)(threadIdx.x & 31)) {}
+  __device__ __forceinline__ PagedPlan(const PagesView& pv_, const BatchArgs& ba_, const Divisor& rows)
+      : pv(pv_), ba(ba_), unit(rows), lane((int)(threadIdx.x & 31)) {}
 
   // Finds the start of this CTA's range; false: it has none.
   __device__ bool start(int cta, int grid) {
@@ -163,7 +173,7 @@ struct PagedPlan {
         take(s, b0, src);
         const int before = src > 0 ? __shfl_sync(0xffffffffu, inc, src - 1) : 0;
         enter(g - before);
-        u.kvh = div(x0 - base, unit_cost());
+        u.kvh = (int)quotient(x0 - base, unit_cost());
         ubase = base + (int64_t)u.kvh * unit_cost();
         u.j0 = at_cost(x0 - ubase);
         return u.j0 < u.nt ? clip() : next();
@@ -178,8 +188,8 @@ struct PagedPlan {
     u.j0 = 0;
     if (++u.kvh == pv.Hkv) {
       u.kvh = 0;
-      int q = u.f0 / unit_rows + 1;
-      if (q * unit_rows >= u.seq.T * pv.G) {
+      int q = u.f0 / unit + 1;
+      if (q * unit.d >= u.seq.T * pv.G) {
         q = 0;
         // sequences without rows are passed over; there is one with some, as the
         // list goes on
@@ -199,18 +209,18 @@ struct PagedPlan {
  private:
   // Whether the unit from row f0 on has half of the rows or fewer.
   __device__ __forceinline__ bool is_half(int T, int f0) const {
-    return 2 * (T * pv.G - f0) <= unit_rows;
+    return 2 * (T * pv.G - f0) <= unit.d;
   }
   __device__ __forceinline__ int tile_cost() const { return COST != SPLIT && half ? SPLIT : COST; }
   __device__ __forceinline__ int64_t unit_cost() const {
     return (int64_t)u.nt * tile_cost() + EXTRA;
   }
   __device__ __forceinline__ int groups_of(const PagedSeq& s) const {
-    return (s.T * pv.G + unit_rows - 1) / unit_rows;
+    return s.T > 0 ? (s.T * pv.G - 1) / unit + 1 : 0;
   }
   __device__ __forceinline__ Hull hull_of(int T, int L, int m, int f0) const {
-    const int f1 = min(f0 + unit_rows, T * pv.G) - 1;
-    return Hull(L - T + f0 / pv.G, L - T + f1 / pv.G, m, ba.window);
+    const int f1 = min(f0 + unit.d, T * pv.G) - 1;
+    return Hull(L - T + f0 / pv.by_G, L - T + f1 / pv.by_G, m, ba.window);
   }
   __device__ __forceinline__ PagedSeq lane_seq(int b) const {
     PagedSeq s;
@@ -246,9 +256,9 @@ struct PagedPlan {
     const int L = __shfl_sync(0xffffffffu, s.L, src);
     const int m = __shfl_sync(0xffffffffu, s.m, src);
     if (g >= count) return 0;
-    const int q = g - (e - (T * pv.G + unit_rows - 1) / unit_rows);
-    const int64_t tiles = Tiles(hull_of(T, L, m, q * unit_rows)).nt;
-    return (tiles * (is_half(T, q * unit_rows) ? SPLIT : COST) + EXTRA) * pv.Hkv;
+    const int q = g - (e - (T > 0 ? (T * pv.G - 1) / unit + 1 : 0));
+    const int64_t tiles = Tiles(hull_of(T, L, m, q * unit.d)).nt;
+    return (tiles * (is_half(T, q * unit.d) ? SPLIT : COST) + EXTRA) * pv.Hkv;
   }
   __device__ __forceinline__ void take(const PagedSeq& s, int b0, int src) {
     u.b = b0 + src;
@@ -258,7 +268,7 @@ struct PagedPlan {
     u.seq.m = __shfl_sync(0xffffffffu, s.m, src);
   }
   __device__ __forceinline__ void enter(int q) {
-    u.f0 = q * unit_rows;
+    u.f0 = q * unit.d;
     u.hull = hull_of(u.seq.T, u.seq.L, u.seq.m, u.f0);
     const Tiles t(u.hull);
     u.np = t.np;
@@ -266,20 +276,16 @@ struct PagedPlan {
     u.nt = t.nt;
     half = is_half(u.seq.T, u.f0);
   }
-  static __device__ __forceinline__ int div(int64_t a, int64_t b) {
-    return (int)((a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b));
-  }
   __device__ __forceinline__ int64_t from(int c) const {
-    const int64_t p = total * c;
-    return p >> 32 ? p / ctas : (int64_t)((uint32_t)p / (uint32_t)ctas);
+    return quotient(total * c, ctas);
   }
   // The last CTA whose range begins at or before cost x.
-  __device__ __forceinline__ int owner(int64_t x) const { return div((x + 1) * ctas - 1, total); }
+  __device__ __forceinline__ int owner(int64_t x) const { return (int)quotient((x + 1) * ctas - 1, total); }
   // The unit's first tile that begins at or after cost x of it.
   __device__ __forceinline__ int at_cost(int64_t x) const {
     return x <= 0 ? 0
            : x <= EXTRA ? 1
-                        : min(div(x - EXTRA + tile_cost() - 1, tile_cost()), u.nt);
+                        : min((int)quotient(x - EXTRA + tile_cost() - 1, tile_cost()), u.nt);
   }
   __device__ __forceinline__ bool clip() {
     if (ubase + (u.j0 > 0 ? u.j0 * (int64_t)tile_cost() + EXTRA : 0) >= x1) return false;

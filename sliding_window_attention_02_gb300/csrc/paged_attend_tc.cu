@@ -102,6 +102,7 @@ constexpr uint64_t kWaitLimitNs = 1000000000ull;
 struct Shape {
   int npt;      // tokens of a query tile
   int G;        // query heads of a KV head
+  Divisor unit; // rows of a unit of two query tiles
   int box;      // rows of a K/V box: a page's, at most a tile's
 };
 
@@ -567,13 +568,13 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     if (lane == 0) prefetch_tmap(&tmQ);
     int qi = 0, tiles = 0;                       // query tiles requested, key tiles planned
     int k = 0;
-    Plan plan(pv, ba, 2 * sh.npt * sh.G);
+    Plan plan(pv, ba, sh.unit);
     for (bool more = plan.start(cta, gridDim.x); more; more = plan.next()) {
       const PagedUnit& u = plan.u;
       Segment w;
       w.b = u.b;
       w.kvh = u.kvh;
-      w.i0 = u.f0 / sh.G;
+      w.i0 = u.f0 / pv.by_G;
       w.row0 = u.seq.row0;
       w.T = u.seq.T;
       w.tok0 = u.seq.L - u.seq.T;
@@ -635,7 +636,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     // -------------------------------------------------- softmax and epilogue
     const int half = warp >> 2;
     const int r = threadIdx.x & 127;                    // row of the query tile
-    const int rg = r / sh.G, hg = r - rg * sh.G;        // its token in the tile, its head
+    const int rg = r / pv.by_G, hg = r - rg * sh.G;        // its token in the tile, its head
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const float sl2 = rsqrtf((float)D) * kLog2e;
     const uint32_t s_addr = tmem + lane_off + tm_s(half);
@@ -959,6 +960,7 @@ cudaError_t launch_d(const PagesView& pv, const PagesMaps& maps, const BatchArgs
   Shape sh;
   sh.G = pv.G;
   sh.npt = BM / sh.G;
+  sh.unit = Divisor(2 * sh.npt * sh.G);
   sh.box = std::min(pv.P, BN);
   CUtensorMap mq;
   const int64_t stride = ba.rows < 2 ? (int64_t)pv.H * D : a.q_stride;

@@ -116,6 +116,7 @@ __host__ __device__ constexpr size_t partial_floats(int D) { return (size_t)kRow
 
 struct Shape {
   int G, box;
+  Divisor unit;  // rows of a unit
   int64_t q_stride;
 };
 
@@ -329,7 +330,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmK,
   } else if (warp == kPlanWarp) {
     // ------------------------------------------------------------ planner
     Segment* out = reinterpret_cast<Segment*>(smem + SM::OFF_SEG);
-    Plan plan(pv, ba, NG);
+    Plan plan(pv, ba, sh.unit);
     int k = 0;
     for (bool more = plan.start(cta, gridDim.x); more; more = plan.next()) {
       if (k >= NSEG && !wait_all(SM::B_SEGFREE + k % NSEG, k / NSEG - 1)) break;
@@ -378,7 +379,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmK,
       const Hull hull = w.hull;
       const int rows = w.rows, m = w.m, j1 = w.j1;
       const int tok = w.tok0, f0 = w.f0, n = ba.window;
-      const int a0 = tok + f0 / sh.G, a1 = tok + (f0 + rows - 1) / sh.G;
+      const int a0 = tok + f0 / pv.by_G, a1 = tok + (f0 + rows - 1) / pv.by_G;
       float m_ref[NG], l_t[NG];
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
@@ -395,7 +396,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmK,
           } else {
 #pragma unroll 1
             for (int g = 0; g < rows; ++g) {
-              const int x = tok + (f0 + g) / sh.G;
+              const int x = tok + (f0 + g) / pv.by_G;
               if (t > x || (t >= m && t <= x - n)) sees &= ~(1u << g);
             }
           }
@@ -528,8 +529,8 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmK,
         qv[g] = __float2bfloat16(0.f);
         if (mine && g < w.rows)
           qv[g] = static_cast<const __nv_bfloat16*>(
-              a.q)[(int64_t)(w.row0 + f / sh.G) * sh.q_stride +
-                   (int64_t)(w.kvh * sh.G + f % sh.G) * D + e];
+              a.q)[(int64_t)(w.row0 + f / pv.by_G) * sh.q_stride +
+                   (int64_t)(w.kvh * sh.G + f % pv.by_G) * D + e];
       }
       if (mine)
 #pragma unroll
@@ -563,7 +564,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmK,
       // Row g of the unit is chunk row f / G, query head kvh * G + f % G.
       auto out_row = [&](int g) {
         const int f = w.f0 + g;
-        return (int64_t)(w.row0 + f / sh.G) * pv.H + w.kvh * sh.G + f % sh.G;
+        return (int64_t)(w.row0 + f / pv.by_G) * pv.H + w.kvh * sh.G + f % pv.by_G;
       };
       __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o);
       if (w.whole) {
@@ -669,6 +670,7 @@ cudaError_t launch_g(const PagesView& pv, const PagesMaps& maps, const BatchArgs
                      const AttendArgs& a, cudaStream_t s) {
   Shape sh;
   sh.G = pv.G;
+  sh.unit = Divisor(NG);
   sh.box = std::min(pv.P, BN);
   sh.q_stride = a.q_stride;
   auto kern = paged_decode_tc_kernel<D, NG>;

@@ -73,6 +73,7 @@ struct Smem {
 
 struct Shape {
   int npt;      // tokens of a row tile
+  Divisor by_npt;
   int G;        // query heads of a KV head
   int box;      // rows of a key box: a page's, at most a tile's
   int all;      // 1: tiles that nobody sees are listed as well
@@ -90,7 +91,7 @@ struct Segment {
 static_assert(sizeof(Segment) <= 64, "segment");
 
 // Row tiles [lo, hi) that may see a token of the key tile at x0.
-__device__ __forceinline__ void row_tiles(const Segment& w, int j, int npt, int n, int& lo,
+__device__ __forceinline__ void row_tiles(const Segment& w, int j, const Divisor& npt, int n, int& lo,
                                           int& hi) {
   if (w.T == 0 || (j >= w.np && j < w.np + w.gap)) {
     lo = hi = 0;
@@ -98,7 +99,7 @@ __device__ __forceinline__ void row_tiles(const Segment& w, int j, int npt, int 
   }
   const int x0 = w.tile(j) * BN, tok0 = w.L - w.T;
   lo = max(x0 - tok0, 0) / npt;
-  hi = x0 < w.m ? w.nrt : min(w.nrt, max(x0 + BN - 1 + n - 1 - tok0, -1) / npt + 1);
+  hi = x0 < w.m ? w.nrt : min(w.nrt, max(x0 + BN - 1 + n - 1 - tok0, 0) / npt + 1);
   if (x0 >= w.m && x0 + BN - 1 + n - 1 < tok0) hi = lo;
 }
 
@@ -129,10 +130,10 @@ struct WeighPlan {
     }
     w.gap = sh.all ? w.kb - w.np : 0;
     nt = w.np + w.gap + tiles - w.kb;
-    w.nrt = (T + sh.npt - 1) / sh.npt;
+    w.nrt = T > 0 ? (T - 1) / sh.by_npt + 1 : 0;
     cA = kTileCost + w.nrt;
     // tokens that see a band tile: n + 127 of them at most
-    cB = kTileCost + (int)min((int64_t)w.nrt, ((int64_t)ba.window + BN - 2) / sh.npt + 2);
+    cB = kTileCost + min(w.nrt, (ba.window + BN - 2) / sh.by_npt + 2);
   }
   __device__ __forceinline__ int64_t cost_before(int j) const {
     const int a = min(j, w.np), g = min(j - a, w.gap);
@@ -142,9 +143,9 @@ struct WeighPlan {
   __device__ __forceinline__ int at(int64_t x) const {
     if (x <= 0) return 0;
     const int64_t a = (int64_t)w.np * cA;
-    if (x <= a) return (int)((x + cA - 1) / cA);
+    if (x <= a) return (int)quotient(x + cA - 1, cA);
     if (x <= a + w.gap) return w.np + (int)(x - a);
-    return (int)min((int64_t)nt, w.np + w.gap + (x - a - w.gap + cB - 1) / cB);
+    return (int)min((int64_t)nt, w.np + w.gap + quotient(x - a - w.gap + cB - 1, cB));
   }
   __device__ __forceinline__ PagedSeq lane_seq(int b) const {
     PagedSeq s;
@@ -180,8 +181,8 @@ struct WeighPlan {
       }
       total += __shfl_sync(0xffffffffu, inc, 31);
     }
-    x0 = total * cta / ctas;
-    x1 = total * (cta + 1) / ctas;
+    x0 = quotient(total * cta, ctas);
+    x1 = quotient(total * (cta + 1), ctas);
     if (x0 >= x1) return false;
     for (int b0 = 0;; b0 += 32) {
       if (b0 > 0) {
@@ -200,7 +201,7 @@ struct WeighPlan {
       break;
     }
     const int64_t per = cost_before(nt);
-    w.kvh = (int)((x0 - base) / per);
+    w.kvh = (int)quotient(x0 - base, per);
     base += w.kvh * per;
     return clip() || next();
   }
@@ -296,7 +297,7 @@ paged_weigh_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       const Hull hull(w.L - w.T, w.L - 1, w.m, n);
       for (int j = w.j0; ok && j < w.j1; ++j) {
         int lo, hi;
-        row_tiles(w, j, sh.npt, n, lo, hi);
+        row_tiles(w, j, sh.by_npt, n, lo, hi);
         if (lo >= hi) continue;
         const int t0 = w.tile(j) * BN + lane * sh.box;
         int page = -1;                         // of this lane's box; -1: nobody sees it
@@ -339,7 +340,7 @@ paged_weigh_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
         bool have = false;
         for (int j = w.j0; ok && j < w.j1; ++j) {
           int lo, hi;
-          row_tiles(w, j, sh.npt, n, lo, hi);
+          row_tiles(w, j, sh.by_npt, n, lo, hi);
           if (lo >= hi) continue;
           const uint32_t s = gi % NS;
           if (!(ok = wait(SM::B_FULL + s, gi / NS))) break;
@@ -393,7 +394,7 @@ paged_weigh_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                       w.row0 + r * sh.npt, bar(SM::B_QF + s));
       }
       for (int c = lane; c < NR; c += 32) {
-        const int i = r * sh.npt + c / sh.G;
+        const int i = r * sh.npt + c / pv.by_G;
         float x = 0.f;
         if (c < sh.npt * sh.G && i < w.T)
           x = lse[(int64_t)(w.row0 + i) * pv.H + w.kvh * sh.G + c % sh.G] * kLog2e;
@@ -409,7 +410,7 @@ paged_weigh_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       bool have = false;
       for (int j = w.j0; ok && j < w.j1; ++j) {
         int lo, hi;
-        row_tiles(w, j, sh.npt, n, lo, hi);
+        row_tiles(w, j, sh.by_npt, n, lo, hi);
         for (int r = lo; ok && r < hi; ++r)
           if (w.nrt > 1 || !have) {
             ok = load(w, r);
@@ -454,7 +455,7 @@ paged_weigh_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       bool have = false;
       for (int j = w.j0; ok && j < w.j1; ++j) {
         int lo, hi;
-        row_tiles(w, j, sh.npt, n, lo, hi);
+        row_tiles(w, j, sh.by_npt, n, lo, hi);
         const int t = w.tile(j) * BN + tid;
         float* out = weights + ((int64_t)w.b * pv.Hkv + w.kvh) * ba.cap + t;
         float old = 0.f;
@@ -528,6 +529,7 @@ cudaError_t launch_r(const PagesView& pv, const PagesMaps& maps, const BatchArgs
   Shape sh;
   sh.G = pv.G;
   sh.npt = NR / pv.G;
+  sh.by_npt = Divisor(sh.npt);
   sh.box = std::min(pv.P, BN);
   sh.all = decay != 1.f;
   sh.decay = decay;

@@ -134,6 +134,7 @@ int rswa_pages_create(int64_t pages, int page_size, int heads, int kv_heads, int
   pv.H = heads;
   pv.Hkv = kv_heads;
   pv.G = heads / kv_heads;
+  pv.by_G = Divisor(pv.G);
   pv.d = head_dim;
   pv.dtype = dtype;
   pv.sms = sms;

@@ -201,12 +201,27 @@ cudaError_t launch_commit_tree(const CacheView& cv, const void* k, const void* v
                                cudaStream_t s);
 
 // A pool of pages: K, V [pages][Hkv][P][d], P tokens a page (a power of two).
+
+// x / d for 0 <= x < 2^31, without a division on the device: m = ceil(2^(31 + s) / d)
+// with s = ceil(log2 d) is off by less than d / 2^(31 + s) of itself, which moves no
+// quotient of such an x over a whole number.
+struct Divisor {
+  int d = 1;
+  uint32_t m = 1u << 31;
+  int s = 0;
+  Divisor() = default;
+  explicit Divisor(int div) : d(div) {
+    while (int64_t(1) << s < div) ++s;
+    m = (uint32_t)(((uint64_t(1) << (31 + s)) + div - 1) / div);
+  }
+};
 struct PagesView {
   void* K;
   void* V;
   int32_t* err;            // first device-side error code (0 = none)
   int pages, P, log2P;
   int H, Hkv, G, d, dtype; // G = H / Hkv
+  Divisor by_G;
   int sms;
 };
 // What a call says of its sequences (rswa_batch).
