@@ -556,6 +556,31 @@ def test_evict_long_sequences(cuda_lib):
               lambda *s: torch.arange(s[-1], device="cuda").float().expand(*s).contiguous())
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("L,Hkv", [
+    ([9000, 4097, 5], 2),             # clusters, weights in registers
+    ([70000], 1),                     # more of them
+    ([140000, 90000], 1),             # and read again
+    ([4500] + [300] * 51, 3),         # a CTA for each head, in registers
+    ([17000] + [40] * 51, 3),         # and read again
+])
+def test_evict_slices(cuda_lib, L, Hkv, in_place):
+    """Ties and odd weights across the slices and rounds of long sequences."""
+    def few(*shape):
+        return torch.randint(0, 3, shape, device="cuda").float()
+
+    def odd(*shape):
+        x = torch.randn(shape, device="cuda")
+        x[torch.rand(shape, device="cuda") < 0.3] = float("nan")
+        x[torch.rand(shape, device="cuda") < 0.1] = float("inf")
+        x[torch.rand(shape, device="cuda") < 0.1] = -0.0
+        return x
+
+    for i, weights in enumerate((few, odd, None)):
+        for budget in (37, max(L) // 3, max(L) - 1):
+            run_evict(cuda_lib, L, Hkv, 64, 256, BF, budget, budget // 5, budget // 3, in_place, weights, seed=i)
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
