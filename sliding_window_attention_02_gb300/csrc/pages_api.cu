@@ -58,7 +58,7 @@ int take_batch(const PagesView& pv, const rswa_batch* bt, int64_t rows, BatchArg
   if (!aligned4(bt->table) || !aligned4(bt->lens) || !aligned4(bt->prefix) ||
       !aligned4(bt->starts))
     return RSWA_EINVAL;
-  if (rows < 0 || rows * pv.H >= (int64_t(1) << 31)) return RSWA_EINVAL;
+  if (rows < 0 || rows > ((int64_t(1) << 31) - 1) / pv.H) return RSWA_EINVAL;
   if (!bt->starts && rows % bt->batch != 0) return RSWA_EINVAL;
   out->table = bt->table;
   out->lens = bt->lens;
@@ -75,6 +75,11 @@ int take_batch(const PagesView& pv, const rswa_batch* bt, int64_t rows, BatchArg
 
 int64_t pool_bytes(const PagesView& pv) {
   return (int64_t)pv.pages * pv.Hkv * pv.P * pv.d * (pv.dtype == RSWA_F32 ? 4 : 2);
+}
+
+// More weights than a 64-bit number of bytes counts.
+bool too_many(const PagesView& pv, const BatchArgs& ba) {
+  return (int64_t)ba.B * pv.Hkv > (int64_t(1) << 60) / ba.cap;
 }
 
 // Whether `out` shares a byte with the pool or with what describes the batch.
@@ -247,7 +252,8 @@ int rswa_pages_weigh(rswa_pages* pages, const rswa_batch* batch, int64_t rows, c
   BatchArgs ba{};
   const int st = take_batch(pv, batch, rows, &ba);
   if (st != RSWA_OK) return st;
-  if (!weights || !aligned4(weights) || !(decay >= 0.f) || decay > 1.f) return RSWA_EINVAL;
+  if (!weights || !aligned4(weights) || !(decay >= 0.f) || decay > 1.f || too_many(pv, ba))
+    return RSWA_EINVAL;
   const int64_t len = (int64_t)pv.H * pv.d, elt = pv.dtype == RSWA_F32 ? 4 : 2;
   const Span out{weights, (int64_t)ba.B * pv.Hkv * ba.cap * 4};
   if (meets_batch(pv, ba, out)) return RSWA_EINVAL;
@@ -288,7 +294,7 @@ int rswa_pages_evict(rswa_pages* pages, const rswa_batch* batch, const float* we
     return RSWA_EINVAL;
   const int64_t heads = (int64_t)ba.B * pv.Hkv;
   const int64_t rows = std::min<int64_t>(budget, ba.cap);
-  if (heads * ((rows + 31) / 32) >= (int64_t(1) << 31)) return RSWA_EINVAL;
+  if (too_many(pv, ba) || heads * ((rows + 31) / 32) >= (int64_t(1) << 31)) return RSWA_EINVAL;
   const size_t need = paged_evict_workspace(pv, ba.B, budget, kept != nullptr);
   if (workspace_bytes < need) return RSWA_ECAPACITY;
   const int64_t wb = heads * ba.cap * 4;

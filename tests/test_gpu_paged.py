@@ -888,3 +888,20 @@ def test_pool_beyond_32_bit_offsets(cuda_lib):
             at = torch.tensor(paged.evict(wn[b, h, :c.L[b]], 200, 4, 50), device="cuda")
             assert torch.equal(c.tokens(K, b, 200)[:, h], c.K[b][at, h])
             assert torch.equal(c.tokens(V, b, 200)[:, h], c.V[b][at, h])
+
+
+def test_refusals_of_counts_that_wrap(cuda_lib):
+    """Rows and weights whose products pass 64 bits."""
+    c = Case(cuda_lib, [100], [3], 16, 16, 64, 16, seed=3)
+    pages, lib = c.pages, c.pages._lib
+    o, lse, w = torch.empty_like(c.q), torch.empty(3, 16, device="cuda"), torch.zeros(1, 16, c.width * 16, device="cuda")
+    ws = torch.zeros(cuda_lib.rswa_pages_attend_workspace(pages.handle, 3), dtype=torch.uint8, device="cuda")
+    for rows in (1 << 60, 1 << 59, (1 << 63) - 1, (1 << 31) // 16):
+        stride = 16 * 64
+        assert lib.rswa_pages_append(pages.handle, c.batch.ref, rows, c.k.data_ptr(), stride, c.v.data_ptr(), stride,
+                                     None) == 1
+        assert lib.rswa_pages_attend(pages.handle, c.batch.ref, rows, c.q.data_ptr(), stride, o.data_ptr(),
+                                     lse.data_ptr(), ws.data_ptr(), ws.numel(), None) == 1
+        assert lib.rswa_pages_weigh(pages.handle, c.batch.ref, rows, c.q.data_ptr(), stride, lse.data_ptr(),
+                                    w.data_ptr(), 1.0, None) == 1
+    assert pages.sync_status() == 0
