@@ -12,6 +12,9 @@
 // distributed shared memory.  What a small call waits for is a chain of reads (the
 // row's sequence, its pages, the rows) and the join; beyond some 50000 pairs of a query
 // row and a key it is bound by those, as every CTA reads its keys through L2 for itself.
+// Measured: one token of 10 heads over 488 (288 in the prefix) 4.25 us in a graph, 5.3 a
+// call; float32, 3 sequences of 4 / 2 heads, d 64, up to 90 rows of 700 tokens, 6.4 (below:
+// the rule between the paths, with all three measured).
 #include <algorithm>
 
 #include "attend.cuh"
@@ -260,21 +263,23 @@ static int64_t core_units(const PagesView& pv, int64_t rows) {
 // How a call is served.  The host knows the rows and what the tables can hold, not the
 // lengths.  us on the CUDA cores / in units of few rows / of tiles; bf16, d 128:
 //   sequences, rows each, heads   keys 512          2048             8192
-//    1   1   10                   4.2/9.7/12.2      6.0/10.6/19.1    17.4/14.8/29.3
-//    1   4   10                   5.7/11.6/12.4     11.7/13.7/18.8   36.3/23.9/28.7
-//    1  16   10                   11.1/13.8/12.5    35.2/15.8/19.1   127/22.1/27.8
-//    1   1   32 / 8               5.5/11.4/12.3     9.2/13.5/18.6    22.9/23.1/28.5
-//    1   8   32 / 8               9.2/13.7/12.5     23.4/16.2/18.2   76.7/24.8/26.7
-//    8   1   32 / 8               9.2/12.5/12.9     30.4/20.1/23.6   112/48.8/64.3
-//    8   4   32 / 8               24.1/15.4/13.2    101/26.3/24.2    402/68.7/64.6
-//   16  16   10 (512, 1024, 4096) 86/21/22          161/34/29        581/104/75
-//   64   1   10                   37.2/33.6/52.2    131/104/136
-//   64   4   10                   93/36.7/54.2      317/105/137
-//   64  16   10                   332/70.8/55.5     1126/200/140
-//   64   1   32 / 8               62.9/32.9/48.6    223/84/114
+//    1   1   10                   4.3/9.7/11.2      6.0/10.4/18.7    17.2/14.5/28.8
+//    1   4   10                   5.8/10.5/11.5     11.7/11.5/18.3   36.3/16.0/27.3
+//    1  16   10                   11.1/12.8/11.8    35.0/15.0/18.3   127/21.6/27.0
+//    1   1   32 / 8               5.5/10.4/11.3     9.2/11.3/18.0    23.1/15.2/27.0
+//    1   8   32 / 8               9.2/12.9/11.7     23.3/15.6/17.2   76.4/24.1/25.4
+//    8   1   32 / 8               9.2/11.5/12.0     30.3/18.8/22.5   112/47.6/61.8
+//    8   4   32 / 8               24.2/14.5/12.5    101/25.6/22.7    402/67.8/62.4
+//   16  16   10 (512, 1024, 4096) 86/20/20          161/34/27        582/105/71
+//   64   1   10                   37.2/33.2/50.5    131/104/130
+//   64   4   10                   93/34.8/52.2      317/105/132
+//   64  16   10                   332/64.9/52.9     1126/202/134
+//   64   1   32 / 8               62.7/31.5/45.0    223/87/108
 // The CUDA cores' CTAs have at most so many keys, and all of them so many elements of
 // keys, before the tensor cores are ahead; units of few rows read a sequence's keys
-// again for every 8 rows, which costs little while all units have CTAs at once.
+// again for every 8 rows, which costs little while all units have CTAs at once.  Over 300
+// shapes the path taken is at worst 1.45 times the best one (1 sequence of 4 rows of 16 /
+// 2 heads over 4096 keys: 23.2/15.9/18.5).
 constexpr int64_t kCoreKeys = 6144, kCoreWork = 10 << 20, kFewRows = 8, kFewUnits = 40;
 enum class Path { kCudaCores, kFewRows, kTiles };
 static bool few_rows(const PagesView& pv, int64_t rows, int64_t batch) {

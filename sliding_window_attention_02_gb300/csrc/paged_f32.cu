@@ -7,7 +7,8 @@
 // FMAs) and 4 rows x d / 16 columns of the output (d 128: 12 reads for 128 FMAs);
 // copies of the next tile run meanwhile (cp.async, two stages).  Rows of 16 threads
 // share a query row, so that its softmax statistics and its weights stay within half
-// a warp.
+// a warp.  Measured: 8 sequences of 256 rows of 10 heads over 512 keys, attention 179 us
+// and weights 83; with keys read for every row 800 and 367.
 #include <algorithm>
 
 #include "paged.cuh"

@@ -5,7 +5,9 @@
 // CUDA-core form.  A CTA takes kKeys tokens of one (sequence, KV head): a lane
 // group holds a few of its keys in registers and goes over all rows that may see
 // one of them, so that a token's sum is made in one place, in the order of the
-// rows, without atomics.
+// rows, without atomics.  For float32 with few rows and for groups of more than 64
+// heads: bound by a lane group's chain of row reads (float32, one sequence of a row of
+// 10 heads over 512 keys 3.0 us, tiles of 64 x 64 7.8; 8 of 64 rows 118 and 32).
 #include <algorithm>
 
 #include "attend.cuh"

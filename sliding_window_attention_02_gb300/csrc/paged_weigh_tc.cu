@@ -21,6 +21,12 @@
 // page of a tile), warp 5 TMEM allocator and MMA issuer, warp 6 query rows (TMA) and
 // their lse, warp 7 planner.  TMEM: S^T twice.  Every wait is bounded; on a timeout the
 // CTA drains its copies and MMAs, frees TMEM and sets the pool's device flag.
+//
+// Measured: 64 tokens of 32 / 8 heads over 256..4096 (262 MB) 46 us, 0.84 of the measured
+// copy, the rest start and end; on the CUDA cores 231.  64 rows of 10 heads over 10272
+// tokens 10.8 (9.5 in a graph) for a floor of 4.0: start, plan and first keys 5, a
+// tile's turn 1; on the CUDA cores 174.  NR is 64 where one tile of 16 does not hold a
+// chunk's rows.
 #include <cuda.h>
 
 #include <algorithm>
