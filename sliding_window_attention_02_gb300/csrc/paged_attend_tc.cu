@@ -991,7 +991,9 @@ bool make_pages_maps(const PagesView& pv, PagesMaps* maps) {
   const uint64_t rows = (uint64_t)pv.pages * pv.Hkv * pv.P;
   const uint32_t box = (uint32_t)std::min(pv.P, BN);
   return make_tmap_rows_bf16(&maps->k, pv.K, pv.d, rows, box) &&
-         make_tmap_rows_bf16(&maps->v, pv.V, pv.d, rows, box);
+         make_tmap_rows_bf16(&maps->v, pv.V, pv.d, rows, box) &&
+         make_tmap_rows_bf16(&maps->k32, pv.K, pv.d, rows, std::min(box, 32u)) &&
+         make_tmap_rows_bf16(&maps->v32, pv.V, pv.d, rows, std::min(box, 32u));
 }
 
 bool paged_attend_tc_supported(const PagesView& pv) {

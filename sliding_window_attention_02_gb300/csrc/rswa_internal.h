@@ -242,10 +242,10 @@ struct AttendArgs {
 cudaError_t launch_paged_append(const PagesView& pv, const BatchArgs& ba, const void* k,
                                 int64_t k_stride, const void* v, int64_t v_stride,
                                 cudaStream_t s);
-// Tensor maps of a bf16 pool (boxes of a page's rows, at most 128): the pool stays
-// where it is, so a handle makes them once.
+// Tensor maps of a bf16 pool (boxes of a page's rows, at most 128; at most 32): the pool
+// stays where it is, so a handle makes them once.
 struct PagesMaps {
-  CUtensorMap k, v;
+  CUtensorMap k, v, k32, v32;
 };
 bool make_pages_maps(const PagesView& pv, PagesMaps* maps);
 // maps: of bf16 pools, else unused.
