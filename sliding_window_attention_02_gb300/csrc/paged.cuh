@@ -45,12 +45,18 @@ struct PagedSeq {
   }
 };
 
-// Page `x` of sequence b; one outside the pool is flagged and read as page 0.
-__device__ __forceinline__ int page_at(const PagesView& pv, const BatchArgs& ba, int b, int x) {
-  const int p = ba.table[(size_t)b * ba.max_pages + x];
+// Page `x` of sequence b; one outside the pool is flagged and read as page 0.  In two
+// halves, its read and what waits for it.
+__device__ __forceinline__ int page_entry(const BatchArgs& ba, int b, int x) {
+  return ba.table[(size_t)b * ba.max_pages + x];
+}
+__device__ __forceinline__ int page_of_entry(const PagesView& pv, int p) {
   if ((unsigned)p < (unsigned)pv.pages) return p;
   flag_error(pv.err, kErrBadBatch);
   return 0;
+}
+__device__ __forceinline__ int page_at(const PagesView& pv, const BatchArgs& ba, int b, int x) {
+  return page_of_entry(pv, page_entry(ba, b, x));
 }
 
 // Tokens that some of the tokens a0 .. a1 see: [0, p) and [w0, end), p <= w0 <= end.

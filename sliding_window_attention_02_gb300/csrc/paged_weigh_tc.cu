@@ -22,8 +22,9 @@
 // their lse, warp 7 planner.  TMEM: S^T twice.  Every wait is bounded; on a timeout the
 // CTA drains its copies and MMAs, frees TMEM and sets the pool's device flag.
 //
-// Measured: 64 tokens of 32 / 8 heads over 256..4096 (262 MB) 46 us, 0.84 of the measured
-// copy, the rest start and end; on the CUDA cores 231.  64 rows of 10 heads over 10272
+// Measured: 64 tokens of 32 / 8 heads over 256..4096 (262 MB) 43.8 us, 0.88 of the measured
+// copy, the rest start and end (46.2 with a tile's pages looked up when its turn comes);
+// on the CUDA cores 231.  64 rows of 10 heads over 10272
 // tokens 10.8 (9.5 in a graph) for a floor of 4.0: start, plan and first keys 5, a
 // tile's turn 1; on the CUDA cores 174.  NR is 64 where one tile of 16 does not hold a
 // chunk's rows.
@@ -301,14 +302,25 @@ paged_weigh_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     for (int k = 0; ok && has_segment(k); ++k) {
       const Segment w = segs[k % NSEG];
       const Hull hull(w.L - w.T, w.L - 1, w.m, n);
+      // Whether somebody sees a token of this lane's box of tile j, and its page's entry,
+      // read a tile ahead.
+      auto seen = [&](int j) {
+        const int t0 = w.tile(j) * BN + lane * sh.box;
+        return lane * sh.box < BN && hull.meets(t0, t0 + sh.box);
+      };
+      auto entry = [&](int j) {
+        if (j >= w.j1 || !seen(j)) return 0;
+        return page_entry(ba, w.b, (w.tile(j) * BN + lane * sh.box) >> pv.log2P);
+      };
+      int next = entry(w.j0);
       for (int j = w.j0; ok && j < w.j1; ++j) {
+        const int at = next;
+        next = entry(j + 1);
         int lo, hi;
         row_tiles(w, j, sh.by_npt, n, lo, hi);
         if (lo >= hi) continue;
         const int t0 = w.tile(j) * BN + lane * sh.box;
-        int page = -1;                         // of this lane's box; -1: nobody sees it
-        if (lane * sh.box < BN && hull.meets(t0, t0 + sh.box))
-          page = page_at(pv, ba, w.b, t0 >> pv.log2P);
+        const int page = seen(j) ? page_of_entry(pv, at) : -1;
         const int row = (page * pv.Hkv + w.kvh) * pv.P + (t0 & (pv.P - 1));
         const uint32_t bytes =
             __popc(__ballot_sync(0xffffffffu, page >= 0)) * (uint32_t)(sh.box * 128 * NSUB);
