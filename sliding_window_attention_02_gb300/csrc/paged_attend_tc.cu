@@ -157,22 +157,22 @@ __device__ __forceinline__ float* half_partial(void* ws, int p, int first, int h
 }
 
 // A row's `chunks` chunks of 32 columns, and its lse, from the partials of CTAs first ..
-// last, in their order; the reads of two partials are on their way together.
+// last (two at least), in their order; the reads of two are on their way together.
+// The same sums in the same order as join_own's: which of them joins a unit depends on
+// when its CTAs end, the result does not.
 template <int D>
 __device__ __noinline__ void join_row(void* ws, int first, int last, int half, int r, int chunks,
                                       __nv_bfloat16* orow, float* lse) {
   auto part = [&](int p) { return half_partial(ws, p, first, half, D); };
-  float M = -INFINITY, L = 0.f;
-#pragma unroll 1
-  for (int p = first; p <= last; p += 2) {
-    const float* a = part(p) + (size_t)BM * D + r;
-    const float* b = part(min(p + 1, last)) + (size_t)BM * D + r;
-    const float m0 = __ldcg(a), l0 = __ldcg(a + BM);
-    const float m1 = p < last ? __ldcg(b) : -INFINITY, l1 = p < last ? __ldcg(b + BM) : 0.f;
-    const float mn = fmaxf(M, fmaxf(m0, m1)), ref = mn == -INFINITY ? 0.f : mn;
-    L = fmaf(l1, ex2(m1 - ref), fmaf(l0, ex2(m0 - ref), L * ex2(M - ref)));
-    M = mn;
-  }
+  auto stat = [&](int p) { return part(p) + (size_t)BM * D + r; };     // m, and l BM behind
+  const float m0 = __ldcg(stat(first)), l0 = __ldcg(stat(first) + BM);
+  const float m1 = __ldcg(stat(first + 1)), l1 = __ldcg(stat(first + 1) + BM);
+  float M = fmaxf(m0, m1);
+  for (int p = first + 2; p <= last; ++p) M = fmaxf(M, __ldcg(stat(p)));
+  const float ref = M == -INFINITY ? 0.f : M;
+  float L = fmaf(l1, ex2(m1 - ref), __fmul_rn(l0, ex2(m0 - ref)));
+  for (int p = first + 2; p <= last; ++p)
+    L = fmaf(__ldcg(stat(p) + BM), ex2(__ldcg(stat(p)) - ref), L);
   const float inv = 1.f / L;
 #pragma unroll 1
   for (int c = 0; c < chunks; ++c) {
@@ -185,8 +185,8 @@ __device__ __noinline__ void join_row(void* ws, int first, int last, int half, i
       const float* b = part(min(p + 1, last));
       const float4* s0 = reinterpret_cast<const float4*>(a) + (size_t)c * 8 * BM + r;
       const float4* s1 = reinterpret_cast<const float4*>(b) + (size_t)c * 8 * BM + r;
-      const float w0 = ex2(__ldcg(a + (size_t)BM * D + r) - M);
-      const float w1 = p < last ? ex2(__ldcg(b + (size_t)BM * D + r) - M) : 0.f;
+      const float w0 = ex2(__ldcg(stat(p)) - ref);
+      const float w1 = p < last ? ex2(__ldcg(stat(p + 1)) - ref) : 0.f;
       float4 u[8], v[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -232,13 +232,11 @@ __device__ __noinline__ void join_own(void* ws, int first, int last, int half, i
     M = fmaxf(M, __ldcg(part(p) + (size_t)BM * D + r));
   const float ref = M == -INFINITY ? 0.f : M;
   const float own = ex2(M0 - ref), w1 = ex2(m1 - ref);
-  L = fmaf(l1, w1, L * own);
+  L = fmaf(l1, w1, __fmul_rn(L, own));
   for (int p = first + 2; live && p <= last; ++p) {
     const float* a = part(p) + (size_t)BM * D + r;
-    L = fmaf(__ldcg(a + BM), ex2(__ldcg(a) - M), L);
+    L = fmaf(__ldcg(a + BM), ex2(__ldcg(a) - ref), L);
   }
-  a0 *= own;
-  a1 *= own;
   const float inv = 1.f / L;
 #pragma unroll 1
   for (int c = 0; c < chunks; ++c) {
@@ -263,6 +261,8 @@ __device__ __noinline__ void join_own(void* ws, int first, int last, int half, i
       for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(ov[e]), a1, x[e]);
     }
     if (!live) continue;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] = __fmul_rn(x[e], own);
     auto add = [&](const float4* w, float wp) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -275,7 +275,7 @@ __device__ __noinline__ void join_own(void* ws, int first, int last, int half, i
     add(v, w1);
 #pragma unroll 1
     for (int p = first + 2; p <= last; ++p) {
-      const float wp = ex2(__ldcg(part(p) + (size_t)BM * D + r) - M);
+      const float wp = ex2(__ldcg(part(p) + (size_t)BM * D + r) - ref);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = __ldcg(columns(part(p), c) + (size_t)e * BM);
       add(v, wp);

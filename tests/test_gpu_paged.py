@@ -691,6 +691,85 @@ def test_captured_step_replays_with_new_lengths(cuda_lib, H, Hkv):
     assert c.pages.sync_status() == 0
 
 
+def test_captured_eviction_replays_with_new_weights(cuda_lib):
+    """In place, in a graph: the lengths, weights and pages are read when it runs,
+    and a call outside the graph on the same workspace leaves it as it was."""
+    rswa = cuda_lib
+    L0 = [700, 90, 4300]
+    c = Case(rswa, L0, [0, 0, 0], 2, 2, 64, 32, seed=5)
+    w = torch.rand(3, 2, c.width * 32, device="cuda")
+    kept = torch.empty(3, 2, 128, dtype=torch.int32, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        c.pages.evict(c.batch, w, 128, 3, 20, kept=kept)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            c.pages.evict(c.batch, w, 128, 3, 20, kept=kept)
+    s.synchronize()
+    for i, L in enumerate((L0, [129, 40, 0], [699, 1, 4299], [128, 90, 4300])):
+        assert all(x <= y for x, y in zip(L, L0))
+        for b in range(3):
+            c.write(b, L0[b])
+        c.lens.copy_(ints(L))
+        w.uniform_()
+        wn = w.cpu().numpy()
+        if i % 2:
+            with torch.cuda.stream(s):
+                s.wait_stream(torch.cuda.current_stream())
+                c.pages.evict(c.batch, w, 128, 3, 20, kept=kept)
+        else:
+            graph.replay()
+        torch.cuda.synchronize()
+        for b in range(3):
+            n = min(L[b], 128)
+            for h in range(2):
+                want = paged.evict(wn[b, h, :L[b]], 128, 3, 20)
+                assert kept[b, h].tolist() == want + [-1] * (128 - n)
+                at = torch.tensor(want, dtype=torch.long, device="cuda")
+                assert torch.equal(c.tokens(c.Kp, b, n)[:, h], c.K[b][at, h])
+                assert torch.equal(c.tokens(c.Vp, b, n)[:, h], c.V[b][at, h])
+                np.testing.assert_array_equal(w[b, h, :n].cpu().numpy(), wn[b, h, want])
+    assert c.pages.sync_status() == 0
+
+
+def test_large_and_small_calls_overlap(cuda_lib):
+    """Tiles of many rows, single tokens, weights and evictions of other pools on four
+    streams at once."""
+    rswa = cuda_lib
+    big = Case(rswa, [3000, 700], [600, 1], 10, 10, 128, 64, seed=1)
+    few = Case(rswa, [900] * 40, [1] * 40, 10, 10, 128, 32, seed=2)
+    cut = Case(rswa, [5000, 60], [0, 0], 4, 4, 64, 16, seed=3)
+    (ob, lb), (of, _) = big.attend(), few.attend()
+    w0 = torch.rand(2, 4, cut.width * 16, device="cuda")
+    w_big = torch.zeros(2, 10, big.width * 64, device="cuda")
+    big.pages.weigh(big.batch, big.q, lb, w_big, 0.0)
+    want = [paged.evict(w0[b, h, :n].cpu().numpy(), 300, 4, 30) for b, n in ((0, 5000), (1, 60)) for h in range(4)]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(8):
+        o1, o2 = torch.empty_like(ob), torch.empty_like(of)
+        w1, w2 = torch.zeros_like(w_big), w0.clone()
+        kept = torch.empty(2, 4, 300, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        big.pages.attend(big.batch, big.q, o1, stream=streams[0])
+        few.pages.attend(few.batch, few.q, o2, stream=streams[1])
+        big.pages.weigh(big.batch, big.q, lb, w1, 0.0, stream=streams[2])
+        cut.pages.evict(cut.batch, w2, 300, 4, 30, kept=kept, stream=streams[3])
+        big.pages.attend(big.batch, big.q, o1, stream=streams[0])
+        outs.append((o1, o2, w1, kept))
+    torch.cuda.synchronize()
+    for o1, o2, w1, kept in outs:
+        assert torch.equal(o1, ob) and torch.equal(o2, of)
+        for b, n in ((0, 3000), (1, 700)):
+            assert torch.equal(w1[b, :, :n], w_big[b, :, :n])
+        got = [[x for x in row if x >= 0] for row in kept.flatten(0, 1).tolist()]
+        assert got == want
+    for c in (big, few, cut):
+        assert c.pages.sync_status() == 0
+
+
 def test_two_layers_share_a_batch_and_calls_overlap(cuda_lib):
     """Two pools, one description; two streams, each its own workspace."""
     rswa = cuda_lib
