@@ -516,7 +516,8 @@ RSWA_API int rswa_pages_attend_workspace(rswa_pages* pages, int64_t rows, size_t
  *   workspace  of rswa_pages_attend_workspace bytes, 256-byte aligned.
  * Tokens that a row sees must be finite; every other row of a page may hold
  * anything.  On the tensor cores (bf16 but for small work) the softmax weights are
- * rounded to bf16 for their product with the values, not for the sum.
+ * rounded to bf16 for their product with the values, not for the sum.  Sums are made
+ * in a fixed order: the result does not vary from call to call.
  * Errors: RSWA_EHANDLE, RSWA_EINVAL, RSWA_ECAPACITY (workspace too small),
  * RSWA_ECUDA.
  */
