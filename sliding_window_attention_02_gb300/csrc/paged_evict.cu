@@ -114,7 +114,7 @@ evict_select_kernel(PagesView pv, BatchArgs ba, EvictArgs a, int chunks) {
     }
     return;                                              // as do all of the cluster
   }
-  if (peers > 1) cluster_arrive_release();
+  if (peers > 1) cluster_arrive_relaxed();               // tells only that it has begun
   auto meet = [&]() {
     if (peers > 1) {
       cluster_arrive_release();
