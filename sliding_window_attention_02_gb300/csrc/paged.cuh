@@ -110,8 +110,9 @@ struct PagedUnit {
 //
 // A group, the units of the same rows, is one entry of the sums that find a CTA's
 // range: 32 groups at a time, a lane each.  What a launch waits for before its first
-// loads is this code, run once: it is kept short (40 pages, one sequence of 16
-// groups: 2.7 us; with sums sequence by sequence and 64-bit divisions 4 to 5).
+// loads is this code, run once: it is kept short (40 pages, one sequence of 16 groups:
+// 2.7 us; with sums sequence by sequence and 64-bit divisions 4 to 5; with divisions by G
+// and by a unit's rows instead of multiplications 24 ragged chunks took 67.8 us for 66.2).
 template <int TILE, int COST, int SPLIT, int EXTRA, int MINCOST>
 struct PagedPlan {
   static_assert(MINCOST >= COST + EXTRA && COST >= SPLIT, "a range holds a tile at least");
