@@ -515,9 +515,11 @@ RSWA_API int rswa_pages_attend_workspace(rswa_pages* pages, int64_t rows, size_t
  *              logits, or NULL.
  *   workspace  of rswa_pages_attend_workspace bytes, 256-byte aligned.
  * Tokens that a row sees must be finite; every other row of a page may hold
- * anything.  On the tensor cores (bf16 but for small work) the softmax weights are
- * rounded to bf16 for their product with the values, not for the sum.  Sums are made
- * in a fixed order: the result does not vary from call to call.
+ * anything.  Of bf16 caches, chunks of many rows are done in tiles in which the softmax
+ * weights are rounded to bf16 for their product with the values, not for the sum; in
+ * calls of few rows (at most 8 / (heads / kv_heads) tokens a sequence on average, or
+ * small work) weights are good to 2^-16.  Sums are made in a fixed order: the result does
+ * not vary from call to call.
  * Errors: RSWA_EHANDLE, RSWA_EINVAL, RSWA_ECAPACITY (workspace too small),
  * RSWA_ECUDA.
  */

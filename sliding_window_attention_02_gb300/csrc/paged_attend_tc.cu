@@ -781,8 +781,11 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
               tmem_st16(o_addr + c, ov);
             }
           }
-          // P over S, and its sum.  P is rounded to bf16 for the product with V,
-          // whose two operands are of one 16-bit type; l sums it unrounded.
+          // P over S, and its sum.  P is rounded to bf16 (2^-8 of it) for the product with
+          // V, whose two operands are of one 16-bit type; l sums it unrounded.  What the
+          // rounding takes off as a second operand doubles that product: 4096 rows behind 6176
+          // tokens 174.6 us instead of 137.6, 24 ragged chunks 73.1 instead of 65.6, for an
+          // error of the output of 0.0017 instead of 0.0023.
           const float nref = (m_run == -INFINITY) ? 0.f : -m_run;
           const uint64_t sl2x2 = f2_pack(sl2, sl2), nref2 = f2_pack(nref, nref);
           uint64_t ps2 = 0;

@@ -7,6 +7,11 @@
 // the accumulators in TMEM.  A key tile is read once for all rows of the unit and takes two short
 // products, so the launch runs at the rate at which tiles arrive.
 //
+// A weight is two bf16 parts, as the product with V wants 16-bit operands: it rounded,
+// and what that took off.  Together they are off by 2^-16 of it.  The second parts are the
+// columns that 8 rows leave free, so they cost no product (64 tokens of 10 heads 72.9 us with
+// and without, of 32 / 8 heads 85.0 and 85.2).
+//
 // Keys are fetched in boxes of a page's rows, at most 32, without the boxes in which no
 // row sees a token (64 tokens over 2048, 1500 in the prefix and a window of 128, pages of
 // 256: 86.6 us, boxes of 128 rows 89.2, of 16 86.1, but 104.9 for 103.6 without a mask); V^T
@@ -64,12 +69,14 @@ struct Smem {
   static constexpr int NSUB = D / 64;
   static constexpr uint32_t kTile = NSUB * kSub;
   static constexpr int NS = 6 / NSUB;          // ring slots (a K or a V tile)
-  // Queries and weights as the MMAs' N rows: 8 are kept, the other eight are whatever
-  // follows them here, with results that nobody reads.
+  // Queries as the MMAs' N rows: 8 are kept, the other eight are whatever follows them
+  // here, with results that nobody reads.  Weights: row g's rounded to bf16, and in row 8 +
+  // g what that took off.
   static constexpr uint32_t kNAtom = kRows * 128;                 // [kRows][64] bf16
+  static constexpr uint32_t kPAtom = 2 * kNAtom;                  // [NQ][64]
   static constexpr uint32_t OFF_RING = 0;
   static constexpr uint32_t OFF_Q = OFF_RING + NS * kTile;        // two of [kRows][D]
-  static constexpr uint32_t OFF_P = OFF_Q + 2 * 2 * kNAtom;       // two of [kRows][128]
+  static constexpr uint32_t OFF_P = OFF_Q + 2 * 2 * kNAtom;       // two of [NQ][128]
   static constexpr int B_FULL = 0;             // NS
   static constexpr int B_EMPTY = B_FULL + NS;  // NS
   static constexpr int B_S = B_EMPTY + NS;     // 2: S^T(j) in TMEM
@@ -87,14 +94,13 @@ struct Smem {
   static constexpr int B_SEGFREE = B_SEG + NSEG;   // NSEG left by the end warps (128)
   static constexpr int B_FIN = B_SEGFREE + NSEG;
   static constexpr int NBAR = B_FIN + 1;
-  static constexpr uint32_t OFF_BAR = OFF_P + 2 * 2 * kNAtom;
+  static constexpr uint32_t OFF_BAR = OFF_P + 2 * 2 * kPAtom;
   static constexpr uint32_t OFF_FLAGS = OFF_BAR + 8 * NBAR;       // NS words
   static constexpr uint32_t OFF_SEG = (OFF_FLAGS + 4 * NS + 15) & ~15u;
   static constexpr uint32_t OFF_ML = OFF_SEG + NSEG * 128;        // [2][NQ] m, [2][4][NQ] l
   static constexpr uint32_t OFF_RED = OFF_ML + (2 * NQ + 2 * 4 * NQ) * 4;   // [2][4][NQ] max
   static constexpr uint32_t OFF_MISC = OFF_RED + 2 * 4 * NQ * 4;
   static constexpr uint32_t kBytes = OFF_MISC + 32 + 1024;        // + alignment slack
-  static_assert(OFF_MISC - OFF_BAR >= 1024, "8 rows behind the last weights");
   // The value operand's second 64 columns: the tile's other atom, or, at head_dim 64,
   // the rows 8 further on (columns of O^T that belong to nobody): 1 KB past the ring
   // at most.
@@ -156,7 +162,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmK,
                        AttendArgs a, Shape sh, uint64_t wait_ns) {
   using SM = Smem<D>;
   constexpr int NSUB = SM::NSUB, NS = SM::NS;
-  constexpr uint32_t kTile = SM::kTile, kNAtom = SM::kNAtom;
+  constexpr uint32_t kTile = SM::kTile, kNAtom = SM::kNAtom, kPAtom = SM::kPAtom;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -284,13 +290,13 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmK,
         if (!wait(SM::B_P + (pj & 1), pj >> 1)) return false;
         tc_fence_after();
         const uint32_t vb = sb + SM::OFF_RING + slot * kTile;
-        const uint32_t pb = sb + SM::OFF_P + (pj & 1) * 2 * kNAtom;
+        const uint32_t pb = sb + SM::OFF_P + (pj & 1) * 2 * kPAtom;
         uint32_t acc = pfirst ? 0u : 1u;
 #pragma unroll
         for (int k = 0; k < BN / 16; ++k)
           if (flags >> k & 1u) {
             mma_bf16_ss(tmem + TM_O + 16 * (ps & 1), desc_sw128(vb + k * 2048, SM::kAtomStep, 1024),
-                        desc_sw128(pb + (k >> 2) * kNAtom + (k & 3) * 32, 16, 1024), idesc_o,
+                        desc_sw128(pb + (k >> 2) * kPAtom + (k & 3) * 32, 16, 1024), idesc_o,
                         acc);
             acc = 1u;
           }
@@ -460,8 +466,10 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmK,
             tmem_ld16(tmem + lane_off + TM_O + 16 * (s & 1), ov);
             tmem_wait_ld();
 #pragma unroll
-            for (int g = 0; g < NG; ++g)
+            for (int g = 0; g < NG; ++g) {
               ov[g] = __float_as_uint(__uint_as_float(ov[g]) * alpha[g]);
+              ov[kRows + g] = __float_as_uint(__uint_as_float(ov[kRows + g]) * alpha[g]);
+            }
             tmem_st16(tmem + lane_off + TM_O + 16 * (s & 1), ov);
             tmem_wait_st();
           }
@@ -471,14 +479,17 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmK,
           ok = false;
           break;
         }
-        uint8_t* pbuf = smem + SM::OFF_P + (j & 1) * 2 * kNAtom;
+        uint8_t* pbuf = smem + SM::OFF_P + (j & 1) * 2 * kPAtom;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           const float ref = (m_ref[g] == -INFINITY) ? 0.f : m_ref[g];
           const float p = fast_exp2(sc[g] - ref);
           l_t[g] += p;
-          *reinterpret_cast<__nv_bfloat16*>(pbuf + sw128_off(g, tid, kNAtom)) =
-              __float2bfloat16(p);
+          const __nv_bfloat16 hi = __float2bfloat16(p);
+          uint8_t* to = pbuf + sw128_off(g, tid, kPAtom);
+          *reinterpret_cast<__nv_bfloat16*>(to) = hi;
+          *reinterpret_cast<__nv_bfloat16*>(to + kNAtom) =
+              __float2bfloat16(p - __bfloat162float(hi));
         }
         // A value row that no row of the unit sees, in a step that holds others that
         // one does: zero, as 0 x NaN is NaN.
@@ -568,6 +579,10 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmK,
         lg[g] = (lw[g] + lw[NQ + g]) + (lw[2 * NQ + g] + lw[3 * NQ + g]);
       }
       mbar_arrive(bar(SM::B_MLFREE + (s & 1)));
+      float og[NG];                                     // both parts of the weights
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+        og[g] = __uint_as_float(ov[g]) + __uint_as_float(ov[kRows + g]);
       // Row g of the unit is chunk row f / G, query head kvh * G + f % G.
       auto out_row = [&](int g) {
         const int f = w.f0 + g;
@@ -579,7 +594,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmK,
         for (int g = 0; g < NG; ++g) {
           if (g >= rows) break;
           const int64_t row = out_row(g);
-          if (mine) o[row * D + e] = __float2bfloat16(__uint_as_float(ov[g]) / lg[g]);
+          if (mine) o[row * D + e] = __float2bfloat16(og[g] / lg[g]);
           if (e == 0 && a.lse) a.lse[row] = (mg[g] + log2f(lg[g])) * kLn2;
         }
       } else {
@@ -587,7 +602,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmK,
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           if (g >= rows) break;
-          if (mine) P[g * (D + 4) + e] = __uint_as_float(ov[g]);
+          if (mine) P[g * (D + 4) + e] = og[g];
           if (e == 0) {
             P[g * (D + 4) + D] = mg[g];
             P[g * (D + 4) + D + 1] = lg[g];

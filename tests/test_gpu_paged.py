@@ -201,6 +201,25 @@ def test_attend_sharp_softmax(cuda_lib):
             check_attend(c, *c.attend(), rows_of=[0, 77, T - 1])
 
 
+@pytest.mark.parametrize("H,Hkv,d,T", [(10, 10, 128, 1), (32, 8, 128, 1), (16, 2, 64, 1), (10, 10, 64, 2),
+                                       (10, 10, 128, 4), (8, 4, 128, 4)])
+def test_attend_few_rows_keeps_its_weights(cuda_lib, H, Hkv, d, T):
+    """In units of few rows the weights are two bf16 parts: a rounding takes 2^-8 of a weight
+    off, and of that its second part all but 2^-8.  The output's own rounding is what is left."""
+    g = np.random.default_rng(H * d + T)
+    L = [int(x) for x in g.integers(T, 700, 64)]
+    c = Case(cuda_lib, L, [T] * 64, H, Hkv, d, 32, BF, [40] * 64, 300, seed=T, uniform=H != 8)
+    c.m = [min(40, l) for l in L]
+    o, _ = c.attend()
+    for b in range(64):
+        K, V = f64(c.K[b]), f64(c.V[b])
+        ro, _, mass, size = paged.attend(f64(c.q[c.rows(b)]), K, V, c.m[b], c.n)
+        tol = (2 * logit_error(c, size, min(L[b], c.n + c.m[b]))[..., None] + HALF[BF] ** 2) * mass
+        tol = tol + HALF[BF] * (np.abs(ro) + tol)
+        err = np.abs(f64(o[c.rows(b)]) - ro)
+        assert (err <= tol).all(), f"sequence {b}: {(err / tol).max():.3g} of the bound"
+
+
 def test_attend_holes_are_not_read(cuda_lib):
     """Pages between the prefix and the window are gone, masked rows NaN."""
     for dtype, H, Hkv, T in ((BF, 32, 8, 1), (BF, 10, 10, 1), (BF, 32, 8, 37), (F32, 4, 2, 5),
