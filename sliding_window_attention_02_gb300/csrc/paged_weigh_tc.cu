@@ -69,7 +69,9 @@ struct Smem {
   static constexpr int B_S = B_QE + 2;         // 2: S^T in TMEM
   static constexpr int B_SFREE = B_S + 2;      // 2: S^T read (128)
   static constexpr int B_SEG = B_SFREE + 2;    // NSEG segments handed over
-  static constexpr int B_SEGFREE = B_SEG + NSEG;   // NSEG left by the softmax warps (128)
+  // NSEG read by the key, MMA and query warps and left by the softmax warps (3 + 128): a
+  // segment that nobody sees makes none of them wait for another
+  static constexpr int B_SEGFREE = B_SEG + NSEG;
   static constexpr int B_FIN = B_SEGFREE + NSEG;
   static constexpr int NBAR = B_FIN + 1;
   static constexpr uint32_t OFF_MISC = OFF_BAR + 8 * NBAR;
@@ -265,10 +267,9 @@ paged_weigh_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     for (int k = 0; k < SM::NBAR; ++k)
       mbar_init(bar(k), k >= SM::B_QF && k < SM::B_QE     ? 2u
                         : k >= SM::B_QE && k < SM::B_S    ? 129u
-                        : (k >= SM::B_SFREE && k < SM::B_SEG) ||
-                                (k >= SM::B_SEGFREE && k < SM::B_FIN)
-                            ? 128u
-                            : 1u);
+                        : k >= SM::B_SFREE && k < SM::B_SEG  ? 128u
+                        : k >= SM::B_SEGFREE && k < SM::B_FIN ? 131u
+                                                             : 1u);
     *abort_flag = 0;
     *never = 0;
     fence_mbar_init();
@@ -291,6 +292,13 @@ paged_weigh_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
   auto has_segment = [&](int k) {
     return wait_all(SM::B_SEG + k % NSEG, k / NSEG) && segs[k % NSEG].j1 > 0;
   };
+  // Segment k, copied by a whole warp, which then needs its slot no longer.
+  auto take_segment = [&](int k) {
+    const Segment w = segs[k % NSEG];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(SM::B_SEGFREE + k % NSEG));
+    return w;
+  };
   const int n = ba.window;
 
   if (warp == kProducerWarp) {
@@ -300,8 +308,9 @@ paged_weigh_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
     uint32_t gi = 0;
     bool ok = true;
     for (int k = 0; ok && has_segment(k); ++k) {
-      const Segment w = segs[k % NSEG];
-      const Hull hull(w.L - w.T, w.L - 1, w.m, n);
+      const Segment w = take_segment(k);
+      Hull hull(w.L - w.T, w.L - 1, w.m, n);
+      if (w.T == 0) hull.p = hull.w0 = hull.end = 0;     // nobody sees a token
       // Whether somebody sees a token of this lane's box of tile j, and its page's entry,
       // read a tile ahead.
       auto seen = [&](int j) {
@@ -354,6 +363,7 @@ paged_weigh_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       for (int k = 0; ok; ++k) {
         if (!wait(SM::B_SEG + k % NSEG, k / NSEG) || segs[k % NSEG].j1 == 0) break;
         const Segment w = segs[k % NSEG];
+        mbar_arrive(bar(SM::B_SEGFREE + k % NSEG));
         const bool keep = w.nrt == 1;          // one row tile serves the whole segment
         bool have = false;
         for (int j = w.j0; ok && j < w.j1; ++j) {
@@ -424,7 +434,7 @@ paged_weigh_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       return true;
     };
     for (int k = 0; ok && has_segment(k); ++k) {
-      const Segment w = segs[k % NSEG];
+      const Segment w = take_segment(k);
       bool have = false;
       for (int j = w.j0; ok && j < w.j1; ++j) {
         int lo, hi;

@@ -464,6 +464,33 @@ def test_weigh_shapes(cuda_lib, H, Hkv, d, dtype):
         check_weigh(c, lse, old, w, 1.0)
 
 
+@pytest.mark.parametrize("H,Hkv", [(8, 8), (32, 8)])
+@pytest.mark.parametrize("decay", [0.0, 0.5, 1.0])
+@pytest.mark.parametrize("rows", [0, 1, 3])
+def test_weigh_many_segments(cuda_lib, H, Hkv, decay, rows):
+    """More (sequence, KV head) than the planner hands over at once to any CTA, most of
+    which nobody sees, so that the warps that sum run ahead of those that fetch."""
+    g = np.random.default_rng(rows)
+    B = 400
+    L = [int(x) for x in g.integers(rows + 1, 900, B)]
+    live = set(g.choice(B, 25, replace=False).tolist()) if rows else set()
+    T = [rows if b in live else 0 for b in range(B)]
+    m = [int(x) for x in g.integers(0, 60, B)]
+    c = Case(cuda_lib, L, T, H, Hkv, 64, 16, BF, m, 70, seed=rows, hole=1 << 30)
+    c.m = [min(x, l) for x, l in zip(m, L)]
+    lse = torch.empty(0, H, device="cuda")
+    if rows:
+        _, lse = c.attend()
+    old = torch.rand(B, Hkv, c.width * 16, device="cuda")
+    if decay == 0.0:
+        old[:] = float("nan")                          # not read
+    for _ in range(3):
+        w = old.clone()
+        c.pages.weigh(c.batch, c.q, lse, w, decay)
+        assert c.pages.sync_status() == 0
+        check_weigh(c, lse, old, w, decay)
+
+
 def test_weigh_holes_are_not_read(cuda_lib):
     for dtype, T in ((BF, 1), (BF, 40), (F32, 3)):
         c = Case(cuda_lib, [600], [T], 8, 2, 128, 16, dtype, [5], 70, seed=T, hole=1 << 30)
