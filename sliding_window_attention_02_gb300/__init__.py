@@ -38,6 +38,7 @@ __all__ = [
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_HERE)
 RSWA_F32, RSWA_BF16 = 0, 1
+RSWA_EDEVICE = 6               # of rswa_status
 _LIB = None
 
 _c_i64 = ctypes.c_int64
@@ -869,6 +870,13 @@ class _Workspaces:
         self.at[stream] = (w.data_ptr(), w.numel())
         return self.at[stream]
 
+    def zero(self):
+        """All of them as they were made; waits for it."""
+        import torch
+        for _, w in self.all:
+            w.zero_()
+        torch.cuda.synchronize(self.index)
+
 
 _NO_WORKSPACE = (None, 0, -1)
 
@@ -1009,7 +1017,13 @@ class RswaPages:
             raise RswaError(status, "rswa_pages_evict")
 
     def sync_status(self):
-        return rswa_pages_sync_status(self.handle)
+        """rswa_pages_sync_status: waits for the device; the status code, not raised.
+        After RSWA_EDEVICE the pool's own workspaces are zeroed again; one that the
+        caller passes is the caller's to zero."""
+        status = rswa_pages_sync_status(self.handle)
+        if status == RSWA_EDEVICE:
+            self._attend_ws.zero()
+        return status
 
     def slabs(self):
         """(K, V) views of the pools [pages][kv_heads][page_size][d]."""

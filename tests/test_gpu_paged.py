@@ -335,6 +335,43 @@ def test_waits_that_run_out(cuda_lib, H, Hkv, d, T):
     assert c.pages.sync_status() == 0
 
 
+@pytest.mark.parametrize("H,Hkv,T", [(10, 10, 1), (32, 8, 1), (32, 8, 70)])
+def test_own_workspaces_after_waits_that_run_out(cuda_lib, H, Hkv, T):
+    """The pool's own workspaces, of two streams and of a graph: sync_status leaves them
+    fit for the next call."""
+    rswa = cuda_lib
+    c = Case(rswa, [900] * 40, [T] * 40, H, Hkv, 128, 32, seed=1, uniform=True)
+    want, lse = c.attend()
+    check_attend(c, want, lse, rows_of=[0])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    o = torch.empty_like(want)
+    with torch.cuda.stream(s):
+        c.pages.attend(c.batch, c.q, o, lse)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            c.pages.attend(c.batch, c.q, o, lse)
+    s.synchronize()
+    told = 0
+    for limit in [1] + [250 * x for x in range(1, 120)]:   # some CTAs give up, others have ended
+        rswa.rswa_debug_set_wait_limit_ns(limit)
+        try:
+            c.attend()
+            c.pages.attend(c.batch, c.q, o, lse, stream=s)
+        finally:
+            rswa.rswa_debug_set_wait_limit_ns(0)
+        status = c.pages.sync_status()
+        assert status in (0, RSWA_EDEVICE)
+        told += status != 0
+        assert torch.equal(c.attend()[0], want), limit
+        o.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want), limit
+        assert c.pages.sync_status() == 0
+    assert told > 0
+
+
 def test_attend_strided_queries_in_place_and_streams(cuda_lib):
     c = Case(cuda_lib, [200, 90], [30, 3], 10, 10, 128, 32, seed=2)
     qkv = torch.full((33, 30, 128), float("nan"), dtype=BF, device="cuda")
