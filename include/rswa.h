@@ -447,7 +447,8 @@ typedef struct rswa_pages rswa_pages;
  * has are neither read nor written.
  * A row range outside 0 .. rows or of negative length, a length outside 0 ..
  * max_pages * page_size or below T_b sets the device flag (RSWA_EDEVICE of
- * rswa_pages_sync_status), and the sequence is taken as empty.  A page outside
+ * rswa_pages_sync_status), and the sequence is taken as empty; the others are served
+ * (where a wrong `starts` makes two of them claim a row, results are undefined).  A page outside
  * the pool sets the flag where it is read or written; a write is left out, results
  * that depend on a read are undefined.  Only the entries of pages that hold a
  * token which is read or written are looked at: others may hold anything.

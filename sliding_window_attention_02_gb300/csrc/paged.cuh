@@ -45,6 +45,36 @@ struct PagedSeq {
   }
 };
 
+// The sequence of chunk row `row`, found by a whole warp; T is 0 where it is nobody's.  Of
+// 32 sequences, every lane reads one: where their rows are and what the one that is found
+// needs, in one go.  Each range is looked at for itself, so that a wrong one, which need not
+// lie between its neighbours, hides no other.
+__device__ __forceinline__ int find_row(const PagesView& pv, const BatchArgs& ba, int row,
+                                        PagedSeq& s) {
+  if (!ba.starts) {
+    const int b = row / ba.each;
+    s.load(pv, ba, b);
+    return b;
+  }
+  const int lane = (int)(threadIdx.x & 31);
+  s.row0 = s.T = s.L = s.m = 0;
+  for (int b0 = 0; b0 < ba.B; b0 += 32) {
+    PagedSeq mine;
+    mine.row0 = mine.T = mine.L = mine.m = 0;
+    if (b0 + lane < ba.B) mine.load(pv, ba, b0 + lane);
+    const uint32_t on =
+        __ballot_sync(0xffffffffu, row >= mine.row0 && row < mine.row0 + mine.T);
+    if (!on) continue;
+    const int src = __ffs(on) - 1;
+    s.row0 = __shfl_sync(0xffffffffu, mine.row0, src);
+    s.T = __shfl_sync(0xffffffffu, mine.T, src);
+    s.L = __shfl_sync(0xffffffffu, mine.L, src);
+    s.m = __shfl_sync(0xffffffffu, mine.m, src);
+    return b0 + src;
+  }
+  return 0;
+}
+
 // Page `x` of sequence b; one outside the pool is flagged and read as page 0.  In two
 // halves, its read and what waits for it.
 __device__ __forceinline__ int page_entry(const BatchArgs& ba, int b, int x) {

@@ -45,22 +45,9 @@ paged_append_kernel(PagesView pv, BatchArgs ba, const char* __restrict__ k, int6
     }
   };
   fetch(0);
-  int b = 0;
-  if (ba.starts) {
-    // the sequences that end at or before the row
-    for (int b0 = 0; b0 < ba.B; b0 += 32) {
-      const int i = b0 + lane;
-      const uint32_t on = __ballot_sync(0xffffffffu, i < ba.B && ba.starts[i + 1] <= row);
-      b += __popc(on);
-      if (on != 0xffffffffu) break;
-    }
-  } else {
-    b = row / ba.each;
-  }
-  if (b >= ba.B) return;                       // a row past the last sequence
   PagedSeq s;
-  s.load(pv, ba, b);
-  if (row < s.row0 || row >= s.row0 + s.T) return;
+  const int b = find_row(pv, ba, row, s);
+  if (s.T == 0) return;                        // nobody's row
   const int a = s.L - s.T + row - s.row0;
   const int page = ba.table[(size_t)b * ba.max_pages + (a >> pv.log2P)];
   if ((unsigned)page >= (unsigned)pv.pages) {

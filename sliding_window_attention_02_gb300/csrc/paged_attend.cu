@@ -157,32 +157,8 @@ paged_attend_kernel(PagesView pv, BatchArgs ba, AttendArgs a) {
 #pragma unroll
     for (int e = 0; e < EPL; ++e) qf[r][e] *= sl2;
   }
-  // The row's sequence.  Of 32 sequences, every lane reads one: where their rows end
-  // and what the one that is found needs, in one go.
   PagedSeq s;
-  s.row0 = s.T = s.L = s.m = 0;
-  int b = 0;
-  if (ba.starts) {
-    for (int b0 = 0; b0 < ba.B; b0 += 32) {
-      PagedSeq mine;
-      mine.row0 = mine.T = mine.L = mine.m = 0;
-      const int x = b0 + lane;
-      if (x < ba.B) mine.load(pv, ba, x);
-      const uint32_t on =
-          __ballot_sync(0xffffffffu, row >= mine.row0 && row < mine.row0 + mine.T);
-      if (!on) continue;
-      const int src = __ffs(on) - 1;
-      b = b0 + src;
-      s.row0 = __shfl_sync(0xffffffffu, mine.row0, src);
-      s.T = __shfl_sync(0xffffffffu, mine.T, src);
-      s.L = __shfl_sync(0xffffffffu, mine.L, src);
-      s.m = __shfl_sync(0xffffffffu, mine.m, src);
-      break;
-    }
-  } else {
-    b = row / ba.each;
-    s.load(pv, ba, b);
-  }
+  const int b = find_row(pv, ba, row, s);
   if (s.T == 0) return;                        // nobody's row; as do all of the cluster
   const int tok = s.L - s.T + row - s.row0, m = s.m;
   const Hull hull(tok, tok, m, n);

@@ -943,6 +943,41 @@ def test_bad_descriptions_are_flagged(cuda_lib):
             assert (c.pages.sync_status() == RSWA_EDEVICE) == (value != 4), (what, value)
 
 
+@pytest.mark.parametrize("H,Hkv,dtype", [(8, 2, BF), (4, 4, F32)])
+@pytest.mark.parametrize("B,at", [(4, 1), (4, 2), (40, 5), (70, 33), (70, 64)])
+@pytest.mark.parametrize("value", [10 ** 6, -7])
+def test_a_wrong_range_in_the_middle_hides_no_other(cuda_lib, H, Hkv, dtype, B, at, value):
+    """starts[at] out of range: the sequences before and behind it are empty, every other
+    one is stored, attended and weighed."""
+    g = np.random.default_rng(B + at)
+    T = [int(x) for x in g.integers(1, 4, B)]
+    L = [int(t + x) for t, x in zip(T, g.integers(0, 60, B))]
+    c = Case(cuda_lib, L, T, H, Hkv, 64, 16, dtype, seed=at, stored=False)
+    c.batch.starts[at] = value
+    c.pages.append(c.batch, c.k, c.v)
+    assert c.pages.sync_status() == RSWA_EDEVICE
+    for b in range(B):
+        old = L[b] - T[b]
+        for pool, rows in ((c.Kp, c.K), (c.Vp, c.V)):
+            got = c.tokens(pool, b, L[b])
+            assert torch.equal(got[:old], rows[b][:old])
+            if b in (at - 1, at):
+                assert torch.isnan(got[old:]).all(), b
+            else:
+                assert torch.equal(got[old:], rows[b][old:]), b
+    o, lse = c.attend()
+    assert c.pages.sync_status() == RSWA_EDEVICE
+    for b in (at - 1, at):
+        assert torch.isnan(o[c.rows(b)]).all()
+    c.T = [0 if b in (at - 1, at) else t for b, t in enumerate(T)]
+    check_attend(c, o, lse)
+    lse = torch.nan_to_num(lse)                        # of rows that nobody has
+    w = torch.zeros(B, Hkv, c.width * 16, device="cuda")
+    c.pages.weigh(c.batch, c.q, lse, w)
+    assert c.pages.sync_status() == RSWA_EDEVICE
+    check_weigh(c, lse, torch.zeros_like(w), w, 1.0)
+
+
 def test_refusals(cuda_lib):
     rswa = cuda_lib
     c = Case(rswa, [100, 60], [3, 2], 8, 2, 128, 16, seed=2)
