@@ -159,6 +159,11 @@ paged_attend_kernel(PagesView pv, BatchArgs ba, AttendArgs a) {
   }
   PagedSeq s;
   const int b = find_row(pv, ba, row, s);
+  if (ba.starts && blockIdx.x == 0)            // wrong descriptions behind it are told too
+    for (int x = 32 + threadIdx.x; x < ba.B; x += kWarps * 32) {
+      PagedSeq other;
+      other.load(pv, ba, x);
+    }
   if (s.T == 0) return;                        // nobody's row; as do all of the cluster
   const int tok = s.L - s.T + row - s.row0, m = s.m;
   const Hull hull(tok, tok, m, n);

@@ -978,6 +978,25 @@ def test_a_wrong_range_in_the_middle_hides_no_other(cuda_lib, H, Hkv, dtype, B, 
     check_weigh(c, lse, torch.zeros_like(w), w, 1.0)
 
 
+@pytest.mark.parametrize("H,Hkv,dtype,rows", [(8, 2, BF, 1), (8, 2, BF, 300), (10, 10, BF, 40), (4, 4, F32, 2),
+                                              (4, 4, F32, 900)])
+@pytest.mark.parametrize("at,value", [(35, -1), (69, 10 ** 6), (64, -(1 << 31))])
+def test_wrong_lengths_without_rows_are_flagged(cuda_lib, H, Hkv, dtype, rows, at, value):
+    """All rows are the first sequence's; a length behind the first 32 is wrong."""
+    L, T = [1000] + [20] * 69, [rows] + [0] * 69
+    c = Case(cuda_lib, L, T, H, Hkv, 64, 16, dtype, seed=1)
+    want, lse = c.attend()
+    assert c.pages.sync_status() == 0
+    c.lens[at] = value
+    o, _ = c.attend()
+    assert c.pages.sync_status() == RSWA_EDEVICE
+    assert torch.equal(o, want)
+    c.pages.append(c.batch, c.k, c.v)
+    assert c.pages.sync_status() == RSWA_EDEVICE
+    c.pages.weigh(c.batch, c.q, lse, torch.zeros(70, Hkv, c.width * 16, device="cuda"))
+    assert c.pages.sync_status() == RSWA_EDEVICE
+
+
 def test_refusals(cuda_lib):
     rswa = cuda_lib
     c = Case(rswa, [100, 60], [3, 2], 8, 2, 128, 16, seed=2)
