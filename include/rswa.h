@@ -547,7 +547,8 @@ RSWA_API int rswa_pages_weigh(rswa_pages* pages, const rswa_batch* batch, int64_
 
 /*
  * Device bytes of workspace of rswa_pages_evict (it need not be initialised; calls
- * that may overlap need one each).  Host-only.  Errors: RSWA_EHANDLE, RSWA_EINVAL.
+ * that may overlap need one each).  batch * kv_heads below 2^31.  Host-only.  Errors:
+ * RSWA_EHANDLE, RSWA_EINVAL.
  */
 RSWA_API int rswa_pages_evict_workspace(rswa_pages* pages, int batch, int64_t budget,
                                         size_t* out_bytes);

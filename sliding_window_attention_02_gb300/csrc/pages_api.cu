@@ -274,6 +274,8 @@ int rswa_pages_evict_workspace(rswa_pages* pages, int batch, int64_t budget, siz
   if (!live(pages)) return RSWA_EHANDLE;
   if (!out_bytes || batch < 1 || batch > (1 << 20) || budget < 1 || budget > (int64_t(1) << 30))
     return RSWA_EINVAL;
+  // as many heads as rswa_pages_evict takes of any budget; more of them wrap the bytes
+  if ((int64_t)batch * pages->pv.Hkv >= (int64_t(1) << 31)) return RSWA_EINVAL;
   *out_bytes = paged_evict_workspace(pages->pv, batch, budget, false);
   return RSWA_OK;
 }

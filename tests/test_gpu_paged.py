@@ -1064,6 +1064,19 @@ def test_refusals(cuda_lib):
     assert pages.sync_status() == 4
 
 
+def test_eviction_workspaces_that_wrap(cuda_lib):
+    """Heads times budget whose bytes pass 64 bits."""
+    rswa = cuda_lib
+    pages = rswa.RswaPages(1, 16, 4096, 64, rswa.RSWA_BF16)
+    for batch, budget in ((1 << 20, 1 << 30), (1 << 20, 1), (1 << 19, 1 << 30)):
+        with pytest.raises(rswa.RswaError) as e:
+            rswa.rswa_pages_evict_workspace(pages.handle, batch, budget)
+        assert e.value.status == 1
+    for batch, budget in (((1 << 19) - 1, 1 << 30), (1000, 1 << 30), (3, 7)):
+        # the kept tokens, and a word for every part of the move
+        assert rswa.rswa_pages_evict_workspace(pages.handle, batch, budget) >= batch * 4096 * (budget + budget // 64) * 4
+
+
 def test_no_rows(cuda_lib):
     c = Case(cuda_lib, [100, 60], [0, 0], 8, 2, 128, 16, seed=2)
     c.pages.append(c.batch, c.k, c.v)
