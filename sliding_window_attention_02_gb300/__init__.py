@@ -893,6 +893,9 @@ class RswaPages:
         self.buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
         ix = self.buf.get_device()
         with torch.cuda.device(ix):
+            # its block may be one that the current stream still writes, and the flag is
+            # zeroed on another stream
+            torch.cuda.current_stream().synchronize()
             self.handle = rswa_pages_create(pages, page_size, heads, self.kv_heads, head_dim,
                                             dtype, self.buf)
         self._shape = (heads, self.kv_heads, head_dim,

@@ -1077,6 +1077,24 @@ def test_eviction_workspaces_that_wrap(cuda_lib):
         assert rswa.rswa_pages_evict_workspace(pages.handle, batch, budget) >= batch * 4096 * (budget + budget // 64) * 4
 
 
+def test_a_pool_in_memory_that_is_still_written(cuda_lib):
+    """Made on a stream whose queued work writes the block that the pool then gets."""
+    rswa = cuda_lib
+    need = rswa.rswa_pages_footprint(300, 16, 4, 4, 64, rswa.RSWA_BF16)
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(s):
+            old = torch.empty(need, dtype=torch.uint8, device="cuda")
+            at = old.data_ptr()
+            torch.cuda._sleep(100_000_000)             # some 50 ms
+            old.fill_(1)
+            del old
+            pages = rswa.RswaPages(300, 16, 4, 64, rswa.RSWA_BF16)
+        assert pages.buf.data_ptr() == at
+        assert pages.sync_status() == 0
+        pages.close()
+
+
 def test_no_rows(cuda_lib):
     c = Case(cuda_lib, [100, 60], [0, 0], 8, 2, 128, 16, seed=2)
     c.pages.append(c.batch, c.k, c.v)
