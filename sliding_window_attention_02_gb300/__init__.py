@@ -629,6 +629,9 @@ class RswaCache:
         nbytes = rswa_cache_footprint_gqa(m, n, heads, self.kv_heads, head_dim,
                                           batch, dtype)
         self.buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        # its block may be one that the current stream still writes, and the state is
+        # zeroed on another stream
+        torch.cuda.current_stream(self.buf.device).synchronize()
         self.handle = rswa_cache_create_gqa(m, n, heads, self.kv_heads,
                                             head_dim, batch, dtype, self.buf)
         # what the checks of the draft-and-verify calls compare with

@@ -687,3 +687,25 @@ def test_varlen_prefill(cuda_lib):
             f64(Ks[b, :, max(m_list):])[:, filled].transpose(1, 0, 2),
             st["Kr"][filled])
         off += L
+
+
+def test_a_cache_in_memory_that_is_still_written(cuda_lib):
+    """Made on a stream whose queued work writes the block that the cache then
+    gets: its state and its slabs are zero all the same."""
+    rswa = cuda_lib
+    s = torch.cuda.Stream()
+    need = rswa.rswa_cache_footprint(400, 32, 4, 64, 2, rswa.RSWA_BF16)
+    for _ in range(3):
+        with torch.cuda.stream(s):
+            old = torch.empty(need, dtype=torch.uint8, device="cuda")
+            at = old.data_ptr()
+            torch.cuda._sleep(100_000_000)             # some 50 ms
+            old.fill_(1)
+            del old
+            cache = rswa.RswaCache(400, 32, 4, 64, 2, rswa.RSWA_BF16)
+        torch.cuda.synchronize()
+        assert cache.buf.data_ptr() == at
+        assert not cache.buf[:rswa.rswa_cache_kv_offsets(cache.handle)[0]].any()
+        assert not any(x.any() for x in cache.slabs())
+        assert cache.sync_status() == 0
+        cache.close()
