@@ -940,7 +940,9 @@ class RswaPages:
 
     def attend_workspace(self, rows):
         """A workspace for attend calls of up to `rows` rows, like any tensor made on
-        torch's current stream."""
+        torch's current stream.  The calls of several pools (a model's layers) that run
+        one after the other can share one: the largest of theirs serves all, where each
+        pool keeps up to 40 MB for a stream by itself."""
         import torch
         return torch.zeros(rswa_pages_attend_workspace(self.handle, rows),
                            dtype=torch.uint8, device=self.buf.device)
@@ -949,7 +951,9 @@ class RswaPages:
         """Attention of the chunk's rows over the pages (see rswa_pages_attend): q
         of [rows][heads][d] rows (possibly part of longer ones), o contiguous, lse
         float32 [rows][heads] or None.  workspace: from attend_workspace; None: one
-        kept for the stream; a capture takes one that a call there has made."""
+        kept for the stream; a capture takes one that a call there has made.  So
+        graphs captured on one stream, and the calls made on it, share theirs: where
+        they may run at the same time, pass each a workspace of its own."""
         H, Hkv, d, dt, ix = self._shape
         rows = q.shape[0]
         self._check_batch(batch)
@@ -991,12 +995,20 @@ class RswaPages:
         if status:
             raise RswaError(status, "rswa_pages_weigh")
 
+    def evict_workspace(self, sequences, budget):
+        """A workspace for evict calls of so many sequences and this budget, like any
+        tensor made on torch's current stream."""
+        import torch
+        return torch.empty(rswa_pages_evict_workspace(self.handle, sequences, budget),
+                           dtype=torch.uint8, device=self.buf.device)
+
     def evict(self, batch, weights, budget, first=0, last=0, table_out=None, weights_out=None,
               kept=None, workspace=None, stream=None):
         """Cut every sequence down to `budget` tokens: its first and last ones and
         the heaviest of the others, in their order (see rswa_pages_evict).  In
         place, or to the pages of table_out; weights_out: weights itself where
-        None; kept: int32 [B][kv_heads][budget] for the tokens' former indices."""
+        None; kept: int32 [B][kv_heads][budget] for the tokens' former indices;
+        workspace: from evict_workspace, None: one kept for the stream, as attend's."""
         ix = self._shape[4]
         B, width = batch.shape
         self._check_batch(batch)

@@ -898,6 +898,71 @@ def test_workspaces(cuda_lib):
             c.attend()
 
 
+def test_eviction_with_a_workspace_of_its_own(cuda_lib):
+    """On two streams at once, and in graphs that replay at the same time."""
+    cases = [Case(cuda_lib, [700, 90, 4300], [0, 0, 0], 2, 2, 64, 32, seed=i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    ws = [c.pages.evict_workspace(3, 128) for c in cases]
+    ws[0].fill_(0x5a)                                  # any bits
+    w = [torch.rand(3, 2, c.width * 32, device="cuda") for c in cases]
+    kept = [torch.empty(3, 2, 128, dtype=torch.int32, device="cuda") for _ in cases]
+    graphs = []
+    capture = torch.cuda.Stream()
+    for c, s, x, k in zip(cases, ws, w, kept):
+        with torch.cuda.stream(capture):
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1], stream=capture):
+                c.pages.evict(c.batch, x, 128, 3, 20, kept=k, workspace=s)
+    for i in range(4):
+        for c, x in zip(cases, w):
+            x.uniform_()
+            for b in range(3):
+                c.write(b, c.L[b])
+        wn = [x.cpu().numpy() for x in w]
+        torch.cuda.synchronize()
+        for c, s, x, k, st, g in zip(cases, ws, w, kept, streams, graphs):
+            if i % 2:
+                c.pages.evict(c.batch, x, 128, 3, 20, kept=k, workspace=s, stream=st)
+            else:
+                with torch.cuda.stream(st):
+                    g.replay()
+        torch.cuda.synchronize()
+        for c, x, k in zip(cases, wn, kept):
+            for b in range(3):
+                for h in range(2):
+                    want = paged.evict(x[b, h, :c.L[b]], 128, 3, 20)
+                    assert k[b, h].tolist() == want + [-1] * (128 - len(want))
+                    at = torch.tensor(want, dtype=torch.long, device="cuda")
+                    assert torch.equal(c.tokens(c.Kp, b, len(want))[:, h], c.K[b][at, h])
+            assert c.pages.sync_status() == 0
+
+
+def test_one_workspace_serves_several_pools(cuda_lib):
+    """Pools of unlike heads, one after the other and in a graph of all of them."""
+    cases = [Case(cuda_lib, L, T, H, Hkv, d, 32, dtype, seed=H) for H, Hkv, d, dtype, L, T in (
+        (10, 10, 128, BF, [900, 700], [300, 1]), (32, 8, 128, BF, [700] * 40, [1] * 40), (16, 2, 64, BF, [8000], [7]),
+        (4, 2, 64, F32, [90, 700], [3, 1]), (10, 10, 128, BF, [300], [1]))]
+    ws = max((c.pages.attend_workspace(sum(c.T)) for c in cases), key=torch.Tensor.numel)
+    outs = [c.attend(workspace=ws) for c in cases]
+    for c, (o, lse) in zip(cases, outs):
+        check_attend(c, o, lse, rows_of=[0, 6, 299])
+    again = [torch.empty_like(o) for o, _ in outs]
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=s):
+        for c, o in zip(cases, again):
+            c.pages.attend(c.batch, c.q, o, workspace=ws)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for (o, _), x in zip(outs, again):
+            assert torch.equal(o, x)
+            x.zero_()
+    for c in cases:
+        assert not c.pages._attend_ws.all              # none made beside it
+        assert c.pages.sync_status() == 0
+
+
 # ---------------------------------------------------------------------------
 # refusals
 # ---------------------------------------------------------------------------
