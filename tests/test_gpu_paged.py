@@ -963,6 +963,39 @@ def test_one_workspace_serves_several_pools(cuda_lib):
         assert c.pages.sync_status() == 0
 
 
+def test_calls_by_handle(cuda_lib):
+    """The functions that take a handle give what the class gives."""
+    rswa = cuda_lib
+    c = Case(rswa, [200, 90], [30, 3], 8, 2, 128, 32, seed=2, stored=False)
+    need = rswa.rswa_pages_footprint(c.pages.pages, 32, 8, 2, 128, rswa.RSWA_BF16)
+    buf = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    h = rswa.rswa_pages_create(c.pages.pages, 32, 8, 2, 128, rswa.RSWA_BF16, buf)
+    assert rswa.rswa_pages_kv_offsets(h) == rswa.rswa_pages_kv_offsets(c.pages.handle)
+    buf.copy_(c.pages.buf)
+    c.pages.append(c.batch, c.k, c.v)
+    rswa.rswa_pages_append(h, c.batch, c.k, 2 * 128, c.v, 2 * 128)
+    assert torch.equal(buf, c.pages.buf)
+    o, lse = c.attend()
+    o2, lse2 = torch.empty_like(o), torch.empty_like(lse)
+    ws = torch.zeros(rswa.rswa_pages_attend_workspace(h, 33), dtype=torch.uint8, device="cuda")
+    rswa.rswa_pages_attend(h, c.batch, c.q, 8 * 128, o2, ws, lse2)
+    assert torch.equal(o2, o) and torch.equal(lse2, lse)
+    w = torch.rand(2, 2, c.width * 32, device="cuda")
+    w2 = w.clone()
+    c.pages.weigh(c.batch, c.q, lse, w, 0.5)
+    rswa.rswa_pages_weigh(h, c.batch, c.q, 8 * 128, lse, w2, 0.5)
+    assert torch.equal(w2, w)
+    kept, kept2 = (torch.empty(2, 2, 50, dtype=torch.int32, device="cuda") for _ in range(2))
+    c.pages.evict(c.batch, w, 50, 4, 9, kept=kept)
+    ws = torch.empty(rswa.rswa_pages_evict_workspace(h, 2, 50), dtype=torch.uint8, device="cuda")
+    rswa.rswa_pages_evict(h, c.batch, w2, 50, 4, 9, w2, ws, kept=kept2)
+    assert torch.equal(w2, w) and torch.equal(kept2, kept) and torch.equal(buf, c.pages.buf)
+    assert rswa.rswa_pages_sync_status(h) == 0
+    rswa.rswa_pages_destroy(h)
+    with pytest.raises(rswa.RswaError):
+        rswa.rswa_pages_append(h, c.batch, c.k, 2 * 128, c.v, 2 * 128)
+
+
 # ---------------------------------------------------------------------------
 # refusals
 # ---------------------------------------------------------------------------
