@@ -486,7 +486,8 @@ RSWA_API int rswa_pages_destroy(rswa_pages* pages);
  * Store the chunk's keys and values in the sequences' pages.  k, v: `rows` rows of
  * [kv_heads][head_dim] elements, k_stride and v_stride elements apart (multiples
  * of 16 bytes, at least the row's own length), apart from the pool.
- * 0 <= rows, rows * heads < 2^31 (here and below); rows = 0 does nothing.
+ * 0 <= rows, rows * heads < 2^31 (here and below); rows = 0 does nothing, here and in
+ * rswa_pages_attend (rswa_pages_weigh then applies its decay).
  * Calls that write pages which others read or write are to be ordered by the
  * caller; calls on one pool may overlap otherwise.
  * Errors: RSWA_EHANDLE, RSWA_EINVAL, RSWA_ECUDA.

@@ -40,7 +40,7 @@
 // its products are 2048; beside it the start (plan and first loads, 12 to 15K cycles) and the
 // ends of the segments (8 to 12K, a join 13K).  4096 rows of 10 heads behind 6176 tokens:
 // 137 us, 172 GFLOP at 0.66 of the measured cuBLAS rate; 24 sequences of 1 to 512 rows of
-// 32 / 8 heads, window 1000: 65.4.  What carried it: MMAs issued by an elected lane (20 cycles each; a lane chosen by
+// 32 / 8 heads, window 1000: 65.6.  What carried it: MMAs issued by an elected lane (20 cycles each; a lane chosen by
 // comparison 70), 155 -> 147; P handed over in two parts, 147 -> 144; a cut unit joined from its
 // first CTA's accumulators, 144 -> 139.5; costs of pairs and split tiles apart, 78.4 ->
 // 74.1 for the ragged chunks; the rolled softmax, 74.1 -> 67.0.

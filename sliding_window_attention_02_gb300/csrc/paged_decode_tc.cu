@@ -10,7 +10,7 @@
 // A weight is two bf16 parts, as the product with V wants 16-bit operands: it rounded,
 // and what that took off.  Together they are off by 2^-16 of it.  The second parts are the
 // columns that 8 rows leave free, so they cost no product (64 tokens of 10 heads 72.9 us with
-// and without, of 32 / 8 heads 85.0 and 85.2).
+// and without, of 32 / 8 heads 85.0 and 85.2; where units have 8 rows 62.9 and 61.8).
 //
 // Keys are fetched in boxes of a page's rows, at most 32, without the boxes in which no
 // row sees a token (64 tokens over 2048, 1500 in the prefix and a window of 128, pages of
@@ -34,8 +34,8 @@
 // lower ones' and belong to nobody.  Every wait is bounded; on a timeout the CTA drains
 // its copies and MMAs, frees TMEM and sets the pool's device flag.
 //
-// Bound by HBM and by the launch's start and end: 64 tokens of 10 heads over 300..2300 72.6 us, 429 MB at 0.87 of the measured
-// copy; of 32 / 8 heads over 256..4096, 507 MB, 84.2, 0.89.  Rows as M and keys as N, the
+// Bound by HBM and by the launch's start and end: 64 tokens of 10 heads over 300..2300 72.8 us, 429 MB at 0.87 of the measured
+// copy; of 32 / 8 heads over 256..4096, 507 MB, 85.0, 0.88.  Rows as M and keys as N, the
 // tile kernel, are slower (table of the paths in paged_attend.cu), and so were units of up to
 // 16 rows, as the softmax's columns are a thread's serial work.
 #include <cuda.h>
@@ -707,7 +707,9 @@ cudaError_t launch_g(const PagesView& pv, const PagesMaps& maps, const BatchArgs
 template <int D>
 cudaError_t launch_d(const PagesView& pv, const PagesMaps& maps, const BatchArgs& ba,
                      const AttendArgs& a, cudaStream_t s) {
-  // the most rows of a unit, where the host knows them
+  // The most rows of a unit, where the host knows them; with starts it does not, and takes 8:
+  // 64 single tokens of 10 heads over 2048 105.2 us and with starts 108.6, of 32 / 8 heads
+  // 87.1 and 89.7, 200 of 10 heads over 600 103.4 and 108.5.
   const int64_t rows = ba.starts ? kRows : (int64_t)ba.each * pv.G;
   if (rows <= 1) return launch_g<D, 1>(pv, maps, ba, a, s);
   if (rows <= 2) return launch_g<D, 2>(pv, maps, ba, a, s);

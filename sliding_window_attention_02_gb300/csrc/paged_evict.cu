@@ -7,7 +7,7 @@
 // fit.  Ties of that weight stay from the lowest index on.  Counts of what stays give
 // each kept token its place; the weights follow.  The second moves the rows, every
 // read of a CTA in flight at once: bound by HBM (0.95 of a copy's rate for 262 MB).
-// Both, one sequence of 10 heads, 10272 tokens to 2048: 13.0 us (a floor of 3.2); 48
+// Both, one sequence of 10 heads, 10272 tokens to 2048: 13.1 us (a floor of 3.2); 48
 // sequences of 8 heads, 400..2300 to 700: 51.5 (38.7).
 //
 // In place a row's place is at or before where it comes from, so a CTA's writes

@@ -22,10 +22,10 @@
 // their lse, warp 7 planner.  TMEM: S^T twice.  Every wait is bounded; on a timeout the
 // CTA drains its copies and MMAs, frees TMEM and sets the pool's device flag.
 //
-// Measured: 64 tokens of 32 / 8 heads over 256..4096 (262 MB) 43.8 us, 0.88 of the measured
+// Measured: 64 tokens of 32 / 8 heads over 256..4096 (262 MB) 44.5 us, 0.87 of the measured
 // copy, the rest start and end (46.2 with a tile's pages looked up when its turn comes);
 // on the CUDA cores 231.  64 rows of 10 heads over 10272
-// tokens 10.8 (9.5 in a graph) for a floor of 4.0: start, plan and first keys 5, a
+// tokens 10.9 (9.6 in a graph) for a floor of 4.0: start, plan and first keys 5, a
 // tile's turn 1; on the CUDA cores 174.  NR is 64 where one tile of 16 does not hold a
 // chunk's rows.
 #include <cuda.h>
