@@ -664,6 +664,36 @@ def test_evict_slices(cuda_lib, L, Hkv, in_place):
             run_evict(cuda_lib, L, Hkv, 64, 256, BF, budget, budget // 5, budget // 3, in_place, weights, seed=i)
 
 
+@pytest.mark.parametrize("L,spare", [([900, 30, 0], 0), ([900, 30, 0], 5), ([900, 30, 0], 60), ([700] * 80, 900),
+                                     ([3000, 5], 1100)])
+@pytest.mark.parametrize("budget", [1, 300, 2000])
+def test_evict_wide_tables(cuda_lib, L, spare, budget):
+    """Tables that could hold far more than the sequences: the weights' zeros behind what
+    stays reach the table's end, over the weights and beside them."""
+    B, Hkv, P = len(L), 2, 32
+    for in_place in (True, False):
+        c = Case(cuda_lib, L, [0] * B, Hkv, Hkv, 64, P, BF, seed=spare, spare=spare, hole=1 << 30)
+        w = torch.rand(B, Hkv, c.width * P, device="cuda")
+        wn, wo = w.cpu().numpy(), w if in_place else torch.full_like(w, 5.0)
+        kept = torch.full((B, Hkv, budget), 77, dtype=torch.int32, device="cuda")
+        K = c.Kp.clone()
+        c.pages.evict(c.batch, w, budget, budget // 5, budget // 3, weights_out=wo, kept=kept)
+        assert c.pages.sync_status() == 0
+        for b in range(B):
+            n = min(L[b], budget)
+            assert (wo[b, :, n:] == 0).all()
+            for h in range(Hkv):
+                want = paged.evict(wn[b, h, :L[b]], budget, budget // 5, budget // 3)
+                assert kept[b, h].tolist() == want + [-1] * (budget - n)
+                at = torch.tensor(want, dtype=torch.long, device="cuda")
+                assert torch.equal(c.tokens(c.Kp, b, n)[:, h], c.K[b][at, h])
+                np.testing.assert_array_equal(wo[b, h, :n].cpu().numpy(), wn[b, h, want])
+        if not in_place:
+            assert torch.equal(w.cpu(), torch.from_numpy(wn))
+        if budget >= max(L):
+            assert torch.equal(torch.nan_to_num(c.Kp, 9.0), torch.nan_to_num(K, 9.0))
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
