@@ -4,9 +4,9 @@
 // table[b][a / P], head by head.  A warp moves a row: its first reads of the row
 // are on their way while it looks for the row's sequence and page.  Bound by
 // HBM for long chunks, by latency (the sequence, its length, its page, each a
-// round trip) for single tokens.  Measured: 64 tokens of 8 KV heads 2.6 us in a graph,
-// 4.4 a call (the host); 3692 rows of 10 heads, 38 MB to move, 5.5 in a graph (the writes
-// stay in L2), 7.3 a call.  A warp for a row and not a CTA: a CTA's four rows are 16 to
+// round trip) for single tokens.  Measured: 64 tokens of 8 KV heads 2.5 us in a graph,
+// 4.4 a call (the host); 3692 rows of 10 heads, 38 MB to move, 5.3 in a graph (the writes
+// stay in L2), 7.2 a call.  A warp for a row and not a CTA: a CTA's four rows are 16 to
 // 40 KB in flight, and single tokens have no idle lanes' reads to wait for.
 #include <algorithm>
 
